@@ -66,6 +66,11 @@ extern "C" {
 #define SKV_DEV_BAD_HEAD 2       /* a ring head was outside [0, F); that cache was skipped */
 #define SKV_DEV_TAIL_OVERFLOW 4  /* tail_len + blk > tail_cap in verify; that cache was skipped */
 #define SKV_DEV_BAD_TAIL 8       /* tail_len < 0 in verify; that cache was skipped */
+#define SKV_DEV_NO_PAGE 16       /* kv_paged_plan: too few free pages; the requests left out were not planned */
+#define SKV_DEV_BAD_LEN 32       /* a request's length, start or queue state out of range; that request was skipped */
+#define SKV_DEV_BAD_PAGE 64      /* a page or slot outside the pool; read as zeros, not written */
+#define SKV_DEV_BAD_POS 128      /* kv_paged_write: a position outside the rope table; that token was skipped */
+#define SKV_DEV_TABLE_FULL 256   /* kv_paged_plan: a request outgrew its table row or the step's token rows */
 
 /*
  * One set of C independent caches (model layers x batch) of identical
@@ -369,6 +374,177 @@ int stream_attn_verify(const skv_cache* cache, int32_t n_q_head, int32_t blk,
                        const void* v_blk, void* out, const int32_t* target_ids,
                        const int32_t* draft_ids, int32_t* accept_len, int32_t* next_token,
                        void* ws, size_t ws_bytes, float sm_scale, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache: requests of different lengths over one pool of pages, for the
+ * text side of serving, where (unlike the streaming window) a token's
+ * position never changes.  Keys are therefore rotated once, when they are
+ * written, and the attention reads them as they are.  A step is: plan, then
+ * per layer write and attend; every layer shares the step's plan.
+ *
+ * "n_req requests, n_tok token rows": the new tokens of all requests are
+ * packed in request order; request b owns rows [q_start[b], q_start[b+1]).
+ * Rows at or past q_start[n_req] are padding: never read, never written.
+ *
+ * Tensors of 16-bit floats (dtype) are token-major: [n_tok][heads][d] with
+ * the heads of a token adjacent and `*_stride` elements from one token to the
+ * next (a multiple of 8, >= heads * d), so that q, k and v may be parts of one
+ * projection's output.  16-byte alignment as everywhere.
+ */
+#define SKV_BF16 0
+#define SKV_FP16 1
+
+/*
+ * k, v         device [n_page][Hkv][page_size][d]; keys rotated
+ * block_table  device int32 [n_req][max_block]: entry j of a request is the
+ *              page of its tokens [j * page_size, (j + 1) * page_size);
+ *              entries past its pages are not read
+ * rope         device fp32 [rope_len][d/2][2], row = position (any table of
+ *              skv_build_rope_table or skv_build_mrope_table), or NULL: no
+ *              rotation.  Only kv_paged_write reads it
+ * status       device int32 [1]: SKV_DEV_* bits, OR-ed in
+ * page_size is a multiple of 16; n_page * page_size and n_page * Hkv are
+ * below 2^31.  Rows of pages past a request's length may hold anything;
+ * those below it hold finite values.
+ */
+typedef struct skv_paged {
+  int32_t n_page;
+  int32_t page_size;
+  int32_t n_kv_head;
+  int32_t head_dim; /* 64 or 128 */
+  int32_t dtype;    /* SKV_BF16 or SKV_FP16 */
+  int32_t rope_len; /* 0 with rope NULL */
+  int32_t max_block;
+  int32_t reserved; /* 0 */
+  void* k;
+  void* v;
+  int32_t* block_table;
+  const float* rope;
+  int32_t* status;
+} skv_paged;
+
+/*
+ * kv_paged_plan -- pages, tables and slot maps of one step, from the
+ * requests' lengths, on the device.  Of `cache` it uses n_page, page_size,
+ * max_block, block_table and status.
+ *
+ * state:   device int32 [n_req + 2]: tokens that each request holds already,
+ *          then head and count of the free queue
+ * new_len: device int32 [n_req]: new tokens of each request this step (0: it
+ *          pauses); -1: it has finished, its pages are freed
+ * queue:   device int32 [n_page], ring of free pages: entries head, head + 1,
+ *          .. (mod n_page), count of them.  Initially all pages in any order.
+ *
+ * Writes, for request b holding c tokens and getting n:
+ *   block_table[b]  entries of the pages that tokens [c, c + n) newly need,
+ *                   taken from the queue's head in request order
+ *   queue           a finished request's pages, appended at the tail in
+ *                   request order (free from the next step on)
+ *   q_start         int32 [n_req + 1]: running sum of the new tokens
+ *   kv_len          int32 [n_req]: c + n, what paged_attn reads; 0 where the
+ *                   request has finished or could not be planned
+ *   next_state      int32 [n_req + 2]: the state after the step (a finished
+ *                   request holds 0 tokens).  Not `state` itself: the caller
+ *                   advances by copying it there, or drops it and plans again
+ *   position, slot  int32 [n_tok], per token row: its position c + i in its
+ *                   request, and page * page_size + row of its place in the
+ *                   pool; 0 and -1 in padding rows
+ * Integer results, the same on every run.  The call reads nothing that it
+ * writes, so it may be repeated on the same state.
+ *
+ * A request that needs pages when too few are left sets SKV_DEV_NO_PAGE; one
+ * whose table row is too short, or whose rows end past n_tok,
+ * SKV_DEV_TABLE_FULL.  It keeps its row span and its state, its slots are -1
+ * and its kv_len is 0, so that the calls below skip it and its output rows
+ * are zeros; those after it are planned if they can be.  A held length
+ * outside [0, max_block * page_size] or a new_len below -1 sets
+ * SKV_DEV_BAD_LEN: that request gets no rows, kv_len 0 and keeps its state.
+ * n_req <= SKV_PAGED_MAX_REQUESTS, n_tok <= 2^30.
+ */
+#define SKV_PAGED_MAX_REQUESTS 4096
+int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const int32_t* state,
+                  const int32_t* new_len, int32_t* queue, int32_t* q_start, int32_t* kv_len,
+                  int32_t* next_state, int32_t* position, int32_t* slot, void* stream);
+
+/*
+ * kv_paged_write -- a step's tokens into the pages, for one layer: k is
+ * rotated at the token's position (rotate-half, fp32, rounded once) and
+ * stored with v at the token's slot; q is rotated likewise into q_out
+ * (device [n_tok][Hq][d], contiguous; it may be q itself where q is
+ * contiguous).  Without a rope table they are copied.  Tokens with a negative
+ * slot are skipped: nothing of theirs is read or written.  A slot outside the
+ * pool sets SKV_DEV_BAD_PAGE, a position outside the table SKV_DEV_BAD_POS;
+ * both skip the token.  Two tokens with one slot leave either's row there.
+ * position may be NULL with rope NULL; q and q_out may both be NULL.
+ */
+int kv_paged_write(const skv_paged* cache, int32_t n_q_head, int32_t n_tok, const void* q,
+                   int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, const int32_t* position, const int32_t* slot, void* q_out,
+                   void* stream);
+
+/* Bytes of device workspace that paged_attn and cross_attn need: the same for
+ * every shape and length (it depends on the device's SM count alone). */
+size_t skv_attn_workspace_bytes(void);
+
+/*
+ * paged_attn -- attention of each request's new tokens over its pages: token
+ * i of request b, whose span has n rows, sits at position kv_len[b] - n + i
+ * and sees the request's tokens up to its own; its own K/V are in the pages
+ * already.  n = 1 is a decode step, n > 1 a prompt chunk or a drafted block;
+ * requests of a call may differ.
+ *
+ * q:    [n_tok][Hq][d], rotated (kv_paged_write's q_out); query head h reads
+ *       kv head h / (Hq / Hkv)
+ * out:  device [n_tok][Hq][d], contiguous: softmax(sm_scale q.k) v,
+ *       accumulated in fp32, rounded once
+ * lse:  device fp32 [Hq][n_tok], natural log of the sum of exp of the scaled
+ *       scores, or NULL
+ * A row that sees no key (kv_len 0) gets zeros and lse -inf.
+ * kv_len[b] outside [n, max_block * page_size] (0 apart) sets SKV_DEV_BAD_LEN
+ * and counts as 0; a span outside [0, n_tok] sets it and is skipped.  A table
+ * entry outside the pool sets SKV_DEV_BAD_PAGE; its keys and values count as
+ * zeros.
+ * ws: workspace of ws_bytes >= skv_attn_workspace_bytes(), zero-filled before
+ *     its first use and left ready by each call (zero it again after
+ *     SKV_DEV_TIMEOUT).  Calls that may run at the same time, captured graphs
+ *     among them, need workspaces of their own.
+ * Needs Hq % Hkv == 0, Hq / Hkv <= 128 and n_tok * Hq < 2^31.
+ */
+int paged_attn(const skv_paged* cache, int32_t n_q_head, int32_t n_req, int32_t n_tok,
+               const void* q, int64_t q_stride, const int32_t* q_start, const int32_t* kv_len,
+               void* out, float* lse, void* ws, size_t ws_bytes, float sm_scale, void* stream);
+
+/*
+ * An encoder's states (or any fixed context): keys and values packed
+ * token-major, [n_key][Hkv][d] with k_stride / v_stride elements from token
+ * to token.  Request b reads tokens [k_start[b], k_start[b] + k_len[b]);
+ * requests may share tokens, and a padded batch is k_start[b] = b * padded
+ * length.  Tokens that no request reads may hold anything.
+ */
+typedef struct skv_states {
+  int32_t n_key;
+  int32_t n_kv_head;
+  int32_t head_dim; /* 64 or 128 */
+  int32_t dtype;    /* SKV_BF16 or SKV_FP16 */
+  int64_t k_stride;
+  int64_t v_stride;
+  const void* k;
+  const void* v;
+  const int32_t* k_start; /* device int32 [n_req] */
+  const int32_t* k_len;   /* device int32 [n_req] */
+  int32_t* status;
+} skv_states;
+
+/*
+ * cross_attn -- attention of each request's queries to all of its states (no
+ * causal mask, no rotation).  q, q_start, out, lse, ws and the limits are
+ * paged_attn's; q rows may be of another length than the states.  A state
+ * range outside [0, n_key] sets SKV_DEV_BAD_LEN and counts as empty: zeros
+ * and lse -inf, as for k_len 0.
+ */
+int cross_attn(const skv_states* states, int32_t n_q_head, int32_t n_req, int32_t n_tok,
+               const void* q, int64_t q_stride, const int32_t* q_start, void* out, float* lse,
+               void* ws, size_t ws_bytes, float sm_scale, void* stream);
 
 #ifdef __cplusplus
 }

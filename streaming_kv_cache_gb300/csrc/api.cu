@@ -101,6 +101,7 @@ int check_insert_args(const skv_cache* cache, const void* k_new, const void* v_n
 }
 
 int record_cuda_error(cudaError_t e) { return cuda_fail(e); }
+int check_device() { return ::check_device(); }
 
 }  // namespace skv
 
@@ -119,6 +120,11 @@ const char* skv_status_string(int code) {
     case SKV_DEV_BAD_HEAD: return "device: ring head outside [0, F)";
     case SKV_DEV_TAIL_OVERFLOW: return "device: tail_len + blk exceeds tail_cap";
     case SKV_DEV_BAD_TAIL: return "device: negative tail_len";
+    case SKV_DEV_NO_PAGE: return "device: too few free pages";
+    case SKV_DEV_BAD_LEN: return "device: a request's length, start or queue state out of range";
+    case SKV_DEV_BAD_PAGE: return "device: a page or slot outside the pool";
+    case SKV_DEV_BAD_POS: return "device: a position outside the rope table";
+    case SKV_DEV_TABLE_FULL: return "device: a request outgrew its table row or the step's token rows";
     default: return code > 0 ? "device: several status bits set" : "unknown status";
   }
 }

@@ -56,5 +56,6 @@ size_t verify_ws_bytes(const Geom& g, int Hq, int blk);
 
 int check_insert_args(const skv_cache* cache, const void* k_new, const void* v_new);
 int record_cuda_error(cudaError_t e);
+int check_device();   // SKV_OK on an sm_103 device
 
 }  // namespace skv

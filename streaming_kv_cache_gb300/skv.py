@@ -17,13 +17,17 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "li
 SKV_OK, SKV_ERR_INVALID, SKV_ERR_UNSUPPORTED, SKV_ERR_CUDA, SKV_ERR_TOO_LARGE = 0, -1, -2, -3, -4
 SKV_NOALLOC_MAX_CACHE_VIEWS = 16384
 SKV_DEV_TIMEOUT, SKV_DEV_BAD_HEAD, SKV_DEV_TAIL_OVERFLOW, SKV_DEV_BAD_TAIL = 1, 2, 4, 8
+SKV_DEV_NO_PAGE, SKV_DEV_BAD_LEN, SKV_DEV_BAD_PAGE, SKV_DEV_BAD_POS, SKV_DEV_TABLE_FULL = 16, 32, 64, 128, 256
+SKV_PAGED_MAX_REQUESTS = 4096
+_DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1}   # SKV_BF16, SKV_FP16
 
 # every function the C header declares
 EXPORTS = ("skv_version", "skv_status_string", "skv_last_cuda_error", "skv_row_cap",
            "skv_build_rope_table", "skv_build_mrope_table", "kv_write_rows", "kv_stream_insert", "kv_stream_insert_noalloc",
            "stream_attn_prefill", "stream_attn_prefill_insert", "stream_attn_prefill_tail",
            "stream_attn_window",
-           "skv_verify_workspace_bytes", "stream_attn_verify")
+           "skv_verify_workspace_bytes", "stream_attn_verify",
+           "kv_paged_plan", "kv_paged_write", "skv_attn_workspace_bytes", "paged_attn", "cross_attn")
 
 
 class SkvError(RuntimeError):
@@ -48,6 +52,25 @@ class skv_cache(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class skv_paged(ctypes.Structure):
+    _fields_ = [("n_page", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv_head", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("rope_len", ctypes.c_int32),
+                ("max_block", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("rope", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
+class skv_states(ctypes.Structure):
+    _fields_ = [("n_key", ctypes.c_int32), ("n_kv_head", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_start", ctypes.c_void_p), ("k_len", ctypes.c_void_p),
+                ("status", ctypes.c_void_p)]
+
+
 _lib_handle = None
 
 
@@ -60,7 +83,7 @@ def lib():
                               % _LIB_PATH)
         L = ctypes.CDLL(_LIB_PATH)
         P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
-        cp = ctypes.POINTER(skv_cache)
+        cp, pp, I64 = ctypes.POINTER(skv_cache), ctypes.POINTER(skv_paged), ctypes.c_int64
         sig = {
             "skv_version": ([], ctypes.c_int),
             "skv_status_string": ([ctypes.c_int], ctypes.c_char_p),
@@ -80,6 +103,13 @@ def lib():
             "skv_verify_workspace_bytes": ([cp, I32, I32], SZ),
             "stream_attn_verify": ([cp, I32, I32, P, P, P, P, P, P, P, P, P, P, SZ,
                                     ctypes.c_float, P], ctypes.c_int),
+            "kv_paged_plan": ([pp, I32, I32, P, P, P, P, P, P, P, P, P], ctypes.c_int),
+            "kv_paged_write": ([pp, I32, I32, P, I64, P, I64, P, I64, P, P, P, P], ctypes.c_int),
+            "skv_attn_workspace_bytes": ([], SZ),
+            "paged_attn": ([pp, I32, I32, I32, P, I64, P, P, P, P, P, SZ, ctypes.c_float, P],
+                           ctypes.c_int),
+            "cross_attn": ([ctypes.POINTER(skv_states), I32, I32, I32, P, I64, P, P, P, P, SZ,
+                            ctypes.c_float, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -373,3 +403,292 @@ def stream_attn_verify(cache: StreamCache, tail_len: torch.Tensor, q_blk: torch.
         _ptr(accept_len) if ids else None, _ptr(next_token) if ids else None,
         _ptr(ws), ws.numel(), float(sm_scale), _stream()), "stream_attn_verify")
     return out, (accept_len if ids else None), (next_token if ids else None)
+
+
+# --------------------------------------------- paged cache, cross attention
+
+
+def _on_current(t, name):
+    """The tensor lives on the current device, where the call launches."""
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+
+
+def _rows(t, heads, d, dtype, name) -> int:
+    """Token stride of a token-major tensor [tokens][heads][d] whose heads of
+    a token are adjacent (a part of a wider projection's rows, say)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device.type != "cuda":
+        raise ValueError("%s must be on a CUDA device" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError("%s must have shape (tokens, %d, %d), got %s" % (name, heads, d, tuple(t.shape)))
+    n, (s0, s1, s2) = t.shape[0], t.stride()
+    if n == 0:
+        return heads * d
+    if s2 != 1 or (heads > 1 and s1 != d):
+        raise ValueError("%s must have its heads adjacent within a token" % name)
+    return s0 if n > 1 else heads * d
+
+
+class PagedPlan:
+    """The plan of one step (see kv_paged_plan in include/skv.h): int32
+    tensors q_start [n_req + 1], kv_len [n_req], next_state [n_req + 2],
+    position [n_tok] and slot [n_tok]."""
+
+    __slots__ = ("q_start", "kv_len", "next_state", "position", "slot")
+
+    def __init__(self, q_start, kv_len, next_state, position, slot):
+        self.q_start, self.kv_len, self.next_state = q_start, kv_len, next_state
+        self.position, self.slot = position, slot
+
+    @classmethod
+    def empty(cls, n_req, n_tok, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.empty(n_req + 1, **i32), torch.empty(n_req, **i32), torch.empty(n_req + 2, **i32),
+                   torch.empty(n_tok, **i32), torch.empty(n_tok, **i32))
+
+
+class PagedCache:
+    """A pool of pages for requests of different lengths, in device memory.
+
+    Tensors (owned by this object; they stay where they are for its life):
+      k, v         bf16 or fp16 [n_page][Hkv][page_size][d], per layer
+      block_table  int32 [n_req][max_block]  pages of each request
+      page_queue   int32 [n_page]            ring of free pages
+      state        int32 [n_req + 2]         tokens held per request, queue head and count
+      rope         fp32 [rope_len][d/2][2]   (cos, sin) table, or None
+      status       int32 [1]                 device status bits
+
+    theta gives the rope table of positions below max_block * page_size
+    (None: keys and queries are not rotated).  The layers of a model share
+    everything but k and v: layer(i) is the cache of one of them.
+    """
+
+    def __init__(self, n_page, page_size, Hkv, d, n_req, max_block, theta=None, dtype=torch.bfloat16,
+                 n_layer=1, device="cuda"):
+        dev = torch.device(device)
+        shape = (n_layer, n_page, Hkv, page_size, d)
+        i32 = dict(dtype=torch.int32, device=dev)
+        rope = None
+        if theta is not None:
+            rope = torch.empty((max_block * page_size, d // 2, 2), dtype=torch.float32, device=dev)
+            with torch.cuda.device(dev):
+                skv_build_rope_table(rope, theta)
+        state = torch.zeros((n_req + 2,), **i32)
+        state[-1] = n_page
+        self._k, self._v = (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
+        self._set(self._k[0], self._v[0], torch.zeros((n_req, max_block), **i32),
+                  torch.arange(n_page, **i32), state, rope, torch.zeros((1,), **i32), page_size)
+
+    @classmethod
+    def wrap(cls, k=None, v=None, block_table=None, page_queue=None, state=None, rope=None, status=None,
+             page_size=None):
+        """A cache over tensors that the caller owns.  k and v may be left
+        out where only kv_paged_plan is called, page_queue and state where it
+        is not; status is made where it is not given."""
+        self = cls.__new__(cls)
+        if status is None:
+            status = torch.zeros((1,), dtype=torch.int32, device=block_table.device)
+        self._k = k[None] if k is not None else None
+        self._v = v[None] if v is not None else None
+        self._set(k, v, block_table, page_queue, state, rope, status, page_size)
+        return self
+
+    def _set(self, k, v, block_table, page_queue, state, rope, status, page_size):
+        if (k is None) != (v is None):
+            raise ValueError("k and v come together")
+        if k is None and (page_queue is None or page_size is None):
+            raise ValueError("a cache without k and v needs page_queue and page_size")
+        if block_table is None or block_table.dim() != 2:
+            raise ValueError("block_table must be a (requests, max_block) tensor")
+        _need(block_table, block_table.shape, torch.int32, "block_table")
+        _need(status, (1,), torch.int32, "status")
+        hkv = d = code = 0
+        if k is not None:
+            if k.dim() != 4:
+                raise ValueError("k must have shape (pages, kv heads, page_size, d), got %s" % (tuple(k.shape),))
+            if k.dtype not in _DTYPE_CODE:
+                raise TypeError("k must be bfloat16 or float16, got %s" % k.dtype)
+            if page_size is not None and page_size != k.shape[2]:
+                raise ValueError("page_size %d, but k has pages of %d" % (page_size, k.shape[2]))
+            _need(k, k.shape, k.dtype, "k")
+            _need(v, k.shape, k.dtype, "v")
+            (n_page, hkv, page_size, d), code = k.shape, _DTYPE_CODE[k.dtype]
+        else:
+            n_page = page_queue.numel()
+        if page_queue is not None:
+            _need(page_queue, (n_page,), torch.int32, "page_queue")
+        if state is not None:
+            _need(state, (block_table.shape[0] + 2,), torch.int32, "state")
+        if rope is not None:
+            _need(rope, (rope.shape[0], d // 2, 2), torch.float32, "rope table")
+        for name, t in (("k", k), ("v", v), ("page_queue", page_queue), ("state", state), ("rope", rope),
+                        ("status", status)):
+            if t is not None and t.device != block_table.device:
+                raise ValueError("%s is on %s, block_table on %s" % (name, t.device, block_table.device))
+        self.k, self.v, self.block_table, self.page_queue = k, v, block_table, page_queue
+        self.state, self.rope, self.status = state, rope, status
+        self.n_page, self.page_size, self.Hkv, self.d = n_page, page_size, hkv, d
+        self.n_req, self.max_block = block_table.shape
+        ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        self._desc = skv_paged(n_page, page_size, hkv, d, code, rope.shape[0] if rope is not None else 0,
+                               self.max_block, 0, ptr(k), ptr(v), ptr(block_table), ptr(rope), ptr(status))
+        self._ref = ctypes.byref(self._desc)
+
+    def layer(self, i: int) -> "PagedCache":
+        """The cache of layer i: its own k and v, everything else shared."""
+        c = PagedCache.__new__(PagedCache)
+        c._k, c._v = self._k[i:i + 1], self._v[i:i + 1]
+        c._set(self._k[i], self._v[i], self.block_table, self.page_queue, self.state, self.rope, self.status,
+               self.page_size)
+        return c
+
+    def advance(self, plan: PagedPlan):
+        """Take the state that a plan leads to as the cache's state."""
+        self.state.copy_(plan.next_state)
+
+    def device_status(self) -> int:
+        return int(self.status.item())
+
+
+def kv_paged_plan(cache: PagedCache, new_len: torch.Tensor, n_tok: int,
+                  plan: PagedPlan | None = None) -> PagedPlan:
+    """The pages, tables and slot maps of one step: new_len[b] new tokens for
+    request b (-1: it has finished), packed into n_tok token rows.  The
+    cache's state stays until cache.advance(plan)."""
+    if cache.state is None or cache.page_queue is None:
+        raise ValueError("the cache has no state and page_queue to plan with")
+    n_req = cache.n_req
+    _need(new_len, (n_req,), torch.int32, "new_len")
+    _on_current(new_len, "new_len")
+    _on_current(cache.block_table, "the cache")
+    if plan is None:
+        plan = PagedPlan.empty(n_req, n_tok, new_len.device)
+    _need(plan.q_start, (n_req + 1,), torch.int32, "q_start")
+    _need(plan.kv_len, (n_req,), torch.int32, "kv_len")
+    _need(plan.next_state, (n_req + 2,), torch.int32, "next_state")
+    _need(plan.position, (n_tok,), torch.int32, "position")
+    _need(plan.slot, (n_tok,), torch.int32, "slot")
+    _check(lib().kv_paged_plan(cache._ref, n_req, n_tok, cache.state.data_ptr(), new_len.data_ptr(),
+                               cache.page_queue.data_ptr(), plan.q_start.data_ptr(), plan.kv_len.data_ptr(),
+                               plan.next_state.data_ptr(), plan.position.data_ptr(), plan.slot.data_ptr(),
+                               _stream()), "kv_paged_plan")
+    return plan
+
+
+def _need_pages(cache):
+    if cache.k is None:
+        raise ValueError("the cache has no k and v")
+
+
+def kv_paged_write(cache: PagedCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
+                   position: torch.Tensor | None, slot: torch.Tensor,
+                   q_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """A step's k (rotated) and v into the cache's pages; returns q rotated
+    (None for q None).  q, k and v are token-major and may be parts of one
+    projection's output."""
+    _need_pages(cache)
+    n, hkv, d, dt = k.shape[0], cache.Hkv, cache.d, cache.k.dtype
+    ks, vs = _rows(k, hkv, d, dt, "k"), _rows(v, hkv, d, dt, "v")
+    if v.shape[0] != n:
+        raise ValueError("k has %d tokens, v %d" % (n, v.shape[0]))
+    _need(slot, (n,), torch.int32, "slot")
+    if cache.rope is not None or position is not None:
+        _need(position, (n,), torch.int32, "position")
+    hq = qs = 0
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qs = _rows(q, hq, d, dt, "q")
+        if q.shape[0] != n:
+            raise ValueError("k has %d tokens, q %d" % (n, q.shape[0]))
+        if q_out is None:
+            q_out = torch.empty((n, hq, d), dtype=dt, device=q.device)
+        _need(q_out, (n, hq, d), dt, "q_out")
+        _on_current(q, "q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _on_current(k, "k")
+    _on_current(cache.k, "the cache")
+    _check(lib().kv_paged_write(cache._ref, hq, n, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(position),
+                                slot.data_ptr(), _ptr(q_out), _stream()), "kv_paged_write")
+    return q_out
+
+
+def attn_workspace(device="cuda") -> torch.Tensor:
+    """A zero-filled workspace for paged_attn and cross_attn (any shape)."""
+    with torch.cuda.device(torch.device(device)):
+        n = max(16, int(lib().skv_attn_workspace_bytes()))
+        return torch.zeros((n,), dtype=torch.uint8, device=device)
+
+
+def _attn_args(q, n_req, q_start, out, lse, ws):
+    n, hq, d = q.shape
+    _need(q_start, (n_req + 1,), torch.int32, "q_start")
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
+    _need(out, (n, hq, d), q.dtype, "out")
+    lse = _lse_2d(lse, hq, n, q.device)
+    _on_current(q, "q")
+    if ws is None:
+        ws = attn_workspace(q.device)
+    _need(ws, (ws.numel(),), torch.uint8, "ws")
+    _on_current(ws, "ws")
+    return out, lse, ws
+
+
+def _lse_2d(lse, hq, n, device):
+    if lse is True:
+        return torch.empty((hq, n), dtype=torch.float32, device=device)
+    if isinstance(lse, torch.Tensor):
+        _need(lse, (hq, n), torch.float32, "lse")
+        return lse
+    return None
+
+
+def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+               sm_scale: float, out: torch.Tensor | None = None, lse: torch.Tensor | bool | None = None,
+               ws: torch.Tensor | None = None):
+    """Attention of each request's new tokens over its pages (chunks and
+    single tokens together).  q is rotated already (kv_paged_write).  Returns
+    out (and lse [Hq][tokens] when asked for)."""
+    _need_pages(cache)
+    hq = q.shape[1] if q.dim() == 3 else 0
+    qs = _rows(q, hq, cache.d, cache.k.dtype, "q")
+    _need(kv_len, (cache.n_req,), torch.int32, "kv_len")
+    out, lse, ws = _attn_args(q, cache.n_req, q_start, out, lse, ws)
+    _on_current(cache.k, "the cache")
+    _check(lib().paged_attn(cache._ref, hq, cache.n_req, q.shape[0], q.data_ptr(), qs, q_start.data_ptr(),
+                            kv_len.data_ptr(), out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
+                            float(sm_scale), _stream()), "paged_attn")
+    return (out, lse) if lse is not None else out
+
+
+def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, k_start: torch.Tensor,
+               k_len: torch.Tensor, sm_scale: float, *, status: torch.Tensor, out: torch.Tensor | None = None,
+               lse: torch.Tensor | bool | None = None, ws: torch.Tensor | None = None):
+    """Attention of packed queries to each request's packed states k, v
+    [tokens][Hkv][d]: request b reads rows [k_start[b], k_start[b] + k_len[b]).
+    status collects device status bits.  Returns out (and lse when asked for)."""
+    if k.dim() != 3 or k.dtype not in _DTYPE_CODE:
+        raise ValueError("k must be a bfloat16 or float16 tensor (tokens, kv heads, d), got %s %s" % (k.dtype, tuple(k.shape)))
+    n_key, hkv, d = k.shape
+    ks, vs = _rows(k, hkv, d, k.dtype, "k"), _rows(v, hkv, d, k.dtype, "v")
+    if v.shape[0] != n_key:
+        raise ValueError("k has %d tokens, v %d" % (n_key, v.shape[0]))
+    hq = q.shape[1] if q.dim() == 3 else 0
+    qs = _rows(q, hq, d, k.dtype, "q")
+    n_req = k_start.numel()
+    _need(k_start, (n_req,), torch.int32, "k_start")
+    _need(k_len, (n_req,), torch.int32, "k_len")
+    _need(status, (1,), torch.int32, "status")
+    out, lse, ws = _attn_args(q, n_req, q_start, out, lse, ws)
+    _on_current(k, "k")
+    desc = skv_states(n_key, hkv, d, _DTYPE_CODE[k.dtype], ks, vs, k.data_ptr(), v.data_ptr(), k_start.data_ptr(),
+                      k_len.data_ptr(), status.data_ptr())
+    _check(lib().cross_attn(ctypes.byref(desc), hq, n_req, q.shape[0], q.data_ptr(), qs, q_start.data_ptr(),
+                            out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), float(sm_scale), _stream()),
+           "cross_attn")
+    return (out, lse) if lse is not None else out
