@@ -1,101 +1,952 @@
-// paged_attn and cross_attn: attention of packed queries over each request's
-// pages or packed states.
+// paged_attn and cross_attn on the 5th-generation tensor cores (tcgen05 +
+// TMEM): attention of packed queries over each request's pages or packed
+// states.
 //
-// One warp per (token, query head): a lane holds d/32 dimensions of the query
-// and the output, every key is one dot product across the warp, and the
-// softmax keeps a running maximum and sum.
+//   S = Q K^T,  P = exp(scale S - m),  O = P V / sum P,  lse = m + log sum P
+//
+// in one pass over the keys: the maximum m is taken on a row's first key tile
+// and kept until a later tile's probability sum passes LAG_LIMIT, then O and
+// the sum are scaled down to the new one (see p_pass).
+//
+// A unit is NQ query tiles of one (request, kv head): a tile packs TQ =
+// floor(128 / G) tokens x the G query heads that share the kv head into the
+// 128 rows of an MMA.  The units' key tiles (128 keys each; a causal unit ends
+// at its last token's key) form one sequence, ordered by request, kv head and
+// query block, and CTA b of a persistent grid takes tiles [b W, (b + 1) W) of
+// it: every SM streams the same number of tiles whatever the lengths, which
+// the host never sees.  Each CTA finds its place by a scan over the requests'
+// tile counts (closed forms, see unit_prefix).  A unit that several CTAs
+// share leaves fp32 partials (O, m, sum) in the workspace, and the last of
+// them to arrive merges the pieces in their order, so results do not depend
+// on timing.
+//
+// Two forms.  NQ = 2, for calls with more than TQ tokens per request: two
+// query tiles share every key tile, and one tile's softmax runs under the
+// other's MMAs (compute-bound).  NQ = 1, for decode: one query tile, two
+// score buffers, so that Q K^T of the next key tile runs under the softmax
+// (bound by streaming K and V from HBM; most MMA rows are idle).
+//
+//   warps 0 .. 4 NQ - 1  softmax and epilogue, a warpgroup per query tile
+//   then one warp each   K producer (TMA), V producer (TMA), MMA issuer,
+//                        scheduler (splits the CTA's share into pieces of
+//                        units, loads the pieces' queries by TMA)
+//
+// Keys and values are read as they lie: K rows are the K-major B operand of
+// Q K^T, token-major V rows the MN-major B operand of P V.  A TMA box is 64
+// dimensions x BR rows, BR the largest power of two (at most 128) that
+// divides the page size, so that a key tile is 128 / BR boxes from any pages.
+// Value rows past the request's length are set to zero in shared memory: a
+// probability of 0 does not cancel a NaN there.
+#include <cudaTypedefs.h>
 #include <math.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "ragged.h"
 #include "skv.h"
+#include "tc.cuh"
 
 namespace skv {
 
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn();
+
 namespace {
 
-constexpr int NT = 256;
+constexpr int BM = 128;   // rows of a query tile
+constexpr int BN = 128;   // keys of a key tile
+constexpr int NP = 4;     // pieces in flight between the scheduler and the other warps
+constexpr uint64_t WAIT_NS = 2000000000ull;   // limit of every wait
+constexpr uint64_t DRAIN_NS = 500000000ull;   // of the wait for own copies and MMAs on the way out
 
-template <bool F16>
-__device__ __forceinline__ float to_f32(uint16_t x) {
-  return F16 ? __half2float(__ushort_as_half(x)) : __uint_as_float((uint32_t)x << 16);
+template <int D, int NQ>
+struct RCfg {
+  static constexpr int SM_WARPS = 4 * NQ;
+  static constexpr int WARP_K = SM_WARPS, WARP_V = SM_WARPS + 1, WARP_MMA = SM_WARPS + 2, WARP_SCHED = SM_WARPS + 3;
+  static constexpr int NT = 128 * (NQ + 1);
+  // K and V stages: what the 227 KB hold beside the queries (for d = 64 as
+  // many bytes in flight as for 128)
+  static constexpr int KST = D == 128 ? (NQ == 2 ? 2 : 3) : (NQ == 2 ? 4 : 6);
+  static constexpr int VST = D == 128 ? 3 : (NQ == 2 ? 4 : 6);
+  static constexpr int QT = BM * D * 2;        // bytes of a query tile
+  static constexpr int KT = BN * D * 2;        // of a key or value tile
+  static constexpr int HALF = BM * 128;        // one 64-dimension half of either
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + NQ * QT;
+  static constexpr int V_OFF = K_OFF + KST * KT;
+  static constexpr int BAR_OFF = V_OFF + VST * KT;
+  static constexpr int MISC_OFF = BAR_OFF + 48 * 8;
+  static constexpr int PIECE_OFF = MISC_OFF + 256;
+  static constexpr int SCAN_OFF = PIECE_OFF + NP * 64;   // running sums of the prologue, one per warp
+  static constexpr int BYTES = SCAN_OFF + 16 * 8;
+  static constexpr int ALLOC = BYTES + 1024;             // slack for 1024-byte alignment
+  static_assert(ALLOC <= 232448, "shared memory");
+};
+
+template <int KST, int VST, int NQ>
+struct RBars {
+  enum : int {
+    QFULL = 0,                 // the piece's queries landed (TMA)
+    QEMPTY,                    // MMA commit: the piece's Q K^T are done with them
+    KFULL,                     // K tile landed
+    KEMPTY = KFULL + KST,      // MMA commit: K stage free
+    VFULL = KEMPTY + KST,      // V tile landed
+    VEMPTY = VFULL + VST,      // MMA commit: V stage free
+    SFULL = VEMPTY + VST,      // MMA commit: scores in buffer x
+    PFULL = SFULL + 2,         // softmax warps: probabilities in buffer x
+    PVDONE = PFULL + 2,        // MMA commit: the P V from buffer x landed in O
+    OFREE = PVDONE + 2,        // softmax warps: O of query tile i read out
+    PCFULL = OFREE + NQ,       // scheduler: piece published
+    PCEMPTY = PCFULL + NP,     // every other warp has read it
+    DRAIN = PCEMPTY + NP,      // MMA commit: everything issued is complete
+    COUNT
+  };
+  static_assert(COUNT <= 48, "barrier slots");
+};
+
+struct RParams {
+  RaggedArgs a;
+  int G, TQ, TB;          // query heads per kv head, tokens per query tile and per unit
+  int BR, boxes;          // rows per TMA box, boxes per key tile
+  int min_share;          // tiles per CTA at least
+  float scale_log2;
+  int* ws_count;          // [2 * CTAs] arrivals per unit (named by its first CTA) and query tile
+  float* ws_ml;           // [2 * CTAs][NQ * BM][2]
+  float* ws_o;            // [2 * CTAs][NQ * BM][D]
+};
+
+// One piece of a CTA's share: key tiles [ta, ta + nt) of a unit.
+struct Piece {
+  int nt;          // 0: no more pieces
+  int ta;
+  int b, h;
+  int row0;        // the unit's first token row
+  int ntok;        // its tokens
+  int kv;          // keys of the request
+  int pos0;        // keys that the unit's first token sees, less one
+  int step;        // 1: each later token sees one more (causal), 0: all see the same
+  int krow;        // first state of the request (cross attention)
+  int n, k;        // pieces of the unit, and which one this is
+  int cta0;        // CTA of the unit's first piece
+  int slot;        // workspace slot of this piece
+};
+static_assert(sizeof(Piece) <= 64, "piece slot");
+
+// sum over i < n of floor((a i + b) / m), by the Euclid-like reduction of
+// counting lattice points under a line: O(log) steps.
+__device__ unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a,
+                                        unsigned long long b) {
+  unsigned long long ans = 0;
+  while (n) {
+    if (a >= m) {
+      ans += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      ans += n * (b / m);
+      b %= m;
+    }
+    const unsigned long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const unsigned long long t = m;
+    m = a;
+    a = t;
+  }
+  return ans;
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(NT) ragged_attn_kernel(const RaggedArgs a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = blockIdx.x * (long long)(NT / 32) + (threadIdx.x >> 5);
-  const int tok = (int)(w / a.Hq), hq = (int)(w % a.Hq);
-  if (tok >= a.n_tok) return;
-  int b = -1;
-  Span s{};
-  for (int i = 0; i < a.n_req; ++i) {
-    const Span t = request_span(a, i);
-    if (t.bad && w == 0 && lane == 0) set_status(a.status, SKV_DEV_BAD_LEN);
-    if (tok >= t.q0 && tok < t.q0 + t.L) {
-      b = i;
-      s = t;
-    }
-  }
-  if (b < 0) return;
-  const int h = hq / (a.Hq / a.Hkv);
-  const int n = a.k_start ? s.kv : min(s.kv, s.kv - s.L + (tok - s.q0) + 1);
-  float q[E], o[E], m = -INFINITY, l = 0.f;
+// Key tiles of query block qb of a request (at least one, so that a block
+// without keys is visited and gets its zeros), and of the blocks before qb.
+__device__ __forceinline__ int unit_tiles(const Span& s, bool causal, int TB, int qb) {
+  if (s.kv == 0) return 1;
+  const long long seen = causal ? (long long)(s.kv - s.L) + min((long long)(qb + 1) * TB, (long long)s.L) : s.kv;
+  return (int)((seen + BN - 1) / BN);
+}
+__device__ __forceinline__ long long unit_prefix(const Span& s, bool causal, int TB, int nqb, int qb) {
+  if (qb == 0) return 0;
+  if (s.kv == 0 || !causal) return (long long)qb * unit_tiles(s, causal, TB, 0);
+  const int full = min(qb, nqb - 1);       // blocks that end at a multiple of TB
+  long long t = (long long)floor_sum(full, BN, TB, (long long)(s.kv - s.L) + TB + BN - 1);
+  if (qb > full) t += unit_tiles(s, causal, TB, nqb - 1);
+  return t;
+}
+
+// Token-major V as the MN-major B operand: 64 dimensions (128 bytes) by 8
+// keys per 1024-byte swizzle group; the next 8 keys follow it, the next 64
+// dimensions lie HALF bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t half) {
+  return (tc::sdesc_sw128(saddr) & ~(uint64_t(0x3FFF) << 16)) | ((uint64_t)(half >> 4) << 16);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (F16) return pack_f16x2_sat(lo, hi);
+  else return pack_bf16x2(lo, hi);
+}
+
+// Merge rows first, first + step, .. (< rows) of query tile i of a unit whose
+// n pieces left partials: weights 2^(m_k - M) / sum, over the pieces in their
+// order, a warp per row, U rows and KU pieces in flight.
+template <int D, int NQ, bool F16, int U, int KU>
+__device__ __noinline__ void merge_rows(const RParams& p, const Piece& pc, int i, int rows, int first, int step,
+                                        int lane) {
+  constexpr uint32_t FULL = 0xffffffffu;
+  constexpr int E = D / 32;                       // columns per lane
+  constexpr int ROWS = NQ * BM;
+  const RaggedArgs& a = p.a;
+  // piece 0 is the last of its CTA's share, every other the first
+  auto slot = [&](int k) { return (size_t)2 * (pc.cta0 + k) + (k == 0 ? 1 : 0); };
+  for (int r0 = first; r0 < rows; r0 += U * step) {
+    float acc[U][E], M[U], den[U];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = to_f32<F16>(a.q[tok * a.q_stride + (size_t)hq * D + lane * E + e]);
-    o[e] = 0.f;
-  }
-  for (int j = 0; j < n; ++j) {
-    const uint16_t *k = nullptr, *v = nullptr;
-    if (a.k_start) {
-      const long long r = (long long)a.k_start[b] + j;
-      k = a.k + r * a.k_stride + (size_t)h * D;
-      v = a.v + r * a.v_stride + (size_t)h * D;
-    } else {
-      const int page = a.table[(size_t)b * a.max_block + j / a.page_size];
-      if (page >= 0 && page < a.n_page) {
-        const size_t r = (((size_t)page * a.Hkv + h) * a.page_size + j % a.page_size) * D;
-        k = a.k + r;
-        v = a.v + r;
-      } else if (lane == 0) {
-        set_status(a.status, SKV_DEV_BAD_PAGE);
+    for (int u = 0; u < U; ++u) {
+      M[u] = -INFINITY;
+      den[u] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
+    }
+    for (int k0 = 0; k0 < pc.n; k0 += 32) {
+      const int nk = min(32, pc.n - k0);
+      float w[U];
+      float2 ml[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * step;
+        ml[u] = lane < nk && r < rows
+                    ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot(k0 + lane) * ROWS + i * BM + r)
+                    : make_float2(-INFINITY, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        // a piece without any visible key left l = 0 and has no weight
+        float mx = ml[u].y == 0.f ? -INFINITY : ml[u].x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
+        const float m_new = fmaxf(M[u], mx);
+        const float al = M[u] == -INFINITY ? 0.f : exp2f(M[u] - m_new);
+        w[u] = ml[u].y == 0.f ? 0.f : exp2f(ml[u].x - m_new);
+        float s = w[u] * ml[u].y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
+        den[u] = den[u] * al + s;
+        M[u] = m_new;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[u][e] *= al;
+      }
+      for (int kk = 0; kk < nk; kk += KU) {
+        float v[U][KU][E];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int x = 0; x < KU; ++x) {
+            const int r = r0 + u * step;
+            const bool on = kk + x < nk && r < rows;
+            const float* src = p.ws_o + (slot(on ? k0 + kk + x : 0) * ROWS + i * BM + (on ? r : 0)) * D + lane * E;
+            if constexpr (E == 4) {
+              const float4 t = on ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
+              v[u][x][0] = t.x;
+              v[u][x][1] = t.y;
+              v[u][x][2] = t.z;
+              v[u][x][3] = t.w;
+            } else {
+              const float2 t = on ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
+              v[u][x][0] = t.x;
+              v[u][x][1] = t.y;
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int x = 0; x < KU; ++x) {
+            const float wk = __shfl_sync(FULL, w[u], (kk + x) & 31);
+            if (kk + x < nk && wk != 0.f)
+#pragma unroll
+              for (int e = 0; e < E; ++e) acc[u][e] += wk * v[u][x][e];
+          }
       }
     }
-    float z = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) z += k ? q[e] * to_f32<F16>(k[lane * E + e]) : 0.f;
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * step;
+      if (r >= rows) continue;
+      const float inv = den[u] == 0.f ? 0.f : 1.f / den[u];
+      const int tok = pc.row0 + i * p.TQ + r / p.G, hq = pc.h * p.G + r % p.G;
+      uint16_t* dst = a.out + ((size_t)tok * a.Hq + hq) * D + lane * E;
+      uint32_t o[E / 2];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
-    z *= a.sm_scale;
-    const float m_new = fmaxf(m, z), al = expf(m - m_new), p = expf(z - m_new);
-    l = l * al + p;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * al + (v ? p * to_f32<F16>(v[lane * E + e]) : 0.f);
-    m = m_new;
+      for (int e = 0; e < E; e += 2) o[e / 2] = pack16<F16>(acc[u][e] * inv, acc[u][e + 1] * inv);
+      if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = o[0];
+      if (a.lse && lane == 0)
+        a.lse[(size_t)hq * a.n_tok + tok] = den[u] == 0.f ? -INFINITY : (M[u] + __log2f(den[u])) * 0.69314718055994531f;
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+}
+
+template <int D, bool F16, int NQ, bool PAGED>
+__global__ void __launch_bounds__(RCfg<D, NQ>::NT, 1)
+ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ RParams p) {
+  using C = RCfg<D, NQ>;
+  using B = RBars<C::KST, C::VST, NQ>;
+  constexpr int KST = C::KST, VST = C::VST;
+  // Largest probability sum of a tile that keeps the old maximum.  P is
+  // rounded to the values' type relative to its own size, so it may exceed 1;
+  // fp16 ends at 65504.
+  constexpr float LAG_LIMIT = F16 ? 16384.0f : 1048576.0f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = tc::smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::BAR_OFF + 8u * i; };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  volatile int* s_last = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);   // per query tile: merge it here
+  volatile int* s_b0 = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 16);
+  volatile long long* s_off = reinterpret_cast<volatile long long*>(smem + C::MISC_OFF + 24);
+  Piece* s_piece = reinterpret_cast<Piece*>(smem + C::PIECE_OFF);
+  long long* s_scan = reinterpret_cast<long long*>(smem + C::SCAN_OFF);
+
+  const RaggedArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int TB = p.TB;
+
+  // ------------------------------------------------------------ this CTA's share
+  long long total, share, g0;
+  {
+    const int per = (a.n_req + C::NT - 1) / C::NT;
+    const int i0 = min(a.n_req, tid * per), i1 = min(a.n_req, i0 + per);
+    auto cost = [&](int b) -> long long {
+      const Span s = request_span(a, b);
+      if (s.bad && blockIdx.x == 0) set_status(a.status, SKV_DEV_BAD_LEN);
+      if (s.L == 0) return 0;
+      const int nqb = (s.L + TB - 1) / TB;
+      return a.Hkv * unit_prefix(s, PAGED, TB, nqb, nqb);
+    };
+    long long sum = 0;
+    for (int b = i0; b < i1; ++b) sum += cost(b);
+    long long incl = sum;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float x = o[e] * inv;
-    a.out[((size_t)tok * a.Hq + hq) * D + lane * E + e] =
-        F16 ? __half_as_ushort(__float2half_rn(x)) : __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += t;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < C::NT / 32; ++w) {
+      if (w == warp) before = total;
+      total += s_scan[w];
+    }
+    share = max((long long)p.min_share, (total + gridDim.x - 1) / gridDim.x);
+    g0 = blockIdx.x * share;
+    if (g0 >= total) return;               // no tiles left for this CTA
+    long long at = before + incl - sum;    // tiles before this thread's requests
+    if (g0 >= at && g0 < at + sum) {
+      int b = i0;
+      for (; b < i1 - 1; ++b) {
+        const long long c = cost(b);
+        if (g0 < at + c) break;
+        at += c;
+      }
+      *s_b0 = b;
+      *s_off = g0 - at;
+    }
   }
-  if (a.lse && lane == 0) a.lse[(size_t)hq * a.n_tok + tok] = l > 0.f ? m + logf(l) : -INFINITY;
+  const long long g1 = min(g0 + share, total);
+
+  if (tid == 0) {
+    for (int i = 0; i < B::COUNT; ++i) {
+      int count = 1;
+      if (i >= B::PFULL && i < B::PFULL + 2) count = 4;
+      if (i >= B::OFREE && i < B::OFREE + NQ) count = 4;
+      if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + C::SM_WARPS;
+      tc::mbar_init(bar(i), count);
+    }
+    *s_abort = 0;
+    tc::fence_barrier_init();
+    tc::fence_proxy_async_smem();
+  }
+  if (warp == C::WARP_K) {
+    tc::tmem_alloc(tc::smem_u32(s_tmem), 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  auto wait = [&](int b, uint32_t phase) { return tc::mbar_wait(bar(b), phase & 1, WAIT_NS, s_abort); };
+  auto wait_short = [&](int b, uint32_t phase) { return tc::mbar_wait_short(bar(b), phase & 1, WAIT_NS, s_abort); };
+  // piece number pi into registers, its slot given back (whole warps)
+  auto take_piece = [&](int pi, Piece& pc) {
+    const int s = pi % NP;
+    if (!__all_sync(0xffffffffu, wait(B::PCFULL + s, pi / NP))) return false;
+    pc = s_piece[s];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar(B::PCEMPTY + s));
+    return true;
+  };
+  auto tiles_of = [&](const Piece& pc) { return NQ == 1 || pc.ntok <= p.TQ ? 1 : 2; };   // query tiles with rows
+
+  if (warp >= C::SM_WARPS) {
+    // 2 x 128 x 208 + 128 x 88 = the 384 x 168 registers of the launch
+    if constexpr (NQ == 2) tc::setmaxnreg_dec<88>();
+    if (warp == C::WARP_K || warp == C::WARP_V) {
+      // ---------------------------------------------------------- producers
+      const bool is_k = warp == C::WARP_K;
+      const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
+      const int nst = is_k ? KST : VST, full = is_k ? B::KFULL : B::VFULL, empty = is_k ? B::KEMPTY : B::VEMPTY;
+      const uint32_t base = sbase + (is_k ? C::K_OFF : C::V_OFF);
+      if (lane == 0) tc::prefetch_tmap(map);
+      int gt = 0;
+      Piece pc;
+      bool ok = true;
+      for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+        // lane x issues box x of a tile: the page of its first row
+        const int32_t* row = PAGED ? a.table + (size_t)pc.b * a.max_block : nullptr;
+        auto page_of = [&](int j) {
+          const int r = (pc.ta + j) * BN + lane * p.BR;
+          return PAGED && j < pc.nt && lane < p.boxes && r < pc.kv ? __ldg(row + r / a.page_size) : -1;
+        };
+        int id = page_of(0);
+        for (int j = 0; j < pc.nt; ++j, ++gt) {
+          const int s = gt % nst, r0 = (pc.ta + j) * BN;
+          const int n_box = (max(0, min(BN, pc.kv - r0)) + p.BR - 1) / p.BR;
+          if (gt >= nst) ok = wait(empty + s, gt / nst - 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar(full + s), n_box * p.BR * 128 * (D / 64));
+          __syncwarp();
+          if (lane < n_box) {
+            const int r = r0 + lane * p.BR;
+            int y, z;
+            if constexpr (PAGED) {
+              // a page outside the pool reads as the zeros outside the map
+              const bool in = id >= 0 && id < a.n_page;
+              if (!in) set_status(a.status, SKV_DEV_BAD_PAGE);
+              y = r % a.page_size;
+              z = in ? id * a.Hkv + pc.h : -1;
+            } else {
+              y = pc.h;
+              z = pc.krow + r;
+            }
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+              tc::tma_load_3d(base + s * C::KT + hf * C::HALF + lane * p.BR * 128, map, bar(full + s), hf * 64, y, z);
+          }
+          id = page_of(j + 1);
+        }
+        if (!ok) break;
+      }
+      if (!ok && lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
+      // the copies this warp started land before the CTA exits
+      for (int j = max(0, gt - nst); j < gt; ++j) {
+        volatile int never = 0;
+        tc::mbar_wait(bar(full + j % nst), (j / nst) & 1, DRAIN_NS, &never);
+      }
+    } else if (warp == C::WARP_MMA) {
+      // --------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16(BM, BN) : tc::idesc_bf16(BM, BN);
+      constexpr uint32_t idesc_pv = (F16 ? tc::idesc_f16(BM, D) : tc::idesc_bf16(BM, D)) | (1u << 16);
+      const uint64_t dq0 = tc::sdesc_sw128(sbase + C::Q_OFF);
+      const uint64_t dk0 = tc::sdesc_sw128(sbase + C::K_OFF);
+      const uint64_t dv0 = sdesc_mn(sbase + C::V_OFF, C::HALF);
+      auto issue_qk = [&](int i, int ks, int buf) {
+        const uint64_t dq = tc::opaque(dq0 + ((uint32_t)(i * C::QT) >> 4));
+        const uint64_t dk = tc::opaque(dk0 + ((uint32_t)(ks * C::KT) >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
+          tc::mma_ss(tmem + buf * BN, dq + off, dk + off, idesc_qk, kk > 0);
+        }
+      };
+      auto issue_pv = [&](int i, int vs, int buf, bool fresh) {
+        const uint64_t dv = tc::opaque(dv0 + ((uint32_t)(vs * C::KT) >> 4));
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          tc::mma_ts(tmem + 256 + i * 128, tmem + buf * BN + kk * 8, dv + ((kk * 2048) >> 4), idesc_pv,
+                     (!fresh || kk > 0) ? 1u : 0u);
+      };
+      // Tiles with a P V still to come: the last one issued.  cnt[i] counts the
+      // key tiles of query tile i, pcs[i] the pieces it was part of.
+      int gt = 0, cnt[2] = {0, 0}, pcs[2] = {0, 0};
+      bool prev = false, prev_fresh = false;
+      int prev_nq = 0;
+      bool ok = true;
+      // P V of query tile i of the tile before; its V stage is gt - 1's
+      auto pv = [&](int i) {
+        const int c = cnt[i] - 1, x = NQ == 2 ? i : c & 1, ph = NQ == 2 ? c : c >> 1;
+        if (!(ok = wait_short(B::VFULL + (gt - 1) % VST, (gt - 1) / VST))) return;
+        if (!(ok = wait_short(B::PFULL + x, ph))) return;
+        // the piece before has been read out of O
+        if (prev_fresh && pcs[i] > 1 && !(ok = wait_short(B::OFREE + i, pcs[i] - 2))) return;
+        tc::tc_fence_after();
+        issue_pv(i, (gt - 1) % VST, x, prev_fresh);
+        tc::mma_commit(bar(B::PVDONE + x));
+      };
+      Piece pc;
+      for (int pi = 0; ok && (ok = take_piece(pi, pc)); ++pi) {
+        if (lane == 0) {
+          const int nq = pc.nt ? tiles_of(pc) : 0;
+          for (int j = 0; ok && j < max(pc.nt, 1); ++j) {
+            const bool work = pc.nt > 0;
+            // at a piece's start the P V before it do not wait for its queries
+            if (NQ == 2 || j == 0 || !work) {
+              if (prev) pv(0);
+              if (!ok) break;
+              if (NQ == 1 && prev) {
+                tc::mma_commit(bar(B::VEMPTY + (gt - 1) % VST));
+                prev = false;
+              }
+            }
+            if (work) {
+              if (j == 0 && !(ok = wait_short(B::QFULL, pi))) break;
+              if (!(ok = wait_short(B::KFULL + gt % KST, gt / KST))) break;
+              tc::tc_fence_after();
+              const int x = NQ == 2 ? 0 : cnt[0] & 1;
+              issue_qk(0, gt % KST, x);
+              tc::mma_commit(bar(B::SFULL + x));
+            }
+            if (prev) {
+              if (NQ == 1) pv(0);
+              else if (prev_nq == 2) pv(1);
+              if (!ok) break;
+              tc::mma_commit(bar(B::VEMPTY + (gt - 1) % VST));
+            }
+            prev = false;
+            if (work) {
+              if (nq == 2) {
+                issue_qk(1, gt % KST, 1);
+                tc::mma_commit(bar(B::SFULL + 1));
+              }
+              tc::mma_commit(bar(B::KEMPTY + gt % KST));
+              if (j == pc.nt - 1) tc::mma_commit(bar(B::QEMPTY));
+              prev = true;
+              prev_fresh = j == 0;
+              prev_nq = nq;
+              for (int i = 0; i < nq; ++i) {
+                ++cnt[i];
+                if (j == 0) ++pcs[i];
+              }
+              ++gt;
+            }
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!pc.nt) break;
+      }
+      if (lane == 0) {
+        if (!ok) set_status(a.status, SKV_DEV_TIMEOUT);
+        // every MMA issued completes before TMEM is released
+        tc::mma_commit(bar(B::DRAIN));
+        volatile int never = 0;
+        tc::mbar_wait(bar(B::DRAIN), 0, DRAIN_NS, &never);
+      }
+    } else {
+      // ---------------------------------------------------------- scheduler
+      if (lane == 0) {
+        tc::prefetch_tmap(&tmap_q);
+        int b = *s_b0;
+        long long off = *s_off, g = g0;
+        Span s = request_span(a, b);
+        int nqb = (s.L + TB - 1) / TB, h, qb, t;
+        {
+          const long long per_head = unit_prefix(s, PAGED, TB, nqb, nqb);
+          h = (int)(off / per_head);
+          off -= h * per_head;
+          int lo = 0, hi = nqb - 1;       // the last block whose tiles start at or before off
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (unit_prefix(s, PAGED, TB, nqb, mid) <= off) lo = mid;
+            else hi = mid - 1;
+          }
+          qb = lo;
+          t = (int)(off - unit_prefix(s, PAGED, TB, nqb, qb));
+        }
+        bool ok = true;
+        int loaded = 0;                   // pieces whose queries are on their way
+        for (int pi = 0; ok; ++pi) {
+          Piece pc{};
+          if (g < g1) {
+            const int nt_unit = unit_tiles(s, PAGED, TB, qb);
+            const long long u0 = g - t, u1 = u0 + nt_unit;
+            pc.nt = (int)(min(u1, g1) - g);
+            pc.ta = t;
+            pc.b = b;
+            pc.h = h;
+            pc.row0 = s.q0 + qb * TB;
+            pc.ntok = min(TB, s.L - qb * TB);
+            pc.kv = s.kv;
+            pc.step = PAGED && s.kv ? 1 : 0;
+            pc.pos0 = pc.step ? s.kv - s.L + qb * TB : s.kv - 1;
+            pc.krow = PAGED ? 0 : a.k_start[b];
+            pc.n = 1;
+            if (u0 < g0 || u1 > g1) {
+              pc.cta0 = (int)(u0 / share);
+              pc.n = (int)((u1 - 1) / share) - pc.cta0 + 1;
+              pc.k = (int)blockIdx.x - pc.cta0;
+              pc.slot = 2 * (int)blockIdx.x + (pc.k == 0 ? 1 : 0);
+            }
+            g += pc.nt;
+            // the next unit
+            t = 0;
+            if (++qb == nqb) {
+              qb = 0;
+              if (++h == a.Hkv) {
+                h = 0;
+                do s = request_span(a, ++b < a.n_req ? b : a.n_req - 1);
+                while (s.L == 0 && b < a.n_req - 1);
+                nqb = (s.L + TB - 1) / TB;
+              }
+            }
+          }
+          const int slot = pi % NP;
+          if (pi >= NP && !(ok = wait(B::PCEMPTY + slot, pi / NP - 1))) break;
+          s_piece[slot] = pc;
+          tc::mbar_arrive(bar(B::PCFULL + slot));
+          if (!pc.nt) break;
+          // its queries, once the piece before is done with the buffer
+          if (pi > 0 && !(ok = wait(B::QEMPTY, pi - 1))) break;
+          const int nq = tiles_of(pc);
+          tc::mbar_arrive_expect_tx(bar(B::QFULL), nq * p.TQ * p.G * 128 * (D / 64));
+          for (int i = 0; i < nq; ++i)
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+              tc::tma_load_3d(sbase + C::Q_OFF + i * C::QT + hf * C::HALF, &tmap_q, bar(B::QFULL), hf * 64, pc.h * p.G,
+                              pc.row0 + i * p.TQ);
+          loaded = pi + 1;
+        }
+        if (!ok) set_status(a.status, SKV_DEV_TIMEOUT);
+        if (loaded) {
+          volatile int never = 0;
+          tc::mbar_wait(bar(B::QFULL), (loaded - 1) & 1, DRAIN_NS, &never);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------- softmax and epilogue
+    if constexpr (NQ == 2) tc::setmaxnreg_inc<208>();
+    const int i = warp >> 2, lg = warp & 3;        // query tile, TMEM lane group
+    const int row = lg * 32 + lane;
+    const uint32_t t_lane = (uint32_t)(lg * 32) << 16;
+    const uint32_t tO = tmem + t_lane + 256 + i * 128;
+    const int tok = row / p.G, gq = row - tok * p.G;
+    const float sl = p.scale_log2;
+    int gt = 0, cnt = 0;                           // key tiles of the CTA and of this query tile so far
+    Piece pc;
+    bool ok = true;
+    for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+      if (i >= tiles_of(pc)) {
+        gt += pc.nt;
+        continue;
+      }
+      const int ntok = min(p.TQ, pc.ntok - i * p.TQ);   // tokens in this query tile
+      const bool valid = tok < ntok;
+      const bool active = lg * 32 < ntok * p.G;         // some row of the warp is valid
+      const int lim = pc.pos0 + pc.step * (i * p.TQ + tok);   // the last key this row sees
+      float m_used = 0.f, l = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < pc.nt; ++j, ++gt, ++cnt) {
+        const int x = NQ == 2 ? i : cnt & 1, ph = NQ == 2 ? cnt : cnt >> 1;
+        const int r0 = (pc.ta + j) * BN;
+        const uint32_t tS = tmem + t_lane + x * BN;
+        // tcgen05.ld/st are warp-collective: every branch around them is warp-uniform
+        ok = __all_sync(0xffffffffu, wait(B::SFULL + x, ph));
+        if (!ok) break;
+        if (active) {
+          tc::tc_fence_after();
+          uint32_t v[BN];
+#pragma unroll
+          for (int cb = 0; cb < BN / 32; ++cb)
+            tc::tmem_ld32(tS + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(v + cb * 32));
+          const int n_see = lim + 1 - r0;          // keys of the tile that the row sees
+          tc::tmem_wait_ld();
+          if (!__all_sync(0xffffffffu, n_see >= BN)) {
+#pragma unroll
+            for (int k = 0; k < BN; ++k)
+              if (k >= n_see) v[k] = __float_as_uint(-INFINITY);
+          }
+          auto row_max = [&]() {
+            float m4[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m4[q] = fmaxf(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
+#pragma unroll
+            for (int k = 8; k < BN; k += 2)
+              m4[(k >> 1) & 3] = fmax3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
+          };
+          // P = 2^(s scale - m) in the values' type into the first 64 columns
+          // of the scores (rounded once: the products of P V take 16-bit
+          // operands); the sum is taken in fp32 before that rounding
+          auto p_pass = [&]() {
+            const uint64_t sl2 = f2_pack(sl, sl), nm2 = f2_pack(-m_used, -m_used);
+            uint64_t l2[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) l2[q] = 0ull;
+#pragma unroll
+            for (int cb = 0; cb < BN / 32; ++cb) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int k = 0; k < 32; k += 2) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(v[cb * 32 + k]), __uint_as_float(v[cb * 32 + k + 1])), sl2, nm2),
+                          x0, x1);
+                const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
+                l2[(k >> 1) & 3] = f2_add(l2[(k >> 1) & 3], f2_pack(p0, p1));
+                pk[k >> 1] = pack16<F16>(p0, p1);
+              }
+              tc::tmem_st16(tS + cb * 16, pk);
+            }
+            const uint64_t s2 = f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3]));
+            float s0, s1;
+            f2_unpack(s2, s0, s1);
+            return s0 + s1;
+          };
+          if (j == 0) {
+            const float mx = row_max();
+            m_used = mx == -INFINITY ? 0.f : mx;
+          }
+          float ts = p_pass();
+          if (__any_sync(0xffffffffu, valid && !(ts <= LAG_LIMIT))) {
+            tc::tmem_wait_st();
+            if (NQ == 1 && j > 0) {
+              // two query tiles: these scores were issued after the P V before
+              // them; one: that P V may still be running
+              ok = __all_sync(0xffffffffu, wait(B::PVDONE + ((cnt - 1) & 1), (cnt - 1) >> 1));
+              if (!ok) break;
+              tc::tc_fence_after();
+            }
+            const float mx = row_max();
+            const float m_new = mx > m_used ? mx : m_used;
+            const float alpha = tc::ex2(m_used - m_new);
+            l *= alpha;
+            if (j > 0) {
+#pragma unroll 1
+              for (int cb = 0; cb < D / 16; ++cb) {   // 16 columns at a time: the score row stays live
+                uint32_t o[16];
+                tc::tmem_ld16(tO + cb * 16, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tc::tmem_st16(tO + cb * 16, o);
+              }
+            }
+            m_used = m_new;
+            ts = p_pass();
+          }
+          l += ts;
+        }
+        if (i == 0 && r0 + BN > pc.kv) {
+          // value rows past the keys (the rest of a page, another request's
+          // states, or whatever the stage held before)
+          ok = __all_sync(0xffffffffu, wait(B::VFULL + gt % VST, gt / VST));
+          if (!ok) break;
+          if (r0 + row >= pc.kv) {
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                *reinterpret_cast<uint4*>(smem + C::V_OFF + (gt % VST) * C::KT + hf * C::HALF + row * 128 + c * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+          }
+          tc::fence_proxy_async_smem();
+        }
+        if (active) {
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(B::PFULL + x));
+      }
+      if (!ok) break;
+      {
+        const int c = cnt - 1, x = NQ == 2 ? i : c & 1, ph = NQ == 2 ? c : c >> 1;
+        ok = __all_sync(0xffffffffu, wait(B::PVDONE + x, ph));
+        if (!ok) break;
+      }
+      tc::tc_fence_after();
+      const int hq = pc.h * p.G + gq, trow = pc.row0 + i * p.TQ + tok;
+      if (active) {
+        if (pc.n == 1) {
+          const float inv_l = l == 0.f ? 0.f : 1.f / l;
+          uint16_t* orow = a.out + ((size_t)(valid ? trow : 0) * a.Hq + hq) * D;
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t o[32];
+            tc::tmem_ld32(tO + cb * 32, o);
+            tc::tmem_wait_ld();
+            if (valid) {
+              uint4 pk[4];
+              uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                pw[k] = pack16<F16>(__uint_as_float(o[2 * k]) * inv_l, __uint_as_float(o[2 * k + 1]) * inv_l);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(orow + cb * 32)[k] = pk[k];
+            }
+          }
+          if (valid && a.lse)
+            a.lse[(size_t)hq * a.n_tok + trow] = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
+        } else {
+          const size_t wrow = (size_t)pc.slot * (NQ * BM) + i * BM + row;
+          float* orow = p.ws_o + wrow * D;
+#pragma unroll 1
+          for (int cb = 0; cb < D / 32; ++cb) {
+            uint32_t o[32];
+            tc::tmem_ld32(tO + cb * 32, o);
+            tc::tmem_wait_ld();
+            if (valid) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                reinterpret_cast<uint4*>(orow + cb * 32)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+          if (valid) *reinterpret_cast<float2*>(p.ws_ml + wrow * 2) = make_float2(m_used, l);
+        }
+      }
+      // O is read out: the next piece's first P V may overwrite it
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(B::OFREE + i));
+      if (pc.n > 1) {
+        tc::bar_sync_n(1 + i, 128);
+        if (row == 0) {
+          __threadfence();
+          int* count = p.ws_count + 2 * pc.cta0 + i;
+          const bool last = atomicAdd(count, 1) == pc.n - 1;
+          if (last) {
+            *count = 0;                  // ready for the next call
+            __threadfence();
+          }
+          s_last[i] = last;
+        }
+        tc::bar_sync_n(1 + i, 128);
+        if (s_last[i]) {
+          const int rows = ntok * p.G;
+          // few rows (decode): one per warp, many pieces in flight
+          if (rows <= 4) merge_rows<D, NQ, F16, 1, 16>(p, pc, i, rows, lg, 4, lane);
+          else merge_rows<D, NQ, F16, 4, 4>(p, pc, i, rows, lg, 4, lane);
+        }
+      }
+    }
+    if (!ok && lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
+  }
+
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == C::WARP_K) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// SM count per device ordinal, asked once (threads that race store the same value)
+std::atomic<int> g_sms[64];
+
+int sm_count() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 152;
+  int n = g_sms[dev].load(std::memory_order_relaxed);
+  if (!n) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    g_sms[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+template <typename K>
+cudaError_t set_smem_once(K kernel, int bytes, int variant) {
+  static std::atomic<int> done[64][16];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev][variant].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev][variant].store(1, std::memory_order_relaxed);
+  return e;
+}
+
+// Workspace: arrival counters (a 4 KB block), then (m, sum) and O of two
+// pieces per CTA, the first and the last of its share (any piece between is a
+// whole unit), at the larger form's rows and head size.
+constexpr int MAX_CTAS = 512;
+constexpr size_t WS_HEAD = 2 * MAX_CTAS * sizeof(int);
+size_t ws_ml_bytes() { return (size_t)2 * sm_count() * 2 * BM * 2 * sizeof(float); }
+
+bool encode_3d(CUtensorMap* m, bool f16, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
+               const cuuint32_t (&box)[3]) {
+  auto fn = tmap_encode_fn();
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn && fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
-size_t ragged_ws_bytes() { return 0; }
+size_t ragged_ws_bytes() { return WS_HEAD + ws_ml_bytes() + (size_t)2 * sm_count() * 2 * BM * 128 * sizeof(float); }
 
 cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_t st) {
-  const long long warps = (long long)a.n_tok * a.Hq;
-  const unsigned grid = (unsigned)((warps + NT / 32 - 1) / (NT / 32));
-  auto launch = [&](auto kernel) { kernel<<<grid, NT, 0, st>>>(a); };
-  if (d == 128) f16 ? launch(ragged_attn_kernel<128, true>) : launch(ragged_attn_kernel<128, false>);
-  else f16 ? launch(ragged_attn_kernel<64, true>) : launch(ragged_attn_kernel<64, false>);
-  return cudaGetLastError();
+  RParams p;
+  p.a = a;
+  p.G = a.Hq / a.Hkv;
+  p.TQ = BM / p.G;
+  const bool paged = a.k_start == nullptr;
+  // more tokens than one query tile per request holds, on average: two tiles
+  // per unit (a request that needs one leaves the second idle)
+  const bool wide = a.n_tok > (long long)a.n_req * p.TQ;
+  p.TB = (wide ? 2 : 1) * p.TQ;
+  const int grid = min(sm_count(), MAX_CTAS);
+  p.min_share = wide ? 4 : 1;
+  p.BR = BN;
+  if (paged)
+    while (a.page_size % p.BR) p.BR /= 2;
+  p.boxes = BN / p.BR;
+  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  char* ws = static_cast<char*>(a.ws);
+  p.ws_count = reinterpret_cast<int*>(ws);
+  p.ws_ml = reinterpret_cast<float*>(ws + WS_HEAD);
+  p.ws_o = reinterpret_cast<float*>(ws + WS_HEAD + ws_ml_bytes());
+
+  CUtensorMap tq, tk, tv;
+  const cuuint64_t dd = (cuuint64_t)d;
+  if (!encode_3d(&tq, f16, a.q, {dd, (cuuint64_t)a.Hq, (cuuint64_t)a.n_tok}, {dd * 2, (cuuint64_t)a.q_stride * 2},
+                 {64, (cuuint32_t)p.G, (cuuint32_t)p.TQ}))
+    return cudaErrorInvalidValue;
+  for (int i = 0; i < 2; ++i) {
+    const void* base = i ? a.v : a.k;
+    bool ok;
+    if (paged) {
+      ok = encode_3d(i ? &tv : &tk, f16, base, {dd, (cuuint64_t)a.page_size, (cuuint64_t)a.n_page * a.Hkv},
+                     {dd * 2, dd * 2 * a.page_size}, {64, (cuuint32_t)p.BR, 1});
+    } else if (a.n_key > 0) {
+      ok = encode_3d(i ? &tv : &tk, f16, base, {dd, (cuuint64_t)a.Hkv, (cuuint64_t)a.n_key},
+                     {dd * 2, (cuuint64_t)(i ? a.v_stride : a.k_stride) * 2}, {64, 1, (cuuint32_t)BN});
+    } else {
+      (i ? tv : tk) = tq;      // no states at all: the map is never read
+      ok = true;
+    }
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  auto launch = [&](auto kernel, int smem, int threads, int variant) -> cudaError_t {
+    const cudaError_t e = set_smem_once(kernel, smem, variant);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, threads, smem, st>>>(tq, tk, tv, p);
+    return cudaGetLastError();
+  };
+#define SKV_RAGGED(DD, FF, NN, PP, VAR) \
+  launch(ragged_attn_kernel<DD, FF, NN, PP>, RCfg<DD, NN>::ALLOC, RCfg<DD, NN>::NT, VAR)
+#define SKV_RAGGED_FORMS(DD, FF, VAR)                                                                    \
+  (wide ? (paged ? SKV_RAGGED(DD, FF, 2, true, VAR) : SKV_RAGGED(DD, FF, 2, false, VAR + 1))             \
+        : (paged ? SKV_RAGGED(DD, FF, 1, true, VAR + 2) : SKV_RAGGED(DD, FF, 1, false, VAR + 3)))
+  if (d == 128) return f16 ? SKV_RAGGED_FORMS(128, true, 0) : SKV_RAGGED_FORMS(128, false, 4);
+  return f16 ? SKV_RAGGED_FORMS(64, true, 8) : SKV_RAGGED_FORMS(64, false, 12);
+#undef SKV_RAGGED_FORMS
+#undef SKV_RAGGED
 }
 
 }  // namespace skv
