@@ -111,8 +111,8 @@ struct RParams {
   int min_share;          // tiles per CTA at least
   float scale_log2;
   int* ws_count;          // [2 * CTAs] arrivals per unit (named by its first CTA) and query tile
-  float* ws_ml;           // [2 * CTAs][NQ * BM][2]
-  float* ws_o;            // [2 * CTAs][NQ * BM][D]
+  float* ws_ml;           // [2 * CTAs][NQ][BM][2]
+  float* ws_o;            // [2 * CTAs][NQ][D / 4][BM][4], see ws_index
 };
 
 // One piece of a CTA's share: key tiles [ta, ta + nt) of a unit.
@@ -186,102 +186,87 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   else return pack_bf16x2(lo, hi);
 }
 
-// Merge rows first, first + step, .. (< rows) of query tile i of a unit whose
-// n pieces left partials: weights 2^(m_k - M) / sum, over the pieces in their
-// order, a warp per row, U rows and KU pieces in flight.
-template <int D, int NQ, bool F16, int U, int KU>
-__device__ __noinline__ void merge_rows(const RParams& p, const Piece& pc, int i, int rows, int first, int step,
-                                        int lane) {
-  constexpr uint32_t FULL = 0xffffffffu;
-  constexpr int E = D / 32;                       // columns per lane
-  constexpr int ROWS = NQ * BM;
+// Workspace offset (floats) of columns [4 c, 4 c + 4) of row r of a slot's
+// query tile i: a column group of all rows is contiguous, so that a warp whose
+// lanes hold consecutive rows reads and writes whole lines.
+template <int D, int NQ>
+__device__ __forceinline__ size_t ws_index(int slot, int i, int c, int r) {
+  return ((((size_t)slot * NQ + i) * (D / 4) + c) * BM + r) * 4;
+}
+
+// Merge query tile i of a unit whose n pieces left partials (O_k, m_k, l_k):
+// O = sum_k w_k O_k / sum_k w_k l_k with w_k = 2^(m_k - M), by the 128 threads
+// of a softmax warpgroup, over the pieces in their order.  A thread takes one
+// row and every `lanes`-th group of 4 columns: a full tile's rows a thread
+// each, a decode step's few rows spread over all threads.  CU column groups of
+// KU pieces are loaded together with their (m, l), M following as it grows,
+// so that up to KU pieces take one round trip.
+template <int D, int NQ, bool F16, int CU, int KU>
+__device__ __noinline__ void merge_pieces(const RParams& p, const Piece& pc, int i, int rows, int t) {
+  constexpr int CG = D / 4;     // column groups
   const RaggedArgs& a = p.a;
   // piece 0 is the last of its CTA's share, every other the first
-  auto slot = [&](int k) { return (size_t)2 * (pc.cta0 + k) + (k == 0 ? 1 : 0); };
-  for (int r0 = first; r0 < rows; r0 += U * step) {
-    float acc[U][E], M[U], den[U];
+  auto slot = [&](int k) { return 2 * (pc.cta0 + k) + (k == 0 ? 1 : 0); };
+  const int lanes = BM / rows;            // threads per row
+  const int r = t % rows, c0 = t / rows;
+  if (c0 >= lanes) return;
+  const int tok = pc.row0 + i * p.TQ + r / p.G, hq = pc.h * p.G + r % p.G;
+  uint16_t* dst = a.out + ((size_t)tok * a.Hq + hq) * D;
+  for (int c = c0; c < CG; c += CU * lanes) {
+    float4 acc[CU];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      M[u] = -INFINITY;
-      den[u] = 0.f;
+    for (int u = 0; u < CU; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, den = 0.f;
+    for (int k0 = 0; k0 < pc.n; k0 += KU) {
+      float4 v[KU][CU];
+      float2 ml[KU];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[u][e] = 0.f;
-    }
-    for (int k0 = 0; k0 < pc.n; k0 += 32) {
-      const int nk = min(32, pc.n - k0);
-      float w[U];
-      float2 ml[U];
+      for (int x = 0; x < KU; ++x) {
+        const bool on = k0 + x < pc.n;
+        ml[x] = on ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)slot(k0 + x) * NQ + i) * BM + r)
+                   : make_float2(0.f, 0.f);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = r0 + u * step;
-        ml[u] = lane < nk && r < rows
-                    ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + slot(k0 + lane) * ROWS + i * BM + r)
-                    : make_float2(-INFINITY, 0.f);
+        for (int u = 0; u < CU; ++u)
+          v[x][u] = on && c + u * lanes < CG
+                        ? __ldcg(reinterpret_cast<const float4*>(p.ws_o + ws_index<D, NQ>(slot(k0 + x), i, c + u * lanes, r)))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float mx = M;
+#pragma unroll
+      for (int x = 0; x < KU; ++x)
+        if (ml[x].y != 0.f) mx = fmaxf(mx, ml[x].x);   // a piece without a visible key left l = 0
+      const float al = M == -INFINITY ? 0.f : exp2f(M - mx);
+      den *= al;
+#pragma unroll
+      for (int u = 0; u < CU; ++u) {
+        acc[u].x *= al;
+        acc[u].y *= al;
+        acc[u].z *= al;
+        acc[u].w *= al;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        // a piece without any visible key left l = 0 and has no weight
-        float mx = ml[u].y == 0.f ? -INFINITY : ml[u].x;
+      for (int x = 0; x < KU; ++x) {
+        if (ml[x].y == 0.f) continue;
+        const float w = exp2f(ml[x].x - mx);
+        den += w * ml[x].y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, o));
-        const float m_new = fmaxf(M[u], mx);
-        const float al = M[u] == -INFINITY ? 0.f : exp2f(M[u] - m_new);
-        w[u] = ml[u].y == 0.f ? 0.f : exp2f(ml[u].x - m_new);
-        float s = w[u] * ml[u].y;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(FULL, s, o);
-        den[u] = den[u] * al + s;
-        M[u] = m_new;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[u][e] *= al;
+        for (int u = 0; u < CU; ++u) {
+          acc[u].x += w * v[x][u].x;
+          acc[u].y += w * v[x][u].y;
+          acc[u].z += w * v[x][u].z;
+          acc[u].w += w * v[x][u].w;
+        }
       }
-      for (int kk = 0; kk < nk; kk += KU) {
-        float v[U][KU][E];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int x = 0; x < KU; ++x) {
-            const int r = r0 + u * step;
-            const bool on = kk + x < nk && r < rows;
-            const float* src = p.ws_o + (slot(on ? k0 + kk + x : 0) * ROWS + i * BM + (on ? r : 0)) * D + lane * E;
-            if constexpr (E == 4) {
-              const float4 t = on ? __ldcg(reinterpret_cast<const float4*>(src)) : make_float4(0.f, 0.f, 0.f, 0.f);
-              v[u][x][0] = t.x;
-              v[u][x][1] = t.y;
-              v[u][x][2] = t.z;
-              v[u][x][3] = t.w;
-            } else {
-              const float2 t = on ? __ldcg(reinterpret_cast<const float2*>(src)) : make_float2(0.f, 0.f);
-              v[u][x][0] = t.x;
-              v[u][x][1] = t.y;
-            }
-          }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int x = 0; x < KU; ++x) {
-            const float wk = __shfl_sync(FULL, w[u], (kk + x) & 31);
-            if (kk + x < nk && wk != 0.f)
-#pragma unroll
-              for (int e = 0; e < E; ++e) acc[u][e] += wk * v[u][x][e];
-          }
-      }
+      M = mx;
     }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * step;
-      if (r >= rows) continue;
-      const float inv = den[u] == 0.f ? 0.f : 1.f / den[u];
-      const int tok = pc.row0 + i * p.TQ + r / p.G, hq = pc.h * p.G + r % p.G;
-      uint16_t* dst = a.out + ((size_t)tok * a.Hq + hq) * D + lane * E;
-      uint32_t o[E / 2];
-#pragma unroll
-      for (int e = 0; e < E; e += 2) o[e / 2] = pack16<F16>(acc[u][e] * inv, acc[u][e + 1] * inv);
-      if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-      else *reinterpret_cast<uint32_t*>(dst) = o[0];
-      if (a.lse && lane == 0)
-        a.lse[(size_t)hq * a.n_tok + tok] = den[u] == 0.f ? -INFINITY : (M[u] + __log2f(den[u])) * 0.69314718055994531f;
-    }
+    for (int u = 0; u < CU; ++u)
+      if (c + u * lanes < CG)
+        *reinterpret_cast<uint2*>(dst + (c + u * lanes) * 4) =
+            make_uint2(pack16<F16>(acc[u].x * inv, acc[u].y * inv), pack16<F16>(acc[u].z * inv, acc[u].w * inv));
+    if (a.lse && c == 0)
+      a.lse[(size_t)hq * a.n_tok + tok] = den == 0.f ? -INFINITY : (M + __log2f(den)) * 0.69314718055994531f;
   }
 }
 
@@ -311,6 +296,32 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   const RaggedArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int TB = p.TB;
+
+  // what needs none of the call's inputs runs while the kernel before this
+  // one on the stream ends
+  if (tid == 0) {
+    for (int i = 0; i < B::COUNT; ++i) {
+      int count = 1;
+      if (i >= B::PFULL && i < B::PFULL + 2) count = 4;
+      if (i >= B::OFREE && i < B::OFREE + NQ) count = 4;
+      if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + C::SM_WARPS;
+      tc::mbar_init(bar(i), count);
+    }
+    *s_abort = 0;
+    tc::fence_barrier_init();
+    tc::fence_proxy_async_smem();
+  }
+  if (warp == C::WARP_K) {
+    tc::tmem_alloc(tc::smem_u32(s_tmem), 512);
+    tc::tmem_relinquish();
+  }
+  if (lane == 0) {
+    if (warp == C::WARP_K) tc::prefetch_tmap(&tmap_k);
+    if (warp == C::WARP_V) tc::prefetch_tmap(&tmap_v);
+    if (warp == C::WARP_SCHED) tc::prefetch_tmap(&tmap_q);
+  }
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
 
   // ------------------------------------------------------------ this CTA's share
   long long total, share, g0;
@@ -343,7 +354,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     }
     share = max((long long)p.min_share, (total + gridDim.x - 1) / gridDim.x);
     g0 = blockIdx.x * share;
-    if (g0 >= total) return;               // no tiles left for this CTA
+    if (g0 >= total) {                     // no tiles left for this CTA
+      if (warp == C::WARP_K) tc::tmem_dealloc(*s_tmem, 512);
+      return;
+    }
     long long at = before + incl - sum;    // tiles before this thread's requests
     if (g0 >= at && g0 < at + sum) {
       int b = i0;
@@ -358,22 +372,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   }
   const long long g1 = min(g0 + share, total);
 
-  if (tid == 0) {
-    for (int i = 0; i < B::COUNT; ++i) {
-      int count = 1;
-      if (i >= B::PFULL && i < B::PFULL + 2) count = 4;
-      if (i >= B::OFREE && i < B::OFREE + NQ) count = 4;
-      if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + C::SM_WARPS;
-      tc::mbar_init(bar(i), count);
-    }
-    *s_abort = 0;
-    tc::fence_barrier_init();
-    tc::fence_proxy_async_smem();
-  }
-  if (warp == C::WARP_K) {
-    tc::tmem_alloc(tc::smem_u32(s_tmem), 512);
-    tc::tmem_relinquish();
-  }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
@@ -400,7 +398,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
       const int nst = is_k ? KST : VST, full = is_k ? B::KFULL : B::VFULL, empty = is_k ? B::KEMPTY : B::VEMPTY;
       const uint32_t base = sbase + (is_k ? C::K_OFF : C::V_OFF);
-      if (lane == 0) tc::prefetch_tmap(map);
       int gt = 0;
       Piece pc;
       bool ok = true;
@@ -548,7 +545,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     } else {
       // ---------------------------------------------------------- scheduler
       if (lane == 0) {
-        tc::prefetch_tmap(&tmap_q);
         int b = *s_b0;
         long long off = *s_off, g = g0;
         Span s = request_span(a, b);
@@ -791,8 +787,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           if (valid && a.lse)
             a.lse[(size_t)hq * a.n_tok + trow] = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
         } else {
-          const size_t wrow = (size_t)pc.slot * (NQ * BM) + i * BM + row;
-          float* orow = p.ws_o + wrow * D;
 #pragma unroll 1
           for (int cb = 0; cb < D / 32; ++cb) {
             uint32_t o[32];
@@ -801,10 +795,12 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             if (valid) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                reinterpret_cast<uint4*>(orow + cb * 32)[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                *reinterpret_cast<uint4*>(p.ws_o + ws_index<D, NQ>(pc.slot, i, cb * 8 + k, row)) =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             }
           }
-          if (valid) *reinterpret_cast<float2*>(p.ws_ml + wrow * 2) = make_float2(m_used, l);
+          if (valid)
+            reinterpret_cast<float2*>(p.ws_ml)[((size_t)pc.slot * NQ + i) * BM + row] = make_float2(m_used, l);
         }
       }
       // O is read out: the next piece's first P V may overwrite it
@@ -826,9 +822,9 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         tc::bar_sync_n(1 + i, 128);
         if (s_last[i]) {
           const int rows = ntok * p.G;
-          // few rows (decode): one per warp, many pieces in flight
-          if (rows <= 4) merge_rows<D, NQ, F16, 1, 16>(p, pc, i, rows, lg, 4, lane);
-          else merge_rows<D, NQ, F16, 4, 4>(p, pc, i, rows, lg, 4, lane);
+          // few rows (decode): a thread has one column group, many pieces in flight
+          if (rows * (D / 4) <= BM) merge_pieces<D, NQ, F16, 1, 20>(p, pc, i, rows, row);
+          else merge_pieces<D, NQ, F16, 8, 4>(p, pc, i, rows, row);
         }
       }
     }
@@ -935,8 +931,7 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   auto launch = [&](auto kernel, int smem, int threads, int variant) -> cudaError_t {
     const cudaError_t e = set_smem_once(kernel, smem, variant);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, threads, smem, st>>>(tq, tk, tv, p);
-    return cudaGetLastError();
+    return launch_dependent(kernel, grid, threads, smem, st, tq, tk, tv, p);
   };
 #define SKV_RAGGED(DD, FF, NN, PP, VAR) \
   launch(ragged_attn_kernel<DD, FF, NN, PP>, RCfg<DD, NN>::ALLOC, RCfg<DD, NN>::NT, VAR)

@@ -7,6 +7,7 @@
 #include "common.cuh"
 #include "ragged.h"
 #include "skv.h"
+#include "tc.cuh"
 
 namespace skv {
 
@@ -84,6 +85,8 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
   const long long row_tokens = (long long)a.max_block * ps;   // what a table row holds
   auto pages = [&](int x) { return (int)(((long long)x + ps - 1) / ps); };
   const bool reporter = blockIdx.x == 0;
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
 
   int head = a.state[n], count = a.state[n + 1];
   if (head < 0 || head >= a.n_page || count < 0 || count > a.n_page) {
@@ -229,6 +232,8 @@ __global__ void __launch_bounds__(WT) paged_write_kernel(const WriteArgs a) {
   const long long rest = item / NCH;
   const int grp = (int)(rest % groups);
   const long long tok = rest / groups;
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
   if (tok >= a.n_tok) return;
   const int slot = a.slot[tok];
   if (slot < 0) return;
@@ -298,8 +303,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_relaxed);
   }
-  paged_plan_kernel<<<grid, PT, smem, st>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(paged_plan_kernel, grid, PT, smem, st, a);
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, int d, bool f16, cudaStream_t st) {
@@ -308,10 +312,9 @@ cudaError_t launch_paged_write(const WriteArgs& a, int d, bool f16, cudaStream_t
   const long long blocks = (items + WT - 1) / WT;
   if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  auto launch = [&](auto kernel) { kernel<<<(unsigned)blocks, WT, 0, st>>>(a); };
-  if (d == 128) f16 ? launch(paged_write_kernel<128, true>) : launch(paged_write_kernel<128, false>);
-  else f16 ? launch(paged_write_kernel<64, true>) : launch(paged_write_kernel<64, false>);
-  return cudaGetLastError();
+  auto launch = [&](auto kernel) { return launch_dependent(kernel, (int)blocks, WT, 0, st, a); };
+  if (d == 128) return f16 ? launch(paged_write_kernel<128, true>) : launch(paged_write_kernel<128, false>);
+  return f16 ? launch(paged_write_kernel<64, true>) : launch(paged_write_kernel<64, false>);
 }
 
 }  // namespace skv

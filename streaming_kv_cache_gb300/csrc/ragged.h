@@ -59,6 +59,24 @@ struct RaggedArgs {
 cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_t st);
 size_t ragged_ws_bytes();
 
+// Launch as a programmatic dependent of the kernel before it on the stream:
+// its CTAs may start while that one still ends, and wait for it
+// (grid_dep_wait) before they read or write anything of the caller's.
+template <typename... K, typename... A>
+cudaError_t launch_dependent(void (*kernel)(K...), int grid, int threads, int smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // One request as the attention sees it: rows [q0, q0 + L) of the queries, kv
 // keys; row t sees the first kv - L + t + 1 of them (paged) or all (states).
 // Lengths out of range make it harmless: a bad span has no rows, bad keys

@@ -408,23 +408,49 @@ def stream_attn_verify(cache: StreamCache, tail_len: torch.Tensor, q_blk: torch.
 # --------------------------------------------- paged cache, cross attention
 
 
-def _on_current(t, name):
-    """The tensor lives on the current device, where the call launches."""
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+def _on(t, shape, dtype, name, dev):
+    """_need, and the tensor lives on device dev, where the call launches.
+    A decode step makes many small calls, so what a good tensor has to pass
+    is one short expression."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        _need(t, shape, dtype, name)
+        _on_dev(t.get_device(), name, dev)
 
 
-def _rows(t, heads, d, dtype, name) -> int:
+def _on_dev(index, name, dev):
+    if index != dev:
+        raise ValueError("%s is on cuda:%d, but the current device is cuda:%d" % (name, index, dev))
+
+
+def _call_device(t, name):
+    """The device that a call on t launches on: t's, and the current one."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % name)
+    dev = torch.cuda.current_device()
+    _on_dev(t.get_device(), name, dev)
+    return dev
+
+
+def _raw_stream(dev):
+    """The current torch stream of device dev, without making a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _rows(t, heads, d, dtype, name, dev) -> int:
     """Token stride of a token-major tensor [tokens][heads][d] whose heads of
     a token are adjacent (a part of a wider projection's rows, say)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("%s must be on a CUDA device" % name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
         raise ValueError("%s must have shape (tokens, %d, %d), got %s" % (name, heads, d, tuple(t.shape)))
+    _on_dev(t.get_device(), name, dev)
     n, (s0, s1, s2) = t.shape[0], t.stride()
     if n == 0:
         return heads * d
@@ -436,13 +462,25 @@ def _rows(t, heads, d, dtype, name) -> int:
 class PagedPlan:
     """The plan of one step (see kv_paged_plan in include/skv.h): int32
     tensors q_start [n_req + 1], kv_len [n_req], next_state [n_req + 2],
-    position [n_tok] and slot [n_tok]."""
+    position [n_tok] and slot [n_tok], which stay where they are."""
 
-    __slots__ = ("q_start", "kv_len", "next_state", "position", "slot")
+    __slots__ = ("_t", "_args", "n_req", "n_tok", "_dev")
 
     def __init__(self, q_start, kv_len, next_state, position, slot):
-        self.q_start, self.kv_len, self.next_state = q_start, kv_len, next_state
-        self.position, self.slot = position, slot
+        self._t = (q_start, kv_len, next_state, position, slot)
+        n_req, n_tok = kv_len.numel(), slot.numel()
+        for t, n, name in zip(self._t, (n_req + 1, n_req, n_req + 2, n_tok, n_tok),
+                              ("q_start", "kv_len", "next_state", "position", "slot")):
+            _need(t, (n,), torch.int32, name)
+            _on_dev(t.get_device(), name, q_start.get_device())
+        self.n_req, self.n_tok, self._dev = n_req, n_tok, q_start.get_device()
+        self._args = tuple(ctypes.c_void_p(t.data_ptr()) for t in self._t)
+
+    q_start = property(lambda self: self._t[0])
+    kv_len = property(lambda self: self._t[1])
+    next_state = property(lambda self: self._t[2])
+    position = property(lambda self: self._t[3])
+    slot = property(lambda self: self._t[4])
 
     @classmethod
     def empty(cls, n_req, n_tok, device="cuda"):
@@ -534,9 +572,11 @@ class PagedCache:
         self.n_page, self.page_size, self.Hkv, self.d = n_page, page_size, hkv, d
         self.n_req, self.max_block = block_table.shape
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        self._state_arg, self._queue_arg = ctypes.c_void_p(ptr(state)), ctypes.c_void_p(ptr(page_queue))
         self._desc = skv_paged(n_page, page_size, hkv, d, code, rope.shape[0] if rope is not None else 0,
                                self.max_block, 0, ptr(k), ptr(v), ptr(block_table), ptr(rope), ptr(status))
-        self._ref = ctypes.byref(self._desc)
+        self._ref, self._dev = ctypes.byref(self._desc), block_table.get_device()
+        self._dtype = k.dtype if k is not None else None
 
     def layer(self, i: int) -> "PagedCache":
         """The cache of layer i: its own k and v, everything else shared."""
@@ -561,27 +601,25 @@ def kv_paged_plan(cache: PagedCache, new_len: torch.Tensor, n_tok: int,
     cache's state stays until cache.advance(plan)."""
     if cache.state is None or cache.page_queue is None:
         raise ValueError("the cache has no state and page_queue to plan with")
-    n_req = cache.n_req
-    _need(new_len, (n_req,), torch.int32, "new_len")
-    _on_current(new_len, "new_len")
-    _on_current(cache.block_table, "the cache")
+    n_req, dev = cache.n_req, _call_device(new_len, "new_len")
+    _on_dev(cache._dev, "the cache", dev)
+    _on(new_len, (n_req,), torch.int32, "new_len", dev)
     if plan is None:
         plan = PagedPlan.empty(n_req, n_tok, new_len.device)
-    _need(plan.q_start, (n_req + 1,), torch.int32, "q_start")
-    _need(plan.kv_len, (n_req,), torch.int32, "kv_len")
-    _need(plan.next_state, (n_req + 2,), torch.int32, "next_state")
-    _need(plan.position, (n_tok,), torch.int32, "position")
-    _need(plan.slot, (n_tok,), torch.int32, "slot")
-    _check(lib().kv_paged_plan(cache._ref, n_req, n_tok, cache.state.data_ptr(), new_len.data_ptr(),
-                               cache.page_queue.data_ptr(), plan.q_start.data_ptr(), plan.kv_len.data_ptr(),
-                               plan.next_state.data_ptr(), plan.position.data_ptr(), plan.slot.data_ptr(),
-                               _stream()), "kv_paged_plan")
+    if plan.n_req != n_req or plan.n_tok != n_tok:
+        raise ValueError("the plan is for %d requests and %d tokens, not %d and %d" % (plan.n_req, plan.n_tok, n_req, n_tok))
+    _on_dev(plan._dev, "the plan", dev)
+    rc = lib().kv_paged_plan(cache._ref, n_req, n_tok, cache._state_arg, new_len.data_ptr(), cache._queue_arg,
+                             *plan._args, _raw_stream(dev))
+    if rc:
+        _check(rc, "kv_paged_plan")
     return plan
 
 
-def _need_pages(cache):
+def _need_pages(cache, dev):
     if cache.k is None:
         raise ValueError("the cache has no k and v")
+    _on_dev(cache._dev, "the cache", dev)
 
 
 def kv_paged_write(cache: PagedCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor,
@@ -590,30 +628,32 @@ def kv_paged_write(cache: PagedCache, q: torch.Tensor | None, k: torch.Tensor, v
     """A step's k (rotated) and v into the cache's pages; returns q rotated
     (None for q None).  q, k and v are token-major and may be parts of one
     projection's output."""
-    _need_pages(cache)
-    n, hkv, d, dt = k.shape[0], cache.Hkv, cache.d, cache.k.dtype
-    ks, vs = _rows(k, hkv, d, dt, "k"), _rows(v, hkv, d, dt, "v")
+    dev = _call_device(k, "k")
+    _need_pages(cache, dev)
+    n, hkv, d, dt = k.shape[0], cache.Hkv, cache.d, cache._dtype
+    ks, vs = _rows(k, hkv, d, dt, "k", dev), _rows(v, hkv, d, dt, "v", dev)
     if v.shape[0] != n:
         raise ValueError("k has %d tokens, v %d" % (n, v.shape[0]))
-    _need(slot, (n,), torch.int32, "slot")
+    _on(slot, (n,), torch.int32, "slot", dev)
     if cache.rope is not None or position is not None:
-        _need(position, (n,), torch.int32, "position")
+        _on(position, (n,), torch.int32, "position", dev)
     hq = qs = 0
     if q is not None:
         hq = q.shape[1] if q.dim() == 3 else 0
-        qs = _rows(q, hq, d, dt, "q")
+        qs = _rows(q, hq, d, dt, "q", dev)
         if q.shape[0] != n:
             raise ValueError("k has %d tokens, q %d" % (n, q.shape[0]))
         if q_out is None:
             q_out = torch.empty((n, hq, d), dtype=dt, device=q.device)
-        _need(q_out, (n, hq, d), dt, "q_out")
-        _on_current(q, "q")
+        else:
+            _on(q_out, (n, hq, d), dt, "q_out", dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _on_current(k, "k")
-    _on_current(cache.k, "the cache")
-    _check(lib().kv_paged_write(cache._ref, hq, n, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(position),
-                                slot.data_ptr(), _ptr(q_out), _stream()), "kv_paged_write")
+    rc = lib().kv_paged_write(cache._ref, hq, n, q.data_ptr() if q is not None else None, qs, k.data_ptr(), ks,
+                              v.data_ptr(), vs, position.data_ptr() if position is not None else None,
+                              slot.data_ptr(), q_out.data_ptr() if q is not None else None, _raw_stream(dev))
+    if rc:
+        _check(rc, "kv_paged_write")
     return q_out
 
 
@@ -624,28 +664,24 @@ def attn_workspace(device="cuda") -> torch.Tensor:
         return torch.zeros((n,), dtype=torch.uint8, device=device)
 
 
-def _attn_args(q, n_req, q_start, out, lse, ws):
+def _attn_args(q, n_req, q_start, out, lse, ws, dev):
     n, hq, d = q.shape
-    _need(q_start, (n_req + 1,), torch.int32, "q_start")
+    _on(q_start, (n_req + 1,), torch.int32, "q_start", dev)
     if out is None:
         out = torch.empty((n, hq, d), dtype=q.dtype, device=q.device)
-    _need(out, (n, hq, d), q.dtype, "out")
-    lse = _lse_2d(lse, hq, n, q.device)
-    _on_current(q, "q")
+    else:
+        _on(out, (n, hq, d), q.dtype, "out", dev)
+    if lse is True:
+        lse = torch.empty((hq, n), dtype=torch.float32, device=q.device)
+    elif isinstance(lse, torch.Tensor):
+        _on(lse, (hq, n), torch.float32, "lse", dev)
+    else:
+        lse = None
     if ws is None:
         ws = attn_workspace(q.device)
-    _need(ws, (ws.numel(),), torch.uint8, "ws")
-    _on_current(ws, "ws")
+    else:
+        _on(ws, (ws.numel(),), torch.uint8, "ws", dev)
     return out, lse, ws
-
-
-def _lse_2d(lse, hq, n, device):
-    if lse is True:
-        return torch.empty((hq, n), dtype=torch.float32, device=device)
-    if isinstance(lse, torch.Tensor):
-        _need(lse, (hq, n), torch.float32, "lse")
-        return lse
-    return None
 
 
 def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
@@ -654,15 +690,17 @@ def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len
     """Attention of each request's new tokens over its pages (chunks and
     single tokens together).  q is rotated already (kv_paged_write).  Returns
     out (and lse [Hq][tokens] when asked for)."""
-    _need_pages(cache)
-    hq = q.shape[1] if q.dim() == 3 else 0
-    qs = _rows(q, hq, cache.d, cache.k.dtype, "q")
-    _need(kv_len, (cache.n_req,), torch.int32, "kv_len")
-    out, lse, ws = _attn_args(q, cache.n_req, q_start, out, lse, ws)
-    _on_current(cache.k, "the cache")
-    _check(lib().paged_attn(cache._ref, hq, cache.n_req, q.shape[0], q.data_ptr(), qs, q_start.data_ptr(),
-                            kv_len.data_ptr(), out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(),
-                            float(sm_scale), _stream()), "paged_attn")
+    dev = _call_device(q, "q")
+    _need_pages(cache, dev)
+    hq, n_req = q.shape[1] if q.dim() == 3 else 0, cache.n_req
+    qs = _rows(q, hq, cache.d, cache._dtype, "q", dev)
+    _on(kv_len, (n_req,), torch.int32, "kv_len", dev)
+    out, lse, ws = _attn_args(q, n_req, q_start, out, lse, ws, dev)
+    rc = lib().paged_attn(cache._ref, hq, n_req, q.shape[0], q.data_ptr(), qs, q_start.data_ptr(), kv_len.data_ptr(),
+                          out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.numel(),
+                          sm_scale, _raw_stream(dev))
+    if rc:
+        _check(rc, "paged_attn")
     return (out, lse) if lse is not None else out
 
 
@@ -674,21 +712,23 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch
     status collects device status bits.  Returns out (and lse when asked for)."""
     if k.dim() != 3 or k.dtype not in _DTYPE_CODE:
         raise ValueError("k must be a bfloat16 or float16 tensor (tokens, kv heads, d), got %s %s" % (k.dtype, tuple(k.shape)))
+    dev = _call_device(k, "k")
     n_key, hkv, d = k.shape
-    ks, vs = _rows(k, hkv, d, k.dtype, "k"), _rows(v, hkv, d, k.dtype, "v")
+    ks, vs = _rows(k, hkv, d, k.dtype, "k", dev), _rows(v, hkv, d, k.dtype, "v", dev)
     if v.shape[0] != n_key:
         raise ValueError("k has %d tokens, v %d" % (n_key, v.shape[0]))
     hq = q.shape[1] if q.dim() == 3 else 0
-    qs = _rows(q, hq, d, k.dtype, "q")
+    qs = _rows(q, hq, d, k.dtype, "q", dev)
     n_req = k_start.numel()
-    _need(k_start, (n_req,), torch.int32, "k_start")
-    _need(k_len, (n_req,), torch.int32, "k_len")
-    _need(status, (1,), torch.int32, "status")
-    out, lse, ws = _attn_args(q, n_req, q_start, out, lse, ws)
-    _on_current(k, "k")
+    _on(k_start, (n_req,), torch.int32, "k_start", dev)
+    _on(k_len, (n_req,), torch.int32, "k_len", dev)
+    _on(status, (1,), torch.int32, "status", dev)
+    out, lse, ws = _attn_args(q, n_req, q_start, out, lse, ws, dev)
     desc = skv_states(n_key, hkv, d, _DTYPE_CODE[k.dtype], ks, vs, k.data_ptr(), v.data_ptr(), k_start.data_ptr(),
                       k_len.data_ptr(), status.data_ptr())
-    _check(lib().cross_attn(ctypes.byref(desc), hq, n_req, q.shape[0], q.data_ptr(), qs, q_start.data_ptr(),
-                            out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), float(sm_scale), _stream()),
-           "cross_attn")
+    rc = lib().cross_attn(ctypes.byref(desc), hq, n_req, q.shape[0], q.data_ptr(), qs, q_start.data_ptr(),
+                          out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.numel(),
+                          sm_scale, _raw_stream(dev))
+    if rc:
+        _check(rc, "cross_attn")
     return (out, lse) if lse is not None else out
