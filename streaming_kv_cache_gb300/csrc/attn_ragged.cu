@@ -26,10 +26,12 @@
 // score buffers, so that Q K^T of the next key tile runs under the softmax
 // (bound by streaming K and V from HBM; most MMA rows are idle).
 //
-//   warps 0 .. 4 NQ - 1  softmax and epilogue, a warpgroup per query tile
-//   then one warp each   K producer (TMA), V producer (TMA), MMA issuer,
-//                        scheduler (splits the CTA's share into pieces of
-//                        units, loads the pieces' queries by TMA)
+//   warps 0 .. 7        softmax and epilogue.  NQ = 2: a warpgroup per query
+//                       tile, a thread per row.  NQ = 1: a row's keys (and
+//                       its output columns) are halved between two threads
+//   then one warp each  K producer (TMA), V producer (TMA), MMA issuer,
+//                       scheduler (splits the CTA's share into pieces of
+//                       units, loads the pieces' queries by TMA)
 //
 // Keys and values are read as they lie: K rows are the K-major B operand of
 // Q K^T, token-major V rows the MN-major B operand of P V.  A TMA box is 64
@@ -56,14 +58,13 @@ namespace {
 constexpr int BM = 128;   // rows of a query tile
 constexpr int BN = 128;   // keys of a key tile
 constexpr int NP = 4;     // pieces in flight between the scheduler and the other warps
-constexpr uint64_t WAIT_NS = 2000000000ull;   // limit of every wait
-constexpr uint64_t DRAIN_NS = 500000000ull;   // of the wait for own copies and MMAs on the way out
 
 template <int D, int NQ>
 struct RCfg {
-  static constexpr int SM_WARPS = 4 * NQ;
+  static constexpr int SPLIT = NQ == 2 ? 1 : 2;    // threads per row
+  static constexpr int SM_WARPS = 4 * NQ * SPLIT;
   static constexpr int WARP_K = SM_WARPS, WARP_V = SM_WARPS + 1, WARP_MMA = SM_WARPS + 2, WARP_SCHED = SM_WARPS + 3;
-  static constexpr int NT = 128 * (NQ + 1);
+  static constexpr int NT = 32 * SM_WARPS + 128;
   // K and V stages: what the 227 KB hold beside the queries (for d = 64 as
   // many bytes in flight as for 128)
   static constexpr int KST = D == 128 ? (NQ == 2 ? 2 : 3) : (NQ == 2 ? 4 : 6);
@@ -75,11 +76,12 @@ struct RCfg {
   static constexpr int K_OFF = Q_OFF + NQ * QT;
   static constexpr int V_OFF = K_OFF + KST * KT;
   static constexpr int BAR_OFF = V_OFF + VST * KT;
-  static constexpr int MISC_OFF = BAR_OFF + 48 * 8;
-  static constexpr int PIECE_OFF = MISC_OFF + 256;
-  static constexpr int SCAN_OFF = PIECE_OFF + NP * 64;   // running sums of the prologue, one per warp
-  static constexpr int BYTES = SCAN_OFF + 16 * 8;
-  static constexpr int ALLOC = BYTES + 1024;             // slack for 1024-byte alignment
+  static constexpr int MISC_OFF = BAR_OFF + 44 * 8;
+  static constexpr int PIECE_OFF = MISC_OFF + 64;
+  static constexpr int SCAN_OFF = PIECE_OFF + NP * 64;       // running sums of the prologue, one per warp
+  static constexpr int RED_OFF = SCAN_OFF + NT / 32 * 8;     // per row: what its two threads exchange
+  static constexpr int BYTES = RED_OFF + NQ * BM * 4;
+  static constexpr int ALLOC = BYTES + 1024;                 // slack for 1024-byte alignment
   static_assert(ALLOC <= 232448, "shared memory");
 };
 
@@ -101,7 +103,7 @@ struct RBars {
     DRAIN = PCEMPTY + NP,      // MMA commit: everything issued is complete
     COUNT
   };
-  static_assert(COUNT <= 48, "barrier slots");
+  static_assert(COUNT <= 44, "barrier slots");
 };
 
 struct RParams {
@@ -132,29 +134,37 @@ struct Piece {
 };
 static_assert(sizeof(Piece) <= 64, "piece slot");
 
-// sum over i < n of floor((a i + b) / m), by the Euclid-like reduction of
-// counting lattice points under a line: O(log) steps.
-__device__ unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a,
-                                        unsigned long long b) {
+// sum over i < n of floor((a i + b) / BN), by the Euclid-like reduction of
+// counting lattice points under a line: O(log) steps.  a n + b < 2^32.
+__device__ __forceinline__ unsigned long long floor_sum(uint32_t n, uint32_t a, uint32_t b) {
   unsigned long long ans = 0;
+  uint32_t m = BN;
   while (n) {
     if (a >= m) {
-      ans += n * (n - 1) / 2 * (a / m);
-      a %= m;
+      const uint32_t q = a / m;
+      ans += (unsigned long long)n * (n - 1) / 2 * q;
+      a -= q * m;
     }
     if (b >= m) {
-      ans += n * (b / m);
-      b %= m;
+      const uint32_t q = b / m;
+      ans += (unsigned long long)n * q;
+      b -= q * m;
     }
-    const unsigned long long y = a * n + b;
+    const uint32_t y = a * n + b;
     if (y < m) break;
     n = y / m;
-    b = y % m;
-    const unsigned long long t = m;
+    b = y - n * m;
+    const uint32_t t = m;
     m = a;
     a = t;
   }
   return ans;
+}
+
+// x / y for x, y >= 0; most values fit 32 bits, whose division is short
+__device__ __forceinline__ long long udiv(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+  return x / y;
 }
 
 // Key tiles of query block qb of a request (at least one, so that a block
@@ -168,7 +178,7 @@ __device__ __forceinline__ long long unit_prefix(const Span& s, bool causal, int
   if (qb == 0) return 0;
   if (s.kv == 0 || !causal) return (long long)qb * unit_tiles(s, causal, TB, 0);
   const int full = min(qb, nqb - 1);       // blocks that end at a multiple of TB
-  long long t = (long long)floor_sum(full, BN, TB, (long long)(s.kv - s.L) + TB + BN - 1);
+  long long t = (long long)floor_sum(full, TB, (uint32_t)(s.kv - s.L) + TB + BN - 1);
   if (qb > full) t += unit_tiles(s, causal, TB, nqb - 1);
   return t;
 }
@@ -195,34 +205,35 @@ __device__ __forceinline__ size_t ws_index(int slot, int i, int c, int r) {
 }
 
 // Merge query tile i of a unit whose n pieces left partials (O_k, m_k, l_k):
-// O = sum_k w_k O_k / sum_k w_k l_k with w_k = 2^(m_k - M), by the 128 threads
-// of a softmax warpgroup, over the pieces in their order.  A thread takes one
+// O = sum_k w_k O_k / sum_k w_k l_k with w_k = 2^(m_k - M), by the TT threads
+// of a query tile, over the pieces in their order.  A thread takes one
 // row and every `lanes`-th group of 4 columns: a full tile's rows a thread
 // each, a decode step's few rows spread over all threads.  CU column groups of
 // KU pieces are loaded together with their (m, l), M following as it grows,
 // so that up to KU pieces take one round trip.
 template <int D, int NQ, bool F16, int CU, int KU>
-__device__ __noinline__ void merge_pieces(const RParams& p, const Piece& pc, int i, int rows, int t) {
+__device__ __noinline__ void merge_pieces(const RParams& p, int cta0, int n, int row0, int h, int i, int rows, int t) {
   constexpr int CG = D / 4;     // column groups
   const RaggedArgs& a = p.a;
   // piece 0 is the last of its CTA's share, every other the first
-  auto slot = [&](int k) { return 2 * (pc.cta0 + k) + (k == 0 ? 1 : 0); };
-  const int lanes = BM / rows;            // threads per row
+  auto slot = [&](int k) { return 2 * (cta0 + k) + (k == 0 ? 1 : 0); };
+  constexpr int TT = BM * RCfg<D, NQ>::SPLIT;
+  const int lanes = TT / rows;            // threads per row
   const int r = t % rows, c0 = t / rows;
   if (c0 >= lanes) return;
-  const int tok = pc.row0 + i * p.TQ + r / p.G, hq = pc.h * p.G + r % p.G;
+  const int tok = row0 + i * p.TQ + r / p.G, hq = h * p.G + r % p.G;
   uint16_t* dst = a.out + ((size_t)tok * a.Hq + hq) * D;
   for (int c = c0; c < CG; c += CU * lanes) {
     float4 acc[CU];
 #pragma unroll
     for (int u = 0; u < CU; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, den = 0.f;
-    for (int k0 = 0; k0 < pc.n; k0 += KU) {
+    for (int k0 = 0; k0 < n; k0 += KU) {
       float4 v[KU][CU];
       float2 ml[KU];
 #pragma unroll
       for (int x = 0; x < KU; ++x) {
-        const bool on = k0 + x < pc.n;
+        const bool on = k0 + x < n;
         ml[x] = on ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)slot(k0 + x) * NQ + i) * BM + r)
                    : make_float2(0.f, 0.f);
 #pragma unroll
@@ -286,10 +297,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   const uint32_t sbase = tc::smem_u32(smem);
   auto bar = [&](int i) { return sbase + C::BAR_OFF + 8u * i; };
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
-  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
   volatile int* s_last = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);   // per query tile: merge it here
-  volatile int* s_b0 = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 16);
-  volatile long long* s_off = reinterpret_cast<volatile long long*>(smem + C::MISC_OFF + 24);
+  volatile long long* s_off = reinterpret_cast<volatile long long*>(smem + C::MISC_OFF + 16);
+  int* s_first = reinterpret_cast<int*>(smem + C::MISC_OFF + 24);   // the share's first request and its span
+  float* s_red = reinterpret_cast<float*>(smem + C::RED_OFF);
   Piece* s_piece = reinterpret_cast<Piece*>(smem + C::PIECE_OFF);
   long long* s_scan = reinterpret_cast<long long*>(smem + C::SCAN_OFF);
 
@@ -302,12 +313,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < B::COUNT; ++i) {
       int count = 1;
-      if (i >= B::PFULL && i < B::PFULL + 2) count = 4;
-      if (i >= B::OFREE && i < B::OFREE + NQ) count = 4;
+      if (i >= B::PFULL && i < B::PFULL + 2) count = 4 * C::SPLIT;
+      if (i >= B::OFREE && i < B::OFREE + NQ) count = 4 * C::SPLIT;
       if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + C::SM_WARPS;
       tc::mbar_init(bar(i), count);
     }
-    *s_abort = 0;
     tc::fence_barrier_init();
     tc::fence_proxy_async_smem();
   }
@@ -328,15 +338,18 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   {
     const int per = (a.n_req + C::NT - 1) / C::NT;
     const int i0 = min(a.n_req, tid * per), i1 = min(a.n_req, i0 + per);
-    auto cost = [&](int b) -> long long {
-      const Span s = request_span(a, b);
-      if (s.bad && blockIdx.x == 0) set_status(a.status, SKV_DEV_BAD_LEN);
+    auto cost = [&](const Span& s) -> long long {
       if (s.L == 0) return 0;
       const int nqb = (s.L + TB - 1) / TB;
       return a.Hkv * unit_prefix(s, PAGED, TB, nqb, nqb);
     };
     long long sum = 0;
-    for (int b = i0; b < i1; ++b) sum += cost(b);
+    Span sp{};                             // the thread's last request (most have one)
+    for (int b = i0; b < i1; ++b) {
+      sp = request_span(a, b);
+      if (sp.bad && blockIdx.x == 0) set_status(a.status, SKV_DEV_BAD_LEN);
+      sum += cost(sp);
+    }
     long long incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -352,7 +365,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (w == warp) before = total;
       total += s_scan[w];
     }
-    share = max((long long)p.min_share, (total + gridDim.x - 1) / gridDim.x);
+    share = max((long long)p.min_share, udiv(total + gridDim.x - 1, gridDim.x));
     g0 = blockIdx.x * share;
     if (g0 >= total) {                     // no tiles left for this CTA
       if (warp == C::WARP_K) tc::tmem_dealloc(*s_tmem, 512);
@@ -362,11 +375,16 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if (g0 >= at && g0 < at + sum) {
       int b = i0;
       for (; b < i1 - 1; ++b) {
-        const long long c = cost(b);
+        sp = request_span(a, b);
+        const long long c = cost(sp);
         if (g0 < at + c) break;
         at += c;
       }
-      *s_b0 = b;
+      if (b == i1 - 1) sp = request_span(a, b);
+      s_first[0] = b;
+      s_first[1] = sp.q0;
+      s_first[2] = sp.L;
+      s_first[3] = sp.kv;
       *s_off = g0 - at;
     }
   }
@@ -376,8 +394,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  auto wait = [&](int b, uint32_t phase) { return tc::mbar_wait(bar(b), phase & 1, WAIT_NS, s_abort); };
-  auto wait_short = [&](int b, uint32_t phase) { return tc::mbar_wait_short(bar(b), phase & 1, WAIT_NS, s_abort); };
+  // the waits of the key loop: asleep (producers, softmax) or polling (the
+  // MMA issuer, on the critical path)
+  auto wait = [&](int b, uint32_t phase) { return tc::mbar_sleep(bar(b), phase & 1); };
+  auto wait_short = [&](int b, uint32_t phase) { return tc::mbar_poll(bar(b), phase & 1); };
   // piece number pi into registers, its slot given back (whole warps)
   auto take_piece = [&](int pi, Piece& pc) {
     const int s = pi % NP;
@@ -390,7 +410,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   auto tiles_of = [&](const Piece& pc) { return NQ == 1 || pc.ntok <= p.TQ ? 1 : 2; };   // query tiles with rows
 
   if (warp >= C::SM_WARPS) {
-    // 2 x 128 x 208 + 128 x 88 = the 384 x 168 registers of the launch
+    // 256 x 208 + 128 x 88 = the 384 x 168 registers of the launch
     if constexpr (NQ == 2) tc::setmaxnreg_dec<88>();
     if (warp == C::WARP_K || warp == C::WARP_V) {
       // ---------------------------------------------------------- producers
@@ -398,7 +418,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
       const int nst = is_k ? KST : VST, full = is_k ? B::KFULL : B::VFULL, empty = is_k ? B::KEMPTY : B::VEMPTY;
       const uint32_t base = sbase + (is_k ? C::K_OFF : C::V_OFF);
-      int gt = 0;
+      int st = 0, n = 0;                // stage, tiles issued
+      uint32_t eph = 1;                 // phase of EMPTY: nothing to wait for in the first round
       Piece pc;
       bool ok = true;
       for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
@@ -409,41 +430,38 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           return PAGED && j < pc.nt && lane < p.boxes && r < pc.kv ? __ldg(row + r / a.page_size) : -1;
         };
         int id = page_of(0);
-        for (int j = 0; j < pc.nt; ++j, ++gt) {
-          const int s = gt % nst, r0 = (pc.ta + j) * BN;
+        for (int j = 0; j < pc.nt; ++j, ++n) {
+          const int r0 = (pc.ta + j) * BN;
           const int n_box = (max(0, min(BN, pc.kv - r0)) + p.BR - 1) / p.BR;
-          if (gt >= nst) ok = wait(empty + s, gt / nst - 1);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, wait(empty + st, eph));
           if (!ok) break;
-          if (lane == 0) tc::mbar_arrive_expect_tx(bar(full + s), n_box * p.BR * 128 * (D / 64));
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar(full + st), n_box * p.BR * 128 * (D / 64));
           __syncwarp();
           if (lane < n_box) {
             const int r = r0 + lane * p.BR;
-            int y, z;
+            int y = pc.h, z = pc.krow + r;
             if constexpr (PAGED) {
               // a page outside the pool reads as the zeros outside the map
               const bool in = id >= 0 && id < a.n_page;
               if (!in) set_status(a.status, SKV_DEV_BAD_PAGE);
               y = r % a.page_size;
               z = in ? id * a.Hkv + pc.h : -1;
-            } else {
-              y = pc.h;
-              z = pc.krow + r;
             }
 #pragma unroll
             for (int hf = 0; hf < D / 64; ++hf)
-              tc::tma_load_3d(base + s * C::KT + hf * C::HALF + lane * p.BR * 128, map, bar(full + s), hf * 64, y, z);
+              tc::tma_load_3d(base + st * C::KT + hf * C::HALF + lane * p.BR * 128, map, bar(full + st), hf * 64, y, z);
           }
           id = page_of(j + 1);
+          if (++st == nst) {
+            st = 0;
+            eph ^= 1;
+          }
         }
         if (!ok) break;
       }
       if (!ok && lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
       // the copies this warp started land before the CTA exits
-      for (int j = max(0, gt - nst); j < gt; ++j) {
-        volatile int never = 0;
-        tc::mbar_wait(bar(full + j % nst), (j / nst) & 1, DRAIN_NS, &never);
-      }
+      for (int j = max(0, n - nst); j < n; ++j) wait(full + j % nst, j / nst);
     } else if (warp == C::WARP_MMA) {
       // --------------------------------------------------------- MMA issuer
       constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16(BM, BN) : tc::idesc_bf16(BM, BN);
@@ -464,104 +482,130 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const uint64_t dv = tc::opaque(dv0 + ((uint32_t)(vs * C::KT) >> 4));
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          tc::mma_ts(tmem + 256 + i * 128, tmem + buf * BN + kk * 8, dv + ((kk * 2048) >> 4), idesc_pv,
-                     (!fresh || kk > 0) ? 1u : 0u);
+          tc::mma_ts(tmem + 256 + i * 128, tmem + buf * BN + (kk >> 2) * 64 + (kk & 3) * 8, dv + ((kk * 2048) >> 4),
+                     idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
       };
-      // Tiles with a P V still to come: the last one issued.  cnt[i] counts the
-      // key tiles of query tile i, pcs[i] the pieces it was part of.
-      int gt = 0, cnt[2] = {0, 0}, pcs[2] = {0, 0};
-      bool prev = false, prev_fresh = false;
-      int prev_nq = 0;
-      bool ok = true;
-      // P V of query tile i of the tile before; its V stage is gt - 1's
-      auto pv = [&](int i) {
-        const int c = cnt[i] - 1, x = NQ == 2 ? i : c & 1, ph = NQ == 2 ? c : c >> 1;
-        if (!(ok = wait_short(B::VFULL + (gt - 1) % VST, (gt - 1) / VST))) return;
-        if (!(ok = wait_short(B::PFULL + x, ph))) return;
-        // the piece before has been read out of O
-        if (prev_fresh && pcs[i] > 1 && !(ok = wait_short(B::OFREE + i, pcs[i] - 2))) return;
-        tc::tc_fence_after();
-        issue_pv(i, (gt - 1) % VST, x, prev_fresh);
-        tc::mma_commit(bar(B::PVDONE + x));
-      };
-      Piece pc;
-      for (int pi = 0; ok && (ok = take_piece(pi, pc)); ++pi) {
-        if (lane == 0) {
-          const int nq = pc.nt ? tiles_of(pc) : 0;
-          for (int j = 0; ok && j < max(pc.nt, 1); ++j) {
-            const bool work = pc.nt > 0;
-            // at a piece's start the P V before it do not wait for its queries
-            if (NQ == 2 || j == 0 || !work) {
-              if (prev) pv(0);
-              if (!ok) break;
-              if (NQ == 1 && prev) {
-                tc::mma_commit(bar(B::VEMPTY + (gt - 1) % VST));
-                prev = false;
+      // One thread issues everything.  The tensor pipe takes only a few MMAs
+      // ahead, so what this thread does between two MMAs may leave it idle: the
+      // state is a few scalars (stage numbers and barrier phases), no struct
+      // and no division, and a wait is a few instructions.
+      if (lane == 0) {
+        bool ok = true;
+        int ks = 0, vs = 0, buf = 0;                  // K and V stage; NQ = 1: score buffer of the next tile
+        uint32_t kph = 0, vph = 0, qph = 0;           // their phases, and the queries'
+        uint32_t pph0 = 0, pph1 = 0;                  // phases of PFULL 0 and 1
+        uint32_t oph0 = 1, oph1 = 1;                  // of OFREE: nothing to wait for the first time
+        bool prev = false, prev2 = false, fresh = false;   // the tile before: its P V is to come, two query tiles, first of its piece
+        // P V of query tile i of the tile before, from score buffer x
+        auto pv = [&](int i, int x, uint32_t& pph, uint32_t& oph) {
+          ok = wait_short(B::PFULL + x, pph);
+          pph ^= 1;
+          if (fresh) {
+            // the piece before has been read out of O
+            ok = wait_short(B::OFREE + i, oph) && ok;
+            oph ^= 1;
+          }
+          if (!ok) return;
+          tc::tc_fence_after();
+          issue_pv(i, vs, x, fresh);
+          tc::mma_commit(bar(B::PVDONE + x));
+        };
+        auto pv_prev1 = [&]() {                       // NQ = 1: the P V before, from the other score buffer
+          ok = wait_short(B::VFULL + vs, vph);
+          if (!ok) return;
+          if (buf) pv(0, 0, pph0, oph0);
+          else pv(0, 1, pph1, oph0);
+        };
+        auto v_done = [&]() {
+          tc::mma_commit(bar(B::VEMPTY + vs));
+          if (++vs == VST) {
+            vs = 0;
+            vph ^= 1;
+          }
+          prev = false;
+        };
+        for (int pi = 0; ok; ++pi) {
+          const int slot = pi % NP;
+          if (!(ok = wait_short(B::PCFULL + slot, pi / NP))) break;
+          const int nt = s_piece[slot].nt;
+          const bool two = NQ == 2 && s_piece[slot].ntok > p.TQ;
+          tc::mbar_arrive(bar(B::PCEMPTY + slot));
+          for (int j = 0; j < max(nt, 1); ++j) {
+            // at a piece's start (and at the end) the P V before do not wait
+            // for queries to come
+            if (NQ == 2) {
+              if (prev) {
+                if (!(ok = wait_short(B::VFULL + vs, vph))) break;
+                pv(0, 0, pph0, oph0);
+                if (!ok) break;
               }
+            } else if (prev && j == 0) {
+              pv_prev1();
+              if (!ok) break;
+              v_done();
             }
-            if (work) {
-              if (j == 0 && !(ok = wait_short(B::QFULL, pi))) break;
-              if (!(ok = wait_short(B::KFULL + gt % KST, gt / KST))) break;
+            if (nt) {
+              if (j == 0) {
+                if (!(ok = wait_short(B::QFULL, qph))) break;
+                qph ^= 1;
+              }
+              if (!(ok = wait_short(B::KFULL + ks, kph))) break;
               tc::tc_fence_after();
-              const int x = NQ == 2 ? 0 : cnt[0] & 1;
-              issue_qk(0, gt % KST, x);
+              const int x = NQ == 2 ? 0 : buf;
+              issue_qk(0, ks, x);
               tc::mma_commit(bar(B::SFULL + x));
             }
             if (prev) {
-              if (NQ == 1) pv(0);
-              else if (prev_nq == 2) pv(1);
+              if (NQ == 1) pv_prev1();
+              else if (prev2) pv(1, 1, pph1, oph1);
               if (!ok) break;
-              tc::mma_commit(bar(B::VEMPTY + (gt - 1) % VST));
+              v_done();
             }
-            prev = false;
-            if (work) {
-              if (nq == 2) {
-                issue_qk(1, gt % KST, 1);
+            if (nt) {
+              if (two) {
+                issue_qk(1, ks, 1);
                 tc::mma_commit(bar(B::SFULL + 1));
               }
-              tc::mma_commit(bar(B::KEMPTY + gt % KST));
-              if (j == pc.nt - 1) tc::mma_commit(bar(B::QEMPTY));
-              prev = true;
-              prev_fresh = j == 0;
-              prev_nq = nq;
-              for (int i = 0; i < nq; ++i) {
-                ++cnt[i];
-                if (j == 0) ++pcs[i];
+              tc::mma_commit(bar(B::KEMPTY + ks));
+              if (j == nt - 1) tc::mma_commit(bar(B::QEMPTY));
+              if (++ks == KST) {
+                ks = 0;
+                kph ^= 1;
               }
-              ++gt;
+              if (NQ == 1) buf ^= 1;
+              prev = true;
+              prev2 = two;
+              fresh = j == 0;
             }
           }
+          if (!nt) break;
         }
-        ok = __all_sync(0xffffffffu, ok);
-        if (!pc.nt) break;
-      }
-      if (lane == 0) {
         if (!ok) set_status(a.status, SKV_DEV_TIMEOUT);
         // every MMA issued completes before TMEM is released
         tc::mma_commit(bar(B::DRAIN));
-        volatile int never = 0;
-        tc::mbar_wait(bar(B::DRAIN), 0, DRAIN_NS, &never);
+        wait(B::DRAIN, 0);
       }
-    } else {
+    } else if (warp == C::WARP_SCHED) {
       // ---------------------------------------------------------- scheduler
-      if (lane == 0) {
-        int b = *s_b0;
-        long long off = *s_off, g = g0;
-        Span s = request_span(a, b);
-        int nqb = (s.L + TB - 1) / TB, h, qb, t;
-        {
-          const long long per_head = unit_prefix(s, PAGED, TB, nqb, nqb);
-          h = (int)(off / per_head);
-          off -= h * per_head;
-          int lo = 0, hi = nqb - 1;       // the last block whose tiles start at or before off
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (unit_prefix(s, PAGED, TB, nqb, mid) <= off) lo = mid;
-            else hi = mid - 1;
-          }
-          qb = lo;
-          t = (int)(off - unit_prefix(s, PAGED, TB, nqb, qb));
+      int b = s_first[0], h, qb = 0, t;
+      Span s{s_first[1], s_first[2], s_first[3], false};
+      int nqb = (s.L + TB - 1) / TB;
+      {
+        long long off = *s_off;
+        const long long per_head = unit_prefix(s, PAGED, TB, nqb, nqb);
+        h = (int)udiv(off, per_head);
+        off -= h * per_head;
+        // the last block whose tiles start at or before off, 32 candidates at a time
+        for (int hi = nqb; hi - qb > 1;) {
+          const int step = (hi - qb + 31) / 32, x = qb + lane * step;
+          const bool le = x < hi && unit_prefix(s, PAGED, TB, nqb, x) <= off;
+          qb += (31 - __clz(__ballot_sync(0xffffffffu, le))) * step;
+          hi = min(hi, qb + step);
         }
+        t = (int)(off - unit_prefix(s, PAGED, TB, nqb, qb));
+      }
+      if (lane == 0) {
+        long long g = g0;
         bool ok = true;
         int loaded = 0;                   // pieces whose queries are on their way
         for (int pi = 0; ok; ++pi) {
@@ -581,8 +625,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             pc.krow = PAGED ? 0 : a.k_start[b];
             pc.n = 1;
             if (u0 < g0 || u1 > g1) {
-              pc.cta0 = (int)(u0 / share);
-              pc.n = (int)((u1 - 1) / share) - pc.cta0 + 1;
+              pc.cta0 = (int)udiv(u0, share);
+              pc.n = (int)udiv(u1 - 1, share) - pc.cta0 + 1;
               pc.k = (int)blockIdx.x - pc.cta0;
               pc.slot = 2 * (int)blockIdx.x + (pc.k == 0 ? 1 : 0);
             }
@@ -616,21 +660,43 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           loaded = pi + 1;
         }
         if (!ok) set_status(a.status, SKV_DEV_TIMEOUT);
-        if (loaded) {
-          volatile int never = 0;
-          tc::mbar_wait(bar(B::QFULL), (loaded - 1) & 1, DRAIN_NS, &never);
-        }
+        if (loaded) wait(B::QFULL, loaded - 1);
       }
     }
   } else {
     // ------------------------------------------------- softmax and epilogue
     if constexpr (NQ == 2) tc::setmaxnreg_inc<208>();
-    const int i = warp >> 2, lg = warp & 3;        // query tile, TMEM lane group
+    constexpr int SPLIT = C::SPLIT;
+    constexpr int HN = BN / SPLIT, HD = D / SPLIT;   // keys of a tile and output columns of this thread
+    const int lg = warp & 3;                         // TMEM lane group
+    const int i = SPLIT == 1 ? warp >> 2 : 0, hh = SPLIT == 1 ? 0 : warp >> 2;   // query tile, half of the row
     const int row = lg * 32 + lane;
+    // named barriers: the warps of a lane group, and of a query tile
+    const int pair_bar = 1 + lg, tile_bar = 5 + i;
+    constexpr int TT = BM * SPLIT;                   // threads of a query tile
     const uint32_t t_lane = (uint32_t)(lg * 32) << 16;
-    const uint32_t tO = tmem + t_lane + 256 + i * 128;
+    const uint32_t tO = tmem + t_lane + 256 + i * 128 + hh * HD;
     const int tok = row / p.G, gq = row - tok * p.G;
     const float sl = p.scale_log2;
+    // f of the two halves' values of a row, in both threads
+    auto exchange = [&](float x, auto f) {
+      if constexpr (SPLIT == 1) return x;
+      float* r = s_red + i * BM + row;
+      if (hh == 1) *r = x;
+      tc::bar_sync_n(pair_bar, 64);
+      if (hh == 0) *r = x = f(x, *r);
+      tc::bar_sync_n(pair_bar, 64);
+      return hh == 0 ? x : *r;
+    };
+    // a predicate of both threads' warps
+    auto group_and = [&](bool v) {
+      if constexpr (SPLIT == 1) return (bool)__all_sync(0xffffffffu, v);
+      else return tc::bar_and(pair_bar, 64, v);
+    };
+    auto group_or = [&](bool v) {
+      if constexpr (SPLIT == 1) return (bool)__any_sync(0xffffffffu, v);
+      else return tc::bar_or(pair_bar, 64, v);
+    };
     int gt = 0, cnt = 0;                           // key tiles of the CTA and of this query tile so far
     Piece pc;
     bool ok = true;
@@ -641,28 +707,31 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       const int ntok = min(p.TQ, pc.ntok - i * p.TQ);   // tokens in this query tile
       const bool valid = tok < ntok;
-      const bool active = lg * 32 < ntok * p.G;         // some row of the warp is valid
-      const int lim = pc.pos0 + pc.step * (i * p.TQ + tok);   // the last key this row sees
+      const bool active = lg * 32 < ntok * p.G;         // some row of the lane group is valid
+      // keys that this row sees, from this thread's first key of a tile 0 on
+      const int n_row = pc.pos0 + pc.step * (i * p.TQ + tok) + 1 - hh * HN;
       float m_used = 0.f, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < pc.nt; ++j, ++gt, ++cnt) {
         const int x = NQ == 2 ? i : cnt & 1, ph = NQ == 2 ? cnt : cnt >> 1;
         const int r0 = (pc.ta + j) * BN;
-        const uint32_t tS = tmem + t_lane + x * BN;
-        // tcgen05.ld/st are warp-collective: every branch around them is warp-uniform
-        ok = __all_sync(0xffffffffu, wait(B::SFULL + x, ph));
+        const uint32_t tS = tmem + t_lane + x * BN + hh * HN;
+        // tcgen05.ld/st are warp-collective: every branch around them is
+        // warp-uniform; the two warps of a lane group agree on every barrier
+        ok = wait(B::SFULL + x, ph);
+        ok = active ? group_and(ok) : __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (active) {
           tc::tc_fence_after();
-          uint32_t v[BN];
+          uint32_t v[HN];
 #pragma unroll
-          for (int cb = 0; cb < BN / 32; ++cb)
+          for (int cb = 0; cb < HN / 32; ++cb)
             tc::tmem_ld32(tS + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(v + cb * 32));
-          const int n_see = lim + 1 - r0;          // keys of the tile that the row sees
+          const int n_see = n_row - r0;            // of this thread's keys of the tile
           tc::tmem_wait_ld();
-          if (!__all_sync(0xffffffffu, n_see >= BN)) {
+          if (!__all_sync(0xffffffffu, n_see >= HN)) {
 #pragma unroll
-            for (int k = 0; k < BN; ++k)
+            for (int k = 0; k < HN; ++k)
               if (k >= n_see) v[k] = __float_as_uint(-INFINITY);
           }
           auto row_max = [&]() {
@@ -670,12 +739,13 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
             for (int q = 0; q < 4; ++q) m4[q] = fmaxf(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
 #pragma unroll
-            for (int k = 8; k < BN; k += 2)
+            for (int k = 8; k < HN; k += 2)
               m4[(k >> 1) & 3] = fmax3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
+            return exchange(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl,
+                            [](float a, float b) { return fmaxf(a, b); });
           };
-          // P = 2^(s scale - m) in the values' type into the first 64 columns
-          // of the scores (rounded once: the products of P V take 16-bit
+          // P = 2^(s scale - m) in the values' type over the first half of
+          // either 64 scores (rounded once: the products of P V take 16-bit
           // operands); the sum is taken in fp32 before that rounding
           auto p_pass = [&]() {
             const uint64_t sl2 = f2_pack(sl, sl), nm2 = f2_pack(-m_used, -m_used);
@@ -683,7 +753,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
             for (int q = 0; q < 4; ++q) l2[q] = 0ull;
 #pragma unroll
-            for (int cb = 0; cb < BN / 32; ++cb) {
+            for (int cb = 0; cb < HN / 32; ++cb) {
               uint32_t pk[16];
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
@@ -694,7 +764,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 l2[(k >> 1) & 3] = f2_add(l2[(k >> 1) & 3], f2_pack(p0, p1));
                 pk[k >> 1] = pack16<F16>(p0, p1);
               }
-              tc::tmem_st16(tS + cb * 16, pk);
+              tc::tmem_st16(tS + (cb >> 1) * 64 + (cb & 1) * 16, pk);
             }
             const uint64_t s2 = f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3]));
             float s0, s1;
@@ -705,13 +775,15 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             const float mx = row_max();
             m_used = mx == -INFINITY ? 0.f : mx;
           }
-          float ts = p_pass();
-          if (__any_sync(0xffffffffu, valid && !(ts <= LAG_LIMIT))) {
+          float ts;
+          for (bool again = false;; again = true) {
+            ts = p_pass();
+            if (again || !group_or(valid && !(ts <= LAG_LIMIT))) break;
             tc::tmem_wait_st();
             if (NQ == 1 && j > 0) {
               // two query tiles: these scores were issued after the P V before
               // them; one: that P V may still be running
-              ok = __all_sync(0xffffffffu, wait(B::PVDONE + ((cnt - 1) & 1), (cnt - 1) >> 1));
+              ok = group_and(wait(B::PVDONE + ((cnt - 1) & 1), (cnt - 1) >> 1));
               if (!ok) break;
               tc::tc_fence_after();
             }
@@ -721,7 +793,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             l *= alpha;
             if (j > 0) {
 #pragma unroll 1
-              for (int cb = 0; cb < D / 16; ++cb) {   // 16 columns at a time: the score row stays live
+              for (int cb = 0; cb < HD / 16; ++cb) {   // 16 columns at a time: the scores stay live
                 uint32_t o[16];
                 tc::tmem_ld16(tO + cb * 16, o);
                 tc::tmem_wait_ld();
@@ -731,22 +803,22 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               }
             }
             m_used = m_new;
-            ts = p_pass();
           }
+          if (!ok) break;
           l += ts;
         }
-        if (i == 0 && r0 + BN > pc.kv) {
+        if (r0 + BN > pc.kv) {
           // value rows past the keys (the rest of a page, another request's
-          // states, or whatever the stage held before)
+          // states, or whatever the stage held before); with two query tiles
+          // each sees to it before its own P V, both write the same zeros
           ok = __all_sync(0xffffffffu, wait(B::VFULL + gt % VST, gt / VST));
-          if (!ok) break;
           if (r0 + row >= pc.kv) {
 #pragma unroll
-            for (int hf = 0; hf < D / 64; ++hf)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(smem + C::V_OFF + (gt % VST) * C::KT + hf * C::HALF + row * 128 + c * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < HD / 8; ++c) {
+              const int ch = hh * (HD / 8) + c;
+              *reinterpret_cast<uint4*>(smem + C::V_OFF + (gt % VST) * C::KT + (ch >> 3) * C::HALF + row * 128 +
+                                        (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
           tc::fence_proxy_async_smem();
         }
@@ -757,76 +829,133 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(B::PFULL + x));
       }
-      if (!ok) break;
       {
         const int c = cnt - 1, x = NQ == 2 ? i : c & 1, ph = NQ == 2 ? c : c >> 1;
-        ok = __all_sync(0xffffffffu, wait(B::PVDONE + x, ph));
+        if (ok) ok = __all_sync(0xffffffffu, wait(B::PVDONE + x, ph));
+        // the warps of the query tile go on together (barriers below)
+        ok = tc::bar_and(tile_bar, TT, ok);
         if (!ok) break;
       }
       tc::tc_fence_after();
+      if (active) l = exchange(l, [](float a, float b) { return a + b; });
       const int hq = pc.h * p.G + gq, trow = pc.row0 + i * p.TQ + tok;
-      if (active) {
-        if (pc.n == 1) {
+      const int rows = ntok * p.G;
+      uint16_t* orow = a.out + ((size_t)(valid ? trow : 0) * a.Hq + hq) * D + hh * HD;
+      float* lse = valid && hh == 0 && a.lse ? a.lse + (size_t)hq * a.n_tok + trow : nullptr;
+      auto store_row = [&](int cb, const float (&o)[32], float f) {
+        if (!valid) return;
+        uint4 pk[4];
+        uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) pw[k] = pack16<F16>(o[2 * k] * f, o[2 * k + 1] * f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(orow + cb * 32)[k] = pk[k];
+      };
+      if (pc.n == 1) {
+        if (active) {
           const float inv_l = l == 0.f ? 0.f : 1.f / l;
-          uint16_t* orow = a.out + ((size_t)(valid ? trow : 0) * a.Hq + hq) * D;
 #pragma unroll 1
-          for (int cb = 0; cb < D / 32; ++cb) {
-            uint32_t o[32];
-            tc::tmem_ld32(tO + cb * 32, o);
+          for (int cb = 0; cb < HD / 32; ++cb) {
+            float o[32];
+            tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
             tc::tmem_wait_ld();
-            if (valid) {
-              uint4 pk[4];
-              uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                pw[k] = pack16<F16>(__uint_as_float(o[2 * k]) * inv_l, __uint_as_float(o[2 * k + 1]) * inv_l);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(orow + cb * 32)[k] = pk[k];
-            }
+            store_row(cb, o, inv_l);
           }
-          if (valid && a.lse)
-            a.lse[(size_t)hq * a.n_tok + trow] = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
-        } else {
+          if (lse) *lse = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
+        }
+      } else {
+        // A shared unit.  With few rows every piece goes through the
+        // workspace.  With many, the piece that finds all others there (or
+        // arrives last) takes its own part from TMEM, a thread per half row.
+        const bool big = rows > BM / 2;
+        int* count = p.ws_count + 2 * pc.cta0 + i;
+        const bool leader = row == 0 && hh == 0;
+        if (big) {
+          if (leader) s_last[i] = tc::ld_acquire_gpu(reinterpret_cast<const uint32_t*>(count)) == (uint32_t)(pc.n - 1);
+          tc::bar_sync_n(tile_bar, TT);
+        }
+        bool last = big && s_last[i];
+        if (!last) {
+          if (active) {
 #pragma unroll 1
-          for (int cb = 0; cb < D / 32; ++cb) {
-            uint32_t o[32];
-            tc::tmem_ld32(tO + cb * 32, o);
-            tc::tmem_wait_ld();
-            if (valid) {
+            for (int cb = 0; cb < HD / 32; ++cb) {
+              uint32_t o[32];
+              tc::tmem_ld32(tO + cb * 32, o);
+              tc::tmem_wait_ld();
+              if (valid) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(p.ws_o + ws_index<D, NQ>(pc.slot, i, cb * 8 + k, row)) =
-                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                for (int k = 0; k < 8; ++k)
+                  *reinterpret_cast<uint4*>(p.ws_o + ws_index<D, NQ>(pc.slot, i, hh * (HD / 4) + cb * 8 + k, row)) =
+                      make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              }
             }
+            if (valid && hh == 0)
+              reinterpret_cast<float2*>(p.ws_ml)[((size_t)pc.slot * NQ + i) * BM + row] = make_float2(m_used, l);
           }
-          if (valid)
-            reinterpret_cast<float2*>(p.ws_ml)[((size_t)pc.slot * NQ + i) * BM + row] = make_float2(m_used, l);
+          tc::bar_sync_n(tile_bar, TT);
+          if (leader) {
+            __threadfence();
+            s_last[i] = atomicAdd(count, 1) == pc.n - 1;
+          }
+          tc::bar_sync_n(tile_bar, TT);
+          last = s_last[i];
+        }
+        if (last) {
+          if (leader) *count = 0;          // ready for the next call
+          __threadfence();
+          if (!big) {
+            // few rows (decode): a thread has one column group, many pieces in flight
+            if (rows * (D / 4) <= TT) merge_pieces<D, NQ, F16, 1, 16>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, hh * BM + row);
+            else merge_pieces<D, NQ, F16, 4, 4>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, hh * BM + row);
+          } else if (active) {
+            auto slot = [&](int k) { return 2 * (pc.cta0 + k) + (k == 0 ? 1 : 0); };
+            auto ml_of = [&](int k) {
+              return k == pc.k ? make_float2(m_used, l)
+                               : __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)slot(k) * NQ + i) * BM + row);
+            };
+            float M = -INFINITY, den = 0.f;
+            for (int k = 0; k < pc.n; ++k) {
+              const float2 ml = ml_of(k);
+              if (ml.y == 0.f) continue;     // no key that the row sees
+              const float mx = fmaxf(M, ml.x);
+              den = den * (M == -INFINITY ? 0.f : exp2f(M - mx)) + exp2f(ml.x - mx) * ml.y;
+              M = mx;
+            }
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll 1
+            for (int cb = 0; cb < HD / 32; ++cb) {
+              float acc[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+              for (int k = 0; k < pc.n; ++k) {
+                const float2 ml = ml_of(k);
+                const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
+                float o[32];
+                if (k == pc.k) {
+                  tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+                  tc::tmem_wait_ld();
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    *reinterpret_cast<float4*>(o + 4 * e) = __ldcg(
+                        reinterpret_cast<const float4*>(p.ws_o + ws_index<D, NQ>(slot(k), i, hh * (HD / 4) + cb * 8 + e, row)));
+                }
+                if (w != 0.f) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) acc[e] += w * o[e];
+                }
+              }
+              store_row(cb, acc, inv);
+            }
+            if (lse) *lse = den == 0.f ? -INFINITY : (M + __log2f(den)) * 0.69314718055994531f;
+          }
         }
       }
       // O is read out: the next piece's first P V may overwrite it
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(bar(B::OFREE + i));
-      if (pc.n > 1) {
-        tc::bar_sync_n(1 + i, 128);
-        if (row == 0) {
-          __threadfence();
-          int* count = p.ws_count + 2 * pc.cta0 + i;
-          const bool last = atomicAdd(count, 1) == pc.n - 1;
-          if (last) {
-            *count = 0;                  // ready for the next call
-            __threadfence();
-          }
-          s_last[i] = last;
-        }
-        tc::bar_sync_n(1 + i, 128);
-        if (s_last[i]) {
-          const int rows = ntok * p.G;
-          // few rows (decode): a thread has one column group, many pieces in flight
-          if (rows * (D / 4) <= BM) merge_pieces<D, NQ, F16, 1, 20>(p, pc, i, rows, row);
-          else merge_pieces<D, NQ, F16, 8, 4>(p, pc, i, rows, row);
-        }
-      }
     }
     if (!ok && lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
   }

@@ -159,6 +159,35 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
   return bounded_wait<SW>(mbar_try_wait_short, bar, parity, limit_ns, abort);
 }
 
+// Waits of a few instructions, for loops whose issue must stay short: poll
+// (14 cycles a try when the phase is complete), or sleep in try_wait, up to a
+// millisecond a try.  Both end after a count of tries, about two seconds, and
+// return false.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b32 c;\n mov.b32 c, 200000000;\n mov.b32 %0, 1;\n"
+      "TRY:\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
+      " sub.s32 c, c, 1;\n setp.gt.s32 q, c, 0;\n @q bra TRY;\n mov.b32 %0, 0;\n"
+      "DONE:\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b32 c;\n mov.b32 c, 2000;\n mov.b32 %0, 1;\n"
+      "TRY:\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n @p bra DONE;\n"
+      " sub.s32 c, c, 1;\n setp.gt.s32 q, c, 0;\n @q bra TRY;\n mov.b32 %0, 0;\n"
+      "DONE:\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+      : "memory");
+  return ok != 0;
+}
+
 // A value the compiler must (re)compute where it stands: keeps loop-invariant
 // descriptors from being hoisted and held in registers across a loop.
 __device__ __forceinline__ uint64_t opaque(uint64_t x) {
@@ -356,6 +385,18 @@ __device__ __forceinline__ bool bar_and(int id, int n, bool v) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.and.pred q, %2, %3, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// Named barrier over n threads that also ORs a predicate across them.
+__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, %2, %3, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"((uint32_t)v), "r"(id), "r"(n)
