@@ -67,8 +67,9 @@ struct RCfg {
   static constexpr int NT = 32 * SM_WARPS + 128;
   // K and V stages: what the 227 KB hold beside the queries (for d = 64 as
   // many bytes in flight as for 128)
-  static constexpr int KST = D == 128 ? (NQ == 2 ? 2 : 3) : (NQ == 2 ? 4 : 6);
-  static constexpr int VST = D == 128 ? 3 : (NQ == 2 ? 4 : 6);
+  static constexpr int KST = D == 128 ? 3 : (NQ == 2 ? 4 : 6);
+  static constexpr int VST = D == 128 ? (NQ == 2 ? 2 : 3) : (NQ == 2 ? 4 : 6);
+  static_assert(VST <= KST, "V stages are freed with the K stages (see the producers)");
   static constexpr int QT = BM * D * 2;        // bytes of a query tile
   static constexpr int KT = BN * D * 2;        // of a key or value tile
   static constexpr int HALF = BM * 128;        // one 64-dimension half of either
@@ -91,10 +92,9 @@ struct RBars {
     QFULL = 0,                 // the piece's queries landed (TMA)
     QEMPTY,                    // MMA commit: the piece's Q K^T are done with them
     KFULL,                     // K tile landed
-    KEMPTY = KFULL + KST,      // MMA commit: K stage free
-    VFULL = KEMPTY + KST,      // V tile landed
-    VEMPTY = VFULL + VST,      // MMA commit: V stage free
-    SFULL = VEMPTY + VST,      // MMA commit: scores in buffer x
+    EMPTY = KFULL + KST,       // MMA commit: K stage free, and the V stage of the tile before
+    VFULL = EMPTY + KST,       // V tile landed
+    SFULL = VFULL + VST,       // MMA commit: scores in buffer x
     PFULL = SFULL + 2,         // softmax warps: probabilities in buffer x
     PVDONE = PFULL + 2,        // MMA commit: the P V from buffer x landed in O
     OFREE = PVDONE + 2,        // softmax warps: O of query tile i read out
@@ -394,10 +394,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  // the waits of the key loop: asleep (producers, softmax) or polling (the
-  // MMA issuer, on the critical path)
   auto wait = [&](int b, uint32_t phase) { return tc::mbar_sleep(bar(b), phase & 1); };
-  auto wait_short = [&](int b, uint32_t phase) { return tc::mbar_poll(bar(b), phase & 1); };
   // piece number pi into registers, its slot given back (whole warps)
   auto take_piece = [&](int pi, Piece& pc) {
     const int s = pi % NP;
@@ -416,10 +413,16 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       // ---------------------------------------------------------- producers
       const bool is_k = warp == C::WARP_K;
       const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
-      const int nst = is_k ? KST : VST, full = is_k ? B::KFULL : B::VFULL, empty = is_k ? B::KEMPTY : B::VEMPTY;
+      const int nst = is_k ? KST : VST, full = is_k ? B::KFULL : B::VFULL;
       const uint32_t base = sbase + (is_k ? C::K_OFF : C::V_OFF);
+      // Step n of the MMA issuer (Q K^T of tile n, P V of tile n - 1) ends with
+      // a commit on EMPTY[n mod KST].  It frees the K stage of tile n and the V
+      // stage of tile n - 1: K tile n waits for step n - KST, V tile n for step
+      // n - VST + 1, whose barriers cannot be a phase further by then.
       int st = 0, n = 0;                // stage, tiles issued
-      uint32_t eph = 1;                 // phase of EMPTY: nothing to wait for in the first round
+      int es = 0;                       // EMPTY barrier and phase of the next wait
+      uint32_t eph = 0;
+      if (!is_k) es = 1;                // V tile VST waits for step 1
       Piece pc;
       bool ok = true;
       for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
@@ -433,8 +436,14 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         for (int j = 0; j < pc.nt; ++j, ++n) {
           const int r0 = (pc.ta + j) * BN;
           const int n_box = (max(0, min(BN, pc.kv - r0)) + p.BR - 1) / p.BR;
-          ok = __all_sync(0xffffffffu, wait(empty + st, eph));
-          if (!ok) break;
+          if (n >= nst) {
+            ok = __all_sync(0xffffffffu, wait(B::EMPTY + es, eph));
+            if (!ok) break;
+            if (++es == KST) {
+              es = 0;
+              eph ^= 1;
+            }
+          }
           if (lane == 0) tc::mbar_arrive_expect_tx(bar(full + st), n_box * p.BR * 128 * (D / 64));
           __syncwarp();
           if (lane < n_box) {
@@ -452,10 +461,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               tc::tma_load_3d(base + st * C::KT + hf * C::HALF + lane * p.BR * 128, map, bar(full + st), hf * 64, y, z);
           }
           id = page_of(j + 1);
-          if (++st == nst) {
-            st = 0;
-            eph ^= 1;
-          }
+          if (++st == nst) st = 0;
         }
         if (!ok) break;
       }
@@ -485,106 +491,117 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           tc::mma_ts(tmem + 256 + i * 128, tmem + buf * BN + (kk >> 2) * 64 + (kk & 3) * 8, dv + ((kk * 2048) >> 4),
                      idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
       };
-      // One thread issues everything.  The tensor pipe takes only a few MMAs
-      // ahead, so what this thread does between two MMAs may leave it idle: the
-      // state is a few scalars (stage numbers and barrier phases), no struct
-      // and no division, and a wait is a few instructions.
-      if (lane == 0) {
-        bool ok = true;
-        int ks = 0, vs = 0, buf = 0;                  // K and V stage; NQ = 1: score buffer of the next tile
-        uint32_t kph = 0, vph = 0, qph = 0;           // their phases, and the queries'
-        uint32_t pph0 = 0, pph1 = 0;                  // phases of PFULL 0 and 1
-        uint32_t oph0 = 1, oph1 = 1;                  // of OFREE: nothing to wait for the first time
-        bool prev = false, prev2 = false, fresh = false;   // the tile before: its P V is to come, two query tiles, first of its piece
-        // P V of query tile i of the tile before, from score buffer x
-        auto pv = [&](int i, int x, uint32_t& pph, uint32_t& oph) {
-          ok = wait_short(B::PFULL + x, pph);
-          pph ^= 1;
-          if (fresh) {
-            // the piece before has been read out of O
-            ok = wait_short(B::OFREE + i, oph) && ok;
-            oph ^= 1;
-          }
-          if (!ok) return;
-          tc::tc_fence_after();
+      // The tensor pipe takes only a few MMAs ahead, so what this warp does
+      // between two MMAs may leave it idle: the state is a few scalars (stage
+      // numbers and barrier phases), no struct and no division, and one step
+      // (Q K^T of a tile, P V of the tile before) has four waits and three
+      // commits.  The warp stays converged and one elected lane issues: 17
+      // cycles an MMA, 45 under a branch on the lane.
+      const bool lead = tc::elect_one();
+      bool ok = true;
+      int ks = 0, vs = 0, buf = 0;                  // K and V stage; NQ = 1: score buffer of the next tile
+      uint32_t kph = 0, vph = 0, qph = 0;           // their phases, and the queries'
+      uint32_t pph0 = 0, pph1 = 0;                  // phases of PFULL 0 and 1
+      uint32_t oph0 = 1, oph1 = 1;                  // of OFREE: nothing to wait for the first time
+      bool prev = false, prev2 = false, fresh = false;   // the tile before: its P V is to come, two query tiles, first of its piece
+      bool last = false;                            // it is its piece's last
+      // P V of query tile i of the tile before, from score buffer x
+      auto pv = [&](int i, int x, uint32_t& pph, uint32_t& oph) {
+        ok = wait(B::PFULL + x, pph);
+        pph ^= 1;
+        if (fresh) {
+          // the piece before has been read out of O
+          ok = wait(B::OFREE + i, oph) && ok;
+          oph ^= 1;
+        }
+        if (!ok) return;
+        tc::tc_fence_after();
+        if (lead) {
           issue_pv(i, vs, x, fresh);
-          tc::mma_commit(bar(B::PVDONE + x));
-        };
-        auto pv_prev1 = [&]() {                       // NQ = 1: the P V before, from the other score buffer
-          ok = wait_short(B::VFULL + vs, vph);
-          if (!ok) return;
-          if (buf) pv(0, 0, pph0, oph0);
-          else pv(0, 1, pph1, oph0);
-        };
-        auto v_done = [&]() {
-          tc::mma_commit(bar(B::VEMPTY + vs));
-          if (++vs == VST) {
-            vs = 0;
-            vph ^= 1;
-          }
-          prev = false;
-        };
-        for (int pi = 0; ok; ++pi) {
-          const int slot = pi % NP;
-          if (!(ok = wait_short(B::PCFULL + slot, pi / NP))) break;
-          const int nt = s_piece[slot].nt;
-          const bool two = NQ == 2 && s_piece[slot].ntok > p.TQ;
-          tc::mbar_arrive(bar(B::PCEMPTY + slot));
-          for (int j = 0; j < max(nt, 1); ++j) {
-            // at a piece's start (and at the end) the P V before do not wait
-            // for queries to come
-            if (NQ == 2) {
-              if (prev) {
-                if (!(ok = wait_short(B::VFULL + vs, vph))) break;
-                pv(0, 0, pph0, oph0);
-                if (!ok) break;
-              }
-            } else if (prev && j == 0) {
-              pv_prev1();
+          // two query tiles: the next scores' commit covers this P V
+          if (NQ == 1 || last) tc::mma_commit(bar(B::PVDONE + x));
+        }
+      };
+      auto pv_prev1 = [&]() {                       // NQ = 1: the P V before, from the other score buffer
+        ok = wait(B::VFULL + vs, vph);
+        if (!ok) return;
+        if (buf) pv(0, 0, pph0, oph0);
+        else pv(0, 1, pph1, oph0);
+      };
+      auto v_done = [&]() {
+        if (++vs == VST) {
+          vs = 0;
+          vph ^= 1;
+        }
+        prev = false;
+      };
+      for (int pi = 0; ok; ++pi) {
+        const int slot = pi % NP;
+        if (!(ok = wait(B::PCFULL + slot, pi / NP))) break;
+        const int nt = s_piece[slot].nt;
+        const bool two = NQ == 2 && s_piece[slot].ntok > p.TQ;
+        __syncwarp();
+        if (lead) tc::mbar_arrive(bar(B::PCEMPTY + slot));
+        for (int j = 0; j < max(nt, 1); ++j) {
+          // at a piece's start (and at the end) the P V before do not wait
+          // for queries to come
+          if (NQ == 2) {
+            if (prev) {
+              if (!(ok = wait(B::VFULL + vs, vph))) break;
+              pv(0, 0, pph0, oph0);
               if (!ok) break;
-              v_done();
             }
-            if (nt) {
-              if (j == 0) {
-                if (!(ok = wait_short(B::QFULL, qph))) break;
-                qph ^= 1;
-              }
-              if (!(ok = wait_short(B::KFULL + ks, kph))) break;
-              tc::tc_fence_after();
-              const int x = NQ == 2 ? 0 : buf;
+          } else if (prev && j == 0) {
+            pv_prev1();
+            if (!ok) break;
+            v_done();
+          }
+          if (nt) {
+            if (j == 0) {
+              if (!(ok = wait(B::QFULL, qph))) break;
+              qph ^= 1;
+            }
+            if (!(ok = wait(B::KFULL + ks, kph))) break;
+            const int x = NQ == 2 ? 0 : buf;
+            if (lead) {
               issue_qk(0, ks, x);
               tc::mma_commit(bar(B::SFULL + x));
             }
-            if (prev) {
-              if (NQ == 1) pv_prev1();
-              else if (prev2) pv(1, 1, pph1, oph1);
-              if (!ok) break;
-              v_done();
-            }
-            if (nt) {
+          }
+          if (prev) {
+            if (NQ == 1) pv_prev1();
+            else if (prev2) pv(1, 1, pph1, oph1);
+            if (!ok) break;
+            v_done();
+          }
+          if (nt) {
+            if (lead) {
               if (two) {
                 issue_qk(1, ks, 1);
                 tc::mma_commit(bar(B::SFULL + 1));
               }
-              tc::mma_commit(bar(B::KEMPTY + ks));
+              tc::mma_commit(bar(B::EMPTY + ks));
               if (j == nt - 1) tc::mma_commit(bar(B::QEMPTY));
-              if (++ks == KST) {
-                ks = 0;
-                kph ^= 1;
-              }
-              if (NQ == 1) buf ^= 1;
-              prev = true;
-              prev2 = two;
-              fresh = j == 0;
             }
+            if (++ks == KST) {
+              ks = 0;
+              kph ^= 1;
+            }
+            if (NQ == 1) buf ^= 1;
+            prev = true;
+            prev2 = two;
+            fresh = j == 0;
+            last = j == nt - 1;
           }
-          if (!nt) break;
         }
+        if (!nt) break;
+      }
+      if (lead) {
         if (!ok) set_status(a.status, SKV_DEV_TIMEOUT);
         // every MMA issued completes before TMEM is released
         tc::mma_commit(bar(B::DRAIN));
-        wait(B::DRAIN, 0);
       }
+      wait(B::DRAIN, 0);
     } else if (warp == C::WARP_SCHED) {
       // ---------------------------------------------------------- scheduler
       int b = s_first[0], h, qb = 0, t;
@@ -697,7 +714,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if constexpr (SPLIT == 1) return (bool)__any_sync(0xffffffffu, v);
       else return tc::bar_or(pair_bar, 64, v);
     };
-    int gt = 0, cnt = 0;                           // key tiles of the CTA and of this query tile so far
+    int gt = 0, cnt = 0, pcs = 0;                  // key tiles of the CTA and of this query tile, its pieces so far
     Piece pc;
     bool ok = true;
     for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
@@ -830,7 +847,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (lane == 0) tc::mbar_arrive(bar(B::PFULL + x));
       }
       {
-        const int c = cnt - 1, x = NQ == 2 ? i : c & 1, ph = NQ == 2 ? c : c >> 1;
+        // (two query tiles: one commit per piece, one: one per tile)
+        const int c = cnt - 1, x = NQ == 2 ? i : c & 1, ph = NQ == 2 ? pcs++ : c >> 1;
         if (ok) ok = __all_sync(0xffffffffu, wait(B::PVDONE + x, ph));
         // the warps of the query tile go on together (barriers below)
         ok = tc::bar_and(tile_bar, TT, ok);

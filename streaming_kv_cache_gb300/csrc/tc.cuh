@@ -159,22 +159,9 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
   return bounded_wait<SW>(mbar_try_wait_short, bar, parity, limit_ns, abort);
 }
 
-// Waits of a few instructions, for loops whose issue must stay short: poll
-// (14 cycles a try when the phase is complete), or sleep in try_wait, up to a
-// millisecond a try.  Both end after a count of tries, about two seconds, and
-// return false.
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b32 c;\n mov.b32 c, 200000000;\n mov.b32 %0, 1;\n"
-      "TRY:\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
-      " sub.s32 c, c, 1;\n setp.gt.s32 q, c, 0;\n @q bra TRY;\n mov.b32 %0, 0;\n"
-      "DONE:\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
+// A wait of a few instructions, for loops whose issue must stay short: sleeps
+// in try_wait, up to a millisecond a try, and ends after a count of tries,
+// about two seconds, returning false.
 __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -186,6 +173,13 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
       : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
       : "memory");
   return ok != 0;
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
 }
 
 // A value the compiler must (re)compute where it stands: keeps loop-invariant
