@@ -546,11 +546,14 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           // at a piece's start (and at the end) the P V before do not wait
           // for queries to come
           if (NQ == 2) {
-            if (prev) {
-              if (!(ok = wait(B::VFULL + vs, vph))) break;
-              pv(0, 0, pph0, oph0);
-              if (!ok) break;
-            }
+            // the tiles are waited for first, under the MMAs still in the
+            // pipe: from the probabilities' arrival on, P V and Q K^T go out
+            // back to back
+            if (prev) ok = wait(B::VFULL + vs, vph);
+            if (nt) ok = wait(B::KFULL + ks, kph) && ok;
+            if (!ok) break;
+            if (prev) pv(0, 0, pph0, oph0);
+            if (!ok) break;
           } else if (prev && j == 0) {
             pv_prev1();
             if (!ok) break;
@@ -561,7 +564,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               if (!(ok = wait(B::QFULL, qph))) break;
               qph ^= 1;
             }
-            if (!(ok = wait(B::KFULL + ks, kph))) break;
+            if (NQ == 1 && !(ok = wait(B::KFULL + ks, kph))) break;
             const int x = NQ == 2 ? 0 : buf;
             if (lead) {
               issue_qk(0, ks, x);
@@ -609,17 +612,33 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       int nqb = (s.L + TB - 1) / TB;
       {
         long long off = *s_off;
-        const long long per_head = unit_prefix(s, PAGED, TB, nqb, nqb);
-        h = (int)udiv(off, per_head);
-        off -= h * per_head;
-        // the last block whose tiles start at or before off, 32 candidates at a time
-        for (int hi = nqb; hi - qb > 1;) {
-          const int step = (hi - qb + 31) / 32, x = qb + lane * step;
-          const bool le = x < hi && unit_prefix(s, PAGED, TB, nqb, x) <= off;
-          qb += (31 - __clz(__ballot_sync(0xffffffffu, le))) * step;
-          hi = min(hi, qb + step);
+        if (nqb == 1) {
+          const int per_head = unit_tiles(s, PAGED, TB, 0);
+          h = (int)udiv(off, per_head);
+          t = (int)(off - (long long)h * per_head);
+        } else {
+          const long long per_head = unit_prefix(s, PAGED, TB, nqb, nqb);
+          h = (int)udiv(off, per_head);
+          off -= h * per_head;
+          // the block whose tiles hold off: a running sum over the blocks, 32 at a time
+          for (;; qb += 32) {
+            const int n = qb + lane < nqb ? unit_tiles(s, PAGED, TB, qb + lane) : 0;
+            int incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int x = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += x;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, incl > off);   // blocks that end past off
+            if (past) {
+              const int l = __ffs(past) - 1;
+              qb += l;
+              t = (int)off - __shfl_sync(0xffffffffu, incl - n, l);
+              break;
+            }
+            off -= __shfl_sync(0xffffffffu, incl, 31);
+          }
         }
-        t = (int)(off - unit_prefix(s, PAGED, TB, nqb, qb));
       }
       if (lane == 0) {
         long long g = g0;
@@ -727,6 +746,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       const bool active = lg * 32 < ntok * p.G;         // some row of the lane group is valid
       // keys that this row sees, from this thread's first key of a tile 0 on
       const int n_row = pc.pos0 + pc.step * (i * p.TQ + tok) + 1 - hh * HN;
+      const int n_all = __reduce_min_sync(0xffffffffu, n_row);   // keys that every row of the warp sees
       float m_used = 0.f, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < pc.nt; ++j, ++gt, ++cnt) {
@@ -744,9 +764,9 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
           for (int cb = 0; cb < HN / 32; ++cb)
             tc::tmem_ld32(tS + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(v + cb * 32));
-          const int n_see = n_row - r0;            // of this thread's keys of the tile
           tc::tmem_wait_ld();
-          if (!__all_sync(0xffffffffu, n_see >= HN)) {
+          if (n_all - r0 < HN) {
+            const int n_see = n_row - r0;          // of this thread's keys of the tile
 #pragma unroll
             for (int k = 0; k < HN; ++k)
               if (k >= n_see) v[k] = __float_as_uint(-INFINITY);
@@ -940,31 +960,36 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               M = mx;
             }
             const float inv = den == 0.f ? 0.f : 1.f / den;
+            constexpr int CW = HD < 64 ? HD : 64;   // columns at a time: loads of a piece in flight together
 #pragma unroll 1
-            for (int cb = 0; cb < HD / 32; ++cb) {
-              float acc[32];
+            for (int c0 = 0; c0 < HD; c0 += CW) {
+              float acc[CW];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+              for (int e = 0; e < CW; ++e) acc[e] = 0.f;
 #pragma unroll 1
               for (int k = 0; k < pc.n; ++k) {
-                const float2 ml = ml_of(k);
-                const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
-                float o[32];
+                float o[CW];
                 if (k == pc.k) {
-                  tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+#pragma unroll
+                  for (int cb = 0; cb < CW / 32; ++cb)
+                    tc::tmem_ld32(tO + c0 + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o + cb * 32));
                   tc::tmem_wait_ld();
                 } else {
 #pragma unroll
-                  for (int e = 0; e < 8; ++e)
-                    *reinterpret_cast<float4*>(o + 4 * e) = __ldcg(
-                        reinterpret_cast<const float4*>(p.ws_o + ws_index<D, NQ>(slot(k), i, hh * (HD / 4) + cb * 8 + e, row)));
+                  for (int e = 0; e < CW / 4; ++e)
+                    *reinterpret_cast<float4*>(o + 4 * e) = __ldcg(reinterpret_cast<const float4*>(
+                        p.ws_o + ws_index<D, NQ>(slot(k), i, (hh * HD + c0) / 4 + e, row)));
                 }
+                const float2 ml = ml_of(k);
+                const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
                 if (w != 0.f) {
 #pragma unroll
-                  for (int e = 0; e < 32; ++e) acc[e] += w * o[e];
+                  for (int e = 0; e < CW; ++e) acc[e] += w * o[e];
                 }
               }
-              store_row(cb, acc, inv);
+#pragma unroll
+              for (int cb = 0; cb < CW / 32; ++cb)
+                store_row(c0 / 32 + cb, *reinterpret_cast<const float(*)[32]>(acc + cb * 32), inv);
             }
             if (lse) *lse = den == 0.f ? -INFINITY : (M + __log2f(den)) * 0.69314718055994531f;
           }
