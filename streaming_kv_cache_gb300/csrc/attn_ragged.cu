@@ -110,7 +110,8 @@ struct RParams {
   RaggedArgs a;
   int G, TQ, TB;          // query heads per kv head, tokens per query tile and per unit
   int BR, boxes;          // rows per TMA box, boxes per key tile
-  int min_share;          // tiles per CTA at least
+  int min_share;          // sequence positions per CTA at least
+  int unit_cost;          // positions that a unit takes before its tiles, for what it costs beside them
   float scale_log2;
   int* ws_count;          // [2 * CTAs] arrivals per unit (named by its first CTA) and query tile
   float* ws_ml;           // [2 * CTAs][NQ][BM][2]
@@ -341,7 +342,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     auto cost = [&](const Span& s) -> long long {
       if (s.L == 0) return 0;
       const int nqb = (s.L + TB - 1) / TB;
-      return a.Hkv * unit_prefix(s, PAGED, TB, nqb, nqb);
+      return a.Hkv * (unit_prefix(s, PAGED, TB, nqb, nqb) + (long long)p.unit_cost * nqb);
     };
     long long sum = 0;
     Span sp{};                             // the thread's last request (most have one)
@@ -607,22 +608,24 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       wait(B::DRAIN, 0);
     } else if (warp == C::WARP_SCHED) {
       // ---------------------------------------------------------- scheduler
-      int b = s_first[0], h, qb = 0, t;
+      // A unit takes unit_cost + its tiles positions of the sequence, the tiles
+      // last; the CTA has the tiles at positions [g0, g1).
+      int b = s_first[0], h, qb = 0, t;              // t: positions of the unit before g0
       Span s{s_first[1], s_first[2], s_first[3], false};
       int nqb = (s.L + TB - 1) / TB;
       {
         long long off = *s_off;
         if (nqb == 1) {
-          const int per_head = unit_tiles(s, PAGED, TB, 0);
+          const int per_head = unit_tiles(s, PAGED, TB, 0) + p.unit_cost;
           h = (int)udiv(off, per_head);
           t = (int)(off - (long long)h * per_head);
         } else {
-          const long long per_head = unit_prefix(s, PAGED, TB, nqb, nqb);
+          const long long per_head = unit_prefix(s, PAGED, TB, nqb, nqb) + (long long)p.unit_cost * nqb;
           h = (int)udiv(off, per_head);
           off -= h * per_head;
-          // the block whose tiles hold off: a running sum over the blocks, 32 at a time
+          // the block that holds off: a running sum over the blocks, 32 at a time
           for (;; qb += 32) {
-            const int n = qb + lane < nqb ? unit_tiles(s, PAGED, TB, qb + lane) : 0;
+            const int n = qb + lane < nqb ? unit_tiles(s, PAGED, TB, qb + lane) + p.unit_cost : 0;
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -646,11 +649,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         int loaded = 0;                   // pieces whose queries are on their way
         for (int pi = 0; ok; ++pi) {
           Piece pc{};
-          if (g < g1) {
-            const int nt_unit = unit_tiles(s, PAGED, TB, qb);
-            const long long u0 = g - t, u1 = u0 + nt_unit;
-            pc.nt = (int)(min(u1, g1) - g);
-            pc.ta = t;
+          const int nt_unit = g < g1 ? unit_tiles(s, PAGED, TB, qb) : 0;
+          const long long u0 = g - t + p.unit_cost, u1 = u0 + nt_unit;   // positions of the unit's tiles
+          if (g < g1 && u0 < g1) {
+            pc.ta = max(0, t - p.unit_cost);
+            pc.nt = (int)(min(u1, g1) - u0) - pc.ta;
             pc.b = b;
             pc.h = h;
             pc.row0 = s.q0 + qb * TB;
@@ -666,7 +669,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               pc.k = (int)blockIdx.x - pc.cta0;
               pc.slot = 2 * (int)blockIdx.x + (pc.k == 0 ? 1 : 0);
             }
-            g += pc.nt;
+            g = u1;
             // the next unit
             t = 0;
             if (++qb == nqb) {
@@ -952,13 +955,18 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                : __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)slot(k) * NQ + i) * BM + row);
             };
             float M = -INFINITY, den = 0.f;
-            for (int k = 0; k < pc.n; ++k) {
-              const float2 ml = ml_of(k);
-              if (ml.y == 0.f) continue;     // no key that the row sees
+            float2 ml4[4];                   // the first pieces' (m, l), often all there are
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ml4[k] = k < pc.n ? ml_of(k) : make_float2(0.f, 0.f);
+            auto add = [&](const float2& ml) {
+              if (ml.y == 0.f) return;       // no key that the row sees
               const float mx = fmaxf(M, ml.x);
               den = den * (M == -INFINITY ? 0.f : exp2f(M - mx)) + exp2f(ml.x - mx) * ml.y;
               M = mx;
-            }
+            };
+#pragma unroll
+            for (int k = 0; k < 4; ++k) add(ml4[k]);
+            for (int k = 4; k < pc.n; ++k) add(ml_of(k));
             const float inv = den == 0.f ? 0.f : 1.f / den;
             constexpr int CW = HD < 64 ? HD : 64;   // columns at a time: loads of a piece in flight together
 #pragma unroll 1
@@ -980,7 +988,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     *reinterpret_cast<float4*>(o + 4 * e) = __ldcg(reinterpret_cast<const float4*>(
                         p.ws_o + ws_index<D, NQ>(slot(k), i, (hh * HD + c0) / 4 + e, row)));
                 }
-                const float2 ml = ml_of(k);
+                const float2 ml = k == 0 ? ml4[0] : k == 1 ? ml4[1] : k == 2 ? ml4[2] : k == 3 ? ml4[3] : ml_of(k);
                 const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
                 if (w != 0.f) {
 #pragma unroll
@@ -1070,6 +1078,7 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   p.TB = (wide ? 2 : 1) * p.TQ;
   const int grid = min(sm_count(), MAX_CTAS);
   p.min_share = wide ? 4 : 1;
+  p.unit_cost = wide ? 2 : 1;
   p.BR = BN;
   if (paged)
     while (a.page_size % p.BR) p.BR /= 2;
