@@ -86,6 +86,7 @@ int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const in
   a.n_tok = n_tok;
   a.n_page = cache->n_page;
   a.page_size = cache->page_size;
+  a.ps_m = skv::fastdiv_m((uint32_t)cache->page_size);
   a.max_block = cache->max_block;
   a.state = state;
   a.new_len = new_len;

@@ -26,12 +26,11 @@
 // score buffers, so that Q K^T of the next key tile runs under the softmax
 // (bound by streaming K and V from HBM; most MMA rows are idle).
 //
-//   warps 0 .. 7        softmax and epilogue.  NQ = 2: a warpgroup per query
-//                       tile, a thread per row.  NQ = 1: a row's keys (and
-//                       its output columns) are halved between two threads
-//   then one warp each  K producer (TMA), V producer (TMA), MMA issuer,
-//                       scheduler (splits the CTA's share into pieces of
-//                       units, loads the pieces' queries by TMA)
+//   warps 0 .. 4 NQ - 1  softmax and epilogue: a warpgroup per query tile, a
+//                        thread per row
+//   then one warp each   K producer (TMA), V producer (TMA), MMA issuer,
+//                        scheduler (splits the CTA's share into pieces of
+//                        units, loads the pieces' queries by TMA)
 //
 // Keys and values are read as they lie: K rows are the K-major B operand of
 // Q K^T, token-major V rows the MN-major B operand of P V.  A TMA box is 64
@@ -61,8 +60,7 @@ constexpr int NP = 4;     // pieces in flight between the scheduler and the othe
 
 template <int D, int NQ>
 struct RCfg {
-  static constexpr int SPLIT = NQ == 2 ? 1 : 2;    // threads per row
-  static constexpr int SM_WARPS = 4 * NQ * SPLIT;
+  static constexpr int SM_WARPS = 4 * NQ;
   static constexpr int WARP_K = SM_WARPS, WARP_V = SM_WARPS + 1, WARP_MMA = SM_WARPS + 2, WARP_SCHED = SM_WARPS + 3;
   static constexpr int NT = 32 * SM_WARPS + 128;
   // K and V stages: what the 227 KB hold beside the queries (for d = 64 as
@@ -70,6 +68,13 @@ struct RCfg {
   static constexpr int KST = D == 128 ? 3 : (NQ == 2 ? 4 : 6);
   static constexpr int VST = D == 128 ? (NQ == 2 ? 2 : 3) : (NQ == 2 ? 4 : 6);
   static_assert(VST <= KST, "V stages are freed with the K stages (see the producers)");
+  // 16-bit terms of a probability in P V.  One: each p is rounded once, which
+  // moves the output by about as much as its own rounding.  Decode has the
+  // tensor pipe and the softmax warps idle most of the time (HBM-bound: 64
+  // requests of 4 k keys take 176 us with two terms, 175 with one), so it adds
+  // what the first rounding left as a second term: the output's own rounding
+  // is all there is.
+  static constexpr int P_TERMS = NQ == 1 ? 2 : 1;
   static constexpr int QT = BM * D * 2;        // bytes of a query tile
   static constexpr int KT = BN * D * 2;        // of a key or value tile
   static constexpr int HALF = BM * 128;        // one 64-dimension half of either
@@ -80,8 +85,7 @@ struct RCfg {
   static constexpr int MISC_OFF = BAR_OFF + 44 * 8;
   static constexpr int PIECE_OFF = MISC_OFF + 64;
   static constexpr int SCAN_OFF = PIECE_OFF + NP * 64;       // running sums of the prologue, one per warp
-  static constexpr int RED_OFF = SCAN_OFF + NT / 32 * 8;     // per row: what its two threads exchange
-  static constexpr int BYTES = RED_OFF + NQ * BM * 4;
+  static constexpr int BYTES = SCAN_OFF + NT / 32 * 8;
   static constexpr int ALLOC = BYTES + 1024;                 // slack for 1024-byte alignment
   static_assert(ALLOC <= 232448, "shared memory");
 };
@@ -197,6 +201,18 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   else return pack_bf16x2(lo, hi);
 }
 
+template <bool F16>
+__device__ __forceinline__ void unpack16(uint32_t w, float& lo, float& hi) {
+  if constexpr (F16) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = f.x;
+    hi = f.y;
+  } else {
+    lo = bf16_lo(w);
+    hi = bf16_hi(w);
+  }
+}
+
 // Workspace offset (floats) of columns [4 c, 4 c + 4) of row r of a slot's
 // query tile i: a column group of all rows is contiguous, so that a warp whose
 // lanes hold consecutive rows reads and writes whole lines.
@@ -206,7 +222,7 @@ __device__ __forceinline__ size_t ws_index(int slot, int i, int c, int r) {
 }
 
 // Merge query tile i of a unit whose n pieces left partials (O_k, m_k, l_k):
-// O = sum_k w_k O_k / sum_k w_k l_k with w_k = 2^(m_k - M), by the TT threads
+// O = sum_k w_k O_k / sum_k w_k l_k with w_k = 2^(m_k - M), by the 128 threads
 // of a query tile, over the pieces in their order.  A thread takes one
 // row and every `lanes`-th group of 4 columns: a full tile's rows a thread
 // each, a decode step's few rows spread over all threads.  CU column groups of
@@ -218,8 +234,7 @@ __device__ __noinline__ void merge_pieces(const RParams& p, int cta0, int n, int
   const RaggedArgs& a = p.a;
   // piece 0 is the last of its CTA's share, every other the first
   auto slot = [&](int k) { return 2 * (cta0 + k) + (k == 0 ? 1 : 0); };
-  constexpr int TT = BM * RCfg<D, NQ>::SPLIT;
-  const int lanes = TT / rows;            // threads per row
+  const int lanes = BM / rows;            // threads per row
   const int r = t % rows, c0 = t / rows;
   if (c0 >= lanes) return;
   const int tok = row0 + i * p.TQ + r / p.G, hq = h * p.G + r % p.G;
@@ -301,7 +316,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   volatile int* s_last = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);   // per query tile: merge it here
   volatile long long* s_off = reinterpret_cast<volatile long long*>(smem + C::MISC_OFF + 16);
   int* s_first = reinterpret_cast<int*>(smem + C::MISC_OFF + 24);   // the share's first request and its span
-  float* s_red = reinterpret_cast<float*>(smem + C::RED_OFF);
   Piece* s_piece = reinterpret_cast<Piece*>(smem + C::PIECE_OFF);
   long long* s_scan = reinterpret_cast<long long*>(smem + C::SCAN_OFF);
 
@@ -314,8 +328,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < B::COUNT; ++i) {
       int count = 1;
-      if (i >= B::PFULL && i < B::PFULL + 2) count = 4 * C::SPLIT;
-      if (i >= B::OFREE && i < B::OFREE + NQ) count = 4 * C::SPLIT;
+      if (i >= B::PFULL && i < B::PFULL + 2) count = 4;
+      if (i >= B::OFREE && i < B::OFREE + NQ) count = 4;
       if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + C::SM_WARPS;
       tc::mbar_init(bar(i), count);
     }
@@ -488,9 +502,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       auto issue_pv = [&](int i, int vs, int buf, bool fresh) {
         const uint64_t dv = tc::opaque(dv0 + ((uint32_t)(vs * C::KT) >> 4));
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          tc::mma_ts(tmem + 256 + i * 128, tmem + buf * BN + (kk >> 2) * 64 + (kk & 3) * 8, dv + ((kk * 2048) >> 4),
-                     idesc_pv, (!fresh || kk > 0) ? 1u : 0u);
+        for (int t = 0; t < C::P_TERMS; ++t)
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            tc::mma_ts(tmem + 256 + i * 128, tmem + buf * BN + (kk >> 2) * 64 + t * 32 + (kk & 3) * 8,
+                       dv + ((kk * 2048) >> 4), idesc_pv, (!fresh || t + kk > 0) ? 1u : 0u);
       };
       // The tensor pipe takes only a few MMAs ahead, so what this warp does
       // between two MMAs may leave it idle: the state is a few scalars (stage
@@ -705,37 +721,13 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   } else {
     // ------------------------------------------------- softmax and epilogue
     if constexpr (NQ == 2) tc::setmaxnreg_inc<208>();
-    constexpr int SPLIT = C::SPLIT;
-    constexpr int HN = BN / SPLIT, HD = D / SPLIT;   // keys of a tile and output columns of this thread
-    const int lg = warp & 3;                         // TMEM lane group
-    const int i = SPLIT == 1 ? warp >> 2 : 0, hh = SPLIT == 1 ? 0 : warp >> 2;   // query tile, half of the row
+    const int i = warp >> 2, lg = warp & 3;          // query tile, TMEM lane group
     const int row = lg * 32 + lane;
-    // named barriers: the warps of a lane group, and of a query tile
-    const int pair_bar = 1 + lg, tile_bar = 5 + i;
-    constexpr int TT = BM * SPLIT;                   // threads of a query tile
+    const int tile_bar = 1 + i;                      // named barrier of the query tile's warps
     const uint32_t t_lane = (uint32_t)(lg * 32) << 16;
-    const uint32_t tO = tmem + t_lane + 256 + i * 128 + hh * HD;
+    const uint32_t tO = tmem + t_lane + 256 + i * 128;
     const int tok = row / p.G, gq = row - tok * p.G;
     const float sl = p.scale_log2;
-    // f of the two halves' values of a row, in both threads
-    auto exchange = [&](float x, auto f) {
-      if constexpr (SPLIT == 1) return x;
-      float* r = s_red + i * BM + row;
-      if (hh == 1) *r = x;
-      tc::bar_sync_n(pair_bar, 64);
-      if (hh == 0) *r = x = f(x, *r);
-      tc::bar_sync_n(pair_bar, 64);
-      return hh == 0 ? x : *r;
-    };
-    // a predicate of both threads' warps
-    auto group_and = [&](bool v) {
-      if constexpr (SPLIT == 1) return (bool)__all_sync(0xffffffffu, v);
-      else return tc::bar_and(pair_bar, 64, v);
-    };
-    auto group_or = [&](bool v) {
-      if constexpr (SPLIT == 1) return (bool)__any_sync(0xffffffffu, v);
-      else return tc::bar_or(pair_bar, 64, v);
-    };
     int gt = 0, cnt = 0, pcs = 0;                  // key tiles of the CTA and of this query tile, its pieces so far
     Piece pc;
     bool ok = true;
@@ -747,31 +739,28 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       const int ntok = min(p.TQ, pc.ntok - i * p.TQ);   // tokens in this query tile
       const bool valid = tok < ntok;
       const bool active = lg * 32 < ntok * p.G;         // some row of the lane group is valid
-      // keys that this row sees, from this thread's first key of a tile 0 on
-      const int n_row = pc.pos0 + pc.step * (i * p.TQ + tok) + 1 - hh * HN;
+      const int n_row = pc.pos0 + pc.step * (i * p.TQ + tok) + 1;   // keys that this row sees
       const int n_all = __reduce_min_sync(0xffffffffu, n_row);   // keys that every row of the warp sees
       float m_used = 0.f, l = 0.f;
 #pragma unroll 1
       for (int j = 0; j < pc.nt; ++j, ++gt, ++cnt) {
         const int x = NQ == 2 ? i : cnt & 1, ph = NQ == 2 ? cnt : cnt >> 1;
         const int r0 = (pc.ta + j) * BN;
-        const uint32_t tS = tmem + t_lane + x * BN + hh * HN;
-        // tcgen05.ld/st are warp-collective: every branch around them is
-        // warp-uniform; the two warps of a lane group agree on every barrier
-        ok = wait(B::SFULL + x, ph);
-        ok = active ? group_and(ok) : __all_sync(0xffffffffu, ok);
+        const uint32_t tS = tmem + t_lane + x * BN;
+        // tcgen05.ld/st are warp-collective: every branch around them is warp-uniform
+        ok = __all_sync(0xffffffffu, wait(B::SFULL + x, ph));
         if (!ok) break;
         if (active) {
           tc::tc_fence_after();
-          uint32_t v[HN];
+          uint32_t v[BN];
 #pragma unroll
-          for (int cb = 0; cb < HN / 32; ++cb)
+          for (int cb = 0; cb < BN / 32; ++cb)
             tc::tmem_ld32(tS + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(v + cb * 32));
           tc::tmem_wait_ld();
-          if (n_all - r0 < HN) {
-            const int n_see = n_row - r0;          // of this thread's keys of the tile
+          if (n_all - r0 < BN) {
+            const int n_see = n_row - r0;          // of the tile's keys
 #pragma unroll
-            for (int k = 0; k < HN; ++k)
+            for (int k = 0; k < BN; ++k)
               if (k >= n_see) v[k] = __float_as_uint(-INFINITY);
           }
           auto row_max = [&]() {
@@ -779,22 +768,22 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
             for (int q = 0; q < 4; ++q) m4[q] = fmaxf(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1]));
 #pragma unroll
-            for (int k = 8; k < HN; k += 2)
+            for (int k = 8; k < BN; k += 2)
               m4[(k >> 1) & 3] = fmax3(m4[(k >> 1) & 3], __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-            return exchange(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl,
-                            [](float a, float b) { return fmaxf(a, b); });
+            return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * sl;
           };
           // P = 2^(s scale - m) in the values' type over the first half of
-          // either 64 scores (rounded once: the products of P V take 16-bit
-          // operands); the sum is taken in fp32 before that rounding
+          // either 64 scores (the products of P V take 16-bit operands), its
+          // second term, if there is one, over the other half; the sum is
+          // taken in fp32 before the rounding
           auto p_pass = [&]() {
             const uint64_t sl2 = f2_pack(sl, sl), nm2 = f2_pack(-m_used, -m_used);
             uint64_t l2[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) l2[q] = 0ull;
 #pragma unroll
-            for (int cb = 0; cb < HN / 32; ++cb) {
-              uint32_t pk[16];
+            for (int cb = 0; cb < BN / 32; ++cb) {
+              uint32_t pk[16], pl[16];
 #pragma unroll
               for (int k = 0; k < 32; k += 2) {
                 float x0, x1;
@@ -803,8 +792,14 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 const float p0 = tc::ex2(x0), p1 = tc::ex2(x1);
                 l2[(k >> 1) & 3] = f2_add(l2[(k >> 1) & 3], f2_pack(p0, p1));
                 pk[k >> 1] = pack16<F16>(p0, p1);
+                if constexpr (C::P_TERMS == 2) {
+                  float h0, h1;
+                  unpack16<F16>(pk[k >> 1], h0, h1);
+                  pl[k >> 1] = pack16<F16>(p0 - h0, p1 - h1);
+                }
               }
               tc::tmem_st16(tS + (cb >> 1) * 64 + (cb & 1) * 16, pk);
+              if constexpr (C::P_TERMS == 2) tc::tmem_st16(tS + (cb >> 1) * 64 + 32 + (cb & 1) * 16, pl);
             }
             const uint64_t s2 = f2_add(f2_add(l2[0], l2[1]), f2_add(l2[2], l2[3]));
             float s0, s1;
@@ -818,12 +813,12 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           float ts;
           for (bool again = false;; again = true) {
             ts = p_pass();
-            if (again || !group_or(valid && !(ts <= LAG_LIMIT))) break;
+            if (again || !__any_sync(0xffffffffu, valid && !(ts <= LAG_LIMIT))) break;
             tc::tmem_wait_st();
             if (NQ == 1 && j > 0) {
               // two query tiles: these scores were issued after the P V before
               // them; one: that P V may still be running
-              ok = group_and(wait(B::PVDONE + ((cnt - 1) & 1), (cnt - 1) >> 1));
+              ok = __all_sync(0xffffffffu, wait(B::PVDONE + ((cnt - 1) & 1), (cnt - 1) >> 1));
               if (!ok) break;
               tc::tc_fence_after();
             }
@@ -833,7 +828,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             l *= alpha;
             if (j > 0) {
 #pragma unroll 1
-              for (int cb = 0; cb < HD / 16; ++cb) {   // 16 columns at a time: the scores stay live
+              for (int cb = 0; cb < D / 16; ++cb) {   // 16 columns at a time: the scores stay live
                 uint32_t o[16];
                 tc::tmem_ld16(tO + cb * 16, o);
                 tc::tmem_wait_ld();
@@ -854,10 +849,9 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           ok = __all_sync(0xffffffffu, wait(B::VFULL + gt % VST, gt / VST));
           if (r0 + row >= pc.kv) {
 #pragma unroll
-            for (int c = 0; c < HD / 8; ++c) {
-              const int ch = hh * (HD / 8) + c;
-              *reinterpret_cast<uint4*>(smem + C::V_OFF + (gt % VST) * C::KT + (ch >> 3) * C::HALF + row * 128 +
-                                        (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < D / 8; ++c) {
+              *reinterpret_cast<uint4*>(smem + C::V_OFF + (gt % VST) * C::KT + (c >> 3) * C::HALF + row * 128 +
+                                        (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
           }
           tc::fence_proxy_async_smem();
@@ -874,15 +868,14 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int c = cnt - 1, x = NQ == 2 ? i : c & 1, ph = NQ == 2 ? pcs++ : c >> 1;
         if (ok) ok = __all_sync(0xffffffffu, wait(B::PVDONE + x, ph));
         // the warps of the query tile go on together (barriers below)
-        ok = tc::bar_and(tile_bar, TT, ok);
+        ok = tc::bar_and(tile_bar, BM, ok);
         if (!ok) break;
       }
       tc::tc_fence_after();
-      if (active) l = exchange(l, [](float a, float b) { return a + b; });
       const int hq = pc.h * p.G + gq, trow = pc.row0 + i * p.TQ + tok;
       const int rows = ntok * p.G;
-      uint16_t* orow = a.out + ((size_t)(valid ? trow : 0) * a.Hq + hq) * D + hh * HD;
-      float* lse = valid && hh == 0 && a.lse ? a.lse + (size_t)hq * a.n_tok + trow : nullptr;
+      uint16_t* orow = a.out + ((size_t)(valid ? trow : 0) * a.Hq + hq) * D;
+      float* lse = valid && a.lse ? a.lse + (size_t)hq * a.n_tok + trow : nullptr;
       auto store_row = [&](int cb, const float (&o)[32], float f) {
         if (!valid) return;
         uint4 pk[4];
@@ -896,7 +889,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (active) {
           const float inv_l = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-          for (int cb = 0; cb < HD / 32; ++cb) {
+          for (int cb = 0; cb < D / 32; ++cb) {
             float o[32];
             tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
             tc::tmem_wait_ld();
@@ -907,47 +900,43 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       } else {
         // A shared unit.  With few rows every piece goes through the
         // workspace.  With many, the piece that finds all others there (or
-        // arrives last) takes its own part from TMEM, a thread per half row.
+        // arrives last) takes its own part from TMEM, a thread per row.
         const bool big = rows > BM / 2;
         int* count = p.ws_count + 2 * pc.cta0 + i;
-        const bool leader = row == 0 && hh == 0;
+        const bool leader = row == 0;
         if (big) {
           if (leader) s_last[i] = tc::ld_acquire_gpu(reinterpret_cast<const uint32_t*>(count)) == (uint32_t)(pc.n - 1);
-          tc::bar_sync_n(tile_bar, TT);
+          tc::bar_sync_n(tile_bar, BM);
         }
         bool last = big && s_last[i];
         if (!last) {
           if (active) {
 #pragma unroll 1
-            for (int cb = 0; cb < HD / 32; ++cb) {
+            for (int cb = 0; cb < D / 32; ++cb) {
               uint32_t o[32];
               tc::tmem_ld32(tO + cb * 32, o);
               tc::tmem_wait_ld();
               if (valid) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                  *reinterpret_cast<uint4*>(p.ws_o + ws_index<D, NQ>(pc.slot, i, hh * (HD / 4) + cb * 8 + k, row)) =
+                  *reinterpret_cast<uint4*>(p.ws_o + ws_index<D, NQ>(pc.slot, i, cb * 8 + k, row)) =
                       make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
               }
             }
-            if (valid && hh == 0)
+            if (valid)
               reinterpret_cast<float2*>(p.ws_ml)[((size_t)pc.slot * NQ + i) * BM + row] = make_float2(m_used, l);
           }
-          tc::bar_sync_n(tile_bar, TT);
-          if (leader) {
-            __threadfence();
-            s_last[i] = atomicAdd(count, 1) == pc.n - 1;
-          }
-          tc::bar_sync_n(tile_bar, TT);
+          tc::bar_sync_n(tile_bar, BM);
+          if (leader) s_last[i] = tc::atom_add_acq_rel(count, 1) == pc.n - 1;
+          tc::bar_sync_n(tile_bar, BM);
           last = s_last[i];
         }
         if (last) {
           if (leader) *count = 0;          // ready for the next call
-          __threadfence();
           if (!big) {
             // few rows (decode): a thread has one column group, many pieces in flight
-            if (rows * (D / 4) <= TT) merge_pieces<D, NQ, F16, 1, 16>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, hh * BM + row);
-            else merge_pieces<D, NQ, F16, 4, 4>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, hh * BM + row);
+            if (rows * (D / 4) <= BM) merge_pieces<D, NQ, F16, 1, 16>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, row);
+            else merge_pieces<D, NQ, F16, 4, 4>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, row);
           } else if (active) {
             auto slot = [&](int k) { return 2 * (pc.cta0 + k) + (k == 0 ? 1 : 0); };
             auto ml_of = [&](int k) {
@@ -968,9 +957,9 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             for (int k = 0; k < 4; ++k) add(ml4[k]);
             for (int k = 4; k < pc.n; ++k) add(ml_of(k));
             const float inv = den == 0.f ? 0.f : 1.f / den;
-            constexpr int CW = HD < 64 ? HD : 64;   // columns at a time: loads of a piece in flight together
+            constexpr int CW = 64;           // columns at a time: loads of a piece in flight together
 #pragma unroll 1
-            for (int c0 = 0; c0 < HD; c0 += CW) {
+            for (int c0 = 0; c0 < D; c0 += CW) {
               float acc[CW];
 #pragma unroll
               for (int e = 0; e < CW; ++e) acc[e] = 0.f;
@@ -986,7 +975,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
                   for (int e = 0; e < CW / 4; ++e)
                     *reinterpret_cast<float4*>(o + 4 * e) = __ldcg(reinterpret_cast<const float4*>(
-                        p.ws_o + ws_index<D, NQ>(slot(k), i, (hh * HD + c0) / 4 + e, row)));
+                        p.ws_o + ws_index<D, NQ>(slot(k), i, c0 / 4 + e, row)));
                 }
                 const float2 ml = k == 0 ? ml4[0] : k == 1 ? ml4[1] : k == 2 ? ml4[2] : k == 3 ? ml4[3] : ml_of(k);
                 const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);

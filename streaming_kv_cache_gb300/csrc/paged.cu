@@ -26,38 +26,51 @@ namespace {
 
 constexpr int PT = 512;                      // threads per CTA
 
-// exclusive sums of v[0 .. n) in shared memory, in place, with the total in
-// v[n]; sums saturate at cap
-__device__ void block_scan(int* v, int n, int cap, int* warp_sum) {
+// exclusive sums of K arrays v[k][0 .. n) in shared memory, in place, with the
+// totals in v[k][n]; sums saturate at cap
+template <int K>
+__device__ void block_scan(int* const (&v)[K], int n, int cap, int (*warp_sum)[PT / 32]) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (n + PT - 1) / PT;
   const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
   auto add = [&](int a, int b) { return a > cap - b ? cap : a + b; };
-  int s = 0;
-  for (int i = i0; i < i1; ++i) s = add(s, v[i]);
-  int incl = s;
+  int incl[K];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl = add(incl, t);
+  for (int k = 0; k < K; ++k) {
+    int s = 0;
+    for (int i = i0; i < i1; ++i) s = add(s, v[k][i]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s = add(s, t);
+    }
+    incl[k] = s;
+    if (lane == 31) warp_sum[k][warp] = s;
   }
-  if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  int base = 0, total = 0;
-  for (int w = 0; w < PT / 32; ++w) {
-    if (w == warp) base = total;
-    total = add(total, warp_sum[w]);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    // every warp adds up the warps' sums for itself, a lane each
+    static_assert(PT / 32 <= 32, "a lane per warp");
+    int s = lane < PT / 32 ? warp_sum[k][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < PT / 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s = add(s, t);
+    }
+    const int total = __shfl_sync(0xffffffffu, s, PT / 32 - 1);
+    const int base = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0;
+    // sums before this thread's items: those of its warp's earlier lanes too
+    int excl = __shfl_up_sync(0xffffffffu, incl[k], 1);
+    if (lane == 0) excl = 0;
+    int run = add(base, excl);
+    for (int i = i0; i < i1; ++i) {
+      const int x = v[k][i];
+      v[k][i] = run;
+      run = add(run, x);
+    }
+    if (tid == 0) v[k][n] = total;
   }
-  // sums before this thread's items: those of its warp's earlier lanes too
-  int excl = __shfl_up_sync(0xffffffffu, incl, 1);
-  if (lane == 0) excl = 0;
-  int run = add(base, excl);
-  for (int i = i0; i < i1; ++i) {
-    const int x = v[i];
-    v[i] = run;
-    run = add(run, x);
-  }
-  if (tid == 0) v[n] = total;
   __syncthreads();
 }
 
@@ -78,35 +91,45 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
   int* s_tok = sm;                 // running sums of the new tokens
   int* s_need = s_tok + n + 1;     // of the pages needed
   int* s_back = s_need + n + 1;    // of the pages given back
-  int* s_ctx = s_back + n + 1;     // tokens held
-  __shared__ int warp_sum[PT / 32];
+  int* s_ctx = s_back + n + 1;     // tokens held (-1: left out altogether)
+  int* s_new = s_ctx + n;          // new_len
+  __shared__ int warp_sum[2][PT / 32];
   const int tid = threadIdx.x;
-  const int ps = a.page_size;
+  const uint32_t ps = (uint32_t)a.page_size;
   const long long row_tokens = (long long)a.max_block * ps;   // what a table row holds
-  auto pages = [&](int x) { return (int)(((long long)x + ps - 1) / ps); };
+  // 32-bit quotients by multiply-high throughout: x and page_size are below 2^31
+  auto pages = [&](int x) {
+    int rem;
+    const int q = fastdiv(x, (int)ps, a.ps_m, rem);
+    return q + (rem > 0);
+  };
   const bool reporter = blockIdx.x == 0;
   tc::grid_dep_launch();
   tc::grid_dep_wait();
 
   int head = a.state[n], count = a.state[n + 1];
+  for (int b = tid; b < n; b += PT) {
+    const int c = a.state[b], w = a.new_len[b];
+    const bool bad = c < 0 || c > row_tokens || w < -1;
+    if (bad && reporter) set_status(a.status, SKV_DEV_BAD_LEN);
+    s_ctx[b] = bad ? -1 : c;
+    s_new[b] = w;
+    s_tok[b] = bad ? 0 : max(w, 0);
+    s_back[b] = !bad && w == -1 ? pages(c) : 0;
+  }
   if (head < 0 || head >= a.n_page || count < 0 || count > a.n_page) {
     head = 0;
     count = 0;
     if (reporter && tid == 0) set_status(a.status, SKV_DEV_BAD_LEN);
   }
-  for (int b = tid; b < n; b += PT) {
-    int c = a.state[b], w = a.new_len[b];
-    const bool bad = c < 0 || c > row_tokens || w < -1;
-    if (bad && reporter) set_status(a.status, SKV_DEV_BAD_LEN);
-    s_ctx[b] = bad ? -1 : c;                       // -1: left out altogether
-    s_tok[b] = bad ? 0 : max(w, 0);
-    s_back[b] = !bad && w == -1 ? pages(c) : 0;
-  }
   __syncthreads();
-  // token sums go one past the rows there are; a span that ends there does not fit
-  block_scan(s_tok, n, a.n_tok < 0x7FFFFFFF ? a.n_tok + 1 : 0x7FFFFFFF, warp_sum);
+  {
+    // token sums go one past the rows there are; a span that ends there does not fit
+    int* const v[1] = {s_tok};
+    block_scan<1>(v, n, a.n_tok + 1, warp_sum);
+  }
   for (int b = tid; b < n; b += PT) {
-    const int c = s_ctx[b], w = a.new_len[b];
+    const int c = s_ctx[b], w = s_new[b];
     int need = 0;
     if (c >= 0 && w > 0) {
       const bool fits = s_tok[b + 1] <= a.n_tok && (long long)c + w <= row_tokens;
@@ -116,8 +139,10 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
     s_need[b] = need;
   }
   __syncthreads();
-  block_scan(s_need, n, 0x7FFFFFFF, warp_sum);
-  block_scan(s_back, n, 0x7FFFFFFF, warp_sum);
+  {
+    int* const v[2] = {s_need, s_back};
+    block_scan<2>(v, n, 0x7FFFFFFF, warp_sum);
+  }
 
   // A request is planned if its rows, its table and the free pages hold it.
   // The sums of the needs only grow, so the requests that get pages are those
@@ -126,8 +151,8 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
     return c >= 0 && (w == 0 || (w > 0 && s_tok[b + 1] <= a.n_tok && (long long)c + w <= row_tokens &&
                                  (s_need[b + 1] == s_need[b] || s_need[b + 1] <= count)));
   };
-  int given = 0;   // the largest running sum of the needs that the queue covers
-  {
+  int given = s_need[n];   // the largest running sum of the needs that the queue covers
+  if (given > count) {
     int lo = 0, hi = n;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -138,24 +163,19 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
   }
   const int room = a.n_page - count;               // a consistent state gives back at most this
   const int back = min(s_back[n], room);
+  // entry i of the queue, i < 2 n_page - head
+  auto ring = [&](uint32_t i) {
+    i += (uint32_t)head;
+    return i >= (uint32_t)a.n_page ? i - (uint32_t)a.n_page : i;
+  };
   if (reporter && tid == 0) {
     if (s_need[n] > count) set_status(a.status, SKV_DEV_NO_PAGE);
     if (s_back[n] > room) set_status(a.status, SKV_DEV_BAD_LEN);
     a.q_start[n] = min(s_tok[n], a.n_tok);
-    int h = head + given;
-    if (h >= a.n_page) h -= a.n_page;
-    a.next_state[n] = h;
+    a.next_state[n] = (int)ring((uint32_t)given);
     a.next_state[n + 1] = count - given + back;
   }
-  auto ring = [&](long long i) { return (int)(i % a.n_page); };
   const int stride = gridDim.x * PT, first = blockIdx.x * PT + tid;
-  for (int b = first; b < n; b += stride) {
-    const int c = s_ctx[b], w = a.new_len[b];
-    a.q_start[b] = min(s_tok[b], a.n_tok);
-    const bool ok = planned(b, c, w);
-    a.kv_len[b] = ok ? c + w : 0;
-    a.next_state[b] = c >= 0 && w == -1 ? 0 : ok ? c + w : a.state[b];
-  }
   for (int t = first; t < a.n_tok; t += stride) {
     int pos = 0, slot = -1;
     if (t < s_tok[n]) {
@@ -163,26 +183,33 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
       const long long p = (long long)c + (t - s_tok[b]);
       pos = (int)min(p, 0x7FFFFFFFLL);
       if (planned(b, c, w)) {
-        const int j = pos / ps, old = pages(c);
+        int r;
+        const int j = fastdiv(pos, (int)ps, a.ps_m, r), old = pages(c);
         // a new page comes straight from the queue: its table entry may be
         // another CTA's to write
-        const int page = j < old ? a.table[(size_t)b * a.max_block + j]
-                                 : a.queue[ring((long long)head + s_need[b] + j - old)];
-        if (page >= 0 && page < a.n_page) slot = page * ps + pos % ps;
+        const int page = j < old ? a.table[(size_t)b * a.max_block + j] : a.queue[ring((uint32_t)(s_need[b] + j - old))];
+        if (page >= 0 && page < a.n_page) slot = page * (int)ps + r;
         else set_status(a.status, SKV_DEV_BAD_PAGE);
       }
     }
     a.position[t] = pos;
     a.slot[t] = slot;
   }
+  for (int b = first; b < n; b += stride) {
+    const int c = s_ctx[b], w = s_new[b];
+    a.q_start[b] = min(s_tok[b], a.n_tok);
+    const bool ok = planned(b, c, w);
+    a.kv_len[b] = ok ? c + w : 0;
+    a.next_state[b] = c >= 0 && w == -1 ? 0 : ok ? c + w : c >= 0 ? c : a.state[b];
+  }
   for (int i = first; i < given; i += stride) {
     const int b = find_request(s_need, n, i);
-    a.table[(size_t)b * a.max_block + pages(s_ctx[b]) + (i - s_need[b])] = a.queue[ring((long long)head + i)];
+    a.table[(size_t)b * a.max_block + pages(s_ctx[b]) + (i - s_need[b])] = a.queue[ring((uint32_t)i)];
   }
   // The tail's entries are none of the count that the loops above read.
   for (int i = first; i < back; i += stride) {
     const int b = find_request(s_back, n, i);
-    a.queue[ring((long long)head + count + i)] = a.table[(size_t)b * a.max_block + (i - s_back[b])];
+    a.queue[ring((uint32_t)(count + i))] = a.table[(size_t)b * a.max_block + (i - s_back[b])];
   }
 }
 
@@ -292,14 +319,14 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   const long long items = max((long long)a.n_tok, (long long)a.n_req);
   const long long want = (items + PT - 1) / PT;
   const int grid = (int)min(want > 0 ? want : 1LL, 152LL);
-  const int smem = (4 * a.n_req + 3) * (int)sizeof(int);
+  const int smem = (5 * a.n_req + 3) * (int)sizeof(int);
   static std::atomic<int> done[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (smem > 48 * 1024 && !(dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed))) {
     e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (4 * SKV_PAGED_MAX_REQUESTS + 3) * (int)sizeof(int));
+                             (5 * SKV_PAGED_MAX_REQUESTS + 3) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_relaxed);
   }

@@ -11,6 +11,7 @@ namespace skv {
 
 struct PlanArgs {
   int n_req, n_tok, n_page, page_size, max_block;
+  uint32_t ps_m;            // fastdiv multiplier of page_size
   const int32_t* state;     // [n_req + 2] held tokens, queue head, queue count
   const int32_t* new_len;   // [n_req]
   int32_t* queue;           // [n_page] ring of free pages

@@ -103,6 +103,15 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t* p) {
   return v;
 }
 
+// Arrive on a counter in global memory: what this thread has seen happen (its
+// CTA's stores before a barrier among them) is visible to whoever reads the
+// counter after it, and what the earlier arrivals saw is visible here.
+__device__ __forceinline__ int atom_add_acq_rel(int* p, int v) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+  return old;
+}
+
 // Barrier across every CTA of a cooperative launch (all of them are resident
 // at once, so a CTA that waits here never holds back one that has not
 // started).  count and gen are two words of global memory, count zero

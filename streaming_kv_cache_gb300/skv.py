@@ -439,24 +439,26 @@ def _raw_stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _rows(t, heads, d, dtype, name, dev) -> int:
-    """Token stride of a token-major tensor [tokens][heads][d] whose heads of
-    a token are adjacent (a part of a wider projection's rows, say)."""
+def _rows(t, heads, d, dtype, name, dev):
+    """(tokens, heads, token stride) of a token-major tensor [tokens][heads][d]
+    whose heads of a token are adjacent (a part of a wider projection's rows,
+    say); heads None: any number."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be on a CUDA device" % name)
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError("%s must have shape (tokens, %d, %d), got %s" % (name, heads, d, tuple(t.shape)))
-    _on_dev(t.get_device(), name, dev)
-    n, (s0, s1, s2) = t.shape[0], t.stride()
-    if n == 0:
-        return heads * d
-    if s2 != 1 or (heads > 1 and s1 != d):
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads):
+        raise ValueError("%s must have shape (tokens, %s, %d), got %s" % (name, "heads" if heads is None else heads, d, tuple(shape)))
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError("%s must be on a CUDA device" % name)
+        _on_dev(t.get_device(), name, dev)
+    n, heads, _ = shape
+    s0, s1, s2 = t.stride()
+    if n and (s2 != 1 or (s1 != d and heads > 1)):
         raise ValueError("%s must have its heads adjacent within a token" % name)
-    return s0 if n > 1 else heads * d
+    return n, heads, s0 if n > 1 else heads * d
 
 
 class PagedPlan:
@@ -630,19 +632,19 @@ def kv_paged_write(cache: PagedCache, q: torch.Tensor | None, k: torch.Tensor, v
     projection's output."""
     dev = _call_device(k, "k")
     _need_pages(cache, dev)
-    n, hkv, d, dt = k.shape[0], cache.Hkv, cache.d, cache._dtype
-    ks, vs = _rows(k, hkv, d, dt, "k", dev), _rows(v, hkv, d, dt, "v", dev)
-    if v.shape[0] != n:
-        raise ValueError("k has %d tokens, v %d" % (n, v.shape[0]))
+    hkv, d, dt = cache.Hkv, cache.d, cache._dtype
+    n, _, ks = _rows(k, hkv, d, dt, "k", dev)
+    nv, _, vs = _rows(v, hkv, d, dt, "v", dev)
+    if nv != n:
+        raise ValueError("k has %d tokens, v %d" % (n, nv))
     _on(slot, (n,), torch.int32, "slot", dev)
     if cache.rope is not None or position is not None:
         _on(position, (n,), torch.int32, "position", dev)
     hq = qs = 0
     if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        qs = _rows(q, hq, d, dt, "q", dev)
-        if q.shape[0] != n:
-            raise ValueError("k has %d tokens, q %d" % (n, q.shape[0]))
+        nq, hq, qs = _rows(q, None, d, dt, "q", dev)
+        if nq != n:
+            raise ValueError("k has %d tokens, q %d" % (n, nq))
         if q_out is None:
             q_out = torch.empty((n, hq, d), dtype=dt, device=q.device)
         else:
@@ -692,11 +694,11 @@ def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len
     out (and lse [Hq][tokens] when asked for)."""
     dev = _call_device(q, "q")
     _need_pages(cache, dev)
-    hq, n_req = q.shape[1] if q.dim() == 3 else 0, cache.n_req
-    qs = _rows(q, hq, cache.d, cache._dtype, "q", dev)
+    n_req = cache.n_req
+    n, hq, qs = _rows(q, None, cache.d, cache._dtype, "q", dev)
     _on(kv_len, (n_req,), torch.int32, "kv_len", dev)
     out, lse, ws = _attn_args(q, n_req, q_start, out, lse, ws, dev)
-    rc = lib().paged_attn(cache._ref, hq, n_req, q.shape[0], q.data_ptr(), qs, q_start.data_ptr(), kv_len.data_ptr(),
+    rc = lib().paged_attn(cache._ref, hq, n_req, n, q.data_ptr(), qs, q_start.data_ptr(), kv_len.data_ptr(),
                           out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.numel(),
                           sm_scale, _raw_stream(dev))
     if rc:
@@ -713,20 +715,20 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch
     if k.dim() != 3 or k.dtype not in _DTYPE_CODE:
         raise ValueError("k must be a bfloat16 or float16 tensor (tokens, kv heads, d), got %s %s" % (k.dtype, tuple(k.shape)))
     dev = _call_device(k, "k")
-    n_key, hkv, d = k.shape
-    ks, vs = _rows(k, hkv, d, k.dtype, "k", dev), _rows(v, hkv, d, k.dtype, "v", dev)
-    if v.shape[0] != n_key:
-        raise ValueError("k has %d tokens, v %d" % (n_key, v.shape[0]))
-    hq = q.shape[1] if q.dim() == 3 else 0
-    qs = _rows(q, hq, d, k.dtype, "q", dev)
+    dt, d = k.dtype, k.shape[2]
+    n_key, hkv, ks = _rows(k, None, d, dt, "k", dev)
+    nv, _, vs = _rows(v, hkv, d, dt, "v", dev)
+    if nv != n_key:
+        raise ValueError("k has %d tokens, v %d" % (n_key, nv))
+    n, hq, qs = _rows(q, None, d, dt, "q", dev)
     n_req = k_start.numel()
     _on(k_start, (n_req,), torch.int32, "k_start", dev)
     _on(k_len, (n_req,), torch.int32, "k_len", dev)
     _on(status, (1,), torch.int32, "status", dev)
     out, lse, ws = _attn_args(q, n_req, q_start, out, lse, ws, dev)
-    desc = skv_states(n_key, hkv, d, _DTYPE_CODE[k.dtype], ks, vs, k.data_ptr(), v.data_ptr(), k_start.data_ptr(),
+    desc = skv_states(n_key, hkv, d, _DTYPE_CODE[dt], ks, vs, k.data_ptr(), v.data_ptr(), k_start.data_ptr(),
                       k_len.data_ptr(), status.data_ptr())
-    rc = lib().cross_attn(ctypes.byref(desc), hq, n_req, q.shape[0], q.data_ptr(), qs, q_start.data_ptr(),
+    rc = lib().cross_attn(ctypes.byref(desc), hq, n_req, n, q.data_ptr(), qs, q_start.data_ptr(),
                           out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.numel(),
                           sm_scale, _raw_stream(dev))
     if rc:
