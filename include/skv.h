@@ -500,8 +500,8 @@ size_t skv_attn_workspace_bytes(void);
  * lse:  device fp32 [Hq][n_tok], natural log of the sum of exp of the scaled
  *       scores, or NULL
  * A row that sees no key (kv_len 0) gets zeros and lse -inf.
- * kv_len[b] outside [n, max_block * page_size] (0 apart) sets SKV_DEV_BAD_LEN
- * and counts as 0; a span outside [0, n_tok] sets it and is skipped.  A table
+ * kv_len[b] outside [n, max_block * page_size] (0 apart) or above 2^30 sets
+ * SKV_DEV_BAD_LEN and counts as 0; a span outside [0, n_tok] sets it and is skipped.  A table
  * entry outside the pool sets SKV_DEV_BAD_PAGE; its keys and values count as
  * zeros.
  * ws: workspace of ws_bytes >= skv_attn_workspace_bytes(), zero-filled before
@@ -519,7 +519,7 @@ int paged_attn(const skv_paged* cache, int32_t n_q_head, int32_t n_req, int32_t 
  * token-major, [n_key][Hkv][d] with k_stride / v_stride elements from token
  * to token.  Request b reads tokens [k_start[b], k_start[b] + k_len[b]);
  * requests may share tokens, and a padded batch is k_start[b] = b * padded
- * length.  Tokens that no request reads may hold anything.
+ * length.  Tokens that no request reads may hold anything.  n_key <= 2^30.
  */
 typedef struct skv_states {
   int32_t n_key;

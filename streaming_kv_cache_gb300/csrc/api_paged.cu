@@ -195,6 +195,7 @@ int cross_attn(const skv_states* states, int32_t n_q_head, int32_t n_req, int32_
   int rc = check_heads(s->n_kv_head, s->head_dim, s->dtype);
   if (rc) return rc;
   if (s->n_key < 0 || !aligned(s->status, 4)) return SKV_ERR_INVALID;
+  if (s->n_key > skv::kMaxKeys) return SKV_ERR_UNSUPPORTED;
   bool empty;
   rc = check_attn(n_q_head, s->n_kv_head, s->head_dim, n_req, n_tok, q, q_stride, q_start, out, lse, ws, ws_bytes,
                   sm_scale, &empty);

@@ -81,7 +81,9 @@ cudaError_t launch_dependent(void (*kernel)(K...), int grid, int threads, int sm
 // One request as the attention sees it: rows [q0, q0 + L) of the queries, kv
 // keys; row t sees the first kv - L + t + 1 of them (paged) or all (states).
 // Lengths out of range make it harmless: a bad span has no rows, bad keys
-// are none.
+// are none.  (Key indices stay below 2^30, so that those of the last tile and
+// the boxes past it do not pass 2^31.)
+constexpr int kMaxKeys = 1 << 30;
 struct Span {
   int q0, L, kv;
   bool bad;
@@ -98,7 +100,7 @@ __device__ __forceinline__ Span request_span(const RaggedArgs& a, int b) {
     const int k0 = a.k_start[b];
     kv_ok = k0 >= 0 && s.kv >= 0 && (long long)k0 + s.kv <= a.n_key;
   } else {
-    kv_ok = s.kv == 0 || (s.kv >= s.L && s.kv <= (long long)a.max_block * a.page_size);
+    kv_ok = s.kv == 0 || (s.kv >= s.L && s.kv <= min((long long)a.max_block * a.page_size, (long long)kMaxKeys));
   }
   if (!kv_ok) {
     s.kv = 0;

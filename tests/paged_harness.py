@@ -37,7 +37,7 @@ def check(got, lse, want, want_lse, mass, dtype, q_norm, k_norm, scale, d, n_key
     """Output and lse against the oracle.
 
     u = half a step of the type.  The output is rounded once (u |o|), the
-    probabilities once (each by u of itself, so u sum p|v|), and a score that
+    probabilities at most once (each by u of itself, so u sum p|v|), and a score that
     is off by e moves its probability by e of itself and the sum by as much
     (2 e sum p|v|); e adds the error of ex2 (2^-22) and of the fp32 row sum
     ((128 + n / 128) 2^-24).  Values under the type's smallest normal have an
@@ -55,7 +55,7 @@ def check(got, lse, want, want_lse, mass, dtype, q_norm, k_norm, scale, d, n_key
     if lse is not None:
         ok = np.isfinite(want_lse)
         assert np.array_equal(lse[np.isneginf(want_lse)], want_lse[np.isneginf(want_lse)]), what
-        err = np.abs(lse - want_lse)[ok]
+        err = np.abs(lse[ok] - want_lse[ok])
         ltol = e + 2.0 ** -22 * (1 + np.abs(want_lse[ok]))
         assert (err <= ltol).all(), "%s: lse off by %.3g" % (what, err.max())
     return worst

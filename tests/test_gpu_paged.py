@@ -265,6 +265,71 @@ def test_paged_lengths_and_pages_out_of_range():
         check(f64(out), None, want, None, mass, dt, 20.0, 20.0, 0.125, d, 50)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [1, 8, 12, 40])
+def test_paged_after_calls_that_left_nan_on_chip(hq, d):
+    """Shared memory and tensor memory hold NaN from another call's keys,
+    values and queries: nothing of them may reach the outputs.  Units of one
+    and of two query tiles follow each other in every share."""
+    dt, page = torch.bfloat16, 32
+    ql, kv = [1, 7, 128, 129, 40, 3, 33, 260], [1, 7, 128, 130, 500, 300, 161, 260]
+    pg = Pages(hq, kv, page, 1, d, dt)
+    cache, qs = pg.cache(skv), starts(ql)
+    q = randn(hq, (int(qs[-1]), hq, d), dt)
+    want, wlse, mass = PO.paged(f64(q), f64(pg.k), f64(pg.v), pg.table, qs, kv, d ** -0.5)
+    ws, other = skv.attn_workspace(), skv.attn_workspace()
+    for i in range(6):
+        dd, n = (d, 192 - d)[i % 2], (600, 1)[i % 3 == 2]
+        pool = torch.full((64, 1, 128, dd), float("nan"), dtype=dt, device="cuda")
+        bad = skv.PagedCache.wrap(k=pool, v=pool, block_table=torch.arange(64, dtype=torch.int32, device="cuda")[None])
+        skv.paged_attn(bad, torch.full((n, hq, dd), float("nan"), dtype=dt, device="cuda"), ints([0, n]), ints([64 * 128]),
+                       0.1, ws=other)
+        out, lse = skv.paged_attn(cache, q, ints(qs), ints(kv), d ** -0.5, lse=True, ws=ws)
+        check(f64(out), f64(lse), want, wlse, mass, dt, 24.0, 24.0, d ** -0.5, d, 500, "call %d" % i)
+    assert cache.device_status() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (5, 1), (1, 1)])
+def test_paged_token_counts_around_the_choice_of_form(hq, hkv):
+    """One query tile per unit up to floor(128 / G) tokens a request, two above."""
+    tq = 128 // (hq // hkv)
+    for ql in ([tq, tq], [tq, tq + 1], [2 * tq, 1], [2 * tq + 1], [tq]):
+        run_paged(skv, sum(ql), ql, [x + 37 for x in ql], 16, hq, hkv, 64, torch.float16, what=str(ql))
+
+
+def test_rows_before_the_first_request():
+    d, dt = 64, torch.bfloat16
+    pg = Pages(2, [70, 9], 16, 1, d, dt)
+    cache, q = pg.cache(skv), randn(1, (12, 2, d), dt)
+    out = torch.full((12, 2, d), 5.0, dtype=dt, device="cuda")
+    skv.paged_attn(cache, q, ints([4, 9, 10]), ints([70, 9]), 0.125, out=out)
+    want, _, mass = PO.paged(f64(q[4:10]), f64(pg.k), f64(pg.v), pg.table, [0, 5, 6], [70, 9], 0.125)
+    check(f64(out[4:10]), None, want, None, mass, dt, 20.0, 20.0, 0.125, d, 70)
+    assert (out[:4] == 5).all() and (out[10:] == 5).all()
+
+
+def test_pool_past_32_bit_offsets():
+    """Pages whose elements and bytes lie past 2^32: writes and reads of the last ones."""
+    hkv, page, d, dt = 8, 64, 128, torch.bfloat16
+    n_page = 70000                                  # 4.6e9 elements a pool
+    k = torch.empty((n_page, hkv, page, d), dtype=dt, device="cuda")
+    v = torch.empty_like(k)
+    table = ints([[n_page - 1, 3, n_page - 2], [35000, n_page - 70, -1]])
+    cache = skv.PagedCache.wrap(k=k, v=v, block_table=table)
+    kv, slots = [150, 100], []
+    for b, n in enumerate(kv):
+        slots += [int(table[b, t // page]) * page + t % page for t in range(n)]
+    kn, vn = randn(1, (250, hkv, d), dt), randn(2, (250, hkv, d), dt)
+    skv.kv_paged_write(cache, None, kn, vn, None, ints(slots))
+    for t in (0, 149, 200):
+        assert torch.equal(k[slots[t] // page, :, slots[t] % page], kn[t])
+    q = randn(3, (2, 16, d), dt)
+    out, lse = skv.paged_attn(cache, q, ints([0, 1, 2]), ints(kv), d ** -0.5, lse=True)
+    assert cache.device_status() == 0
+    o, l, mass = PO.cross(f64(q), f64(kn), f64(vn), [0, 1, 2], [0, 150], kv, d ** -0.5)
+    check(f64(out), f64(lse), o, l, mass, dt, 20.0, 20.0, d ** -0.5, d, 150)
+
+
 def test_paged_results_repeat():
     a = run_paged(skv, 21, [1, 90, 1, 400], [5000, 1000, 33, 1400], 64, 8, 2, 128, torch.bfloat16)
     b = run_paged(skv, 21, [1, 90, 1, 400], [5000, 1000, 33, 1400], 64, 8, 2, 128, torch.bfloat16)

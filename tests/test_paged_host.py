@@ -214,6 +214,7 @@ def test_attention_limits(L):
         assert call(L, hq=258, qs=258 * 64) == skv.SKV_ERR_UNSUPPORTED     # 129 query heads per kv head
         assert call(L, n_tok=1 << 30, hq=4) == skv.SKV_ERR_UNSUPPORTED
     assert _attn(L, kv_len=0) == skv.SKV_ERR_INVALID
+    assert _cross(L, st=_states(n_key=(1 << 30) + 1)) == skv.SKV_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("bad", [
