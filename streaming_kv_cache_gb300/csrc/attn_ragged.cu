@@ -115,6 +115,7 @@ struct RParams {
   int G, TQ, TB;          // query heads per kv head, tokens per query tile and per unit
   int BR, boxes;          // rows per TMA box, boxes per key tile
   int min_share;          // sequence positions per CTA at least
+  float units7;           // seven times the units at least
   int unit_cost;          // positions that a unit takes before its tiles, for what it costs beside them
   float scale_log2;
   int* ws_count;          // [2 * CTAs] arrivals per unit (named by its first CTA) and query tile
@@ -380,7 +381,13 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (w == warp) before = total;
       total += s_scan[w];
     }
+    // Equal shares, but of a few keys each they would cost more to merge than
+    // to read: a tile takes about seven times as long as a piece's part of a
+    // merge, so with T tiles per unit the sum of both is least at sqrt(T / 7)
+    // tiles a piece (one request of 30,000 keys and one kv head: 50 us at two
+    // tiles a piece, 24 so).
     share = max((long long)p.min_share, udiv(total + gridDim.x - 1, gridDim.x));
+    share = max(share, (long long)ceilf(sqrtf((float)total / p.units7)));
     g0 = blockIdx.x * share;
     if (g0 >= total) {                     // no tiles left for this CTA
       if (warp == C::WARP_K) tc::tmem_dealloc(*s_tmem, 512);
@@ -445,7 +452,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int32_t* row = PAGED ? a.table + (size_t)pc.b * a.max_block : nullptr;
         auto page_of = [&](int j) {
           const int r = (pc.ta + j) * BN + lane * p.BR;
-          return PAGED && j < pc.nt && lane < p.boxes && r < pc.kv ? __ldg(row + r / a.page_size) : -1;
+          return PAGED && j < pc.nt && lane < p.boxes && r < pc.kv ? __ldcg(row + r / a.page_size) : -1;
         };
         int id = page_of(0);
         for (int j = 0; j < pc.nt; ++j, ++n) {
@@ -934,8 +941,9 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (last) {
           if (leader) *count = 0;          // ready for the next call
           if (!big) {
-            // few rows (decode): a thread has one column group, many pieces in flight
+            // few rows (decode): a thread has one or two column groups, many pieces in flight
             if (rows * (D / 4) <= BM) merge_pieces<D, NQ, F16, 1, 16>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, row);
+            else if (rows * (D / 4) <= 2 * BM) merge_pieces<D, NQ, F16, 2, 8>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, row);
             else merge_pieces<D, NQ, F16, 4, 4>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, row);
           } else if (active) {
             auto slot = [&](int k) { return 2 * (pc.cta0 + k) + (k == 0 ? 1 : 0); };
@@ -943,50 +951,66 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               return k == pc.k ? make_float2(m_used, l)
                                : __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)slot(k) * NQ + i) * BM + row);
             };
+            auto o_of = [&](int k, int c) {      // columns [4 c, 4 c + 4) of another piece
+              return __ldcg(reinterpret_cast<const float4*>(p.ws_o + ws_index<D, NQ>(slot(k), i, c, row)));
+            };
             float M = -INFINITY, den = 0.f;
-            float2 ml4[4];                   // the first pieces' (m, l), often all there are
-#pragma unroll
-            for (int k = 0; k < 4; ++k) ml4[k] = k < pc.n ? ml_of(k) : make_float2(0.f, 0.f);
             auto add = [&](const float2& ml) {
               if (ml.y == 0.f) return;       // no key that the row sees
               const float mx = fmaxf(M, ml.x);
               den = den * (M == -INFINITY ? 0.f : exp2f(M - mx)) + exp2f(ml.x - mx) * ml.y;
               M = mx;
             };
+            auto weight = [&](const float2& ml) { return ml.y == 0.f ? 0.f : exp2f(ml.x - M); };
+            // acc + w o, without what a piece of no weight holds
+            auto mix = [](float w, float o, float acc) { return w == 0.f ? acc : acc + w * o; };
+            if (pc.n == 2) {
+              // the usual case: all of the other piece's row is loaded in one
+              // round trip
+              float4 v[D / 4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) add(ml4[k]);
-            for (int k = 4; k < pc.n; ++k) add(ml_of(k));
-            const float inv = den == 0.f ? 0.f : 1.f / den;
-            constexpr int CW = 64;           // columns at a time: loads of a piece in flight together
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += CW) {
-              float acc[CW];
+              for (int c = 0; c < D / 4; ++c) v[c] = o_of(1 - pc.k, c);
+              const float2 ml0 = ml_of(0), ml1 = ml_of(1);
+              add(ml0);
+              add(ml1);
+              const float w0 = weight(ml0), w1 = weight(ml1), inv = den == 0.f ? 0.f : 1.f / den;
+              const float* vf = reinterpret_cast<const float*>(v);
 #pragma unroll
-              for (int e = 0; e < CW; ++e) acc[e] = 0.f;
-#pragma unroll 1
-              for (int k = 0; k < pc.n; ++k) {
-                float o[CW];
-                if (k == pc.k) {
+              for (int cb = 0; cb < D / 32; ++cb) {
+                float o[32];
+                tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+                tc::tmem_wait_ld();
 #pragma unroll
-                  for (int cb = 0; cb < CW / 32; ++cb)
-                    tc::tmem_ld32(tO + c0 + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o + cb * 32));
-                  tc::tmem_wait_ld();
-                } else {
-#pragma unroll
-                  for (int e = 0; e < CW / 4; ++e)
-                    *reinterpret_cast<float4*>(o + 4 * e) = __ldcg(reinterpret_cast<const float4*>(
-                        p.ws_o + ws_index<D, NQ>(slot(k), i, c0 / 4 + e, row)));
+                for (int e = 0; e < 32; ++e) {
+                  const float x0 = pc.k == 0 ? o[e] : vf[cb * 32 + e], x1 = pc.k == 0 ? vf[cb * 32 + e] : o[e];
+                  o[e] = mix(w1, x1, mix(w0, x0, 0.f));
                 }
-                const float2 ml = k == 0 ? ml4[0] : k == 1 ? ml4[1] : k == 2 ? ml4[2] : k == 3 ? ml4[3] : ml_of(k);
-                const float w = ml.y == 0.f ? 0.f : exp2f(ml.x - M);
-                if (w != 0.f) {
-#pragma unroll
-                  for (int e = 0; e < CW; ++e) acc[e] += w * o[e];
-                }
+                store_row(cb, o, inv);
               }
+            } else {
+              for (int k = 0; k < pc.n; ++k) add(ml_of(k));
+              const float inv = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll 1
+              for (int cb = 0; cb < D / 32; ++cb) {
+                float acc[32];
 #pragma unroll
-              for (int cb = 0; cb < CW / 32; ++cb)
-                store_row(c0 / 32 + cb, *reinterpret_cast<const float(*)[32]>(acc + cb * 32), inv);
+                for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < pc.n; ++k) {
+                  float o[32];
+                  if (k == pc.k) {
+                    tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+                    tc::tmem_wait_ld();
+                  } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) *reinterpret_cast<float4*>(o + 4 * e) = o_of(k, cb * 8 + e);
+                  }
+                  const float w = weight(ml_of(k));
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) acc[e] = mix(w, o[e], acc[e]);
+                }
+                store_row(cb, acc, inv);
+              }
             }
             if (lse) *lse = den == 0.f ? -INFINITY : (M + __log2f(den)) * 0.69314718055994531f;
           }
@@ -1068,6 +1092,7 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   const int grid = min(sm_count(), MAX_CTAS);
   p.min_share = wide ? 4 : 1;
   p.unit_cost = wide ? 2 : 1;
+  p.units7 = 7.f * a.n_req * a.Hkv;
   p.BR = BN;
   if (paged)
     while (a.page_size % p.BR) p.BR /= 2;

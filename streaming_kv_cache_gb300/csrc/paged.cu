@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(WT) paged_write_kernel(const WriteArgs a) {
     }
     const float4* r4 = reinterpret_cast<const float4*>(a.rope) + ((size_t)pos * (D / 2) + c * 8) / 2;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) t[w] = __ldg(r4 + w);
+    for (int w = 0; w < 4; ++w) t[w] = r4[w];
   }
   uint4 x[RPT], y[RPT];
   uint16_t* dst[RPT];

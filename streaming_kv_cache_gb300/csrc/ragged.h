@@ -62,7 +62,8 @@ size_t ragged_ws_bytes();
 
 // Launch as a programmatic dependent of the kernel before it on the stream:
 // its CTAs may start while that one still ends, and wait for it
-// (grid_dep_wait) before they read or write anything of the caller's.
+// (grid_dep_wait) before they read or write anything of the caller's.  They
+// read none of it through the read-only path: it may change after they start.
 template <typename... K, typename... A>
 cudaError_t launch_dependent(void (*kernel)(K...), int grid, int threads, int smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
