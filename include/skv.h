@@ -504,10 +504,11 @@ size_t skv_attn_workspace_bytes(void);
  * SKV_DEV_BAD_LEN and counts as 0; a span outside [0, n_tok] sets it and is skipped.  A table
  * entry outside the pool sets SKV_DEV_BAD_PAGE; its keys and values count as
  * zeros.
- * ws: workspace of ws_bytes >= skv_attn_workspace_bytes(), zero-filled before
- *     its first use and left ready by each call (zero it again after
- *     SKV_DEV_TIMEOUT).  Calls that may run at the same time, captured graphs
- *     among them, need workspaces of their own.
+ * ws: workspace of ws_bytes >= skv_attn_workspace_bytes(), of any contents.
+ *     Calls that may run at the same time, captured graphs among them, need
+ *     workspaces of their own.
+ * The call is two kernel launches: the attention, and the merge of what
+ * several SMs computed of one row.
  * Needs Hq % Hkv == 0, Hq / Hkv <= 128 and n_tok * Hq < 2^31.
  */
 int paged_attn(const skv_paged* cache, int32_t n_q_head, int32_t n_req, int32_t n_tok,

@@ -16,9 +16,9 @@
 // it: every SM streams the same number of tiles whatever the lengths, which
 // the host never sees.  Each CTA finds its place by a scan over the requests'
 // tile counts (closed forms, see unit_prefix).  A unit that several CTAs
-// share leaves fp32 partials (O, m, sum) in the workspace, and the last of
-// them to arrive merges the pieces in their order, so results do not depend
-// on timing.
+// share leaves fp32 partials (O, m, sum) in the workspace, which a second
+// kernel merges in the pieces' order, so results do not depend on timing (see
+// merge_kernel).
 //
 // Two forms.  NQ = 2, for calls with more than TQ tokens per request: two
 // query tiles share every key tile, and one tile's softmax runs under the
@@ -118,7 +118,7 @@ struct RParams {
   float units7;           // seven times the units at least
   int unit_cost;          // positions that a unit takes before its tiles, for what it costs beside them
   float scale_log2;
-  int* ws_count;          // [2 * CTAs] arrivals per unit (named by its first CTA) and query tile
+  int4* ws_unit;          // [CTAs] the shared unit that starts in a CTA: pieces (0: none), first token row, kv head, tokens
   float* ws_ml;           // [2 * CTAs][NQ][BM][2]
   float* ws_o;            // [2 * CTAs][NQ][D / 4][BM][4], see ws_index
 };
@@ -134,9 +134,7 @@ struct Piece {
   int pos0;        // keys that the unit's first token sees, less one
   int step;        // 1: each later token sees one more (causal), 0: all see the same
   int krow;        // first state of the request (cross attention)
-  int n, k;        // pieces of the unit, and which one this is
-  int cta0;        // CTA of the unit's first piece
-  int slot;        // workspace slot of this piece
+  int slot;        // workspace slot of its partials, -1: the piece is the whole unit
 };
 static_assert(sizeof(Piece) <= 64, "piece slot");
 
@@ -222,80 +220,92 @@ __device__ __forceinline__ size_t ws_index(int slot, int i, int c, int r) {
   return ((((size_t)slot * NQ + i) * (D / 4) + c) * BM + r) * 4;
 }
 
-// Merge query tile i of a unit whose n pieces left partials (O_k, m_k, l_k):
-// O = sum_k w_k O_k / sum_k w_k l_k with w_k = 2^(m_k - M), by the 128 threads
-// of a query tile, over the pieces in their order.  A thread takes one
-// row and every `lanes`-th group of 4 columns: a full tile's rows a thread
-// each, a decode step's few rows spread over all threads.  CU column groups of
-// KU pieces are loaded together with their (m, l), M following as it grows,
-// so that up to KU pieces take one round trip.
-template <int D, int NQ, bool F16, int CU, int KU>
-__device__ __noinline__ void merge_pieces(const RParams& p, int cta0, int n, int row0, int h, int i, int rows, int t) {
-  constexpr int CG = D / 4;     // column groups
+// Merge of the units that several CTAs share: O = sum_k w_k O_k / sum_k w_k l_k
+// with w_k = 2^(m_k - M), over the n pieces' partials (O_k, m_k, l_k) in their
+// order.  One CTA after the last piece would have to read all of a unit's
+// partials by itself (36 rows x 13 pieces took it 15 us); here a unit's rows
+// and columns are spread over blocks, which start as the attention's CTAs
+// leave their SMs.  Block (x, i, c) takes a part of query tile i of the unit
+// that starts in CTA c; a thread takes CU groups of 4 columns of a row, with
+// KU pieces in flight, M following as it grows: bound by one or two round
+// trips to L2.
+constexpr int MT = 128;         // threads per block
+constexpr int MERGE_PARTS = 8;  // blocks per query tile: 128 rows x 8 threads, or 32 rows x 32
+
+template <int D, bool F16, int NQ, int CU, int KU>
+__device__ __forceinline__ void merge_part(const RParams& p, const int4& u, int c0, int i, int rows, int t) {
   const RaggedArgs& a = p.a;
+  const int r = t % rows, c = t / rows * CU;     // row, first column group
+  if (c >= D / 4) return;
   // piece 0 is the last of its CTA's share, every other the first
-  auto slot = [&](int k) { return 2 * (cta0 + k) + (k == 0 ? 1 : 0); };
-  const int lanes = BM / rows;            // threads per row
-  const int r = t % rows, c0 = t / rows;
-  if (c0 >= lanes) return;
-  const int tok = row0 + i * p.TQ + r / p.G, hq = h * p.G + r % p.G;
-  uint16_t* dst = a.out + ((size_t)tok * a.Hq + hq) * D;
-  for (int c = c0; c < CG; c += CU * lanes) {
-    float4 acc[CU];
+  auto slot = [&](int k) { return 2 * (c0 + k) + (k == 0 ? 1 : 0); };
+  float4 acc[CU];
 #pragma unroll
-    for (int u = 0; u < CU; ++u) acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    float M = -INFINITY, den = 0.f;
-    for (int k0 = 0; k0 < n; k0 += KU) {
-      float4 v[KU][CU];
-      float2 ml[KU];
+  for (int q = 0; q < CU; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -INFINITY, den = 0.f;
+  for (int k0 = 0; k0 < u.x; k0 += KU) {
+    float4 v[KU][CU];
+    float2 ml[KU];
 #pragma unroll
-      for (int x = 0; x < KU; ++x) {
-        const bool on = k0 + x < n;
-        ml[x] = on ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)slot(k0 + x) * NQ + i) * BM + r)
-                   : make_float2(0.f, 0.f);
+    for (int x = 0; x < KU; ++x) {
+      const bool on = k0 + x < u.x;
+      ml[x] = on ? __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)slot(k0 + x) * NQ + i) * BM + r)
+                 : make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < CU; ++u)
-          v[x][u] = on && c + u * lanes < CG
-                        ? __ldcg(reinterpret_cast<const float4*>(p.ws_o + ws_index<D, NQ>(slot(k0 + x), i, c + u * lanes, r)))
-                        : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      float mx = M;
-#pragma unroll
-      for (int x = 0; x < KU; ++x)
-        if (ml[x].y != 0.f) mx = fmaxf(mx, ml[x].x);   // a piece without a visible key left l = 0
-      const float al = M == -INFINITY ? 0.f : exp2f(M - mx);
-      den *= al;
-#pragma unroll
-      for (int u = 0; u < CU; ++u) {
-        acc[u].x *= al;
-        acc[u].y *= al;
-        acc[u].z *= al;
-        acc[u].w *= al;
-      }
-#pragma unroll
-      for (int x = 0; x < KU; ++x) {
-        if (ml[x].y == 0.f) continue;
-        const float w = exp2f(ml[x].x - mx);
-        den += w * ml[x].y;
-#pragma unroll
-        for (int u = 0; u < CU; ++u) {
-          acc[u].x += w * v[x][u].x;
-          acc[u].y += w * v[x][u].y;
-          acc[u].z += w * v[x][u].z;
-          acc[u].w += w * v[x][u].w;
-        }
-      }
-      M = mx;
+      for (int q = 0; q < CU; ++q)
+        v[x][q] = on ? __ldcg(reinterpret_cast<const float4*>(p.ws_o + ws_index<D, NQ>(slot(k0 + x), i, c + q, r)))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const float inv = den == 0.f ? 0.f : 1.f / den;
+    float mx = M;
 #pragma unroll
-    for (int u = 0; u < CU; ++u)
-      if (c + u * lanes < CG)
-        *reinterpret_cast<uint2*>(dst + (c + u * lanes) * 4) =
-            make_uint2(pack16<F16>(acc[u].x * inv, acc[u].y * inv), pack16<F16>(acc[u].z * inv, acc[u].w * inv));
-    if (a.lse && c == 0)
-      a.lse[(size_t)hq * a.n_tok + tok] = den == 0.f ? -INFINITY : (M + __log2f(den)) * 0.69314718055994531f;
+    for (int x = 0; x < KU; ++x)
+      if (ml[x].y != 0.f) mx = fmaxf(mx, ml[x].x);   // a piece without a visible key left l = 0
+    const float al = M == -INFINITY ? 0.f : exp2f(M - mx);
+    den *= al;
+#pragma unroll
+    for (int q = 0; q < CU; ++q) {
+      acc[q].x *= al;
+      acc[q].y *= al;
+      acc[q].z *= al;
+      acc[q].w *= al;
+    }
+#pragma unroll
+    for (int x = 0; x < KU; ++x) {
+      if (ml[x].y == 0.f) continue;
+      const float w = exp2f(ml[x].x - mx);
+      den += w * ml[x].y;
+#pragma unroll
+      for (int q = 0; q < CU; ++q) {
+        acc[q].x += w * v[x][q].x;
+        acc[q].y += w * v[x][q].y;
+        acc[q].z += w * v[x][q].z;
+        acc[q].w += w * v[x][q].w;
+      }
+    }
+    M = mx;
   }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const int tok = u.y + i * p.TQ + r / p.G, hq = u.z * p.G + r % p.G;
+  uint2* dst = reinterpret_cast<uint2*>(a.out + ((size_t)tok * a.Hq + hq) * D + c * 4);
+#pragma unroll
+  for (int q = 0; q < CU; ++q)
+    dst[q] = make_uint2(pack16<F16>(acc[q].x * inv, acc[q].y * inv), pack16<F16>(acc[q].z * inv, acc[q].w * inv));
+  if (a.lse && c == 0)
+    a.lse[(size_t)hq * a.n_tok + tok] = den == 0.f ? -INFINITY : (M + __log2f(den)) * 0.69314718055994531f;
+}
+
+template <int D, bool F16, int NQ>
+__global__ void __launch_bounds__(MT) merge_kernel(const RParams p) {
+  tc::grid_dep_launch();
+  tc::grid_dep_wait();
+  const int c0 = blockIdx.z, i = blockIdx.y, t = blockIdx.x * MT + threadIdx.x;
+  const int4 u = __ldcg(p.ws_unit + c0);
+  const int rows = min(p.TQ, u.w - i * p.TQ) * p.G;
+  if (u.x == 0 || rows <= 0) return;
+  // few rows (decode): a thread per row and 4 columns, many pieces in flight;
+  // else whole 32-byte sectors of the output a thread
+  if (rows <= MERGE_PARTS * MT / 32) merge_part<D, F16, NQ, 1, 16>(p, u, c0, i, rows, t);
+  else merge_part<D, F16, NQ, 4, 4>(p, u, c0, i, rows, t);
 }
 
 template <int D, bool F16, int NQ, bool PAGED>
@@ -314,7 +324,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   const uint32_t sbase = tc::smem_u32(smem);
   auto bar = [&](int i) { return sbase + C::BAR_OFF + 8u * i; };
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
-  volatile int* s_last = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);   // per query tile: merge it here
   volatile long long* s_off = reinterpret_cast<volatile long long*>(smem + C::MISC_OFF + 16);
   int* s_first = reinterpret_cast<int*>(smem + C::MISC_OFF + 24);   // the share's first request and its span
   Piece* s_piece = reinterpret_cast<Piece*>(smem + C::PIECE_OFF);
@@ -390,6 +399,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     share = max(share, (long long)ceilf(sqrtf((float)total / p.units7)));
     g0 = blockIdx.x * share;
     if (g0 >= total) {                     // no tiles left for this CTA
+      if (tid == 0) p.ws_unit[blockIdx.x] = make_int4(0, 0, 0, 0);
       if (warp == C::WARP_K) tc::tmem_dealloc(*s_tmem, 512);
       return;
     }
@@ -669,6 +679,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (lane == 0) {
         long long g = g0;
         bool ok = true;
+        int4 shared_unit = make_int4(0, 0, 0, 0);   // the unit that starts here and goes on in the next CTA
         int loaded = 0;                   // pieces whose queries are on their way
         for (int pi = 0; ok; ++pi) {
           Piece pc{};
@@ -685,13 +696,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             pc.step = PAGED && s.kv ? 1 : 0;
             pc.pos0 = pc.step ? s.kv - s.L + qb * TB : s.kv - 1;
             pc.krow = PAGED ? 0 : a.k_start[b];
-            pc.n = 1;
-            if (u0 < g0 || u1 > g1) {
-              pc.cta0 = (int)udiv(u0, share);
-              pc.n = (int)udiv(u1 - 1, share) - pc.cta0 + 1;
-              pc.k = (int)blockIdx.x - pc.cta0;
-              pc.slot = 2 * (int)blockIdx.x + (pc.k == 0 ? 1 : 0);
-            }
+            pc.slot = u0 < g0 ? 2 * (int)blockIdx.x : u1 > g1 ? 2 * (int)blockIdx.x + 1 : -1;
+            // (u0 lies in this CTA's share)
+            if (u0 >= g0 && u1 > g1)
+              shared_unit = make_int4((int)udiv(u1 - 1, share) - (int)blockIdx.x + 1, pc.row0, h, pc.ntok);
             g = u1;
             // the next unit
             t = 0;
@@ -722,6 +730,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           loaded = pi + 1;
         }
         if (!ok) set_status(a.status, SKV_DEV_TIMEOUT);
+        p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);   // always written: the merge reads it
         if (loaded) wait(B::QFULL, loaded - 1);
       }
     }
@@ -730,7 +739,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if constexpr (NQ == 2) tc::setmaxnreg_inc<208>();
     const int i = warp >> 2, lg = warp & 3;          // query tile, TMEM lane group
     const int row = lg * 32 + lane;
-    const int tile_bar = 1 + i;                      // named barrier of the query tile's warps
     const uint32_t t_lane = (uint32_t)(lg * 32) << 16;
     const uint32_t tO = tmem + t_lane + 256 + i * 128;
     const int tok = row / p.G, gq = row - tok * p.G;
@@ -874,147 +882,37 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // (two query tiles: one commit per piece, one: one per tile)
         const int c = cnt - 1, x = NQ == 2 ? i : c & 1, ph = NQ == 2 ? pcs++ : c >> 1;
         if (ok) ok = __all_sync(0xffffffffu, wait(B::PVDONE + x, ph));
-        // the warps of the query tile go on together (barriers below)
-        ok = tc::bar_and(tile_bar, BM, ok);
         if (!ok) break;
       }
       tc::tc_fence_after();
       const int hq = pc.h * p.G + gq, trow = pc.row0 + i * p.TQ + tok;
-      const int rows = ntok * p.G;
       uint16_t* orow = a.out + ((size_t)(valid ? trow : 0) * a.Hq + hq) * D;
-      float* lse = valid && a.lse ? a.lse + (size_t)hq * a.n_tok + trow : nullptr;
-      auto store_row = [&](int cb, const float (&o)[32], float f) {
-        if (!valid) return;
-        uint4 pk[4];
-        uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) pw[k] = pack16<F16>(o[2 * k] * f, o[2 * k + 1] * f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(orow + cb * 32)[k] = pk[k];
-      };
-      if (pc.n == 1) {
-        if (active) {
-          const float inv_l = l == 0.f ? 0.f : 1.f / l;
+      if (active) {
+        const float inv_l = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-          for (int cb = 0; cb < D / 32; ++cb) {
-            float o[32];
-            tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
-            tc::tmem_wait_ld();
-            store_row(cb, o, inv_l);
-          }
-          if (lse) *lse = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
-        }
-      } else {
-        // A shared unit.  With few rows every piece goes through the
-        // workspace.  With many, the piece that finds all others there (or
-        // arrives last) takes its own part from TMEM, a thread per row.
-        const bool big = rows > BM / 2;
-        int* count = p.ws_count + 2 * pc.cta0 + i;
-        const bool leader = row == 0;
-        if (big) {
-          if (leader) s_last[i] = tc::ld_acquire_gpu(reinterpret_cast<const uint32_t*>(count)) == (uint32_t)(pc.n - 1);
-          tc::bar_sync_n(tile_bar, BM);
-        }
-        bool last = big && s_last[i];
-        if (!last) {
-          if (active) {
-#pragma unroll 1
-            for (int cb = 0; cb < D / 32; ++cb) {
-              uint32_t o[32];
-              tc::tmem_ld32(tO + cb * 32, o);
-              tc::tmem_wait_ld();
-              if (valid) {
+        for (int cb = 0; cb < D / 32; ++cb) {
+          float o[32];
+          tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+          tc::tmem_wait_ld();
+          if (!valid) continue;
+          if (pc.slot < 0) {
+            uint4 pk[4];
+            uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  *reinterpret_cast<uint4*>(p.ws_o + ws_index<D, NQ>(pc.slot, i, cb * 8 + k, row)) =
-                      make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-              }
-            }
-            if (valid)
-              reinterpret_cast<float2*>(p.ws_ml)[((size_t)pc.slot * NQ + i) * BM + row] = make_float2(m_used, l);
-          }
-          tc::bar_sync_n(tile_bar, BM);
-          if (leader) s_last[i] = tc::atom_add_acq_rel(count, 1) == pc.n - 1;
-          tc::bar_sync_n(tile_bar, BM);
-          last = s_last[i];
-        }
-        if (last) {
-          if (leader) *count = 0;          // ready for the next call
-          if (!big) {
-            // few rows (decode): a thread has one or two column groups, many pieces in flight
-            if (rows * (D / 4) <= BM) merge_pieces<D, NQ, F16, 1, 16>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, row);
-            else if (rows * (D / 4) <= 2 * BM) merge_pieces<D, NQ, F16, 2, 8>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, row);
-            else merge_pieces<D, NQ, F16, 4, 4>(p, pc.cta0, pc.n, pc.row0, pc.h, i, rows, row);
-          } else if (active) {
-            auto slot = [&](int k) { return 2 * (pc.cta0 + k) + (k == 0 ? 1 : 0); };
-            auto ml_of = [&](int k) {
-              return k == pc.k ? make_float2(m_used, l)
-                               : __ldcg(reinterpret_cast<const float2*>(p.ws_ml) + ((size_t)slot(k) * NQ + i) * BM + row);
-            };
-            auto o_of = [&](int k, int c) {      // columns [4 c, 4 c + 4) of another piece
-              return __ldcg(reinterpret_cast<const float4*>(p.ws_o + ws_index<D, NQ>(slot(k), i, c, row)));
-            };
-            float M = -INFINITY, den = 0.f;
-            auto add = [&](const float2& ml) {
-              if (ml.y == 0.f) return;       // no key that the row sees
-              const float mx = fmaxf(M, ml.x);
-              den = den * (M == -INFINITY ? 0.f : exp2f(M - mx)) + exp2f(ml.x - mx) * ml.y;
-              M = mx;
-            };
-            auto weight = [&](const float2& ml) { return ml.y == 0.f ? 0.f : exp2f(ml.x - M); };
-            // acc + w o, without what a piece of no weight holds
-            auto mix = [](float w, float o, float acc) { return w == 0.f ? acc : acc + w * o; };
-            if (pc.n == 2) {
-              // the usual case: all of the other piece's row is loaded in one
-              // round trip
-              float4 v[D / 4];
+            for (int k = 0; k < 16; ++k) pw[k] = pack16<F16>(o[2 * k] * inv_l, o[2 * k + 1] * inv_l);
 #pragma unroll
-              for (int c = 0; c < D / 4; ++c) v[c] = o_of(1 - pc.k, c);
-              const float2 ml0 = ml_of(0), ml1 = ml_of(1);
-              add(ml0);
-              add(ml1);
-              const float w0 = weight(ml0), w1 = weight(ml1), inv = den == 0.f ? 0.f : 1.f / den;
-              const float* vf = reinterpret_cast<const float*>(v);
+            for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(orow + cb * 32)[k] = pk[k];
+          } else {
 #pragma unroll
-              for (int cb = 0; cb < D / 32; ++cb) {
-                float o[32];
-                tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  const float x0 = pc.k == 0 ? o[e] : vf[cb * 32 + e], x1 = pc.k == 0 ? vf[cb * 32 + e] : o[e];
-                  o[e] = mix(w1, x1, mix(w0, x0, 0.f));
-                }
-                store_row(cb, o, inv);
-              }
-            } else {
-              for (int k = 0; k < pc.n; ++k) add(ml_of(k));
-              const float inv = den == 0.f ? 0.f : 1.f / den;
-#pragma unroll 1
-              for (int cb = 0; cb < D / 32; ++cb) {
-                float acc[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) acc[e] = 0.f;
-#pragma unroll 1
-                for (int k = 0; k < pc.n; ++k) {
-                  float o[32];
-                  if (k == pc.k) {
-                    tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
-                    tc::tmem_wait_ld();
-                  } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) *reinterpret_cast<float4*>(o + 4 * e) = o_of(k, cb * 8 + e);
-                  }
-                  const float w = weight(ml_of(k));
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) acc[e] = mix(w, o[e], acc[e]);
-                }
-                store_row(cb, acc, inv);
-              }
-            }
-            if (lse) *lse = den == 0.f ? -INFINITY : (M + __log2f(den)) * 0.69314718055994531f;
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(p.ws_o + ws_index<D, NQ>(pc.slot, i, cb * 8 + k, row)) =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
+        if (valid && pc.slot >= 0)
+          reinterpret_cast<float2*>(p.ws_ml)[((size_t)pc.slot * NQ + i) * BM + row] = make_float2(m_used, l);
+        else if (valid && a.lse)
+          a.lse[(size_t)hq * a.n_tok + trow] = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
       }
       // O is read out: the next piece's first P V may overwrite it
       tc::tc_fence_before();
@@ -1058,11 +956,11 @@ cudaError_t set_smem_once(K kernel, int bytes, int variant) {
   return e;
 }
 
-// Workspace: arrival counters (a 4 KB block), then (m, sum) and O of two
-// pieces per CTA, the first and the last of its share (any piece between is a
-// whole unit), at the larger form's rows and head size.
+// Workspace: the shared units (a word of four per CTA), then (m, sum) and O of
+// two pieces per CTA, the first and the last of its share (any piece between
+// is a whole unit), at the larger form's rows and head size.
 constexpr int MAX_CTAS = 512;
-constexpr size_t WS_HEAD = 2 * MAX_CTAS * sizeof(int);
+constexpr size_t WS_HEAD = MAX_CTAS * sizeof(int4);
 size_t ws_ml_bytes() { return (size_t)2 * sm_count() * 2 * BM * 2 * sizeof(float); }
 
 bool encode_3d(CUtensorMap* m, bool f16, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
@@ -1099,7 +997,7 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   p.boxes = BN / p.BR;
   p.scale_log2 = a.sm_scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(a.ws);
-  p.ws_count = reinterpret_cast<int*>(ws);
+  p.ws_unit = reinterpret_cast<int4*>(ws);
   p.ws_ml = reinterpret_cast<float*>(ws + WS_HEAD);
   p.ws_o = reinterpret_cast<float*>(ws + WS_HEAD + ws_ml_bytes());
 
@@ -1123,13 +1021,15 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
     }
     if (!ok) return cudaErrorInvalidValue;
   }
-  auto launch = [&](auto kernel, int smem, int threads, int variant) -> cudaError_t {
-    const cudaError_t e = set_smem_once(kernel, smem, variant);
+  auto launch = [&](auto kernel, auto merge, int smem, int threads, int variant) -> cudaError_t {
+    cudaError_t e = set_smem_once(kernel, smem, variant);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, grid, threads, smem, st, tq, tk, tv, p);
+    e = launch_dependent(kernel, dim3(grid), threads, smem, st, tq, tk, tv, p);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(merge, dim3(MERGE_PARTS, wide ? 2 : 1, grid), MT, 0, st, p);
   };
 #define SKV_RAGGED(DD, FF, NN, PP, VAR) \
-  launch(ragged_attn_kernel<DD, FF, NN, PP>, RCfg<DD, NN>::ALLOC, RCfg<DD, NN>::NT, VAR)
+  launch(ragged_attn_kernel<DD, FF, NN, PP>, merge_kernel<DD, FF, NN>, RCfg<DD, NN>::ALLOC, RCfg<DD, NN>::NT, VAR)
 #define SKV_RAGGED_FORMS(DD, FF, VAR)                                                                    \
   (wide ? (paged ? SKV_RAGGED(DD, FF, 2, true, VAR) : SKV_RAGGED(DD, FF, 2, false, VAR + 1))             \
         : (paged ? SKV_RAGGED(DD, FF, 1, true, VAR + 2) : SKV_RAGGED(DD, FF, 1, false, VAR + 3)))

@@ -330,7 +330,7 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_relaxed);
   }
-  return launch_dependent(paged_plan_kernel, grid, PT, smem, st, a);
+  return launch_dependent(paged_plan_kernel, dim3(grid), PT, smem, st, a);
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, int d, bool f16, cudaStream_t st) {
@@ -339,7 +339,7 @@ cudaError_t launch_paged_write(const WriteArgs& a, int d, bool f16, cudaStream_t
   const long long blocks = (items + WT - 1) / WT;
   if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
-  auto launch = [&](auto kernel) { return launch_dependent(kernel, (int)blocks, WT, 0, st, a); };
+  auto launch = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)blocks), WT, 0, st, a); };
   if (d == 128) return f16 ? launch(paged_write_kernel<128, true>) : launch(paged_write_kernel<128, false>);
   return f16 ? launch(paged_write_kernel<64, true>) : launch(paged_write_kernel<64, false>);
 }

@@ -65,12 +65,12 @@ size_t ragged_ws_bytes();
 // (grid_dep_wait) before they read or write anything of the caller's.  They
 // read none of it through the read-only path: it may change after they start.
 template <typename... K, typename... A>
-cudaError_t launch_dependent(void (*kernel)(K...), int grid, int threads, int smem, cudaStream_t st, const A&... args) {
+cudaError_t launch_dependent(void (*kernel)(K...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;

@@ -103,15 +103,6 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t* p) {
   return v;
 }
 
-// Arrive on a counter in global memory: what this thread has seen happen (its
-// CTA's stores before a barrier among them) is visible to whoever reads the
-// counter after it, and what the earlier arrivals saw is visible here.
-__device__ __forceinline__ int atom_add_acq_rel(int* p, int v) {
-  int old;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
-
 // Barrier across every CTA of a cooperative launch (all of them are resident
 // at once, so a CTA that waits here never holds back one that has not
 // started).  count and gen are two words of global memory, count zero
@@ -388,18 +379,6 @@ __device__ __forceinline__ bool bar_and(int id, int n, bool v) {
   uint32_t r;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.and.pred q, %2, %3, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-
-// Named barrier over n threads that also ORs a predicate across them.
-__device__ __forceinline__ bool bar_or(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, %2, %3, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"((uint32_t)v), "r"(id), "r"(n)

@@ -660,10 +660,9 @@ def kv_paged_write(cache: PagedCache, q: torch.Tensor | None, k: torch.Tensor, v
 
 
 def attn_workspace(device="cuda") -> torch.Tensor:
-    """A zero-filled workspace for paged_attn and cross_attn (any shape)."""
+    """A workspace for paged_attn and cross_attn (any shape)."""
     with torch.cuda.device(torch.device(device)):
-        n = max(16, int(lib().skv_attn_workspace_bytes()))
-        return torch.zeros((n,), dtype=torch.uint8, device=device)
+        return torch.empty((int(lib().skv_attn_workspace_bytes()),), dtype=torch.uint8, device=device)
 
 
 def _attn_args(q, n_req, q_start, out, lse, ws, dev):

@@ -278,6 +278,7 @@ def test_paged_after_calls_that_left_nan_on_chip(hq, d):
     q = randn(hq, (int(qs[-1]), hq, d), dt)
     want, wlse, mass = PO.paged(f64(q), f64(pg.k), f64(pg.v), pg.table, qs, kv, d ** -0.5)
     ws, other = skv.attn_workspace(), skv.attn_workspace()
+    ws.fill_(255)                                # of any contents
     for i in range(6):
         dd, n = (d, 192 - d)[i % 2], (600, 1)[i % 3 == 2]
         pool = torch.full((64, 1, 128, dd), float("nan"), dtype=dt, device="cuda")
