@@ -84,8 +84,8 @@ struct RCfg {
   static constexpr int BAR_OFF = V_OFF + VST * KT;
   static constexpr int MISC_OFF = BAR_OFF + 44 * 8;
   static constexpr int PIECE_OFF = MISC_OFF + 64;
-  static constexpr int SCAN_OFF = PIECE_OFF + NP * 64;       // running sums of the prologue, one per warp
-  static constexpr int BYTES = SCAN_OFF + NT / 32 * 8;
+  static constexpr int SCAN_OFF = PIECE_OFF + NP * 64;       // sums of the prologue, one of each per warp
+  static constexpr int BYTES = SCAN_OFF + NT / 32 * 16;
   static constexpr int ALLOC = BYTES + 1024;                 // slack for 1024-byte alignment
   static_assert(ALLOC <= 232448, "shared memory");
 };
@@ -115,6 +115,7 @@ struct RParams {
   int G, TQ, TB;          // query heads per kv head, tokens per query tile and per unit
   int BR, boxes;          // rows per TMA box, boxes per key tile
   int min_share;          // sequence positions per CTA at least
+  int whole_slack;        // positions that the longest unit may have over an equal share to keep units whole
   float units7;           // seven times the units at least
   int unit_cost;          // positions that a unit takes before its tiles, for what it costs beside them
   float scale_log2;
@@ -327,7 +328,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   volatile long long* s_off = reinterpret_cast<volatile long long*>(smem + C::MISC_OFF + 16);
   int* s_first = reinterpret_cast<int*>(smem + C::MISC_OFF + 24);   // the share's first request and its span
   Piece* s_piece = reinterpret_cast<Piece*>(smem + C::PIECE_OFF);
-  long long* s_scan = reinterpret_cast<long long*>(smem + C::SCAN_OFF);
+  struct Sums {
+    long long positions;
+    int units, longest;
+  };
+  Sums* s_scan = reinterpret_cast<Sums*>(smem + C::SCAN_OFF);
 
   const RaggedArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -359,36 +364,54 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   tc::grid_dep_wait();
 
   // ------------------------------------------------------------ this CTA's share
+  // Sums over the requests: positions of the sequence, units (as far as they
+  // are fewer than the CTAs), and the longest unit.
   long long total, share, g0;
+  bool whole;                              // a unit per CTA, none of them shared
   {
     const int per = (a.n_req + C::NT - 1) / C::NT;
     const int i0 = min(a.n_req, tid * per), i1 = min(a.n_req, i0 + per);
-    auto cost = [&](const Span& s) -> long long {
-      if (s.L == 0) return 0;
-      const int nqb = (s.L + TB - 1) / TB;
-      return a.Hkv * (unit_prefix(s, PAGED, TB, nqb, nqb) + (long long)p.unit_cost * nqb);
-    };
-    long long sum = 0;
+    constexpr int MANY = 1 << 20;
+    Sums sum{0, 0, 0};
     Span sp{};                             // the thread's last request (most have one)
-    for (int b = i0; b < i1; ++b) {
+    auto count = [&](int b, Sums& s) {
       sp = request_span(a, b);
+      if (sp.L == 0) return;
+      const int nqb = (sp.L + TB - 1) / TB;
+      s.positions += a.Hkv * (unit_prefix(sp, PAGED, TB, nqb, nqb) + (long long)p.unit_cost * nqb);
+      s.units = (int)min((long long)MANY, s.units + (long long)a.Hkv * nqb);
+      s.longest = max(s.longest, unit_tiles(sp, PAGED, TB, nqb - 1));
+    };
+    for (int b = i0; b < i1; ++b) {
+      count(b, sum);
       if (sp.bad && blockIdx.x == 0) set_status(a.status, SKV_DEV_BAD_LEN);
-      sum += cost(sp);
     }
-    long long incl = sum;
+    Sums incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += t;
+      const long long t = __shfl_up_sync(0xffffffffu, incl.positions, o);
+      const int v = __shfl_up_sync(0xffffffffu, incl.units, o);
+      if (lane >= o) {
+        incl.positions += t;
+        incl.units = min(MANY, incl.units + v);
+      }
     }
+    incl.longest = __reduce_max_sync(0xffffffffu, sum.longest);
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    long long before = 0;
+    long long at = incl.positions - sum.positions;   // positions and units before this thread's requests
+    int at_unit = incl.units - sum.units, units = 0, longest = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < C::NT / 32; ++w) {
-      if (w == warp) before = total;
-      total += s_scan[w];
+      const Sums x = s_scan[w];
+      if (w == warp) {
+        at += total;
+        at_unit += units;
+      }
+      total += x.positions;
+      units = min(MANY, units + x.units);
+      longest = max(longest, x.longest);
     }
     // Equal shares, but of a few keys each they would cost more to merge than
     // to read: a tile takes about seven times as long as a piece's part of a
@@ -397,18 +420,27 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     // tiles a piece, 24 so).
     share = max((long long)p.min_share, udiv(total + gridDim.x - 1, gridDim.x));
     share = max(share, (long long)ceilf(sqrtf((float)total / p.units7)));
+    // With a CTA for every unit and the longest not much over an equal share,
+    // units stay whole: what the shares save is less than the partials cost.
+    whole = units <= (int)gridDim.x && longest + p.unit_cost <= share + p.whole_slack;
+    if (whole) {
+      share = 1;
+      total = units;
+      at = at_unit;
+    }
     g0 = blockIdx.x * share;
     if (g0 >= total) {                     // no tiles left for this CTA
       if (tid == 0) p.ws_unit[blockIdx.x] = make_int4(0, 0, 0, 0);
       if (warp == C::WARP_K) tc::tmem_dealloc(*s_tmem, 512);
       return;
     }
-    long long at = before + incl - sum;    // tiles before this thread's requests
-    if (g0 >= at && g0 < at + sum) {
+    const long long mine = whole ? sum.units : sum.positions;
+    if (g0 >= at && g0 < at + mine) {
       int b = i0;
       for (; b < i1 - 1; ++b) {
-        sp = request_span(a, b);
-        const long long c = cost(sp);
+        Sums s{0, 0, 0};
+        count(b, s);
+        const long long c = whole ? s.units : s.positions;
         if (g0 < at + c) break;
         at += c;
       }
@@ -648,7 +680,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       int nqb = (s.L + TB - 1) / TB;
       {
         long long off = *s_off;
-        if (nqb == 1) {
+        if (whole) {
+          h = (int)off / nqb;
+          qb = (int)off - h * nqb;
+          t = 0;
+        } else if (nqb == 1) {
           const int per_head = unit_tiles(s, PAGED, TB, 0) + p.unit_cost;
           h = (int)udiv(off, per_head);
           t = (int)(off - (long long)h * per_head);
@@ -684,10 +720,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         for (int pi = 0; ok; ++pi) {
           Piece pc{};
           const int nt_unit = g < g1 ? unit_tiles(s, PAGED, TB, qb) : 0;
-          const long long u0 = g - t + p.unit_cost, u1 = u0 + nt_unit;   // positions of the unit's tiles
+          // positions of the unit's tiles; a whole unit takes the one of its CTA
+          const long long u0 = whole ? g : g - t + p.unit_cost, u1 = whole ? g + 1 : u0 + nt_unit;
           if (g < g1 && u0 < g1) {
-            pc.ta = max(0, t - p.unit_cost);
-            pc.nt = (int)(min(u1, g1) - u0) - pc.ta;
+            pc.ta = whole ? 0 : max(0, t - p.unit_cost);
+            pc.nt = whole ? nt_unit : (int)(min(u1, g1) - u0) - pc.ta;
             pc.b = b;
             pc.h = h;
             pc.row0 = s.q0 + qb * TB;
@@ -990,6 +1027,7 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   const int grid = min(sm_count(), MAX_CTAS);
   p.min_share = wide ? 4 : 1;
   p.unit_cost = wide ? 2 : 1;
+  p.whole_slack = wide ? 8 : 6;
   p.units7 = 7.f * a.n_req * a.Hkv;
   p.BR = BN;
   if (paged)
