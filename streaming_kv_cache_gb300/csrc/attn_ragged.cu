@@ -226,10 +226,13 @@ __device__ __forceinline__ size_t ws_index(int slot, int i, int c, int r) {
 // order.  One CTA after the last piece would have to read all of a unit's
 // partials by itself (36 rows x 13 pieces took it 15 us); here a unit's rows
 // and columns are spread over blocks, which start as the attention's CTAs
-// leave their SMs.  Block (x, i, c) takes a part of query tile i of the unit
-// that starts in CTA c; a thread takes CU groups of 4 columns of a row, with
-// KU pieces in flight, M following as it grows: bound by one or two round
-// trips to L2.
+// leave their SMs.  Block (c, i, x) takes part x of query tile i of the unit
+// that starts in CTA c (if one does); a thread takes CU groups of 4 columns of
+// a row, with KU pieces in flight, M following as it grows: bound by one or
+// two round trips to L2 (3.3 us of a decode call's 13, launch and all).  Wide
+// units have two or three pieces: few in flight and eight blocks an SM, so
+// that the many blocks without work pass in two rounds; decode units have a
+// dozen: as many in flight as registers allow.
 constexpr int MT = 128;         // threads per block
 constexpr int MERGE_PARTS = 8;  // blocks per query tile: 128 rows x 8 threads, or 32 rows x 32
 
@@ -296,17 +299,17 @@ __device__ __forceinline__ void merge_part(const RParams& p, const int4& u, int 
 }
 
 template <int D, bool F16, int NQ>
-__global__ void __launch_bounds__(MT) merge_kernel(const RParams p) {
+__global__ void __launch_bounds__(MT, NQ == 2 ? 8 : 4) merge_kernel(const RParams p) {
   tc::grid_dep_launch();
   tc::grid_dep_wait();
-  const int c0 = blockIdx.z, i = blockIdx.y, t = blockIdx.x * MT + threadIdx.x;
+  const int c0 = blockIdx.x, i = blockIdx.y, t = blockIdx.z * MT + threadIdx.x;
   const int4 u = __ldcg(p.ws_unit + c0);
   const int rows = min(p.TQ, u.w - i * p.TQ) * p.G;
   if (u.x == 0 || rows <= 0) return;
   // few rows (decode): a thread per row and 4 columns, many pieces in flight;
   // else whole 32-byte sectors of the output a thread
-  if (rows <= MERGE_PARTS * MT / 32) merge_part<D, F16, NQ, 1, 16>(p, u, c0, i, rows, t);
-  else merge_part<D, F16, NQ, 4, 4>(p, u, c0, i, rows, t);
+  if (rows <= MERGE_PARTS * MT / 32) merge_part<D, F16, NQ, 1, NQ == 2 ? 8 : 16>(p, u, c0, i, rows, t);
+  else merge_part<D, F16, NQ, 4, NQ == 2 ? 2 : 4>(p, u, c0, i, rows, t);
 }
 
 template <int D, bool F16, int NQ, bool PAGED>
@@ -1064,7 +1067,7 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
     if (e != cudaSuccess) return e;
     e = launch_dependent(kernel, dim3(grid), threads, smem, st, tq, tk, tv, p);
     if (e != cudaSuccess) return e;
-    return launch_dependent(merge, dim3(MERGE_PARTS, wide ? 2 : 1, grid), MT, 0, st, p);
+    return launch_dependent(merge, dim3(grid, wide ? 2 : 1, MERGE_PARTS), MT, 0, st, p);
   };
 #define SKV_RAGGED(DD, FF, NN, PP, VAR) \
   launch(ragged_attn_kernel<DD, FF, NN, PP>, merge_kernel<DD, FF, NN>, RCfg<DD, NN>::ALLOC, RCfg<DD, NN>::NT, VAR)
