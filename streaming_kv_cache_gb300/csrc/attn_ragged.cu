@@ -300,7 +300,6 @@ __device__ __forceinline__ void merge_part(const RParams& p, const int4& u, int 
 
 template <int D, bool F16, int NQ>
 __global__ void __launch_bounds__(MT, NQ == 2 ? 8 : 4) merge_kernel(const RParams p) {
-  tc::grid_dep_launch();
   tc::grid_dep_wait();
   const int c0 = blockIdx.x, i = blockIdx.y, t = blockIdx.z * MT + threadIdx.x;
   const int4 u = __ldcg(p.ws_unit + c0);
@@ -363,7 +362,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if (warp == C::WARP_V) tc::prefetch_tmap(&tmap_v);
     if (warp == C::WARP_SCHED) tc::prefetch_tmap(&tmap_q);
   }
-  tc::grid_dep_launch();
   tc::grid_dep_wait();
 
   // ------------------------------------------------------------ this CTA's share

@@ -104,7 +104,6 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
     return q + (rem > 0);
   };
   const bool reporter = blockIdx.x == 0;
-  tc::grid_dep_launch();
   tc::grid_dep_wait();
 
   int head = a.state[n], count = a.state[n + 1];
@@ -259,7 +258,6 @@ __global__ void __launch_bounds__(WT) paged_write_kernel(const WriteArgs a) {
   const long long rest = item / NCH;
   const int grp = (int)(rest % groups);
   const long long tok = rest / groups;
-  tc::grid_dep_launch();
   tc::grid_dep_wait();
   if (tok >= a.n_tok) return;
   const int slot = a.slot[tok];

@@ -61,9 +61,13 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
 size_t ragged_ws_bytes();
 
 // Launch as a programmatic dependent of the kernel before it on the stream:
-// its CTAs may start while that one still ends, and wait for it
+// its CTAs may start as that one's last ones leave, and wait for it
 // (grid_dep_wait) before they read or write anything of the caller's.  They
 // read none of it through the read-only path: it may change after they start.
+// The kernels themselves give no early signal to the ones after them: CTAs that
+// start only to wait took SM slots and launch bandwidth (a plan of 2048
+// requests 15.7 us in a row of plans, 8.2 without; a decode call 13.6 and 12.9,
+// 17.1 without the dependent launch).
 template <typename... K, typename... A>
 cudaError_t launch_dependent(void (*kernel)(K...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};

@@ -204,10 +204,8 @@ __device__ __forceinline__ void setmaxnreg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Programmatic dependent launch: the next kernel on the stream may start its
-// set-up now / wait until the kernels before this one have completed and
-// their writes are visible.
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// In a programmatic dependent launch: wait until the kernels before this one
+// on the stream have completed and their writes are visible.
 __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ------------------------------------------------------ CTA pairs (clusters)
