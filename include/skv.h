@@ -393,6 +393,7 @@ int stream_attn_verify(const skv_cache* cache, int32_t n_q_head, int32_t blk,
  */
 #define SKV_BF16 0
 #define SKV_FP16 1
+#define SKV_MAX_KEYS (1 << 26) /* tokens that a request may hold or read */
 
 /*
  * k, v         device [n_page][Hkv][page_size][d]; keys rotated
@@ -454,11 +455,15 @@ typedef struct skv_paged {
  *
  * A request that needs pages when too few are left sets SKV_DEV_NO_PAGE; one
  * whose table row is too short, or whose rows end past n_tok,
- * SKV_DEV_TABLE_FULL.  It keeps its row span and its state, its slots are -1
- * and its kv_len is 0, so that the calls below skip it and its output rows
- * are zeros; those after it are planned if they can be.  A held length
- * outside [0, max_block * page_size] or a new_len below -1 sets
+ * SKV_DEV_TABLE_FULL (a row holds max_block * page_size tokens, and no request
+ * more than SKV_MAX_KEYS).  It keeps its row span and its state, its slots are
+ * -1 and its kv_len is 0, so that the calls below skip it and its output rows
+ * are zeros.  Once the free pages ran out, every later request that needs one
+ * is left out too; those that need none are planned.  A held length outside
+ * [0, max_block * page_size], or above SKV_MAX_KEYS, or a new_len below -1 sets
  * SKV_DEV_BAD_LEN: that request gets no rows, kv_len 0 and keeps its state.
+ * A page is freed once for each request that holds it: requests whose tables
+ * share pages (paged_attn reads them as they are) are not freed here.
  * n_req <= SKV_PAGED_MAX_REQUESTS, n_tok <= 2^30.
  */
 #define SKV_PAGED_MAX_REQUESTS 4096
@@ -500,16 +505,16 @@ size_t skv_attn_workspace_bytes(void);
  * lse:  device fp32 [Hq][n_tok], natural log of the sum of exp of the scaled
  *       scores, or NULL
  * A row that sees no key (kv_len 0) gets zeros and lse -inf.
- * kv_len[b] outside [n, max_block * page_size] (0 apart) or above 2^30 sets
- * SKV_DEV_BAD_LEN and counts as 0; a span outside [0, n_tok] sets it and is skipped.  A table
- * entry outside the pool sets SKV_DEV_BAD_PAGE; its keys and values count as
- * zeros.
+ * kv_len[b] outside [n, max_block * page_size] (0 apart) or above SKV_MAX_KEYS
+ * sets SKV_DEV_BAD_LEN and counts as 0; a span outside [0, n_tok] sets it and
+ * is skipped.  A table entry outside the pool sets SKV_DEV_BAD_PAGE; its keys
+ * and values count as zeros.
  * ws: workspace of ws_bytes >= skv_attn_workspace_bytes(), of any contents.
  *     Calls that may run at the same time, captured graphs among them, need
  *     workspaces of their own.
  * The call is two kernel launches: the attention, and the merge of what
  * several SMs computed of one row.
- * Needs Hq % Hkv == 0, Hq / Hkv <= 128 and n_tok * Hq < 2^31.
+ * Needs Hq % Hkv == 0, Hq / Hkv <= 128, n_tok <= 2^30 and n_tok * Hq < 2^31.
  */
 int paged_attn(const skv_paged* cache, int32_t n_q_head, int32_t n_req, int32_t n_tok,
                const void* q, int64_t q_stride, const int32_t* q_start, const int32_t* kv_len,
@@ -540,8 +545,8 @@ typedef struct skv_states {
  * cross_attn -- attention of each request's queries to all of its states (no
  * causal mask, no rotation).  q, q_start, out, lse, ws and the limits are
  * paged_attn's; q rows may be of another length than the states.  A state
- * range outside [0, n_key] sets SKV_DEV_BAD_LEN and counts as empty: zeros
- * and lse -inf, as for k_len 0.
+ * range outside [0, n_key], or of more than SKV_MAX_KEYS, sets SKV_DEV_BAD_LEN
+ * and counts as empty: zeros and lse -inf, as for k_len 0.
  */
 int cross_attn(const skv_states* states, int32_t n_q_head, int32_t n_req, int32_t n_tok,
                const void* q, int64_t q_stride, const int32_t* q_start, void* out, float* lse,

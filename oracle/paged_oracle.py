@@ -8,6 +8,7 @@ import math
 import numpy as np
 
 NO_PAGE, BAD_LEN, TABLE_FULL = 16, 32, 256
+MAX_KEYS = 1 << 26   # tokens that a request may hold
 
 
 def plan(state, new_len, table, queue, page, n_tok):
@@ -20,7 +21,7 @@ def plan(state, new_len, table, queue, page, n_tok):
     status = 0
     if not (0 <= head < n_page and 0 <= count <= n_page):
         head, count, status = 0, 0, BAD_LEN
-    room = table.shape[1] * page
+    room = min(table.shape[1] * page, MAX_KEYS)
     pages = lambda x: -(-x // page)  # noqa: E731
     q_start, kv_len, nxt, position, slot = [0], [], [], [0] * n_tok, [-1] * n_tok
     wanted, given, back, pushed = 0, 0, 0, []

@@ -50,7 +50,7 @@ int check_attn(int n_q_head, int n_kv_head, int d, int n_req, int n_tok, const v
   if (n_q_head < 1 || n_q_head % n_kv_head) return SKV_ERR_INVALID;
   if (n_q_head / n_kv_head > 128) return SKV_ERR_UNSUPPORTED;
   if (n_req < 0 || n_tok < 0) return SKV_ERR_INVALID;
-  if ((long long)n_tok * n_q_head > 0x7FFFFFFFLL) return SKV_ERR_UNSUPPORTED;
+  if (n_tok > (1 << 30) || (long long)n_tok * n_q_head > 0x7FFFFFFFLL) return SKV_ERR_UNSUPPORTED;
   if (!(sm_scale > 0.f) || isinf(sm_scale)) return SKV_ERR_INVALID;
   if (n_req == 0 || n_tok == 0) {
     *empty = true;
@@ -195,7 +195,7 @@ int cross_attn(const skv_states* states, int32_t n_q_head, int32_t n_req, int32_
   int rc = check_heads(s->n_kv_head, s->head_dim, s->dtype);
   if (rc) return rc;
   if (s->n_key < 0 || !aligned(s->status, 4)) return SKV_ERR_INVALID;
-  if (s->n_key > skv::kMaxKeys) return SKV_ERR_UNSUPPORTED;
+  if (s->n_key > (1 << 30)) return SKV_ERR_UNSUPPORTED;
   bool empty;
   rc = check_attn(n_q_head, s->n_kv_head, s->head_dim, n_req, n_tok, q, q_stride, q_start, out, lse, ws, ws_bytes,
                   sm_scale, &empty);

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
   __shared__ int warp_sum[2][PT / 32];
   const int tid = threadIdx.x;
   const uint32_t ps = (uint32_t)a.page_size;
-  const long long row_tokens = (long long)a.max_block * ps;   // what a table row holds
+  const int row_tokens = (int)min((long long)a.max_block * ps, (long long)kMaxKeys);   // what a request may hold
   // 32-bit quotients by multiply-high throughout: x and page_size are below 2^31
   auto pages = [&](int x) {
     int rem;

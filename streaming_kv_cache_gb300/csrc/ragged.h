@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "skv.h"
 
 namespace skv {
 
@@ -86,9 +87,10 @@ cudaError_t launch_dependent(void (*kernel)(K...), dim3 grid, int threads, int s
 // One request as the attention sees it: rows [q0, q0 + L) of the queries, kv
 // keys; row t sees the first kv - L + t + 1 of them (paged) or all (states).
 // Lengths out of range make it harmless: a bad span has no rows, bad keys
-// are none.  (Key indices stay below 2^30, so that those of the last tile and
-// the boxes past it do not pass 2^31.)
-constexpr int kMaxKeys = 1 << 30;
+// are none.  The limit on a request's keys keeps every index in 32 bits, and a
+// unit's stay in one CTA (half a million key tiles) under the two seconds
+// after which a wait gives up.
+constexpr int kMaxKeys = SKV_MAX_KEYS;
 struct Span {
   int q0, L, kv;
   bool bad;
@@ -103,7 +105,7 @@ __device__ __forceinline__ Span request_span(const RaggedArgs& a, int b) {
   bool kv_ok;
   if (a.k_start) {
     const int k0 = a.k_start[b];
-    kv_ok = k0 >= 0 && s.kv >= 0 && (long long)k0 + s.kv <= a.n_key;
+    kv_ok = k0 >= 0 && s.kv >= 0 && s.kv <= kMaxKeys && (long long)k0 + s.kv <= a.n_key;
   } else {
     kv_ok = s.kv == 0 || (s.kv >= s.L && s.kv <= min((long long)a.max_block * a.page_size, (long long)kMaxKeys));
   }

@@ -18,7 +18,7 @@ SKV_OK, SKV_ERR_INVALID, SKV_ERR_UNSUPPORTED, SKV_ERR_CUDA, SKV_ERR_TOO_LARGE = 
 SKV_NOALLOC_MAX_CACHE_VIEWS = 16384
 SKV_DEV_TIMEOUT, SKV_DEV_BAD_HEAD, SKV_DEV_TAIL_OVERFLOW, SKV_DEV_BAD_TAIL = 1, 2, 4, 8
 SKV_DEV_NO_PAGE, SKV_DEV_BAD_LEN, SKV_DEV_BAD_PAGE, SKV_DEV_BAD_POS, SKV_DEV_TABLE_FULL = 16, 32, 64, 128, 256
-SKV_PAGED_MAX_REQUESTS = 4096
+SKV_PAGED_MAX_REQUESTS, SKV_MAX_KEYS = 4096, 1 << 26
 _DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1}   # SKV_BF16, SKV_FP16
 
 # every function the C header declares

@@ -73,6 +73,18 @@ def test_plan_of_lengths_out_of_range(state, new):
     _run_plan(state, new, table, np.arange(8, dtype=np.int32), 16, 20)
 
 
+@pytest.mark.parametrize("state,new", [
+    ([2 ** 31 - 20, 2 ** 26 - 10, 2 ** 26, 5, 0, 2047], [32, 10, 1, 3]),
+    ([2 ** 31 - 2 ** 20, 2 ** 26 - 10, 2 ** 26 + 1, 2 ** 26, 7, 2000], [-1, 11, 0, -1])])
+def test_plan_of_rows_longer_than_a_request_may_be(state, new):
+    """Table rows of 2^31 tokens: a length above the limit, or one that would
+    pass it (and 2^31) with its new tokens, is left out."""
+    rng = np.random.default_rng(3)
+    table = rng.integers(0, 2047, (4, 2048)).astype(np.int32)
+    want, status = _run_plan(state, new, table, rng.permutation(2047).astype(np.int32), 2 ** 20, 60)
+    assert status & PO.BAD_LEN and status & PO.TABLE_FULL
+
+
 def test_plan_without_requests_or_rows():
     cache = skv.PagedCache.wrap(block_table=torch.zeros((1, 2), dtype=torch.int32, device="cuda"),
                                 page_queue=ints([0, 1]), page_size=16, state=ints([3, 0, 2]))
@@ -329,6 +341,34 @@ def test_pool_past_32_bit_offsets():
     assert cache.device_status() == 0
     o, l, mass = PO.cross(f64(q), f64(kn), f64(vn), [0, 1, 2], [0, 150], kv, d ** -0.5)
     check(f64(out), f64(lse), o, l, mass, dt, 20.0, 20.0, d ** -0.5, d, 150)
+
+
+@pytest.mark.parametrize("over", [0, 1])
+def test_longest_request(over):
+    """Equal scores over the most keys that a request may hold (one page, over
+    and over): the mean of the values; one key more is refused.  Sums of ones are
+    exact.  A CTA's share is less than a page, so its value sums stay below 3
+    times the largest running sum s of the page, and lose at most a step of
+    that per 16 keys: n / 16 2^-23 3 s over all, beside the merge's 152."""
+    page, d, dt = 2 ** 20, 64, torch.bfloat16
+    k = torch.zeros((1, 1, page, d), dtype=dt, device="cuda")
+    v = torch.randn((1, 1, page, d), device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(dt)
+    cache = skv.PagedCache.wrap(k=k, v=v, block_table=torch.zeros((1, 65), dtype=torch.int32, device="cuda"))
+    q = randn(1, (1, 2, d), dt)
+    n = skv.SKV_MAX_KEYS + over
+    out, lse = skv.paged_attn(cache, q, ints([0, 1]), ints([n]), 0.125, lse=True)
+    assert cache.device_status() == (skv.SKV_DEV_BAD_LEN if over else 0)
+    if over:
+        assert (out == 0).all() and torch.isneginf(lse).all()
+        return
+    want = v[0, 0].double().mean(0)
+    s = v[0, 0].double().cumsum(0).abs().amax(0)
+    tol = torch.finfo(dt).eps / 2 * want.abs() + 2.0 ** -27 * 4 * s
+    assert ((out.double() - want).abs() <= tol).all()
+    # log2 n = 26 times ln 2 in fp32: the constant is off by at most 2^-25 of
+    # itself, log2's result by a step of 2^-23 of itself, and the product is
+    # rounded by half a step of 18, 2^-20
+    assert (lse.double() - np.log(n)).abs().max() <= 2.0 ** -20 + np.log(n) * (2.0 ** -25 + 2.0 ** -23)
 
 
 def test_paged_results_repeat():
