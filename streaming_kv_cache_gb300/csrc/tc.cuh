@@ -160,14 +160,17 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
 }
 
 // A wait of a few instructions, for loops whose issue must stay short: sleeps
-// in try_wait, up to a millisecond a try, and ends after a count of tries,
-// about two seconds, returning false.
+// in try_wait (a try ends after 4 us at most on GB300, whatever the hint, and
+// earlier when other barriers are busy, so tries say nothing of the time) and
+// ends after 2^32 cycles, two seconds at least, returning false.
 __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b32 c;\n mov.b32 c, 2000;\n mov.b32 %0, 1;\n"
+      "{\n .reg .pred p, q;\n .reg .b64 t0, t;\n mov.b32 %0, 1;\n"
+      " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n @p bra DONE;\n"
+      " mov.u64 t0, %%clock64;\n"
       "TRY:\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n @p bra DONE;\n"
-      " sub.s32 c, c, 1;\n setp.gt.s32 q, c, 0;\n @q bra TRY;\n mov.b32 %0, 0;\n"
+      " mov.u64 t, %%clock64;\n sub.u64 t, t, t0;\n setp.lt.u64 q, t, 4294967296;\n @q bra TRY;\n mov.b32 %0, 0;\n"
       "DONE:\n}\n"
       : "=r"(ok)
       : "r"(bar), "r"(parity), "r"(kSuspendHintNs)

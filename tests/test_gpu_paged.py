@@ -343,6 +343,18 @@ def test_pool_past_32_bit_offsets():
     check(f64(out), f64(lse), o, l, mass, dt, 20.0, 20.0, d ** -0.5, d, 150)
 
 
+@pytest.mark.parametrize("n_q", [1, 100])
+def test_units_that_take_milliseconds(n_q):
+    """More units than SMs, each of 2,500 key tiles: the scheduler and a query
+    tile's warps wait a whole unit long.  All values are 1, so is the output."""
+    page, d, n, n_req, dt = 64, 64, 320000, 160, torch.bfloat16
+    k = torch.zeros((2, 1, page, d), dtype=dt, device="cuda")
+    cache = skv.PagedCache.wrap(k=k, v=torch.ones_like(k), block_table=torch.ones((n_req, n // page), dtype=torch.int32, device="cuda"))
+    q = torch.zeros((n_req * n_q, 2, d), dtype=dt, device="cuda")
+    out = skv.paged_attn(cache, q, ints(starts([n_q] * n_req)), ints([n] * n_req), 1.0)
+    assert cache.device_status() == 0 and (out == 1).all()
+
+
 @pytest.mark.parametrize("over", [0, 1])
 def test_longest_request(over):
     """Equal scores over the most keys that a request may hold (one page, over
