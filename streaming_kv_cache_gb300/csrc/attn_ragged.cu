@@ -322,6 +322,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   // rounded to the values' type relative to its own size, so it may exceed 1;
   // fp16 ends at 65504.
   constexpr float LAG_LIMIT = F16 ? 16384.0f : 1048576.0f;
+  // log2 of P at a row's maximum.  fp16 also starts at 2^-24: with P = 64 there
+  // a probability is lost below 2^-31 of the largest, so that a million keys far
+  // below one do not vanish (a tile's sum stays at 64 x 128, under the limit).
+  constexpr float P_SHIFT = F16 ? 6.0f : 0.0f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = tc::smem_u32(smem);
@@ -861,7 +865,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           };
           if (j == 0) {
             const float mx = row_max();
-            m_used = mx == -INFINITY ? 0.f : mx;
+            m_used = mx == -INFINITY ? 0.f : mx - P_SHIFT;
           }
           float ts;
           for (bool again = false;; again = true) {
@@ -875,7 +879,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               if (!ok) break;
               tc::tc_fence_after();
             }
-            const float mx = row_max();
+            const float mx = row_max() - P_SHIFT;
             const float m_new = mx > m_used ? mx : m_used;
             const float alpha = tc::ex2(m_used - m_new);
             l *= alpha;

@@ -355,6 +355,34 @@ def test_units_that_take_milliseconds(n_q):
     assert cache.device_status() == 0 and (out == 1).all()
 
 
+@pytest.mark.parametrize("n_q", [1, 100])
+def test_fp16_keys_far_below_the_largest(n_q):
+    """One key of score 0 with value 0 among 65,536 of score -26 ln 2 with value
+    1: together they are worth 2^-10 of it and must not vanish.  q = e_0 and
+    k = 0 or -26 ln 2 e_0 (its fp16 rounding, scale 1): the score is exact, and
+    its P is off by at most an absolute half step, 2^-25 of what 2^6 stands for.  (160 requests of the same pages:
+    most are one CTA's work from the first key on.)"""
+    page, d, n, n_req, dt = 64, 64, 65536 + 64, 160, torch.float16
+    low = float(torch.tensor(26 * np.log(2)).to(dt))
+    k = torch.zeros((2, 1, page, d), dtype=dt, device="cuda")
+    k[:, :, :, 0] = -low
+    k[0, 0, 0, 0] = 0.0
+    v = torch.ones_like(k)
+    v[0, 0, 0] = 0.0
+    table = torch.ones((n_req, n // page), dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    cache = skv.PagedCache.wrap(k=k, v=v, block_table=table)
+    q = torch.zeros((n_req * n_q, 2, d), dtype=dt, device="cuda")
+    q[:, :, 0] = 1.0
+    out = skv.paged_attn(cache, q, ints(starts([n_q] * n_req)), ints([n] * n_req), 1.0).view(n_req, n_q, 2, d)
+    seen = n - n_q + torch.arange(1, n_q + 1, device="cuda").double()[:, None, None]
+    p = np.exp(-low) * (seen - 1)
+    want = p / (1 + p)
+    tol = seen * 2.0 ** -31 + want * (2.0 ** -11 + 2.0 ** -20) + 2.0 ** -25
+    assert cache.device_status() == 0
+    assert ((out.double() - want).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("over", [0, 1])
 def test_longest_request(over):
     """Equal scores over the most keys that a request may hold (one page, over
