@@ -476,10 +476,11 @@ int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const in
  * rotated at the token's position (rotate-half, fp32, rounded once) and
  * stored with v at the token's slot; q is rotated likewise into q_out
  * (device [n_tok][Hq][d], contiguous; it may be q itself where q is
- * contiguous).  Without a rope table they are copied.  Tokens with a negative
+ * contiguous, and overlaps none of q, k and v otherwise).  Without a rope
+ * table they are copied.  Tokens with a negative
  * slot are skipped: nothing of theirs is read or written.  A slot outside the
  * pool sets SKV_DEV_BAD_PAGE, a position outside the table SKV_DEV_BAD_POS;
- * both skip the token.  Two tokens with one slot leave either's row there.
+ * both skip the token.  Of two tokens with one slot a mixture stays there.
  * position may be NULL with rope NULL; q and q_out may both be NULL.
  */
 int kv_paged_write(const skv_paged* cache, int32_t n_q_head, int32_t n_tok, const void* q,
@@ -501,7 +502,8 @@ size_t skv_attn_workspace_bytes(void);
  * q:    [n_tok][Hq][d], rotated (kv_paged_write's q_out); query head h reads
  *       kv head h / (Hq / Hkv)
  * out:  device [n_tok][Hq][d], contiguous: softmax(sm_scale q.k) v,
- *       accumulated in fp32, rounded once
+ *       accumulated in fp32, rounded once.  It may be q itself where q is
+ *       contiguous, and does not overlap it otherwise
  * lse:  device fp32 [Hq][n_tok], natural log of the sum of exp of the scaled
  *       scores, or NULL
  * A row that sees no key (kv_len 0) gets zeros and lse -inf.

@@ -17,6 +17,18 @@ bool tensor_ok(const void* p, int64_t stride, int64_t heads, int d) {
   return aligned(p, 16) && stride >= heads * d && (stride & 7) == 0;
 }
 
+// n rows of `row` elements, `stride` apart, and the contiguous output's n rows
+// of out_row elements share no byte
+bool apart(const void* x, int64_t stride, int64_t row, const void* out, int64_t out_row, int64_t n) {
+  const char *x0 = (const char*)x, *o0 = (const char*)out;
+  return o0 >= x0 + 2 * ((n - 1) * stride + row) || x0 >= o0 + 2 * n * out_row;
+}
+
+// the output is the input itself, row for row, or apart from it
+bool in_place_or_apart(const void* x, int64_t stride, int64_t row, const void* out, int64_t n) {
+  return (x == out && (stride == row || n == 1)) || apart(x, stride, row, out, row, n);
+}
+
 // What every paged call needs of the pool; k, v and rope belong to some calls only.
 int check_pool(const skv_paged* c) {
   if (!c) return SKV_ERR_INVALID;
@@ -57,6 +69,8 @@ int check_attn(int n_q_head, int n_kv_head, int d, int n_req, int n_tok, const v
     return SKV_OK;
   }
   if (!tensor_ok(q, q_stride, n_q_head, d) || !aligned(out, 16) || !aligned(q_start, 4)) return SKV_ERR_INVALID;
+  // a unit's rows are written once its queries have been read
+  if (!in_place_or_apart(q, q_stride, (int64_t)n_q_head * d, out, n_tok)) return SKV_ERR_INVALID;
   if (lse && !aligned(lse, 4)) return SKV_ERR_INVALID;
   const size_t need = skv::ragged_ws_bytes();
   if (ws_bytes < need || (need && !aligned(ws, 16))) return SKV_ERR_INVALID;
@@ -117,12 +131,10 @@ int kv_paged_write(const skv_paged* cache, int32_t n_q_head, int32_t n_tok, cons
   if (!aligned(slot, 4) || (cache->rope && !aligned(position, 4))) return SKV_ERR_INVALID;
   if (q) {
     if (!tensor_ok(q, q_stride, n_q_head, d) || !aligned(q_out, 16)) return SKV_ERR_INVALID;
-    // q_out is q itself (row for row) or apart from it
-    const int64_t row = (int64_t)n_q_head * d;
-    const char *q0 = (const char*)q, *o0 = (const char*)q_out;
-    const bool same = q == q_out && q_stride == row;
-    const bool apart = o0 >= q0 + 2 * ((n_tok - 1) * q_stride + row) || q0 >= o0 + 2 * n_tok * row;
-    if (!same && !apart) return SKV_ERR_INVALID;
+    const int64_t row = (int64_t)n_q_head * d, kv_row = (int64_t)cache->n_kv_head * d;
+    if (!in_place_or_apart(q, q_stride, row, q_out, n_tok) || !apart(k, k_stride, kv_row, q_out, row, n_tok) ||
+        !apart(v, v_stride, kv_row, q_out, row, n_tok))
+      return SKV_ERR_INVALID;
   }
   if ((rc = skv::check_device())) return rc;
   skv::WriteArgs a{};

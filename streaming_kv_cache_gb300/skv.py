@@ -676,10 +676,14 @@ def _attn_args(q, n_req, q_start, out, lse, ws, dev):
         lse = torch.empty((hq, n), dtype=torch.float32, device=q.device)
     elif isinstance(lse, torch.Tensor):
         _on(lse, (hq, n), torch.float32, "lse", dev)
+    elif lse is not None and lse is not False:
+        raise TypeError("lse must be a torch.Tensor, a bool or None")
     else:
         lse = None
     if ws is None:
         ws = attn_workspace(q.device)
+    elif not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a torch.Tensor")
     else:
         _on(ws, (ws.numel(),), torch.uint8, "ws", dev)
     return out, lse, ws
@@ -711,15 +715,17 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch
     """Attention of packed queries to each request's packed states k, v
     [tokens][Hkv][d]: request b reads rows [k_start[b], k_start[b] + k_len[b]).
     status collects device status bits.  Returns out (and lse when asked for)."""
+    dev = _call_device(k, "k")
     if k.dim() != 3 or k.dtype not in _DTYPE_CODE:
         raise ValueError("k must be a bfloat16 or float16 tensor (tokens, kv heads, d), got %s %s" % (k.dtype, tuple(k.shape)))
-    dev = _call_device(k, "k")
     dt, d = k.dtype, k.shape[2]
     n_key, hkv, ks = _rows(k, None, d, dt, "k", dev)
     nv, _, vs = _rows(v, hkv, d, dt, "v", dev)
     if nv != n_key:
         raise ValueError("k has %d tokens, v %d" % (n_key, nv))
     n, hq, qs = _rows(q, None, d, dt, "q", dev)
+    if not isinstance(k_start, torch.Tensor):
+        raise TypeError("k_start must be a torch.Tensor")
     n_req = k_start.numel()
     _on(k_start, (n_req,), torch.int32, "k_start", dev)
     _on(k_len, (n_req,), torch.int32, "k_len", dev)

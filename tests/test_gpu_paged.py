@@ -565,6 +565,83 @@ def test_serving_steps_from_a_graph():
     _serve("bf16", 2, 15, graph=True)
 
 
+@pytest.mark.parametrize("ql", [[1, 1, 1], [1, 150, 60]])
+def test_attention_in_place_of_its_queries(ql):
+    d, dt, kv = 128, torch.bfloat16, [9000, 400, 61]
+    pg = Pages(8, kv, 16, 2, d, dt)
+    cache = pg.cache(skv)
+    q = randn(9, (sum(ql), 12, d), dt)
+    args = (ints(starts(ql)), ints(kv), 0.09)
+    want = skv.paged_attn(cache, q, *args)
+    for _ in range(5):
+        got = q.clone()
+        assert skv.paged_attn(cache, got, *args, out=got) is got
+        assert torch.equal(got, want)
+
+
+def test_requests_that_share_pages():
+    """Two requests over the same first pages, each with a page of its own
+    after them, and a third that is the first one's prefix."""
+    d, dt, page = 64, torch.float16, 32
+    pg = Pages(8, [300, 310, 40], page, 2, d, dt)
+    pg.table[1, :8] = pg.table[0, :8]
+    pg.table[2, :2] = pg.table[0, :2]
+    cache, ql, kv = pg.cache(skv), [3, 1, 40], [300, 310, 40]
+    q = randn(9, (44, 6, d), dt)
+    out, lse = skv.paged_attn(cache, q, ints(starts(ql)), ints(kv), 0.1, lse=True)
+    want, wlse, mass = PO.paged(f64(q), f64(pg.k), f64(pg.v), pg.table, starts(ql), kv, 0.1)
+    check(f64(out), f64(lse), want, wlse, mass, dt, 14.0, 14.0, 0.1, d, 310)
+
+
+def test_captured_on_a_forked_stream():
+    """In one graph: a plan and a write on the captured stream, attention of two
+    caches on streams that fork from it after a copy and join again."""
+    d, dt, page, n_req = 64, torch.bfloat16, 16, 3
+    caches = [skv.PagedCache(40, page, 2, d, n_req, 8, theta=1e4) for _ in range(2)]
+    x, new_len = randn(1, (3 * 20, 8, d), dt), ints([20, 20, 20])
+    q, plans, outs, spaces = torch.empty((60, 4, d), dtype=dt, device="cuda"), [], [], []
+    for _ in range(2):
+        plans.append(skv.PagedPlan.empty(n_req, 60))
+        outs.append(torch.zeros((60, 4, d), dtype=dt, device="cuda"))
+        spaces.append(skv.attn_workspace())
+    rot = [torch.empty_like(q) for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def one(i):
+        c, p = caches[i], plans[i]
+        skv.kv_paged_write(c, q, x[:, 4:6], x[:, 6:], p.position, p.slot, q_out=rot[i])
+        skv.paged_attn(c, rot[i], p.q_start, p.kv_len, 0.125, out=outs[i], ws=spaces[i])
+
+    def both():
+        for c, p in zip(caches, plans):
+            skv.kv_paged_plan(c, new_len, 60, plan=p)
+        q.copy_(x[:, :4])
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            one(1)
+        one(0)
+        main.wait_stream(side)
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for seed in (5, 6):
+        x.copy_(randn(seed, x.shape, dt))
+        both()
+        torch.cuda.synchronize()
+        want = [o.clone() for o in outs]
+        assert torch.equal(*want) and want[0].abs().sum() > 0
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[0])
+    assert all(c.device_status() == 0 for c in caches)
+
+
 def test_two_streams_with_their_own_workspaces():
     d, dt = 128, torch.bfloat16
     kv, ql = [4000, 900, 128], [1, 40, 1]

@@ -209,6 +209,31 @@ def test_bad_attention_arguments(L, bad):
     assert _cross(L, **bad) == skv.SKV_ERR_INVALID
 
 
+def test_outputs_that_overlap_inputs(L):
+    row = 5 * 256 * 2                                                   # bytes of q, and of out
+    for call, q in ((_attn, FAKE * 5), (_cross, FAKE * 6)):
+        for out in (q + 512, q + row - 16, q - 16, q - row + 16):
+            assert call(L, out=out) == skv.SKV_ERR_INVALID, out
+        assert call(L, out=q, qs=264) == skv.SKV_ERR_INVALID            # q itself, but not contiguous
+    kv = 5 * 128 * 2
+    for what in (dict(k=FAKE * 6), dict(v=FAKE * 7)):
+        x, = what.values()
+        for out in (x, x + kv - 16, x - row + 16):
+            assert _write(L, q_out=out, **what) == skv.SKV_ERR_INVALID, (what, out)
+
+
+@no_gpu_here
+def test_outputs_in_place_or_apart(L):
+    row = 5 * 256 * 2
+    for call, q in ((_attn, FAKE * 5), (_cross, FAKE * 6)):
+        for out in (q, q + row, q - row):
+            assert call(L, out=out) in NO_GPU, out
+        assert call(L, out=q, n_tok=1, qs=768) in NO_GPU                # one token has no stride
+    assert _write(L, q_out=FAKE * 5, n=1, qs=768) in NO_GPU
+    # parts of one projection, its queries rotated to another place
+    assert _write(L, q=FAKE * 5, qs=512, k=FAKE * 5 + 512, ks=512, v=FAKE * 5 + 768, vs=512) in NO_GPU
+
+
 def test_attention_limits(L):
     for call in (_attn, _cross):
         assert call(L, hq=258, qs=258 * 64) == skv.SKV_ERR_UNSUPPORTED     # 129 query heads per kv head
@@ -277,3 +302,5 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu(L):
         skv.cross_attn(x, x, x, torch.zeros(2, dtype=torch.int32), one, one, 1.0, status=one)
     with pytest.raises(ValueError):
         skv.PagedCache.wrap(block_table=t)
+    with pytest.raises(TypeError):
+        skv.cross_attn(x, [x], x, one, one, one, 1.0, status=one)
