@@ -539,6 +539,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       for (int j = max(0, n - nst); j < n; ++j) wait(full + j % nst, j / nst);
     } else if (warp == C::WARP_MMA) {
       // --------------------------------------------------------- MMA issuer
+      // all lanes go on or none: they meet again at the next warp-wide step
+      auto wait_all = [&](int b, uint32_t phase) { return (bool)__all_sync(0xffffffffu, wait(b, phase)); };
       constexpr uint32_t idesc_qk = F16 ? tc::idesc_f16(BM, BN) : tc::idesc_bf16(BM, BN);
       constexpr uint32_t idesc_pv = (F16 ? tc::idesc_f16(BM, D) : tc::idesc_bf16(BM, D)) | (1u << 16);
       const uint64_t dq0 = tc::sdesc_sw128(sbase + C::Q_OFF);
@@ -578,11 +580,11 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       bool last = false;                            // it is its piece's last
       // P V of query tile i of the tile before, from score buffer x
       auto pv = [&](int i, int x, uint32_t& pph, uint32_t& oph) {
-        ok = wait(B::PFULL + x, pph);
+        ok = wait_all(B::PFULL + x, pph);
         pph ^= 1;
         if (fresh) {
           // the piece before has been read out of O
-          ok = wait(B::OFREE + i, oph) && ok;
+          ok = wait_all(B::OFREE + i, oph) && ok;
           oph ^= 1;
         }
         if (!ok) return;
@@ -594,7 +596,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
       };
       auto pv_prev1 = [&]() {                       // NQ = 1: the P V before, from the other score buffer
-        ok = wait(B::VFULL + vs, vph);
+        ok = wait_all(B::VFULL + vs, vph);
         if (!ok) return;
         if (buf) pv(0, 0, pph0, oph0);
         else pv(0, 1, pph1, oph0);
@@ -608,7 +610,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       };
       for (int pi = 0; ok; ++pi) {
         const int slot = pi % NP;
-        if (!(ok = wait(B::PCFULL + slot, pi / NP))) break;
+        if (!(ok = wait_all(B::PCFULL + slot, pi / NP))) break;
         const int nt = s_piece[slot].nt;
         const bool two = NQ == 2 && s_piece[slot].ntok > p.TQ;
         __syncwarp();
@@ -620,8 +622,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             // the tiles are waited for first, under the MMAs still in the
             // pipe: from the probabilities' arrival on, P V and Q K^T go out
             // back to back
-            if (prev) ok = wait(B::VFULL + vs, vph);
-            if (nt) ok = wait(B::KFULL + ks, kph) && ok;
+            if (prev) ok = wait_all(B::VFULL + vs, vph);
+            if (nt) ok = wait_all(B::KFULL + ks, kph) && ok;
             if (!ok) break;
             if (prev) pv(0, 0, pph0, oph0);
             if (!ok) break;
@@ -632,10 +634,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
           if (nt) {
             if (j == 0) {
-              if (!(ok = wait(B::QFULL, qph))) break;
+              if (!(ok = wait_all(B::QFULL, qph))) break;
               qph ^= 1;
             }
-            if (NQ == 1 && !(ok = wait(B::KFULL + ks, kph))) break;
+            if (NQ == 1 && !(ok = wait_all(B::KFULL + ks, kph))) break;
             const int x = NQ == 2 ? 0 : buf;
             if (lead) {
               issue_qk(0, ks, x);
@@ -675,7 +677,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // every MMA issued completes before TMEM is released
         tc::mma_commit(bar(B::DRAIN));
       }
-      wait(B::DRAIN, 0);
+      wait_all(B::DRAIN, 0);
     } else if (warp == C::WARP_SCHED) {
       // ---------------------------------------------------------- scheduler
       // A unit takes unit_cost + its tiles positions of the sequence, the tiles
