@@ -22,9 +22,15 @@
 //
 // Two forms.  NQ = 2, for calls with more than TQ tokens per request: two
 // query tiles share every key tile, and one tile's softmax runs under the
-// other's MMAs (compute-bound).  NQ = 1, for decode: one query tile, two
-// score buffers, so that Q K^T of the next key tile runs under the softmax
-// (bound by streaming K and V from HBM; most MMA rows are idle).
+// other's MMAs.  At d = 128 it is bound by the tensor pipe and the waits of the
+// warp that feeds it (four chunks of 2,048 tokens over 6 to 13 k keys, 32 query
+// and 8 kv heads: 0.88 ms, 1430 TFLOP/s); at d = 64, with half the MMA work per
+// score, by the chain from scores over probabilities to the next scores, 2540
+// cycles a key tile for 1060 of MMAs (six requests of 1,536 tokens over up to
+// 12,800 states: 202 us, 940 TFLOP/s).  NQ = 1, for decode: one query tile, two
+// score buffers, so that Q K^T of the next key tile runs under the softmax.  It
+// is bound by streaming K and V from HBM (64 requests of 0.4 to 8 k keys: 175
+// us, 6.3 TB/s); most MMA rows are idle.
 //
 //   warps 0 .. 4 NQ - 1  softmax and epilogue: a warpgroup per query tile, a
 //                        thread per row
@@ -114,8 +120,7 @@ struct RParams {
   RaggedArgs a;
   int G, TQ, TB;          // query heads per kv head, tokens per query tile and per unit
   int BR, boxes;          // rows per TMA box, boxes per key tile
-  int min_share;          // sequence positions per CTA at least
-  int whole_slack;        // positions that the longest unit may have over an equal share to keep units whole
+  int whole_slack;        // positions that the longest unit may have over an equal share to keep units whole: what the partials and their merge take
   float units7;           // seven times the units at least
   int unit_cost;          // positions that a unit takes before its tiles, for what it costs beside them
   float scale_log2;
@@ -229,7 +234,7 @@ __device__ __forceinline__ size_t ws_index(int slot, int i, int c, int r) {
 // leave their SMs.  Block (c, i, x) takes part x of query tile i of the unit
 // that starts in CTA c (if one does); a thread takes CU groups of 4 columns of
 // a row, with KU pieces in flight, M following as it grows: bound by one or
-// two round trips to L2 (3.3 us of a decode call's 13, launch and all).  Wide
+// two round trips to L2 (2.6 us of a decode call's 13, launch and all).  Wide
 // units have two or three pieces: few in flight and eight blocks an SM, so
 // that the many blocks without work pass in two rounds; decode units have a
 // dozen: as many in flight as registers allow.
@@ -421,12 +426,14 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     // Equal shares, but of a few keys each they would cost more to merge than
     // to read: a tile takes about seven times as long as a piece's part of a
     // merge, so with T tiles per unit the sum of both is least at sqrt(T / 7)
-    // tiles a piece (one request of 30,000 keys and one kv head: 50 us at two
-    // tiles a piece, 24 so).
-    share = max((long long)p.min_share, udiv(total + gridDim.x - 1, gridDim.x));
+    // tiles a piece (decode of one request of 30,000 keys and one kv head:
+    // 22.6 us at equal shares of two tiles, 19.4 so).
+    share = max(1LL, udiv(total + gridDim.x - 1, gridDim.x));
     share = max(share, (long long)ceilf(sqrtf((float)total / p.units7)));
     // With a CTA for every unit and the longest not much over an equal share,
-    // units stay whole: what the shares save is less than the partials cost.
+    // units stay whole: what the shares save is less than the partials cost (16
+    // requests of 20 tokens and 4 k keys, 8 kv heads: 51.4 us whole, 56.3 in
+    // shares; single tokens over 2 k keys: 32.1 and 32.5).
     whole = units <= (int)gridDim.x && longest + p.unit_cost <= share + p.whole_slack;
     if (whole) {
       share = 1;
@@ -1027,12 +1034,17 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   p.G = a.Hq / a.Hkv;
   p.TQ = BM / p.G;
   const bool paged = a.k_start == nullptr;
-  // more tokens than one query tile per request holds, on average: two tiles
-  // per unit (a request that needs one leaves the second idle)
+  // More tokens than one query tile per request holds, on average: two tiles
+  // per unit (a request that needs one leaves the second idle).  d = 128, 32
+  // query and 8 kv heads, 4 k keys: one chunk of 512 tokens 44 us wide, 54
+  // narrow; four of 100, 44 and 49; 16 of 20, 57 and 51; d = 64, six requests of
+  // long encodings, 202 and 333.
   const bool wide = a.n_tok > (long long)a.n_req * p.TQ;
   p.TB = (wide ? 2 : 1) * p.TQ;
   const int grid = min(sm_count(), MAX_CTAS);
-  p.min_share = wide ? 4 : 1;
+  // what a piece's queries, first scores and epilogue take, in key tiles (0
+  // instead: 68 us against 62 in a mixed batch of chunks at d = 64, 14.2
+  // against 13.0 in decode of one request)
   p.unit_cost = wide ? 2 : 1;
   p.whole_slack = wide ? 8 : 6;
   p.units7 = 7.f * a.n_req * a.Hkv;
