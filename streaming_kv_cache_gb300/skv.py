@@ -429,7 +429,7 @@ def _call_device(t, name):
         raise TypeError("%s must be a torch.Tensor" % name)
     if not t.is_cuda:
         raise ValueError("%s must be on a CUDA device" % name)
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()   # torch.cuda.current_device() once CUDA is up, as t shows
     _on_dev(t.get_device(), name, dev)
     return dev
 
