@@ -19,6 +19,7 @@ SKV_NOALLOC_MAX_CACHE_VIEWS = 16384
 SKV_DEV_TIMEOUT, SKV_DEV_BAD_HEAD, SKV_DEV_TAIL_OVERFLOW, SKV_DEV_BAD_TAIL = 1, 2, 4, 8
 SKV_DEV_NO_PAGE, SKV_DEV_BAD_LEN, SKV_DEV_BAD_PAGE, SKV_DEV_BAD_POS, SKV_DEV_TABLE_FULL = 16, 32, 64, 128, 256
 SKV_PAGED_MAX_REQUESTS, SKV_MAX_KEYS = 4096, 1 << 26
+_Tensor = torch.Tensor                                 # looked up several times a call
 _DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1}   # SKV_BF16, SKV_FP16
 
 # every function the C header declares
@@ -412,7 +413,7 @@ def _on(t, shape, dtype, name, dev):
     """_need, and the tensor lives on device dev, where the call launches.
     A decode step makes many small calls, so what a good tensor has to pass
     is one short expression."""
-    if not (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev
+    if not (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.get_device() == dev
             and t.is_contiguous()):
         _need(t, shape, dtype, name)
         _on_dev(t.get_device(), name, dev)
@@ -443,22 +444,23 @@ def _rows(t, heads, d, dtype, name, dev):
     """(tokens, heads, token stride) of a token-major tensor [tokens][heads][d]
     whose heads of a token are adjacent (a part of a wider projection's rows,
     say); heads None: any number."""
-    if not isinstance(t, torch.Tensor):
+    if type(t) is not _Tensor and not isinstance(t, _Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads):
-        raise ValueError("%s must have shape (tokens, %s, %d), got %s" % (name, "heads" if heads is None else heads, d, tuple(shape)))
+    stride = t.stride()
+    if len(stride) == 3:
+        n, h, width = t.shape
+    if len(stride) != 3 or width != d or (heads is not None and h != heads):
+        raise ValueError("%s must have shape (tokens, %s, %d), got %s" % (name, "heads" if heads is None else heads, d, tuple(t.shape)))
     if t.get_device() != dev:
         if not t.is_cuda:
             raise ValueError("%s must be on a CUDA device" % name)
         _on_dev(t.get_device(), name, dev)
-    n, heads, _ = shape
-    s0, s1, s2 = t.stride()
-    if n and (s2 != 1 or (s1 != d and heads > 1)):
+    s0, s1, s2 = stride
+    if n and (s2 != 1 or (s1 != d and h > 1)):
         raise ValueError("%s must have its heads adjacent within a token" % name)
-    return n, heads, s0 if n > 1 else heads * d
+    return n, h, s0 if n > 1 else h * d
 
 
 class PagedPlan:
