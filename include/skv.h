@@ -451,7 +451,9 @@ typedef struct skv_paged {
  *                   request, and page * page_size + row of its place in the
  *                   pool; 0 and -1 in padding rows
  * Integer results, the same on every run.  The call reads nothing that it
- * writes, so it may be repeated on the same state.
+ * writes, so it may be repeated on the same state.  What it writes (the queue,
+ * the table and the status word among it) overlaps neither its other outputs
+ * nor state and new_len: refused with SKV_ERR_INVALID.
  *
  * A request that needs pages when too few are left sets SKV_DEV_NO_PAGE; one
  * whose table row is too short, or whose rows end past n_tok,

@@ -29,6 +29,16 @@ bool in_place_or_apart(const void* x, int64_t stride, int64_t row, const void* o
   return (x == out && (stride == row || n == 1)) || apart(x, stride, row, out, row, n);
 }
 
+// n words of 32 bits
+struct Range {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Range& a, const Range& b) {
+  const char *a0 = (const char*)a.p, *b0 = (const char*)b.p;
+  return a.n && b.n && a0 < b0 + 4 * b.n && b0 < a0 + 4 * a.n;
+}
+
 // What every paged call needs of the pool; k, v and rope belong to some calls only.
 int check_pool(const skv_paged* c) {
   if (!c) return SKV_ERR_INVALID;
@@ -92,8 +102,15 @@ int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const in
     return SKV_ERR_INVALID;
   if (n_req && (!aligned(new_len, 4) || !aligned(kv_len, 4))) return SKV_ERR_INVALID;
   if (n_tok && (!aligned(position, 4) || !aligned(slot, 4))) return SKV_ERR_INVALID;
-  // the call reads state while it writes next_state: they may not overlap
-  if (state < next_state + n_req + 2 && next_state < state + n_req + 2) return SKV_ERR_INVALID;
+  // every CTA reads the lengths, the queue and the table while others write
+  // already, so what is written shares no byte with anything else
+  const size_t req = (size_t)n_req, tok = (size_t)n_tok;
+  const Range used[] = {{state, req + 2}, {new_len, req}, {queue, (size_t)cache->n_page},
+                        {cache->block_table, req * (size_t)cache->max_block}, {q_start, req + 1}, {kv_len, req},
+                        {next_state, req + 2}, {position, tok}, {slot, tok}, {cache->status, 1}};
+  for (int i = 2; i < 10; ++i)                     // the first two are only read
+    for (int j = 0; j < i; ++j)
+      if (overlap(used[i], used[j])) return SKV_ERR_INVALID;
   if ((rc = skv::check_device())) return rc;
   skv::PlanArgs a{};
   a.n_req = n_req;
