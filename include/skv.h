@@ -483,7 +483,9 @@ int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const in
  * slot are skipped: nothing of theirs is read or written.  A slot outside the
  * pool sets SKV_DEV_BAD_PAGE, a position outside the table SKV_DEV_BAD_POS;
  * both skip the token.  Of two tokens with one slot a mixture stays there.
- * position may be NULL with rope NULL; q and q_out may both be NULL.
+ * position may be NULL with rope NULL; q and q_out may both be NULL.  The two
+ * pools are apart, and q_out is apart from them, position and slot; the call
+ * does not look for overlaps there.
  */
 int kv_paged_write(const skv_paged* cache, int32_t n_q_head, int32_t n_tok, const void* q,
                    int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -516,6 +518,9 @@ size_t skv_attn_workspace_bytes(void);
  * ws: workspace of ws_bytes >= skv_attn_workspace_bytes(), of any contents.
  *     Calls that may run at the same time, captured graphs among them, need
  *     workspaces of their own.
+ * out, lse and ws are apart from one another and from everything that the
+ * call reads (but for out in place of q); only out over q is looked for and
+ * refused.
  * The call is two kernel launches: the attention, and the merge of what
  * several SMs computed of one row.
  * Needs Hq % Hkv == 0, Hq / Hkv <= 128, n_tok <= 2^30 and n_tok * Hq < 2^31.

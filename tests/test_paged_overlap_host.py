@@ -1,5 +1,4 @@
-"""Host-side refusals of buffers of the paged and cross calls that overlap,
-without a GPU."""
+"""Host-side refusals of buffers of a paged plan that overlap, without a GPU."""
 import ctypes
 import itertools
 
