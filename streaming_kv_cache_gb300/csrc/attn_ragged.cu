@@ -1052,7 +1052,7 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   if (paged)
     while (a.page_size % p.BR) p.BR /= 2;
   p.boxes = BN / p.BR;
-  p.scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.scale_log2 = a.sm_scale * kLog2e;
   char* ws = static_cast<char*>(a.ws);
   p.ws_unit = reinterpret_cast<int4*>(ws);
   p.ws_ml = reinterpret_cast<float*>(ws + WS_HEAD);

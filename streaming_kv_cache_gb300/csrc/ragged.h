@@ -58,6 +58,7 @@ struct RaggedArgs {
   int32_t* status;
   float sm_scale;
 };
+constexpr float kLog2e = 1.4426950408889634f;   // the softmax works to base two: its scale times this
 cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_t st);
 size_t ragged_ws_bytes();
 
