@@ -738,6 +738,25 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
         }
       }
+      // The next request after b that has rows, 16 spans at a time: a cache
+      // may have hundreds of idle slots between two requests (one by one 70 ns
+      // each).
+      auto next_request = [&](int& b) {
+        Span s{0, 0, 0, false};
+        while (s.L == 0 && b < a.n_req - 1) {
+          constexpr int AHEAD = 16;
+          int at[AHEAD + 1];                // ends of request b and of the ones after it
+#pragma unroll
+          for (int x = 0; x <= AHEAD; ++x) at[x] = a.q_start[min(b + 1 + x, a.n_req)];
+          int x = 0;                        // first that does not end where the one before it does
+#pragma unroll
+          for (int y = AHEAD; y > 0; --y)
+            if (at[y] != at[y - 1]) x = y;
+          b = min(b + (x ? x : AHEAD), a.n_req - 1);
+          if (x) s = request_span(a, b);
+        }
+        return s;
+      };
       if (lane == 0) {
         long long g = g0;
         bool ok = true;
@@ -770,9 +789,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
               qb = 0;
               if (++h == a.Hkv) {
                 h = 0;
-                do s = request_span(a, ++b < a.n_req ? b : a.n_req - 1);
-                while (s.L == 0 && b < a.n_req - 1);
-                nqb = (s.L + TB - 1) / TB;
+                if (g < g1) {               // the share goes on: some later request has rows
+                  s = next_request(b);
+                  nqb = (s.L + TB - 1) / TB;
+                }
               }
             }
           }
