@@ -121,7 +121,6 @@ struct RParams {
   int G, TQ, TB;          // query heads per kv head, tokens per query tile and per unit
   int BR, boxes;          // rows per TMA box, boxes per key tile
   int whole_slack;        // positions that the longest unit may have over an equal share to keep units whole: what the partials and their merge take
-  float heads7;           // seven times the kv heads
   int unit_cost;          // positions that a unit takes before its tiles, for what it costs beside them
   float scale_log2;
   int4* ws_unit;          // [CTAs] the shared unit that starts in a CTA: pieces (0: none), first token row, kv head, tokens
@@ -341,16 +340,10 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   Piece* s_piece = reinterpret_cast<Piece*>(smem + C::PIECE_OFF);
   struct Sums {
     long long positions;
-    int units, longest, requests;
+    int units, longest;
   };
-  // a warp's sums: requests (up to 4095 of them) above the 20 bits of longest
-  struct WarpSums {
-    long long positions;
-    int units;
-    uint32_t longest_requests;
-  };
-  static_assert(sizeof(WarpSums) == 16 && kMaxKeys / BN < (1 << 20), "sums of a warp");
-  WarpSums* s_scan = reinterpret_cast<WarpSums*>(smem + C::SCAN_OFF);
+  static_assert(sizeof(Sums) == 16, "sums of a warp");
+  Sums* s_scan = reinterpret_cast<Sums*>(smem + C::SCAN_OFF);
 
   const RaggedArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -382,15 +375,14 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 
   // ------------------------------------------------------------ this CTA's share
   // Sums over the requests: positions of the sequence, units (as far as they
-  // are fewer than the CTAs), the longest unit, and the requests that have
-  // rows (a cache's slots may be idle).
+  // are fewer than a million), and the longest unit.
   long long total, share, g0;
   bool whole;                              // a unit per CTA, none of them shared
   {
     const int per = (a.n_req + C::NT - 1) / C::NT;
     const int i0 = min(a.n_req, tid * per), i1 = min(a.n_req, i0 + per);
     constexpr int MANY = 1 << 20;
-    Sums sum{0, 0, 0, 0};
+    Sums sum{0, 0, 0};
     Span sp{};                             // the thread's last request (most have one)
     auto count = [&](int b, Sums& s) {
       sp = request_span(a, b);
@@ -399,7 +391,6 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       s.positions += a.Hkv * (unit_prefix(sp, PAGED, TB, nqb, nqb) + (long long)p.unit_cost * nqb);
       s.units = (int)min((long long)MANY, s.units + (long long)a.Hkv * nqb);
       s.longest = max(s.longest, unit_tiles(sp, PAGED, TB, nqb - 1));
-      ++s.requests;
     };
     for (int b = i0; b < i1; ++b) {
       count(b, sum);
@@ -416,32 +407,30 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
     }
     incl.longest = __reduce_max_sync(0xffffffffu, sum.longest);
-    incl.requests = __reduce_add_sync(0xffffffffu, sum.requests);
-    if (lane == 31)
-      s_scan[warp] = {incl.positions, incl.units, (uint32_t)incl.longest | (uint32_t)min(incl.requests, 4095) << 20};
+    if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
     long long at = incl.positions - sum.positions;   // positions and units before this thread's requests
-    int at_unit = incl.units - sum.units, units = 0, longest = 0, requests = 0;
+    int at_unit = incl.units - sum.units, units = 0, longest = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < C::NT / 32; ++w) {
-      const WarpSums x = s_scan[w];
+      const Sums x = s_scan[w];
       if (w == warp) {
         at += total;
         at_unit += units;
       }
       total += x.positions;
       units = min(MANY, units + x.units);
-      longest = max(longest, (int)(x.longest_requests & 0xFFFFF));
-      requests += (int)(x.longest_requests >> 20);
+      longest = max(longest, x.longest);
     }
     // Equal shares, but of a few keys each they would cost more to merge than
     // to read: a tile takes about seven times as long as a piece's part of a
-    // merge, so with T tiles per request and kv head the sum of both is least at
-    // sqrt(T / 7) tiles a piece (decode of one request of 30,000 keys and one kv
-    // head: 22.6 us at equal shares of two tiles, 19.4 so).
+    // merge, so with T tiles per unit the sum of both is least at sqrt(T / 7)
+    // tiles a piece (decode of one request of 30,000 keys and one kv head:
+    // 22.6 us at equal shares of two tiles, 19.4 so).  With more units than the
+    // sums count, equal shares are the longer ones anyway.
     share = max(1LL, udiv(total + gridDim.x - 1, gridDim.x));
-    share = max(share, (long long)ceilf(sqrtf((float)total / (p.heads7 * max(requests, 1)))));
+    share = max(share, (long long)ceilf(sqrtf((float)total / (7.f * max(units, 1)))));
     // With a CTA for every unit and the longest not much over an equal share,
     // units stay whole: what the shares save is less than the partials cost (16
     // requests of 20 tokens and 4 k keys, 8 kv heads: 51.4 us whole, 56.3 in
@@ -462,7 +451,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if (g0 >= at && g0 < at + mine) {
       int b = i0;
       for (; b < i1 - 1; ++b) {
-        Sums s{0, 0, 0, 0};
+        Sums s{0, 0, 0};
         count(b, s);
         const long long c = whole ? s.units : s.positions;
         if (g0 < at + c) break;
@@ -1079,7 +1068,6 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   // against 13.0 in decode of one request)
   p.unit_cost = wide ? 2 : 1;
   p.whole_slack = wide ? 8 : 6;
-  p.heads7 = 7.f * a.Hkv;
   p.BR = BN;
   if (paged)
     while (a.page_size % p.BR) p.BR /= 2;
