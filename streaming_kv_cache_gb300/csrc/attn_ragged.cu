@@ -81,6 +81,16 @@ struct RCfg {
   // what the first rounding left as a second term: the output's own rounding
   // is all there is.
   static constexpr int P_TERMS = NQ == 1 ? 2 : 1;
+  // Key tiles that one accumulation in tensor memory takes.  The tensor cores
+  // cut the low bits of every sum off, so a long sum of values of one sign
+  // drifts towards zero, by about 2^-24 of itself per MMA of 16 keys: the mean
+  // of positive values over 320,000 keys in one CTA was 1.1e-3 too small, over 4
+  // million 1.8e-2.  Longer runs are cut into parts of 32,768 keys, a drift of a
+  // quarter of fp16's half step, whose sums are added in fp32 arithmetic that
+  // rounds to nearest.  An addition takes some
+  // 4 us of a part's 300 to 400 (152 requests of 65,536 keys in L2 563 -> 572
+  // us, 16 of 131,072 from HBM 1183 -> 1192); twice as many parts twice that.
+  static constexpr int FOLD = 256;
   static constexpr int QT = BM * D * 2;        // bytes of a query tile
   static constexpr int KT = BN * D * 2;        // of a key or value tile
   static constexpr int HALF = BM * 128;        // one 64-dimension half of either
@@ -128,7 +138,7 @@ struct RParams {
   float* ws_o;            // [2 * CTAs][NQ][D / 4][BM][4], see ws_index
 };
 
-// One piece of a CTA's share: key tiles [ta, ta + nt) of a unit.
+// One piece of a CTA's share, or a part of one: key tiles [ta, ta + nt) of a unit.
 struct Piece {
   int nt;          // 0: no more pieces
   int ta;
@@ -139,9 +149,11 @@ struct Piece {
   int pos0;        // keys that the unit's first token sees, less one
   int step;        // 1: each later token sees one more (causal), 0: all see the same
   int krow;        // first state of the request (cross attention)
-  int slot;        // workspace slot of its partials, -1: the piece is the whole unit
+  int sums;        // 4 times the workspace slot of its sums, | ADDS | LEAVES
 };
 static_assert(sizeof(Piece) <= 64, "piece slot");
+constexpr int ADDS = 1;     // a part that adds the sums of the one before to its own
+constexpr int LEAVES = 2;   // it leaves its sums in the workspace: more parts or other CTAs' pieces of the unit follow
 
 // sum over i < n of floor((a i + b) / BN), by the Euclid-like reduction of
 // counting lattice points under a line: O(log) steps.  a n + b < 2^32.
@@ -750,6 +762,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         long long g = g0;
         bool ok = true;
         int4 shared_unit = make_int4(0, 0, 0, 0);   // the unit that starts here and goes on in the next CTA
+        int part = 0;                     // ADDS: the next piece is a part that goes on
         int loaded = 0;                   // pieces whose queries are on their way
         for (int pi = 0; ok; ++pi) {
           Piece pc{};
@@ -757,8 +770,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           // positions of the unit's tiles; a whole unit takes the one of its CTA
           const long long u0 = whole ? g : g - t + p.unit_cost, u1 = whole ? g + 1 : u0 + nt_unit;
           if (g < g1 && u0 < g1) {
-            pc.ta = whole ? 0 : max(0, t - p.unit_cost);
-            pc.nt = whole ? nt_unit : (int)(min(u1, g1) - u0) - pc.ta;
+            pc.ta = whole ? t : max(0, t - p.unit_cost);
+            pc.nt = (whole ? nt_unit : (int)(min(u1, g1) - u0)) - pc.ta;
             pc.b = b;
             pc.h = h;
             pc.row0 = s.q0 + qb * TB;
@@ -767,20 +780,31 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             pc.step = PAGED && s.kv ? 1 : 0;
             pc.pos0 = pc.step ? s.kv - s.L + qb * TB : s.kv - 1;
             pc.krow = PAGED ? 0 : a.k_start[b];
-            pc.slot = u0 < g0 ? 2 * (int)blockIdx.x : u1 > g1 ? 2 * (int)blockIdx.x + 1 : -1;
+            // a whole unit's parts are added up where the CTA's last piece will
+            // leave its sums
+            pc.sums = 4 * (2 * (int)blockIdx.x + (u0 < g0 ? 0 : 1)) | (u0 < g0 || u1 > g1 ? LEAVES : 0) | part;
             // (u0 lies in this CTA's share)
             if (u0 >= g0 && u1 > g1)
               shared_unit = make_int4((int)udiv(u1 - 1, share) - (int)blockIdx.x + 1, pc.row0, h, pc.ntok);
-            g = u1;
-            // the next unit
-            t = 0;
-            if (++qb == nqb) {
-              qb = 0;
-              if (++h == a.Hkv) {
-                h = 0;
-                if (g < g1) {               // the share goes on: some later request has rows
-                  s = next_request(b);
-                  nqb = (s.L + TB - 1) / TB;
+            part = 0;
+            if (pc.nt > C::FOLD) {          // a long piece in parts
+              pc.nt = C::FOLD;
+              pc.sums |= LEAVES;
+              part = ADDS;
+              t = pc.ta + pc.nt + (whole ? 0 : p.unit_cost);
+              if (!whole) g = u0 + pc.ta + pc.nt;
+            } else {
+              g = u1;
+              // the next unit
+              t = 0;
+              if (++qb == nqb) {
+                qb = 0;
+                if (++h == a.Hkv) {
+                  h = 0;
+                  if (g < g1) {             // the share goes on: some later request has rows
+                    s = next_request(b);
+                    nqb = (s.L + TB - 1) / TB;
+                  }
                 }
               }
             }
@@ -959,6 +983,40 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       tc::tc_fence_after();
       const int hq = pc.h * p.G + gq, trow = pc.row0 + i * p.TQ + tok;
       uint16_t* orow = a.out + ((size_t)(valid ? trow : 0) * a.Hq + hq) * D;
+      const int slot = pc.sums >> 2;
+      float2* ml = reinterpret_cast<float2*>(p.ws_ml) + ((size_t)slot * NQ + i) * BM + row;
+      if (active && (pc.sums & ADDS)) {
+        // add the sums of the part before, which this thread left there (a row
+        // sum of 0: no visible key); rows of no token take whatever is there
+        const float2 old = *ml;
+        const float m = old.y == 0.f ? m_used : l == 0.f ? old.x : fmaxf(old.x, m_used);
+        const float w_new = l == 0.f ? 0.f : exp2f(m_used - m), w_old = old.y == 0.f ? 0.f : exp2f(old.x - m);
+        l = w_new * l + w_old * old.y;
+        m_used = m;
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          float4 x[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            x[k] = *reinterpret_cast<const float4*>(p.ws_o + ws_index<D, NQ>(slot, i, cb * 8 + k, row));
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t o[16];
+            tc::tmem_ld16(tO + cb * 32 + hf * 16, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float4 y = x[hf * 4 + k];
+              o[4 * k] = __float_as_uint(w_new * __uint_as_float(o[4 * k]) + w_old * y.x);
+              o[4 * k + 1] = __float_as_uint(w_new * __uint_as_float(o[4 * k + 1]) + w_old * y.y);
+              o[4 * k + 2] = __float_as_uint(w_new * __uint_as_float(o[4 * k + 2]) + w_old * y.z);
+              o[4 * k + 3] = __float_as_uint(w_new * __uint_as_float(o[4 * k + 3]) + w_old * y.w);
+            }
+            tc::tmem_st16(tO + cb * 32 + hf * 16, o);
+          }
+        }
+        tc::tmem_wait_st();
+      }
       if (active) {
         const float inv_l = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -967,7 +1025,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           tc::tmem_ld32(tO + cb * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
           tc::tmem_wait_ld();
           if (!valid) continue;
-          if (pc.slot < 0) {
+          if (!(pc.sums & LEAVES)) {
             uint4 pk[4];
             uint32_t* pw = reinterpret_cast<uint32_t*>(pk);
 #pragma unroll
@@ -977,12 +1035,12 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<float4*>(p.ws_o + ws_index<D, NQ>(pc.slot, i, cb * 8 + k, row)) =
+              *reinterpret_cast<float4*>(p.ws_o + ws_index<D, NQ>(slot, i, cb * 8 + k, row)) =
                   make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
-        if (valid && pc.slot >= 0)
-          reinterpret_cast<float2*>(p.ws_ml)[((size_t)pc.slot * NQ + i) * BM + row] = make_float2(m_used, l);
+        if (valid && (pc.sums & LEAVES))
+          *ml = make_float2(m_used, l);
         else if (valid && a.lse)
           a.lse[(size_t)hq * a.n_tok + trow] = l == 0.f ? -INFINITY : (m_used + __log2f(l)) * 0.69314718055994531f;
       }

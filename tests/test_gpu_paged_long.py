@@ -11,7 +11,7 @@ from streaming_kv_cache_gb300 import skv
 
 pytestmark = pytest.mark.gpu
 
-PART = 128 * 128        # keys of a part
+PART = 256 * 128        # keys of a part
 
 
 def _inputs(seed, rows, hq, d, n_pool, dt):
@@ -33,11 +33,12 @@ def _want(q, k, v, weight, scale):
     return p @ v[:, 0].double(), lse, p @ v[:, 0].double().abs()
 
 
-def _check(out, lse, want, wlse, mass, dt, q, k, scale, n_key, what):
+def _check(out, lse, want, wlse, mass, dt, q, k, scale, n_key, n_q, what):
     """As paged_harness.check (a rounded output, probabilities rounded once,
     scores and row sums in fp32, the row sums of a part and one step a part),
-    and the value sums: a part's MMAs, at most 2 x 8 a key tile, cut off less
-    than a step (2^-23) of the sum each; its addition rounds by half a step.
+    and the value sums: a part's MMAs, 8 a key tile, 16 for single tokens (two
+    terms of a probability), cut off less than a step (2^-23) of the sum each;
+    its addition rounds by half a step.
     The drift of the mean over all outputs is bounded too: a rounding is
     uniform within u, so the mean over d dimensions of different sizes is
     within 6 u / sqrt(3 d) (six deviations, rows counted once); a cut is half a
@@ -45,10 +46,10 @@ def _check(out, lse, want, wlse, mass, dt, q, k, scale, n_key, what):
     d = q.shape[-1]
     u = torch.finfo(dt).eps / 2
     parts = -(-n_key // PART)
-    tiles = min(128, -(-n_key // 128))
+    tiles = min(PART, n_key) / 128
     q_norm, k_norm = float(q.float().norm(dim=-1).max()), float(k.float().norm(dim=-1).max())
     e = d * 2.0 ** -24 * q_norm * k_norm * scale + 2.0 ** -22 + (128 + tiles + parts) * 2.0 ** -24
-    cut = 16 * tiles * 2.0 ** -23 + 4 * parts * 2.0 ** -24
+    cut = (16 if n_q == 1 else 8) * tiles * 2.0 ** -23 + 4 * parts * 2.0 ** -24
     tol = u * (want.abs() * (1 + u) + mass) + (2 * e + cut) * mass + 2.0 ** -24
     err = out.double() - want
     worst = float((err.abs() / tol).max())
@@ -76,7 +77,7 @@ def test_values_of_one_sign_over_long_contexts(dtype, d, repeat, n_q):
     for b in range(0, n_req, 40):
         rows = slice(b * n_q, (b + 1) * n_q)
         want, wlse, mass = _want(q[rows], k, v, weight, scale)
-        _check(out[rows], lse[:, rows].t(), want, wlse, mass, dt, q, k, scale, n, "request %d" % b)
+        _check(out[rows], lse[:, rows].t(), want, wlse, mass, dt, q, k, scale, n, n_q, "request %d" % b)
 
 
 @pytest.mark.parametrize("dtype,d", [("fp16", 64), ("bf16", 128)])
@@ -101,7 +102,7 @@ def test_lengths_around_the_parts(dtype, d, n_q):
         seen = n - n_q + 1 + torch.arange(n_q, device="cuda")
         weight = (torch.arange(n, device="cuda")[None] < seen[:, None]).double()
         want, wlse, mass = _want(q[rows], k[:n], v[:n], weight, scale)
-        _check(out[rows], lse[:, rows].t(), want, wlse, mass, dt, q, k, scale, n, "request %d of %d keys" % (b, n))
+        _check(out[rows], lse[:, rows].t(), want, wlse, mass, dt, q, k, scale, n, n_q, "request %d of %d keys" % (b, n))
 
 
 @pytest.mark.parametrize("n_q", [1, 70])
@@ -116,7 +117,7 @@ def test_long_states_that_requests_share(n_q):
     for b in (0, 1, 2, 80, 158, 159):
         rows, s = slice(b * n_q, (b + 1) * n_q), slice(start[b], start[b] + length[b])
         want, wlse, mass = _want(q[rows], k[s], v[s], torch.ones((1, length[b]), device="cuda"), scale)
-        _check(out[rows], lse[:, rows].t(), want, wlse, mass, dt, q, k, scale, length[b], "request %d" % b)
+        _check(out[rows], lse[:, rows].t(), want, wlse, mass, dt, q, k, scale, length[b], n_q, "request %d" % b)
 
 
 def test_a_late_key_that_outweighs_the_parts_before_it():
