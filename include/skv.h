@@ -422,6 +422,7 @@ typedef struct skv_paged {
   int32_t* block_table;
   const float* rope;
   int32_t* status;
+  uint64_t wait_ns; /* limit of every bounded wait of paged_attn; 0 = 2 s */
 } skv_paged;
 
 /*
@@ -515,6 +516,10 @@ size_t skv_attn_workspace_bytes(void);
  * sets SKV_DEV_BAD_LEN and counts as 0; a span outside [0, n_tok] sets it and
  * is skipped.  A table entry outside the pool sets SKV_DEV_BAD_PAGE; its keys
  * and values count as zeros.
+ * A wait inside the kernel that passes cache->wait_ns sets SKV_DEV_TIMEOUT:
+ * out and lse are undefined, everything else is as it was and the next call
+ * needs no other workspace.  A wait may be as long as a request and kv head of
+ * one SM takes (some 10 ns a key).
  * ws: workspace of ws_bytes >= skv_attn_workspace_bytes(), of any contents.
  *     Calls that may run at the same time, captured graphs among them, need
  *     workspaces of their own.
@@ -549,6 +554,7 @@ typedef struct skv_states {
   const int32_t* k_start; /* device int32 [n_req] */
   const int32_t* k_len;   /* device int32 [n_req] */
   int32_t* status;
+  uint64_t wait_ns; /* limit of every bounded wait of cross_attn; 0 = 2 s */
 } skv_states;
 
 /*

@@ -212,6 +212,7 @@ int paged_attn(const skv_paged* cache, int32_t n_q_head, int32_t n_req, int32_t 
   a.ws = ws;
   a.status = cache->status;
   a.sm_scale = sm_scale;
+  a.wait_ns = cache->wait_ns;
   const cudaError_t e = skv::launch_ragged_attn(a, cache->head_dim, cache->dtype == SKV_FP16, (cudaStream_t)stream);
   return e == cudaSuccess ? SKV_OK : skv::record_cuda_error(e);
 }
@@ -254,6 +255,7 @@ int cross_attn(const skv_states* states, int32_t n_q_head, int32_t n_req, int32_
   a.ws = ws;
   a.status = s->status;
   a.sm_scale = sm_scale;
+  a.wait_ns = s->wait_ns;
   const cudaError_t e = skv::launch_ragged_attn(a, s->head_dim, s->dtype == SKV_FP16, (cudaStream_t)stream);
   return e == cudaSuccess ? SKV_OK : skv::record_cuda_error(e);
 }

@@ -133,6 +133,8 @@ struct RParams {
   int whole_slack;        // positions that the longest unit may have over an equal share to keep units whole: what the partials and their merge take
   int unit_cost;          // positions that a unit takes before its tiles, for what it costs beside them
   float scale_log2;
+  bool wait_poll;         // LIMITED: the limit is shorter than a try of a wait may sleep
+  uint64_t wait_cycles;   // and the limit of a wait
   int4* ws_unit;          // [CTAs] the shared unit that starts in a CTA: pieces (0: none), first token row, kv head, tokens
   float* ws_ml;           // [2 * CTAs][NQ][BM][2]
   float* ws_o;            // [2 * CTAs][NQ][D / 4][BM][4], see ws_index
@@ -327,7 +329,9 @@ __global__ void __launch_bounds__(MT, NQ == 2 ? 8 : 4) merge_kernel(const RParam
   else merge_part<D, F16, NQ, 4, NQ == 2 ? 2 : 4>(p, u, c0, i, rows, t);
 }
 
-template <int D, bool F16, int NQ, bool PAGED>
+// LIMITED: compiled for a caller's wait limit.  The limit as an operand of every
+// wait cost the normal calls 1 to 5% (152 requests of 65,536 keys 464 -> 487 us).
+template <int D, bool F16, int NQ, bool PAGED, bool LIMITED>
 __global__ void __launch_bounds__(RCfg<D, NQ>::NT, 1)
 ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ RParams p) {
@@ -483,7 +487,17 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  auto wait = [&](int b, uint32_t phase) { return tc::mbar_sleep(bar(b), phase & 1); };
+  auto wait = [&](int b, uint32_t phase) {
+    if constexpr (LIMITED) {
+      if (p.wait_poll) return tc::mbar_poll(bar(b), phase & 1, p.wait_cycles);
+      return tc::mbar_sleep(bar(b), phase & 1, p.wait_cycles);
+    } else {
+      return tc::mbar_sleep(bar(b), phase & 1);
+    }
+  };
+  // for what a warp has started itself and must not leave behind: however short
+  // the caller's limit is
+  auto drain = [&](int b, uint32_t phase) { return tc::mbar_sleep(bar(b), phase & 1); };
   // piece number pi into registers, its slot given back (whole warps)
   auto take_piece = [&](int pi, Piece& pc) {
     const int s = pi % NP;
@@ -556,7 +570,8 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       if (!ok && lane == 0) set_status(a.status, SKV_DEV_TIMEOUT);
       // the copies this warp started land before the CTA exits
-      for (int j = max(0, n - nst); j < n; ++j) wait(full + j % nst, j / nst);
+      for (int j = max(0, n - nst); j < n && drain(full + j % nst, j / nst); ++j) {
+      }
     } else if (warp == C::WARP_MMA) {
       // --------------------------------------------------------- MMA issuer
       // all lanes go on or none: they meet again at the next warp-wide step
@@ -697,7 +712,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // every MMA issued completes before TMEM is released
         tc::mma_commit(bar(B::DRAIN));
       }
-      wait_all(B::DRAIN, 0);
+      drain(B::DRAIN, 0);
     } else if (warp == C::WARP_SCHED) {
       // ---------------------------------------------------------- scheduler
       // A unit takes unit_cost + its tiles positions of the sequence, the tiles
@@ -827,7 +842,7 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         if (!ok) set_status(a.status, SKV_DEV_TIMEOUT);
         p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);   // always written: the merge reads it
-        if (loaded) wait(B::QFULL, loaded - 1);
+        if (loaded) drain(B::QFULL, loaded - 1);
       }
     }
   } else {
@@ -1076,7 +1091,7 @@ int sm_count() {
 
 template <typename K>
 cudaError_t set_smem_once(K kernel, int bytes, int variant) {
-  static std::atomic<int> done[64][16];
+  static std::atomic<int> done[64][32];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1131,6 +1146,9 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
     while (a.page_size % p.BR) p.BR /= 2;
   p.boxes = BN / p.BR;
   p.scale_log2 = a.sm_scale * kLog2e;
+  // in cycles at the 2.07 GHz maximum clock: a slower one only lengthens it
+  p.wait_cycles = (uint64_t)(min(a.wait_ns, (uint64_t)1 << 62) * 2.07);
+  p.wait_poll = a.wait_ns < tc::kSuspendHintNs;
   char* ws = static_cast<char*>(a.ws);
   p.ws_unit = reinterpret_cast<int4*>(ws);
   p.ws_ml = reinterpret_cast<float*>(ws + WS_HEAD);
@@ -1163,8 +1181,11 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
     if (e != cudaSuccess) return e;
     return launch_dependent(merge, dim3(grid, wide ? 2 : 1, MERGE_PARTS), MT, 0, st, p);
   };
-#define SKV_RAGGED(DD, FF, NN, PP, VAR) \
-  launch(ragged_attn_kernel<DD, FF, NN, PP>, merge_kernel<DD, FF, NN>, RCfg<DD, NN>::ALLOC, RCfg<DD, NN>::NT, VAR)
+#define SKV_RAGGED(DD, FF, NN, PP, VAR)                                                                        \
+  (a.wait_ns ? launch(ragged_attn_kernel<DD, FF, NN, PP, true>, merge_kernel<DD, FF, NN>, RCfg<DD, NN>::ALLOC, \
+                      RCfg<DD, NN>::NT, 16 + (VAR))                                                            \
+             : launch(ragged_attn_kernel<DD, FF, NN, PP, false>, merge_kernel<DD, FF, NN>, RCfg<DD, NN>::ALLOC, \
+                      RCfg<DD, NN>::NT, VAR))
 #define SKV_RAGGED_FORMS(DD, FF, VAR)                                                                    \
   (wide ? (paged ? SKV_RAGGED(DD, FF, 2, true, VAR) : SKV_RAGGED(DD, FF, 2, false, VAR + 1))             \
         : (paged ? SKV_RAGGED(DD, FF, 1, true, VAR + 2) : SKV_RAGGED(DD, FF, 1, false, VAR + 3)))

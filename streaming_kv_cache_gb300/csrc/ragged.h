@@ -57,6 +57,7 @@ struct RaggedArgs {
   void* ws;
   int32_t* status;
   float sm_scale;
+  uint64_t wait_ns;         // limit of a wait, 0: two seconds
 };
 constexpr float kLog2e = 1.4426950408889634f;   // the softmax works to base two: its scale times this
 cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_t st);

@@ -162,20 +162,36 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, u
 // A wait of a few instructions, for loops whose issue must stay short: sleeps
 // in try_wait (a try ends after 4 us at most on GB300, whatever the hint, and
 // earlier when other barriers are busy, so tries say nothing of the time) and
-// ends after 2^32 cycles, two seconds at least, returning false.
-__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
+// ends after `cycles` (2^32: two seconds at least), returning false.
+__device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, uint64_t cycles = 1ull << 32) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b64 t0, t;\n mov.b32 %0, 1;\n"
       " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n @p bra DONE;\n"
       " mov.u64 t0, %%clock64;\n"
       "TRY:\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n @p bra DONE;\n"
-      " mov.u64 t, %%clock64;\n sub.u64 t, t, t0;\n setp.lt.u64 q, t, 4294967296;\n @q bra TRY;\n mov.b32 %0, 0;\n"
+      " mov.u64 t, %%clock64;\n sub.u64 t, t, t0;\n setp.lt.u64 q, t, %4;\n @q bra TRY;\n mov.b32 %0, 0;\n"
       "DONE:\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(kSuspendHintNs)
+      : "r"(bar), "r"(parity), "r"(kSuspendHintNs), "l"(cycles)
       : "memory");
   return ok != 0;
+}
+
+// The same without sleeping, for limits shorter than a try of try_wait takes.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint64_t cycles) {
+  const long long t0 = clock64();
+  do {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  } while ((uint64_t)(clock64() - t0) < cycles);
+  return false;
 }
 
 // True in one lane of a converged warp.

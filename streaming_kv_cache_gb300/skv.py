@@ -60,7 +60,7 @@ class skv_paged(ctypes.Structure):
                 ("max_block", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p), ("rope", ctypes.c_void_p),
-                ("status", ctypes.c_void_p)]
+                ("status", ctypes.c_void_p), ("wait_ns", ctypes.c_uint64)]
 
 
 class skv_states(ctypes.Structure):
@@ -69,7 +69,7 @@ class skv_states(ctypes.Structure):
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_start", ctypes.c_void_p), ("k_len", ctypes.c_void_p),
-                ("status", ctypes.c_void_p)]
+                ("status", ctypes.c_void_p), ("wait_ns", ctypes.c_uint64)]
 
 
 _lib_handle = None
@@ -506,11 +506,12 @@ class PagedCache:
 
     theta gives the rope table of positions below max_block * page_size
     (None: keys and queries are not rotated).  The layers of a model share
-    everything but k and v: layer(i) is the cache of one of them.
+    everything but k and v: layer(i) is the cache of one of them.  wait_ns
+    limits every wait inside paged_attn (0: two seconds) and may be set later.
     """
 
     def __init__(self, n_page, page_size, Hkv, d, n_req, max_block, theta=None, dtype=torch.bfloat16,
-                 n_layer=1, device="cuda"):
+                 n_layer=1, device="cuda", wait_ns=0):
         dev = torch.device(device)
         shape = (n_layer, n_page, Hkv, page_size, d)
         i32 = dict(dtype=torch.int32, device=dev)
@@ -524,10 +525,11 @@ class PagedCache:
         self._k, self._v = (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
         self._set(self._k[0], self._v[0], torch.zeros((n_req, max_block), **i32),
                   torch.arange(n_page, **i32), state, rope, torch.zeros((1,), **i32), page_size)
+        self.wait_ns = wait_ns
 
     @classmethod
     def wrap(cls, k=None, v=None, block_table=None, page_queue=None, state=None, rope=None, status=None,
-             page_size=None):
+             page_size=None, wait_ns=0):
         """A cache over tensors that the caller owns.  k and v may be left
         out where only kv_paged_plan is called, page_queue and state where it
         is not; status is made where it is not given."""
@@ -537,6 +539,7 @@ class PagedCache:
         self._k = k[None] if k is not None else None
         self._v = v[None] if v is not None else None
         self._set(k, v, block_table, page_queue, state, rope, status, page_size)
+        self.wait_ns = wait_ns
         return self
 
     def _set(self, k, v, block_table, page_queue, state, rope, status, page_size):
@@ -588,7 +591,16 @@ class PagedCache:
         c._k, c._v = self._k[i:i + 1], self._v[i:i + 1]
         c._set(self._k[i], self._v[i], self.block_table, self.page_queue, self.state, self.rope, self.status,
                self.page_size)
+        c.wait_ns = self.wait_ns
         return c
+
+    @property
+    def wait_ns(self) -> int:
+        return self._desc.wait_ns
+
+    @wait_ns.setter
+    def wait_ns(self, ns):
+        self._desc.wait_ns = int(ns)
 
     def advance(self, plan: PagedPlan):
         """Take the state that a plan leads to as the cache's state."""
@@ -713,10 +725,11 @@ def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len
 
 def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor, k_start: torch.Tensor,
                k_len: torch.Tensor, sm_scale: float, *, status: torch.Tensor, out: torch.Tensor | None = None,
-               lse: torch.Tensor | bool | None = None, ws: torch.Tensor | None = None):
+               lse: torch.Tensor | bool | None = None, ws: torch.Tensor | None = None, wait_ns: int = 0):
     """Attention of packed queries to each request's packed states k, v
     [tokens][Hkv][d]: request b reads rows [k_start[b], k_start[b] + k_len[b]).
-    status collects device status bits.  Returns out (and lse when asked for)."""
+    status collects device status bits; wait_ns limits every wait inside the
+    kernel (0: two seconds).  Returns out (and lse when asked for)."""
     dev = _call_device(k, "k")
     if k.dim() != 3 or k.dtype not in _DTYPE_CODE:
         raise ValueError("k must be a bfloat16 or float16 tensor (tokens, kv heads, d), got %s %s" % (k.dtype, tuple(k.shape)))
@@ -734,7 +747,7 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch
     _on(status, (1,), torch.int32, "status", dev)
     out, lse, ws = _attn_args(q, n_req, q_start, out, lse, ws, dev)
     desc = skv_states(n_key, hkv, d, _DTYPE_CODE[dt], ks, vs, k.data_ptr(), v.data_ptr(), k_start.data_ptr(),
-                      k_len.data_ptr(), status.data_ptr())
+                      k_len.data_ptr(), status.data_ptr(), wait_ns)
     rc = lib().cross_attn(ctypes.byref(desc), hq, n_req, n, q.data_ptr(), qs, q_start.data_ptr(),
                           out.data_ptr(), lse.data_ptr() if lse is not None else None, ws.data_ptr(), ws.numel(),
                           sm_scale, _raw_stream(dev))
