@@ -528,7 +528,7 @@ size_t skv_attn_workspace_bytes(void);
  * refused.
  * The call is two kernel launches: the attention, and the merge of what
  * several SMs computed of one row.
- * Needs Hq % Hkv == 0, Hq / Hkv <= 128, n_tok <= 2^30 and n_tok * Hq < 2^31,
+ * Needs Hq % Hkv == 0, Hq / Hkv <= 128, n_req and n_tok <= 2^30 and n_tok * Hq < 2^31,
  * sm_scale > 0 and sm_scale / ln 2 finite.
  */
 int paged_attn(const skv_paged* cache, int32_t n_q_head, int32_t n_req, int32_t n_tok,

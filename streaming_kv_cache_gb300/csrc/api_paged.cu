@@ -72,7 +72,7 @@ int check_attn(int n_q_head, int n_kv_head, int d, int n_req, int n_tok, const v
   if (n_q_head < 1 || n_q_head % n_kv_head) return SKV_ERR_INVALID;
   if (n_q_head / n_kv_head > 128) return SKV_ERR_UNSUPPORTED;
   if (n_req < 0 || n_tok < 0) return SKV_ERR_INVALID;
-  if (n_tok > (1 << 30) || (long long)n_tok * n_q_head > 0x7FFFFFFFLL) return SKV_ERR_UNSUPPORTED;
+  if (n_req > (1 << 30) || n_tok > (1 << 30) || (long long)n_tok * n_q_head > 0x7FFFFFFFLL) return SKV_ERR_UNSUPPORTED;
   if (!(sm_scale > 0.f) || isinf(sm_scale * skv::kLog2e)) return SKV_ERR_INVALID;
   if (n_req == 0 || n_tok == 0) {
     *empty = true;
