@@ -506,11 +506,21 @@ size_t skv_attn_workspace_bytes(void);
  *
  * q:    [n_tok][Hq][d], rotated (kv_paged_write's q_out); query head h reads
  *       kv head h / (Hq / Hkv)
- * out:  device [n_tok][Hq][d], contiguous: softmax(sm_scale q.k) v,
- *       accumulated in fp32, rounded once.  It may be q itself where q is
- *       contiguous, and does not overlap it otherwise
+ * out:  device [n_tok][Hq][d], contiguous: softmax(sm_scale q.k) v, rounded
+ *       once.  It may be q itself where q is contiguous, and does not overlap
+ *       it otherwise
  * lse:  device fp32 [Hq][n_tok], natural log of the sum of exp of the scaled
  *       scores, or NULL
+ * Maxima and sums are held in fp32.  The probabilities meet the values as
+ * 16-bit floats: in two terms, which leaves the output's own rounding, where
+ * n_tok <= n_req * floor(128 / (Hq / Hkv)), and rounded once each, which adds
+ * about as much, where there are more rows.  n_tok and n_req are the call's:
+ * padding rows and idle requests count, and they choose the form's speed with
+ * it (few tokens in many padding rows 1 to 4% slower; chunks of 512 tokens in a
+ * call of 16 or more mostly idle requests 38 -> 49 us).  Where SMs share a
+ * request's keys depends on all lengths of the call.  So a request's bits, not
+ * their bounds, change with what else is in the call; the same call gives the
+ * same bits.
  * A row that sees no key (kv_len 0) gets zeros and lse -inf.
  * kv_len[b] outside [n, max_block * page_size] (0 apart) or above SKV_MAX_KEYS
  * sets SKV_DEV_BAD_LEN and counts as 0; a span outside [0, n_tok] sets it and

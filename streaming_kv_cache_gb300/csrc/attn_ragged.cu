@@ -86,10 +86,10 @@ struct RCfg {
   // drifts towards zero, by about 2^-24 of itself per MMA of 16 keys: the mean
   // of positive values over 320,000 keys in one CTA was 1.1e-3 too small, over 4
   // million 1.8e-2.  Longer runs are cut into parts of 32,768 keys, a drift of a
-  // quarter of fp16's half step, whose sums are added in fp32 arithmetic that
-  // rounds to nearest.  An addition takes some
-  // 4 us of a part's 300 to 400 (152 requests of 65,536 keys in L2 563 -> 572
-  // us, 16 of 131,072 from HBM 1183 -> 1192); twice as many parts twice that.
+  // quarter of fp16's half step (with P in two terms up to half), whose sums are
+  // added in fp32 arithmetic that rounds to nearest.  An addition takes some 4
+  // us of a part's 300 to 400 (152 requests of 65,536 keys in L2 563 -> 572 us,
+  // 16 of 131,072 from HBM 1183 -> 1192); twice as many parts twice that.
   static constexpr int FOLD = 256;
   static constexpr int QT = BM * D * 2;        // bytes of a query tile
   static constexpr int KT = BN * D * 2;        // of a key or value tile
@@ -1132,7 +1132,10 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   // per unit (a request that needs one leaves the second idle).  d = 128, 32
   // query and 8 kv heads, 4 k keys: one chunk of 512 tokens 44 us wide, 54
   // narrow; four of 100, 44 and 49; 16 of 20, 57 and 51; d = 64, six requests of
-  // long encodings, 202 and 333.
+  // long encodings, 202 and 333.  The host has no lengths, so padding rows and
+  // idle requests count: 64 single tokens take 172 us, and 179 in 4,096 rows; a
+  // chunk of 512 tokens 38, and 49 among 16 to 256 requests that are idle, one
+  // of 4,096 121, and 197 among 256.
   const bool wide = a.n_tok > (long long)a.n_req * p.TQ;
   p.TB = (wide ? 2 : 1) * p.TQ;
   const int grid = min(sm_count(), MAX_CTAS);
