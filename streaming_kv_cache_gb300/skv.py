@@ -507,8 +507,14 @@ class PagedCache:
     theta gives the rope table of positions below max_block * page_size
     (None: keys and queries are not rotated).  The layers of a model share
     everything but k and v: layer(i) is the cache of one of them.  wait_ns
-    limits every wait inside paged_attn (0: two seconds) and may be set later.
+    limits every wait inside paged_attn (0: two seconds) and may be set later;
+    everything else is fixed, because the calls keep its addresses.
     """
+
+    def __setattr__(self, name, value):
+        if "_made" in self.__dict__ and name in self.__dict__:
+            raise AttributeError("%s of a PagedCache is fixed: write into it, or make another cache" % name)
+        object.__setattr__(self, name, value)
 
     def __init__(self, n_page, page_size, Hkv, d, n_req, max_block, theta=None, dtype=torch.bfloat16,
                  n_layer=1, device="cuda", wait_ns=0):
@@ -584,6 +590,7 @@ class PagedCache:
                                self.max_block, 0, ptr(k), ptr(v), ptr(block_table), ptr(rope), ptr(status))
         self._ref, self._dev = ctypes.byref(self._desc), block_table.get_device()
         self._dtype = k.dtype if k is not None else None
+        self._made = True
 
     def layer(self, i: int) -> "PagedCache":
         """The cache of layer i: its own k and v, everything else shared."""
