@@ -540,6 +540,8 @@ class PagedCache:
         out where only kv_paged_plan is called, page_queue and state where it
         is not; status is made where it is not given."""
         self = cls.__new__(cls)
+        if block_table is None:
+            raise ValueError("block_table must be a (requests, max_block) tensor")
         if status is None:
             status = torch.zeros((1,), dtype=torch.int32, device=block_table.device)
         self._k = k[None] if k is not None else None
@@ -594,6 +596,9 @@ class PagedCache:
 
     def layer(self, i: int) -> "PagedCache":
         """The cache of layer i: its own k and v, everything else shared."""
+        if self._k is None:
+            raise ValueError("the cache has no k and v")
+        i = range(self._k.shape[0])[i]
         c = PagedCache.__new__(PagedCache)
         c._k, c._v = self._k[i:i + 1], self._v[i:i + 1]
         c._set(self._k[i], self._v[i], self.block_table, self.page_queue, self.state, self.rope, self.status,

@@ -29,3 +29,25 @@ def test_wait_limit_may_be_set():
     cache = _cache()
     cache.wait_ns = 5
     assert cache.wait_ns == 5
+
+
+def test_layers_by_index():
+    cache = _cache(n_layer=3)
+    for i, j in ((0, 0), (2, 2), (-1, 2), (-3, 0)):
+        c = cache.layer(i)
+        assert c.k.data_ptr() == cache.layer(j).k.data_ptr()
+        assert c.layer(0).k.data_ptr() == c.k.data_ptr() and c.layer(-1).v.data_ptr() == c.v.data_ptr()
+        with pytest.raises(IndexError):
+            c.layer(1)
+    for i in (3, -4):
+        with pytest.raises(IndexError):
+            cache.layer(i)
+
+
+def test_caches_without_their_parts():
+    table = torch.zeros((1, 2), dtype=torch.int32, device="cuda")
+    plan_only = skv.PagedCache.wrap(block_table=table, page_queue=torch.zeros(4, dtype=torch.int32, device="cuda"), page_size=16)
+    with pytest.raises(ValueError):
+        plan_only.layer(0)
+    with pytest.raises(ValueError):
+        skv.PagedCache.wrap(page_queue=table[0], page_size=16)
