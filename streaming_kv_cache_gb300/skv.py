@@ -582,28 +582,29 @@ class PagedCache:
                         ("status", status)):
             if t is not None and t.device != block_table.device:
                 raise ValueError("%s is on %s, block_table on %s" % (name, t.device, block_table.device))
-        self.k, self.v, self.block_table, self.page_queue = k, v, block_table, page_queue
-        self.state, self.rope, self.status = state, rope, status
-        self.n_page, self.page_size, self.Hkv, self.d = n_page, page_size, hkv, d
-        self.n_req, self.max_block = block_table.shape
+        n_req, max_block = block_table.shape
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-        self._state_arg, self._queue_arg = ctypes.c_void_p(ptr(state)), ctypes.c_void_p(ptr(page_queue))
-        self._desc = skv_paged(n_page, page_size, hkv, d, code, rope.shape[0] if rope is not None else 0,
-                               self.max_block, 0, ptr(k), ptr(v), ptr(block_table), ptr(rope), ptr(status))
-        self._ref, self._dev = ctypes.byref(self._desc), block_table.get_device()
-        self._dtype = k.dtype if k is not None else None
-        self._made = True
+        desc = skv_paged(n_page, page_size, hkv, d, code, rope.shape[0] if rope is not None else 0, max_block, 0,
+                         ptr(k), ptr(v), ptr(block_table), ptr(rope), ptr(status))
+        # all at once, past __setattr__: a step may make a cache per layer
+        self.__dict__.update(
+            k=k, v=v, block_table=block_table, page_queue=page_queue, state=state, rope=rope, status=status,
+            n_page=n_page, page_size=page_size, Hkv=hkv, d=d, n_req=n_req, max_block=max_block,
+            _state_arg=ctypes.c_void_p(ptr(state)), _queue_arg=ctypes.c_void_p(ptr(page_queue)),
+            _desc=desc, _ref=ctypes.byref(desc), _dev=block_table.get_device(),
+            _dtype=k.dtype if k is not None else None, _made=True)
 
     def layer(self, i: int) -> "PagedCache":
         """The cache of layer i: its own k and v, everything else shared."""
         if self._k is None:
             raise ValueError("the cache has no k and v")
-        i = range(self._k.shape[0])[i]
+        if i < 0:
+            i = range(len(self._k))[i]
         c = PagedCache.__new__(PagedCache)
-        c._k, c._v = self._k[i:i + 1], self._v[i:i + 1]
+        c.__dict__.update(_k=self._k[i:i + 1], _v=self._v[i:i + 1])
         c._set(self._k[i], self._v[i], self.block_table, self.page_queue, self.state, self.rope, self.status,
                self.page_size)
-        c.wait_ns = self.wait_ns
+        c._desc.wait_ns = self._desc.wait_ns
         return c
 
     @property
