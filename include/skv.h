@@ -511,7 +511,8 @@ size_t skv_attn_workspace_bytes(void);
  *       it otherwise
  * lse:  device fp32 [Hq][n_tok], natural log of the sum of exp of the scaled
  *       scores, or NULL
- * Maxima and sums are held in fp32.  The probabilities meet the values as
+ * Maxima and sums are held in fp32 (fp16: probabilities under 2^-31 of a row's
+ * largest count as zero).  The probabilities meet the values as
  * 16-bit floats: in two terms, which leaves the output's own rounding, where
  * n_tok <= n_req * floor(128 / (Hq / Hkv)), and rounded once each, which adds
  * about as much, where there are more rows.  n_tok and n_req are the call's:
