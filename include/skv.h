@@ -518,7 +518,7 @@ size_t skv_attn_workspace_bytes(void);
  * about as much, where there are more rows.  n_tok and n_req are the call's:
  * padding rows and idle requests count, and they choose the form's speed with
  * it (few tokens in many padding rows 1 to 4% slower; chunks of 512 tokens in a
- * call of 16 or more mostly idle requests 38 -> 49 us).  Where SMs share a
+ * call of 16 or more mostly idle requests 38 -> 48 us).  Where SMs share a
  * request's keys depends on all lengths of the call.  So a request's bits, not
  * their bounds, change with what else is in the call; the same call gives the
  * same bits.

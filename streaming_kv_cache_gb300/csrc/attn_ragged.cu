@@ -24,13 +24,14 @@
 // query tiles share every key tile, and one tile's softmax runs under the
 // other's MMAs.  At d = 128 it is bound by the tensor pipe and the waits of the
 // warp that feeds it (four chunks of 2,048 tokens over 6 to 13 k keys, 32 query
-// and 8 kv heads: 0.88 ms, 1430 TFLOP/s); at d = 64, with half the MMA work per
-// score, by the chain from scores over probabilities to the next scores, 2540
-// cycles a key tile for 1060 of MMAs (six requests of 1,536 tokens over up to
-// 12,800 states: 202 us, 940 TFLOP/s).  NQ = 1, for decode: one query tile, two
-// score buffers, so that Q K^T of the next key tile runs under the softmax.  It
-// is bound by streaming K and V from HBM (64 requests of 0.4 to 8 k keys: 175
-// us, 6.3 TB/s); most MMA rows are idle.
+// and 8 kv heads: 0.81 to 0.93 ms over boxes, 1360 to 1550 TFLOP/s); at d = 64,
+// with half the MMA work per score, by the chain from scores over probabilities
+// to the next scores, 2540 cycles a key tile for 1060 of MMAs (six requests of
+// 1,536 tokens over up to 12,800 states: 203 to 220 us, 860 to 940 TFLOP/s).
+// NQ = 1, for decode: one query tile, two score buffers, so that Q K^T of the
+// next key tile runs under the softmax.  It is bound by streaming K and V from
+// HBM (64 requests of 0.4 to 8 k keys: 172 to 177 us, 6.2 to 6.4 TB/s); most MMA
+// rows are idle.
 //
 //   warps 0 .. 4 NQ - 1  softmax and epilogue: a warpgroup per query tile, a
 //                        thread per row
@@ -1134,8 +1135,8 @@ cudaError_t launch_ragged_attn(const RaggedArgs& a, int d, bool f16, cudaStream_
   // narrow; four of 100, 44 and 49; 16 of 20, 57 and 51; d = 64, six requests of
   // long encodings, 202 and 333.  The host has no lengths, so padding rows and
   // idle requests count: 64 single tokens take 172 us, and 179 in 4,096 rows; a
-  // chunk of 512 tokens 38, and 49 among 16 to 256 requests that are idle, one
-  // of 4,096 121, and 197 among 256.
+  // chunk of 512 tokens 38, and 48 among 16 to 256 requests that are idle, one
+  // of 4,096 122, and 190 to 197 among 256.
   const bool wide = a.n_tok > (long long)a.n_req * p.TQ;
   p.TB = (wide ? 2 : 1) * p.TQ;
   const int grid = min(sm_count(), MAX_CTAS);
