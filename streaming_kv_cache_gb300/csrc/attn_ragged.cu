@@ -24,7 +24,7 @@
 // query tiles share every key tile, and one tile's softmax runs under the
 // other's MMAs.  At d = 128 it is bound by the tensor pipe and the waits of the
 // warp that feeds it (four chunks of 2,048 tokens over 6 to 13 k keys, 32 query
-// and 8 kv heads: 0.81 to 0.93 ms over boxes, 1360 to 1550 TFLOP/s); at d = 64,
+// and 8 kv heads: 0.81 to 0.93 ms on several GPUs, 1360 to 1550 TFLOP/s); at d = 64,
 // with half the MMA work per score, by the chain from scores over probabilities
 // to the next scores, 2540 cycles a key tile for 1060 of MMAs (six requests of
 // 1,536 tokens over up to 12,800 states: 203 to 220 us, 860 to 940 TFLOP/s).
