@@ -579,6 +579,63 @@ int cross_attn(const skv_states* states, int32_t n_q_head, int32_t n_req, int32_
                const void* q, int64_t q_stride, const int32_t* q_start, void* out, float* lse,
                void* ws, size_t ws_bytes, float sm_scale, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Fewer tokens in a paged cache.  A request gives tokens back for two
+ * reasons: drafted tokens that were rejected, at its end, and cached tokens
+ * that a budget evicts, anywhere in it.  Keys are rotated when they are
+ * written, so a token that stays keeps its position whatever place it takes;
+ * after an eviction a request's next position is no longer the number of
+ * tokens that it holds.  A state with evicted words (device int32
+ * [2 * n_req + 2]: tokens held, head and count of the free queue, tokens
+ * evicted so far) keeps the difference.
+ */
+
+/*
+ * kv_paged_plan_evicting -- kv_paged_plan for a state with evicted words:
+ * token i of a request that holds c tokens and has had e evicted sits at
+ * position e + c + i, and next_state has the evicted words behind it (0 for a
+ * request that held nothing or has finished, so that its next tokens start at
+ * position 0).  Everything else is kv_paged_plan's.  A negative evicted word
+ * sets SKV_DEV_BAD_LEN and counts as 0; positions end at 2^31 - 1.
+ */
+int kv_paged_plan_evicting(const skv_paged* cache, int32_t n_req, int32_t n_tok,
+                           const int32_t* state, const int32_t* new_len, int32_t* queue,
+                           int32_t* q_start, int32_t* kv_len, int32_t* next_state,
+                           int32_t* position, int32_t* slot, void* stream);
+
+/*
+ * kv_paged_trim -- requests cut to fewer tokens: request b keeps its first
+ * min(held, keep[b]) tokens, and the pages behind them go to the tail of the
+ * free queue, in request order and front to back (free from the next step
+ * on).  Of `cache` it uses n_page, page_size, max_block, block_table and
+ * status.
+ *
+ * state:   device int32 [n_req + 2] or, unless evicted is 0, [2 * n_req + 2]
+ * keep:    device int32 [n_req]
+ * evicted: 0: state has no evicted words; SKV_TRIM_DRAFTS: it has, and the
+ *          tokens are taken back with their positions (rejected drafts);
+ *          SKV_TRIM_EVICTED: they count as evicted, positions go on (but a
+ *          request that keeps nothing starts anew: evicted word 0)
+ * queue:   device int32 [n_page], as kv_paged_plan has it
+ * next_state: the state after the cut, of state's size.  Not `state` itself:
+ *          the caller advances by copying it there, or drops it
+ *
+ * The call reads nothing that it writes, so it may be repeated on the same
+ * state; queue, next_state and the status word overlap nothing that it uses
+ * (refused with SKV_ERR_INVALID).  A held length outside
+ * [0, max_block * page_size] or above SKV_MAX_KEYS, a negative keep, a
+ * negative evicted word, a queue state outside the pool or more pages given
+ * back than the queue has room for set SKV_DEV_BAD_LEN: such a request keeps
+ * its state, such a word or queue counts as 0 (empty), such pages are lost.
+ * A page outside the pool sets SKV_DEV_BAD_PAGE and is given back as it is.
+ * A page is freed once for each request that gives it back.
+ * n_req <= SKV_PAGED_MAX_REQUESTS.
+ */
+#define SKV_TRIM_DRAFTS 1
+#define SKV_TRIM_EVICTED 2
+int kv_paged_trim(const skv_paged* cache, int32_t n_req, const int32_t* state, const int32_t* keep,
+                  int32_t evicted, int32_t* queue, int32_t* next_state, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

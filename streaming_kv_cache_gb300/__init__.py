@@ -9,7 +9,7 @@ ctypes binding.  Build it with streaming_kv_cache_gb300.build.build().
 """
 from . import synth  # noqa: F401
 from .skv import (EXPORTS, PagedCache, PagedPlan, SkvError, StreamCache, attn_workspace,  # noqa: F401
-                  cross_attn, kv_paged_plan, kv_paged_write, kv_stream_insert,
+                  cross_attn, kv_paged_plan, kv_paged_trim, kv_paged_write, kv_stream_insert,
                   kv_stream_insert_noalloc, kv_write_rows,
                   lib, paged_attn, skv_build_rope_table, skv_row_cap, skv_verify_workspace_bytes,
                   skv_build_mrope_table, status_string, stream_attn_prefill,

@@ -87,13 +87,10 @@ int check_attn(int n_q_head, int n_kv_head, int d, int n_req, int n_tok, const v
   return SKV_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const int32_t* state,
-                  const int32_t* new_len, int32_t* queue, int32_t* q_start, int32_t* kv_len,
-                  int32_t* next_state, int32_t* position, int32_t* slot, void* stream) {
+// kv_paged_plan, and for a state with evicted words kv_paged_plan_evicting
+int plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const int32_t* state, const int32_t* new_len,
+         int32_t* queue, int32_t* q_start, int32_t* kv_len, int32_t* next_state, int32_t* position, int32_t* slot,
+         bool evicting, void* stream) {
   int rc = check_pool(cache);
   if (rc) return rc;
   if (n_req < 0 || n_tok < 0 || n_tok > (1 << 30)) return SKV_ERR_INVALID;
@@ -104,10 +101,10 @@ int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const in
   if (n_tok && (!aligned(position, 4) || !aligned(slot, 4))) return SKV_ERR_INVALID;
   // every CTA reads the lengths, the queue and the table while others write
   // already, so what is written shares no byte with anything else
-  const size_t req = (size_t)n_req, tok = (size_t)n_tok;
-  const Range used[] = {{state, req + 2}, {new_len, req}, {queue, (size_t)cache->n_page},
+  const size_t req = (size_t)n_req, tok = (size_t)n_tok, words = (evicting ? 2 * req : req) + 2;
+  const Range used[] = {{state, words}, {new_len, req}, {queue, (size_t)cache->n_page},
                         {cache->block_table, req * (size_t)cache->max_block}, {q_start, req + 1}, {kv_len, req},
-                        {next_state, req + 2}, {position, tok}, {slot, tok}, {cache->status, 1}};
+                        {next_state, words}, {position, tok}, {slot, tok}, {cache->status, 1}};
   for (int i = 2; i < 10; ++i)                     // the first two are only read
     for (int j = 0; j < i; ++j)
       if (overlap(used[i], used[j])) return SKV_ERR_INVALID;
@@ -129,7 +126,56 @@ int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const in
   a.position = position;
   a.slot = slot;
   a.status = cache->status;
+  a.evicting = evicting;
   const cudaError_t e = skv::launch_paged_plan(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? SKV_OK : skv::record_cuda_error(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv_paged_plan(const skv_paged* cache, int32_t n_req, int32_t n_tok, const int32_t* state,
+                  const int32_t* new_len, int32_t* queue, int32_t* q_start, int32_t* kv_len,
+                  int32_t* next_state, int32_t* position, int32_t* slot, void* stream) {
+  return plan(cache, n_req, n_tok, state, new_len, queue, q_start, kv_len, next_state, position, slot, false, stream);
+}
+
+int kv_paged_plan_evicting(const skv_paged* cache, int32_t n_req, int32_t n_tok, const int32_t* state,
+                           const int32_t* new_len, int32_t* queue, int32_t* q_start, int32_t* kv_len,
+                           int32_t* next_state, int32_t* position, int32_t* slot, void* stream) {
+  return plan(cache, n_req, n_tok, state, new_len, queue, q_start, kv_len, next_state, position, slot, true, stream);
+}
+
+int kv_paged_trim(const skv_paged* cache, int32_t n_req, const int32_t* state, const int32_t* keep,
+                  int32_t evicted, int32_t* queue, int32_t* next_state, void* stream) {
+  int rc = check_pool(cache);
+  if (rc) return rc;
+  if (n_req < 0 || evicted < 0 || evicted > SKV_TRIM_EVICTED) return SKV_ERR_INVALID;
+  if (n_req > SKV_PAGED_MAX_REQUESTS) return SKV_ERR_UNSUPPORTED;
+  if (!aligned(state, 4) || !aligned(queue, 4) || !aligned(next_state, 4)) return SKV_ERR_INVALID;
+  if (n_req && !aligned(keep, 4)) return SKV_ERR_INVALID;
+  const size_t req = (size_t)n_req, words = (evicted ? 2 * req : req) + 2;
+  const Range used[] = {{state, words}, {keep, req}, {cache->block_table, req * (size_t)cache->max_block},
+                        {queue, (size_t)cache->n_page}, {next_state, words}, {cache->status, 1}};
+  for (int i = 3; i < 6; ++i)                      // the first three are only read
+    for (int j = 0; j < i; ++j)
+      if (overlap(used[i], used[j])) return SKV_ERR_INVALID;
+  if ((rc = skv::check_device())) return rc;
+  skv::TrimArgs a{};
+  a.n_req = n_req;
+  a.n_page = cache->n_page;
+  a.page_size = cache->page_size;
+  a.max_block = cache->max_block;
+  a.ps_m = skv::fastdiv_m((uint32_t)cache->page_size);
+  a.state = state;
+  a.keep = keep;
+  a.evicted = evicted;
+  a.table = cache->block_table;
+  a.queue = queue;
+  a.next_state = next_state;
+  a.status = cache->status;
+  const cudaError_t e = skv::launch_paged_trim(a, (cudaStream_t)stream);
   return e == cudaSuccess ? SKV_OK : skv::record_cuda_error(e);
 }
 

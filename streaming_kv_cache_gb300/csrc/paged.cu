@@ -1,7 +1,7 @@
 // The paged cache's bookkeeping and writes: block tables, slot maps and free
-// pages of a step from the requests' lengths (kv_paged_plan), and a step's
-// keys and values into their pages with the rotary embedding of q and k
-// (kv_paged_write).
+// pages of a step from the requests' lengths (kv_paged_plan), requests cut to
+// fewer tokens (kv_paged_trim), and a step's keys and values into their pages
+// with the rotary embedding of q and k (kv_paged_write).
 #include <atomic>
 
 #include "common.cuh"
@@ -86,6 +86,8 @@ __device__ __forceinline__ int find_request(const int* sums, int n, int x) {
   return lo;
 }
 
+// EVICTING: the state's evicted words shift the positions.
+template <bool EVICTING>
 __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
   extern __shared__ int sm[];
   const int n = a.n_req;
@@ -175,6 +177,8 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
     a.next_state[n] = (int)ring((uint32_t)given);
     a.next_state[n + 1] = count - given + back;
   }
+  // tokens evicted from a request that holds c
+  auto evicted = [&](int b, int c) { return c > 0 ? max(a.state[n + 2 + b], 0) : 0; };
   const int stride = gridDim.x * PT, first = blockIdx.x * PT + tid;
   for (int t = first; t < a.n_tok; t += stride) {
     int pos = 0, slot = -1;
@@ -191,6 +195,7 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
         if (page >= 0 && page < a.n_page) slot = page * (int)ps + r;
         else set_status(a.status, SKV_DEV_BAD_PAGE);
       }
+      if constexpr (EVICTING) pos = (int)min((long long)pos + evicted(b, c), 0x7FFFFFFFLL);
     }
     a.position[t] = pos;
     a.slot[t] = slot;
@@ -201,6 +206,11 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
     const bool ok = planned(b, c, w);
     a.kv_len[b] = ok ? c + w : 0;
     a.next_state[b] = c >= 0 && w == -1 ? 0 : ok ? c + w : c >= 0 ? c : a.state[b];
+    if constexpr (EVICTING) {
+      const int e = a.state[n + 2 + b];
+      if (e < 0) set_status(a.status, SKV_DEV_BAD_LEN);
+      a.next_state[n + 2 + b] = c < 0 ? e : w == -1 ? 0 : evicted(b, c);
+    }
   }
   for (int i = first; i < given; i += stride) {
     const int b = find_request(s_need, n, i);
@@ -210,6 +220,77 @@ __global__ void __launch_bounds__(PT) paged_plan_kernel(const PlanArgs a) {
   for (int i = first; i < back; i += stride) {
     const int b = find_request(s_back, n, i);
     a.queue[ring((uint32_t)(count + i))] = a.table[(size_t)b * a.max_block + (i - s_back[b])];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Trim.  One running sum, of the pages that the requests give back, decides
+// where each page goes; as in the plan every CTA repeats the scan, and an item
+// (a request, a page given back) is independent of the others.
+
+__global__ void __launch_bounds__(PT) paged_trim_kernel(const TrimArgs a) {
+  extern __shared__ int sm[];
+  const int n = a.n_req;
+  int* s_back = sm;                // running sums of the pages given back
+  int* s_left = s_back + n + 1;    // pages that stay
+  __shared__ int warp_sum[1][PT / 32];
+  const int tid = threadIdx.x;
+  const int row_tokens = (int)min((long long)a.max_block * a.page_size, (long long)kMaxKeys);
+  auto pages = [&](int x) {
+    int rem;
+    const int q = fastdiv(x, a.page_size, a.ps_m, rem);
+    return q + (rem > 0);
+  };
+  const bool reporter = blockIdx.x == 0;
+  tc::grid_dep_wait();
+
+  int head = a.state[n], count = a.state[n + 1];
+  for (int b = tid; b < n; b += PT) {
+    const int c = a.state[b], k = a.keep[b];
+    const bool bad = c < 0 || c > row_tokens || k < 0;
+    if (bad && reporter) set_status(a.status, SKV_DEV_BAD_LEN);
+    const int left = bad ? 0 : pages(min(c, k));
+    s_left[b] = left;
+    s_back[b] = bad ? 0 : pages(c) - left;
+    if (reporter) {
+      const int kept = bad ? c : min(c, k);
+      a.next_state[b] = kept;
+      if (a.evicted) {
+        const int e = a.state[n + 2 + b];
+        int next = e;
+        if (!bad) {
+          if (e < 0) set_status(a.status, SKV_DEV_BAD_LEN);
+          const long long sum = (long long)max(e, 0) + (a.evicted == SKV_TRIM_EVICTED ? c - kept : 0);
+          next = kept == 0 ? 0 : (int)min(sum, 0x7FFFFFFFLL);
+        }
+        a.next_state[n + 2 + b] = next;
+      }
+    }
+  }
+  if (head < 0 || head >= a.n_page || count < 0 || count > a.n_page) {
+    head = 0;
+    count = 0;
+    if (reporter && tid == 0) set_status(a.status, SKV_DEV_BAD_LEN);
+  }
+  __syncthreads();
+  {
+    int* const v[1] = {s_back};
+    block_scan<1>(v, n, 0x7FFFFFFF, warp_sum);
+  }
+  const int room = a.n_page - count;
+  const int back = min(s_back[n], room);
+  if (reporter && tid == 0) {
+    if (s_back[n] > room) set_status(a.status, SKV_DEV_BAD_LEN);
+    a.next_state[n] = head;
+    a.next_state[n + 1] = count + back;
+  }
+  for (int i = blockIdx.x * PT + tid; i < back; i += gridDim.x * PT) {
+    const int b = find_request(s_back, n, i);
+    const int page = a.table[(size_t)b * a.max_block + s_left[b] + (i - s_back[b])];
+    if (page < 0 || page >= a.n_page) set_status(a.status, SKV_DEV_BAD_PAGE);
+    uint32_t at = (uint32_t)head + (uint32_t)(count + i);
+    if (at >= (uint32_t)a.n_page) at -= (uint32_t)a.n_page;
+    a.queue[at] = page;
   }
 }
 
@@ -325,17 +406,26 @@ cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st) {
   const long long want = (items + PT - 1) / PT;
   const int grid = (int)min(want > 0 ? want : 1LL, 152LL);
   const int smem = (5 * a.n_req + 3) * (int)sizeof(int);
-  static std::atomic<int> done[64];
+  auto kernel = a.evicting ? paged_plan_kernel<true> : paged_plan_kernel<false>;
+  static std::atomic<int> done[2][64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (smem > 48 * 1024 && !(dev >= 0 && dev < 64 && done[dev].load(std::memory_order_relaxed))) {
-    e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (smem > 48 * 1024 && !(dev >= 0 && dev < 64 && done[a.evicting][dev].load(std::memory_order_relaxed))) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (5 * SKV_PAGED_MAX_REQUESTS + 3) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) done[dev].store(1, std::memory_order_relaxed);
+    if (dev >= 0 && dev < 64) done[a.evicting][dev].store(1, std::memory_order_relaxed);
   }
-  return launch_dependent(paged_plan_kernel, dim3(grid), PT, smem, st, a);
+  return launch_dependent(kernel, dim3(grid), PT, smem, st, a);
+}
+
+cudaError_t launch_paged_trim(const TrimArgs& a, cudaStream_t st) {
+  // a thread per page that may come back, as in the plan
+  const long long items = max(1LL, min((long long)a.n_page, (long long)a.n_req * a.max_block));
+  const int grid = (int)min((items + PT - 1) / PT, 152LL);
+  static_assert((2 * SKV_PAGED_MAX_REQUESTS + 1) * sizeof(int) <= 48 * 1024 - 256, "shared memory");
+  return launch_dependent(paged_trim_kernel, dim3(grid), PT, (2 * a.n_req + 1) * (int)sizeof(int), st, a);
 }
 
 cudaError_t launch_paged_write(const WriteArgs& a, int d, bool f16, cudaStream_t st) {

@@ -23,8 +23,22 @@ struct PlanArgs {
   int32_t* position;        // [n_tok]
   int32_t* slot;            // [n_tok]
   int32_t* status;
+  bool evicting;            // state and next_state have n_req evicted words behind them
 };
 cudaError_t launch_paged_plan(const PlanArgs& a, cudaStream_t st);
+
+struct TrimArgs {
+  int n_req, n_page, page_size, max_block;
+  uint32_t ps_m;            // fastdiv multiplier of page_size
+  const int32_t* state;     // [n_req + 2], and n_req evicted words unless evicted is 0
+  const int32_t* keep;      // [n_req]
+  int evicted;              // 0, SKV_TRIM_DRAFTS or SKV_TRIM_EVICTED
+  const int32_t* table;     // [n_req][max_block]
+  int32_t* queue;           // [n_page]
+  int32_t* next_state;
+  int32_t* status;
+};
+cudaError_t launch_paged_trim(const TrimArgs& a, cudaStream_t st);
 
 struct WriteArgs {
   int n_tok, Hq, Hkv, n_page, page_size, rope_len;

@@ -19,6 +19,7 @@ SKV_NOALLOC_MAX_CACHE_VIEWS = 16384
 SKV_DEV_TIMEOUT, SKV_DEV_BAD_HEAD, SKV_DEV_TAIL_OVERFLOW, SKV_DEV_BAD_TAIL = 1, 2, 4, 8
 SKV_DEV_NO_PAGE, SKV_DEV_BAD_LEN, SKV_DEV_BAD_PAGE, SKV_DEV_BAD_POS, SKV_DEV_TABLE_FULL = 16, 32, 64, 128, 256
 SKV_PAGED_MAX_REQUESTS, SKV_MAX_KEYS = 4096, 1 << 26
+SKV_TRIM_DRAFTS, SKV_TRIM_EVICTED = 1, 2
 _Tensor = torch.Tensor                                 # looked up several times a call
 _DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1}   # SKV_BF16, SKV_FP16
 
@@ -28,7 +29,8 @@ EXPORTS = ("skv_version", "skv_status_string", "skv_last_cuda_error", "skv_row_c
            "stream_attn_prefill", "stream_attn_prefill_insert", "stream_attn_prefill_tail",
            "stream_attn_window",
            "skv_verify_workspace_bytes", "stream_attn_verify",
-           "kv_paged_plan", "kv_paged_write", "skv_attn_workspace_bytes", "paged_attn", "cross_attn")
+           "kv_paged_plan", "kv_paged_write", "skv_attn_workspace_bytes", "paged_attn", "cross_attn",
+           "kv_paged_plan_evicting", "kv_paged_trim")
 
 
 class SkvError(RuntimeError):
@@ -111,6 +113,8 @@ def lib():
                            ctypes.c_int),
             "cross_attn": ([ctypes.POINTER(skv_states), I32, I32, I32, P, I64, P, P, P, P, SZ,
                             ctypes.c_float, P], ctypes.c_int),
+            "kv_paged_plan_evicting": ([pp, I32, I32, P, P, P, P, P, P, P, P, P], ctypes.c_int),
+            "kv_paged_trim": ([pp, I32, P, P, I32, P, P, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -465,15 +469,18 @@ def _rows(t, heads, d, dtype, name, dev):
 
 class PagedPlan:
     """The plan of one step (see kv_paged_plan in include/skv.h): int32
-    tensors q_start [n_req + 1], kv_len [n_req], next_state [n_req + 2],
-    position [n_tok] and slot [n_tok], which stay where they are."""
+    tensors q_start [n_req + 1], kv_len [n_req], next_state [n_req + 2] (of an
+    evicting cache [2 * n_req + 2]), position [n_tok] and slot [n_tok], which
+    stay where they are."""
 
-    __slots__ = ("_t", "_args", "n_req", "n_tok", "_dev")
+    __slots__ = ("_t", "_args", "n_req", "n_tok", "_dev", "evicts")
 
     def __init__(self, q_start, kv_len, next_state, position, slot):
         self._t = (q_start, kv_len, next_state, position, slot)
         n_req, n_tok = kv_len.numel(), slot.numel()
-        for t, n, name in zip(self._t, (n_req + 1, n_req, n_req + 2, n_tok, n_tok),
+        self.evicts = n_req > 0 and next_state.numel() == 2 * n_req + 2
+        words = 2 * n_req + 2 if self.evicts else n_req + 2
+        for t, n, name in zip(self._t, (n_req + 1, n_req, words, n_tok, n_tok),
                               ("q_start", "kv_len", "next_state", "position", "slot")):
             _need(t, (n,), torch.int32, name)
             _on_dev(t.get_device(), name, q_start.get_device())
@@ -487,10 +494,10 @@ class PagedPlan:
     slot = property(lambda self: self._t[4])
 
     @classmethod
-    def empty(cls, n_req, n_tok, device="cuda"):
+    def empty(cls, n_req, n_tok, device="cuda", evicts=False):
         i32 = dict(dtype=torch.int32, device=device)
-        return cls(torch.empty(n_req + 1, **i32), torch.empty(n_req, **i32), torch.empty(n_req + 2, **i32),
-                   torch.empty(n_tok, **i32), torch.empty(n_tok, **i32))
+        return cls(torch.empty(n_req + 1, **i32), torch.empty(n_req, **i32),
+                   torch.empty((2 * n_req if evicts else n_req) + 2, **i32), torch.empty(n_tok, **i32), torch.empty(n_tok, **i32))
 
 
 class PagedCache:
@@ -500,12 +507,15 @@ class PagedCache:
       k, v         bf16 or fp16 [n_page][Hkv][page_size][d], per layer
       block_table  int32 [n_req][max_block]  pages of each request
       page_queue   int32 [n_page]            ring of free pages
-      state        int32 [n_req + 2]         tokens held per request, queue head and count
+      state        int32 [n_req + 2]         tokens held per request, queue head and count; with evicts
+                                             [2 * n_req + 2]: and tokens evicted per request
       rope         fp32 [rope_len][d/2][2]   (cos, sin) table, or None
       status       int32 [1]                 device status bits
 
-    theta gives the rope table of positions below max_block * page_size
-    (None: keys and queries are not rotated).  The layers of a model share
+    theta gives the rope table of positions below max_block * page_size, or
+    rope_len (None: keys and queries are not rotated).  evicts: tokens may be
+    evicted, so that a request's positions go on past the tokens that it holds
+    and rope_len is what limits them.  The layers of a model share
     everything but k and v: layer(i) is the cache of one of them.  wait_ns
     limits every wait inside paged_attn (0: two seconds) and may be set later;
     everything else is fixed, because the calls keep its addresses.
@@ -517,17 +527,18 @@ class PagedCache:
         object.__setattr__(self, name, value)
 
     def __init__(self, n_page, page_size, Hkv, d, n_req, max_block, theta=None, dtype=torch.bfloat16,
-                 n_layer=1, device="cuda", wait_ns=0):
+                 n_layer=1, device="cuda", wait_ns=0, evicts=False, rope_len=None):
         dev = torch.device(device)
         shape = (n_layer, n_page, Hkv, page_size, d)
         i32 = dict(dtype=torch.int32, device=dev)
         rope = None
         if theta is not None:
-            rope = torch.empty((max_block * page_size, d // 2, 2), dtype=torch.float32, device=dev)
+            rope = torch.empty((max_block * page_size if rope_len is None else rope_len, d // 2, 2), dtype=torch.float32,
+                               device=dev)
             with torch.cuda.device(dev):
                 skv_build_rope_table(rope, theta)
-        state = torch.zeros((n_req + 2,), **i32)
-        state[-1] = n_page
+        state = torch.zeros(((2 * n_req if evicts else n_req) + 2,), **i32)
+        state[n_req + 1] = n_page
         self._k, self._v = (torch.empty(shape, dtype=dtype, device=dev) for _ in range(2))
         self._set(self._k[0], self._v[0], torch.zeros((n_req, max_block), **i32),
                   torch.arange(n_page, **i32), state, rope, torch.zeros((1,), **i32), page_size)
@@ -536,16 +547,24 @@ class PagedCache:
     @classmethod
     def wrap(cls, k=None, v=None, block_table=None, page_queue=None, state=None, rope=None, status=None,
              page_size=None, wait_ns=0):
-        """A cache over tensors that the caller owns.  k and v may be left
-        out where only kv_paged_plan is called, page_queue and state where it
-        is not; status is made where it is not given."""
+        """A cache over tensors that the caller owns.  k and v (with a layer
+        axis in front for several layers) may be left out where only
+        kv_paged_plan and kv_paged_trim are called, page_queue and state where
+        they are not; status is made where it is not given."""
         self = cls.__new__(cls)
         if block_table is None:
             raise ValueError("block_table must be a (requests, max_block) tensor")
         if status is None:
             status = torch.zeros((1,), dtype=torch.int32, device=block_table.device)
-        self._k = k[None] if k is not None else None
-        self._v = v[None] if v is not None else None
+        if k is not None and v is not None and k.dim() == 5:
+            if not len(k):
+                raise ValueError("k has no layers")
+            _need(k, k.shape, k.dtype, "k")
+            _need(v, k.shape, k.dtype, "v")
+            self._k, self._v, k, v = k, v, k[0], v[0]
+        else:
+            self._k = k[None] if k is not None else None
+            self._v = v[None] if v is not None else None
         self._set(k, v, block_table, page_queue, state, rope, status, page_size)
         self.wait_ns = wait_ns
         return self
@@ -574,15 +593,16 @@ class PagedCache:
             n_page = page_queue.numel()
         if page_queue is not None:
             _need(page_queue, (n_page,), torch.int32, "page_queue")
+        n_req, max_block = block_table.shape
+        evicts = state is not None and n_req > 0 and state.numel() == 2 * n_req + 2
         if state is not None:
-            _need(state, (block_table.shape[0] + 2,), torch.int32, "state")
+            _need(state, ((2 * n_req if evicts else n_req) + 2,), torch.int32, "state")
         if rope is not None:
             _need(rope, (rope.shape[0], d // 2, 2), torch.float32, "rope table")
         for name, t in (("k", k), ("v", v), ("page_queue", page_queue), ("state", state), ("rope", rope),
                         ("status", status)):
             if t is not None and t.device != block_table.device:
                 raise ValueError("%s is on %s, block_table on %s" % (name, t.device, block_table.device))
-        n_req, max_block = block_table.shape
         ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
         desc = skv_paged(n_page, page_size, hkv, d, code, rope.shape[0] if rope is not None else 0, max_block, 0,
                          ptr(k), ptr(v), ptr(block_table), ptr(rope), ptr(status))
@@ -591,7 +611,7 @@ class PagedCache:
             k=k, v=v, block_table=block_table, page_queue=page_queue, state=state, rope=rope, status=status,
             n_page=n_page, page_size=page_size, Hkv=hkv, d=d, n_req=n_req, max_block=max_block,
             _state_arg=ctypes.c_void_p(ptr(state)), _queue_arg=ctypes.c_void_p(ptr(page_queue)),
-            _desc=desc, _ref=ctypes.byref(desc), _dev=block_table.get_device(),
+            _desc=desc, _ref=ctypes.byref(desc), _dev=block_table.get_device(), evicts=evicts,
             _dtype=k.dtype if k is not None else None, _made=True)
 
     def layer(self, i: int) -> "PagedCache":
@@ -615,9 +635,15 @@ class PagedCache:
     def wait_ns(self, ns):
         self._desc.wait_ns = int(ns)
 
-    def advance(self, plan: PagedPlan):
-        """Take the state that a plan leads to as the cache's state."""
-        self.state.copy_(plan.next_state)
+    def advance(self, plan: PagedPlan | torch.Tensor):
+        """Take the state that a plan (or kv_paged_trim's result) leads to as
+        the cache's state."""
+        self.state.copy_(plan if isinstance(plan, torch.Tensor) else plan.next_state)
+
+    @property
+    def evicted(self) -> torch.Tensor | None:
+        """Tokens evicted so far, per request (the state's evicted words)."""
+        return self.state[self.n_req + 2:] if self.evicts else None
 
     def device_status(self) -> int:
         return int(self.status.item())
@@ -634,15 +660,45 @@ def kv_paged_plan(cache: PagedCache, new_len: torch.Tensor, n_tok: int,
     _on_dev(cache._dev, "the cache", dev)
     _on(new_len, (n_req,), torch.int32, "new_len", dev)
     if plan is None:
-        plan = PagedPlan.empty(n_req, n_tok, new_len.device)
+        plan = PagedPlan.empty(n_req, n_tok, new_len.device, cache.evicts)
     if plan.n_req != n_req or plan.n_tok != n_tok:
         raise ValueError("the plan is for %d requests and %d tokens, not %d and %d" % (plan.n_req, plan.n_tok, n_req, n_tok))
+    if plan.evicts != cache.evicts:
+        raise ValueError("the plan's next_state has %sevicted words, the cache's state %s" % (
+            "" if plan.evicts else "no ", "has" if cache.evicts else "has none"))
     _on_dev(plan._dev, "the plan", dev)
-    rc = lib().kv_paged_plan(cache._ref, n_req, n_tok, cache._state_arg, new_len.data_ptr(), cache._queue_arg,
-                             *plan._args, _raw_stream(dev))
+    call = lib().kv_paged_plan_evicting if cache.evicts else lib().kv_paged_plan
+    rc = call(cache._ref, n_req, n_tok, cache._state_arg, new_len.data_ptr(), cache._queue_arg, *plan._args,
+              _raw_stream(dev))
     if rc:
         _check(rc, "kv_paged_plan")
     return plan
+
+
+def kv_paged_trim(cache: PagedCache, keep: torch.Tensor, evict: bool = False,
+                  next_state: torch.Tensor | None = None) -> torch.Tensor:
+    """Requests cut to their first keep[b] tokens; the pages behind them go
+    back to the free queue.  evict: the tokens count as evicted, so that
+    positions go on (an evicting cache only); else they are taken back with
+    their positions, as rejected drafts are.  Returns the state after the cut;
+    the cache's own stays until cache.advance(next_state)."""
+    if cache.state is None or cache.page_queue is None:
+        raise ValueError("the cache has no state and page_queue to trim")
+    if evict and not cache.evicts:
+        raise ValueError("the cache has no evicted words to count in")
+    dev = _call_device(keep, "keep")
+    _on_dev(cache._dev, "the cache", dev)
+    _on(keep, (cache.n_req,), torch.int32, "keep", dev)
+    if next_state is None:
+        next_state = torch.empty_like(cache.state)
+    else:
+        _on(next_state, tuple(cache.state.shape), torch.int32, "next_state", dev)
+    mode = (SKV_TRIM_EVICTED if evict else SKV_TRIM_DRAFTS) if cache.evicts else 0
+    rc = lib().kv_paged_trim(cache._ref, cache.n_req, cache._state_arg, keep.data_ptr(), mode, cache._queue_arg,
+                             next_state.data_ptr(), _raw_stream(dev))
+    if rc:
+        _check(rc, "kv_paged_trim")
+    return next_state
 
 
 def _need_pages(cache, dev):
