@@ -71,6 +71,8 @@ extern "C" {
 #define SKV_DEV_BAD_PAGE 64      /* a page or slot outside the pool; read as zeros, not written */
 #define SKV_DEV_BAD_POS 128      /* kv_paged_write: a position outside the rope table; that token was skipped */
 #define SKV_DEV_TABLE_FULL 256   /* kv_paged_plan: a request outgrew its table row or the step's token rows */
+#define SKV_DEV_BAD_TOKEN 512    /* verify_sampled: a drafted token outside the vocabulary; it was rejected */
+#define SKV_DEV_BAD_PROB 1024    /* verify_sampled: an entry that is no probability (counted as 0), or a row without any */
 
 /*
  * One set of C independent caches (model layers x batch) of identical
@@ -393,6 +395,7 @@ int stream_attn_verify(const skv_cache* cache, int32_t n_q_head, int32_t blk,
  */
 #define SKV_BF16 0
 #define SKV_FP16 1
+#define SKV_FP32 2 /* verify_sampled only */
 #define SKV_MAX_KEYS (1 << 26) /* tokens that a request may hold or read */
 
 /*
@@ -635,6 +638,56 @@ int kv_paged_plan_evicting(const skv_paged* cache, int32_t n_req, int32_t n_tok,
 #define SKV_TRIM_EVICTED 2
 int kv_paged_trim(const skv_paged* cache, int32_t n_req, const int32_t* state, const int32_t* keep,
                   int32_t evicted, int32_t* queue, int32_t* next_state, void* stream);
+
+/*
+ * verify_sampled -- sampled acceptance of drafted tokens: the target model's
+ * probabilities p, the drafter's q and given random numbers decide how many of
+ * a request's drafts are kept and which token follows, so that the tokens are
+ * distributed as the target's own would be.  (stream_attn_verify's ids are the
+ * greedy form.)
+ *
+ * Request b owns rows [q_start[b], q_start[b+1]), n of them (kv_paged_plan's
+ * q_start): row 0 is the last accepted token, rows 1 .. n-1 the drafts.  Row i
+ * of p and q is the distribution after token i.
+ *
+ * token:  device int32 [n_tok]
+ * p:      device [n_tok][n_vocab] of dtype (SKV_BF16, SKV_FP16 or SKV_FP32),
+ *         p_stride >= n_vocab elements from row to row; any alignment of the
+ *         type.  Row n-1 is read only where every draft is accepted
+ * q:      the same, or NULL: the drafter gives no probabilities (it proposed
+ *         each draft with certainty, q(x) = 1).  Row n-1 is not read
+ * u:      device fp32 [n_tok] uniform in [0, 1): draft i + 1 is accepted iff
+ *         u[i] * q_i(x) < p_i(x) (exact); a request's last is not read
+ * r:      device fp32 [n_req] uniform in [0, 1)
+ * kv_len: device int32 [n_req] with held, else NULL: kv_paged_plan's, which
+ *         counts the whole block
+ *
+ * Writes accept_len[b], the drafts accepted before the first that is not;
+ * next_token[b], the smallest index whose running sum of w passes r sum(w),
+ * with w = max(p_i - q_i, 0) of the row i where a draft was rejected (p
+ * without the draft where q is NULL), p of row n-1 where none was, and p too
+ * where w is all zeros; and held[b] = kv_len[b] - n + accept_len[b] + 1, the
+ * tokens of the request that stay, which kv_paged_trim takes as keep (held may
+ * be kv_len itself).  Sums are whole numbers of 2^-55, each entry rounded to
+ * one (under 2^-56: to 0): the same on every run and in any split of a row.
+ *
+ * An entry outside [0, 2] (NaN among them) counts as 0 and sets
+ * SKV_DEV_BAD_PROB where a sum meets it; a row whose sum is 0 or passes 8 sets
+ * it too and gives next_token -1.  u or r outside [0, 1) act as the formulas
+ * say: r <= 0 or NaN takes the first entry above 0, r >= 1 the last.  A draft
+ * outside [0, n_vocab) is rejected and sets SKV_DEV_BAD_TOKEN.  A request
+ * without rows gets 0 and -1, and held its kv_len; so does a span outside
+ * [0, n_tok], which sets SKV_DEV_BAD_LEN.
+ * accept_len, next_token, held and status overlap nothing else of the call's
+ * int32 and uniform arrays (refused), nor p and q (not looked for).
+ * n_req <= SKV_MAX_SAMPLED; n_tok and n_vocab <= 2^30.
+ */
+#define SKV_MAX_SAMPLED (1 << 24)
+int verify_sampled(int32_t n_req, int32_t n_tok, int32_t n_vocab, int32_t dtype,
+                   const int32_t* q_start, const int32_t* token, const void* p, int64_t p_stride,
+                   const void* q, int64_t q_stride, const float* u, const float* r,
+                   const int32_t* kv_len, int32_t* accept_len, int32_t* next_token, int32_t* held,
+                   int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -14,4 +14,4 @@ from .skv import (EXPORTS, PagedCache, PagedPlan, SkvError, StreamCache, attn_wo
                   lib, paged_attn, skv_build_rope_table, skv_row_cap, skv_verify_workspace_bytes,
                   skv_build_mrope_table, status_string, stream_attn_prefill,
                   stream_attn_prefill_insert, stream_attn_prefill_tail, stream_attn_verify,
-                  stream_attn_window, verify_workspace)
+                  stream_attn_window, verify_sampled, verify_workspace)

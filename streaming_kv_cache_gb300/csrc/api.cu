@@ -125,6 +125,8 @@ const char* skv_status_string(int code) {
     case SKV_DEV_BAD_PAGE: return "device: a page or slot outside the pool";
     case SKV_DEV_BAD_POS: return "device: a position outside the rope table";
     case SKV_DEV_TABLE_FULL: return "device: a request outgrew its table row or the step's token rows";
+    case SKV_DEV_BAD_TOKEN: return "device: a drafted token outside the vocabulary";
+    case SKV_DEV_BAD_PROB: return "device: an entry that is no probability, or a row without any";
     default: return code > 0 ? "device: several status bits set" : "unknown status";
   }
 }

@@ -20,8 +20,10 @@ SKV_DEV_TIMEOUT, SKV_DEV_BAD_HEAD, SKV_DEV_TAIL_OVERFLOW, SKV_DEV_BAD_TAIL = 1, 
 SKV_DEV_NO_PAGE, SKV_DEV_BAD_LEN, SKV_DEV_BAD_PAGE, SKV_DEV_BAD_POS, SKV_DEV_TABLE_FULL = 16, 32, 64, 128, 256
 SKV_PAGED_MAX_REQUESTS, SKV_MAX_KEYS = 4096, 1 << 26
 SKV_TRIM_DRAFTS, SKV_TRIM_EVICTED = 1, 2
+SKV_DEV_BAD_TOKEN, SKV_DEV_BAD_PROB, SKV_MAX_SAMPLED = 512, 1024, 1 << 24
 _Tensor = torch.Tensor                                 # looked up several times a call
 _DTYPE_CODE = {torch.bfloat16: 0, torch.float16: 1}   # SKV_BF16, SKV_FP16
+_PROB_CODE = {**_DTYPE_CODE, torch.float32: 2}          # SKV_FP32
 
 # every function the C header declares
 EXPORTS = ("skv_version", "skv_status_string", "skv_last_cuda_error", "skv_row_cap",
@@ -30,7 +32,7 @@ EXPORTS = ("skv_version", "skv_status_string", "skv_last_cuda_error", "skv_row_c
            "stream_attn_window",
            "skv_verify_workspace_bytes", "stream_attn_verify",
            "kv_paged_plan", "kv_paged_write", "skv_attn_workspace_bytes", "paged_attn", "cross_attn",
-           "kv_paged_plan_evicting", "kv_paged_trim")
+           "kv_paged_plan_evicting", "kv_paged_trim", "verify_sampled")
 
 
 class SkvError(RuntimeError):
@@ -115,6 +117,7 @@ def lib():
                             ctypes.c_float, P], ctypes.c_int),
             "kv_paged_plan_evicting": ([pp, I32, I32, P, P, P, P, P, P, P, P, P], ctypes.c_int),
             "kv_paged_trim": ([pp, I32, P, P, I32, P, P, P], ctypes.c_int),
+            "verify_sampled": ([I32, I32, I32, I32, P, P, P, I64, P, I64, P, P, P, P, P, P, P, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -823,3 +826,69 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_start: torch
     if rc:
         _check(rc, "cross_attn")
     return (out, lse) if lse is not None else out
+
+
+# ------------------------------------------- sampled verification, eviction
+
+
+def _prob_rows(t, n, n_vocab, dtype, name, dev):
+    """The row stride of probabilities [rows][vocabulary], rows contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != (n, n_vocab):
+        raise ValueError("%s must have shape (%d, %d), got %s" % (name, n, n_vocab, tuple(t.shape)))
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError("%s must be on a CUDA device" % name)
+        _on_dev(t.get_device(), name, dev)
+    s0, s1 = t.stride()
+    if n_vocab > 1 and s1 != 1:
+        raise ValueError("%s must have contiguous rows" % name)
+    return s0 if n > 1 else n_vocab
+
+
+def verify_sampled(p: torch.Tensor, token: torch.Tensor, q_start: torch.Tensor, u: torch.Tensor, r: torch.Tensor, *,
+                   status: torch.Tensor, q: torch.Tensor | None = None, kv_len: torch.Tensor | None = None,
+                   accept_len: torch.Tensor | None = None, next_token: torch.Tensor | None = None,
+                   held: torch.Tensor | None = None):
+    """Sampled acceptance of drafted tokens (see include/skv.h): p and q
+    [tokens][vocabulary] are the target's and the drafter's probabilities (q
+    None: the drafter proposed with certainty), u [tokens] and r [requests]
+    uniform random numbers.  Returns (accept_len, next_token, held); held, the
+    tokens that stay (kv_paged_trim's keep), is None without kv_len."""
+    dev = _call_device(p, "p")
+    if p.dim() != 2 or p.dtype not in _PROB_CODE:
+        raise ValueError("p must be a bfloat16, float16 or float32 tensor (tokens, vocabulary), got %s %s" % (p.dtype, tuple(p.shape)))
+    n_tok, n_vocab = p.shape
+    ps = _prob_rows(p, n_tok, n_vocab, p.dtype, "p", dev)
+    qs = _prob_rows(q, n_tok, n_vocab, p.dtype, "q", dev) if q is not None else 0
+    if not isinstance(r, torch.Tensor):
+        raise TypeError("r must be a torch.Tensor")
+    n_req = r.numel()
+    _on(r, (n_req,), torch.float32, "r", dev)
+    _on(q_start, (n_req + 1,), torch.int32, "q_start", dev)
+    _on(token, (n_tok,), torch.int32, "token", dev)
+    _on(u, (n_tok,), torch.float32, "u", dev)
+    _on(status, (1,), torch.int32, "status", dev)
+    if kv_len is not None:
+        _on(kv_len, (n_req,), torch.int32, "kv_len", dev)
+    elif held is not None:
+        raise ValueError("held without kv_len")
+    outs = []
+    for t, name in ((accept_len, "accept_len"), (next_token, "next_token"), (held, "held")):
+        if t is not None:
+            _on(t, (n_req,), torch.int32, name, dev)
+        elif name != "held" or kv_len is not None:
+            t = torch.empty((n_req,), dtype=torch.int32, device=p.device)
+        outs.append(t)
+    accept_len, next_token, held = outs
+    rc = lib().verify_sampled(n_req, n_tok, n_vocab, _PROB_CODE[p.dtype], q_start.data_ptr(), token.data_ptr(),
+                              p.data_ptr(), ps, q.data_ptr() if q is not None else None, qs, u.data_ptr(), r.data_ptr(),
+                              kv_len.data_ptr() if kv_len is not None else None, accept_len.data_ptr(),
+                              next_token.data_ptr(), held.data_ptr() if held is not None else None, status.data_ptr(),
+                              _raw_stream(dev))
+    if rc:
+        _check(rc, "verify_sampled")
+    return accept_len, next_token, held

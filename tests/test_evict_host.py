@@ -131,3 +131,65 @@ def test_plan_evicting_counts_the_evicted_words_in_its_overlaps(L):
     assert call(FAKE * 10 + 4 * 7, FAKE * 10) == skv.SKV_ERR_INVALID
     if not torch.cuda.is_available():
         assert call(FAKE * 10 - 4 * 8, FAKE * 10) in NO_GPU
+
+
+# ------------------------------------------------------ sampled verification
+
+def test_oracle_verify_by_hand():
+    p = np.array([[0.5, 0.25, 0.25, 0.0], [0.1, 0.2, 0.3, 0.4], [0.25, 0.25, 0.25, 0.25]])
+    q = np.array([[0.25, 0.5, 0.25, 0.0], [0.4, 0.3, 0.2, 0.1], [9, 9, 9, 9]])
+    # draft 1 has p / q = 1 / 2, draft 0 then 1 / 4
+    assert EO.verify([9, 1, 0], p, q, [0.49, 0.24, 0], 0.5) == (2, 2, 0)       # all accepted: p of the last row
+    assert EO.verify([9, 1, 0], p, q, [0.5, 0.24, 0], 0.9) == (0, 0, 0)        # u q < p is strict; the rest is 0.25 at 0
+    assert EO.verify([9, 1, 0], p, q, [0.49, 0.25, 0], 0.24) == (1, 2, 0)      # the rest 0, 0, 0.1, 0.3
+    assert EO.verify([9, 1, 0], p, q, [0.49, 0.25, 0], 0.26) == (1, 3, 0)
+    assert EO.verify([9, 1], p, None, [0.3, 0], 0.7) == (0, 2, 0)              # without q: p but for the draft
+    assert EO.verify([9], p, q, [0], 0.0) == (0, 0, 0)
+    assert EO.verify([9, 4], p, q, [0, 0], 0.0)[2] == EO.BAD_TOKEN
+
+
+def test_oracle_verify_keeps_the_target_distribution():
+    """Over a fine grid of u and r and the drafter's own draws, the first token
+    that comes out is distributed as the target's."""
+    p, q = np.array([[0.5, 0.2, 0.2, 0.1], [0.25] * 4]), np.array([[0.1, 0.6, 0.2, 0.1], [0.25] * 4])
+    grid = (np.arange(64) + 0.5) / 64
+    out = np.zeros(4)
+    for x in range(4):
+        for u in grid:
+            for r in grid:
+                a, t, status = EO.verify([0, x], p, q, [u, 0], r)
+                assert status == 0
+                out[x if a else t] += q[0, x] / 64 ** 2
+    # a threshold inside a cell of the grid is off by at most a cell
+    np.testing.assert_allclose(out, p[0], atol=2 / 64)
+
+
+def _sampled(L, n_req=3, n_tok=7, vocab=100, dtype=2, q_start=FAKE, token=FAKE * 2, p=FAKE * 3, ps=100, q=FAKE * 4, qs=100,
+             u=FAKE * 5, r=FAKE * 6, kv_len=FAKE * 7, acc=FAKE * 8, nxt=FAKE * 9, held=FAKE * 10, status=FAKE * 11):
+    return L.verify_sampled(n_req, n_tok, vocab, dtype, q_start, token, p, ps, q, qs, u, r, kv_len, acc, nxt, held, status, None)
+
+
+@no_gpu_here
+def test_good_verifications_reach_the_device_check(L):
+    for kw in (dict(), dict(q=None, qs=0), dict(kv_len=None, held=None), dict(dtype=0, p=FAKE + 2), dict(dtype=1, q=FAKE + 2),
+               dict(p=FAKE + 4), dict(ps=101, qs=1000), dict(held=FAKE * 7), dict(n_tok=0, p=None, token=None, u=None)):
+        assert _sampled(L, **kw) in NO_GPU, kw
+
+
+def test_a_verification_of_nothing(L):
+    assert _sampled(L, n_req=0, q_start=None, r=None, acc=None, nxt=None) == skv.SKV_OK
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n_req=-1), dict(n_tok=-1), dict(vocab=0), dict(dtype=3), dict(dtype=-1), dict(q_start=None), dict(token=None),
+    dict(token=FAKE + 2), dict(p=None), dict(p=FAKE + 2), dict(dtype=0, p=FAKE + 1), dict(ps=99), dict(qs=99), dict(q=FAKE + 2),
+    dict(u=None), dict(r=None), dict(r=FAKE + 1), dict(kv_len=None), dict(held=None), dict(acc=None), dict(nxt=None),
+    dict(status=None), dict(status=FAKE + 2), dict(acc=FAKE * 9), dict(nxt=FAKE * 9 - 8 + FAKE), dict(held=FAKE * 7 + 4),
+    dict(acc=FAKE), dict(nxt=FAKE * 2 + 24), dict(held=FAKE * 5 + 4), dict(status=FAKE * 6), dict(acc=FAKE * 7), dict(status=FAKE * 10)])
+def test_bad_verifications(L, bad):
+    assert _sampled(L, **bad) == skv.SKV_ERR_INVALID, bad
+
+
+@pytest.mark.parametrize("big", [dict(n_req=(1 << 24) + 1), dict(n_tok=(1 << 30) + 1), dict(vocab=(1 << 30) + 1)])
+def test_verifications_refused_as_too_large(L, big):
+    assert _sampled(L, **big) == skv.SKV_ERR_UNSUPPORTED
