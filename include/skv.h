@@ -639,6 +639,101 @@ int kv_paged_plan_evicting(const skv_paged* cache, int32_t n_req, int32_t n_tok,
 int kv_paged_trim(const skv_paged* cache, int32_t n_req, const int32_t* state, const int32_t* keep,
                   int32_t evicted, int32_t* queue, int32_t* next_state, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Eviction by accumulated attention weight.  Beside its keys and values each
+ * layer of the cache has, for every token of every kv head,
+ *
+ *   score  device fp32 [n_page][Hkv][page_size]   the attention weight that the
+ *          token has got so far
+ *   pos    device int32, the same shape           its position
+ *
+ * A step of an evicting cache is: plan (kv_paged_plan_evicting), per layer
+ * write, attend and paged_attn_weight; then, for all layers at once,
+ * kv_evict_plan and kv_evict_move; then kv_paged_trim with SKV_TRIM_EVICTED,
+ * once.  After an eviction a place holds another token for every kv head, in no
+ * order of their positions: paged_attn needs none.
+ * A page that several requests hold is not for evicting: what one of them
+ * moves the others read.
+ */
+
+/*
+ * paged_attn_weight -- the weight that each key of a request gets from the
+ * step's rows: w[h][j] = the sum of exp(sm_scale q.k_j - lse) over the rows
+ * that see key j (as in paged_attn) and the query heads of kv head h.  One
+ * layer; of `cache` everything but v and rope.
+ *
+ * q, q_start, kv_len, sm_scale, ws: paged_attn's; lse what it gave, device
+ * fp32 [Hq][n_tok]
+ * position: device int32 [n_tok], kv_paged_plan's
+ * add:   device fp32, a pool like score, or NULL: 0.  It may be score itself
+ *        and is apart from it otherwise
+ * score: of every key before the step of a request with rows, add + w; of the
+ *        step's own tokens, w (what lay there is another token's)
+ * pos:   of the step's own tokens, their position; nothing else is written
+ *
+ * Requests without rows are left out, their entries of score too.  A row
+ * whose lse is not finite gives nothing.  The weights of a row sum to 1 over
+ * its keys and query heads of a kv head to Hq / Hkv; a drafted token that is
+ * rejected later has given its weights all the same.  Scores and sums are
+ * fp32 and the same on every run, except that a page held by several requests
+ * gets the weights of one or more of them.  Lengths, spans and pages out of
+ * range as in paged_attn: the keys of a page outside the pool are skipped.
+ * A wait inside the kernel that passes cache->wait_ns sets SKV_DEV_TIMEOUT:
+ * the requests' scores and positions are then undefined.
+ * score and pos share no byte with anything else of the call (refused).
+ * n_req <= SKV_PAGED_MAX_REQUESTS, other limits as for paged_attn.
+ */
+int paged_attn_weight(const skv_paged* cache, int32_t n_q_head, int32_t n_req, int32_t n_tok,
+                      const void* q, int64_t q_stride, const int32_t* q_start,
+                      const int32_t* kv_len, const float* lse, const int32_t* position,
+                      const float* add, float* score, int32_t* pos, void* ws, size_t ws_bytes,
+                      float sm_scale, void* stream);
+
+/*
+ * kv_evict_plan -- which tokens stay, for every layer, request and kv head:
+ * of a request that holds m = kv_len[b] tokens, more than keep[b], the keep[b]
+ * best.  Tokens at positions below n_sink, and at the n_recent last positions
+ * before evicted[b] + m, come before all others; then those of larger score
+ * (NaN counts as the smallest); of equal ones those at lower indexes.  Of
+ * `cache` it uses n_page, page_size, n_kv_head, max_block, block_table and
+ * status.
+ *
+ * score, pos: n_layer pools, one after the other
+ * keep:    device int32 [n_req]
+ * evicted: device int32 [n_req], a state's evicted words, or NULL: zeros
+ * move:    device int32, pools like pos.  The i-th of the kept tokens at
+ *          indexes >= keep[b], in ascending order, goes to the i-th free place
+ *          below: entries 2 i and 2 i + 1 of the request (at the place of its
+ *          tokens 2 i and 2 i + 1) are the place's index and the token's.
+ *          The others are not written
+ * n_move:  device int32 [n_layer][n_req][Hkv]: how many moves there are; 0
+ *          where no token has to go, and where none is to stay
+ *
+ * Whole numbers, the same on every run; the call reads nothing that it writes
+ * (overlaps are refused).  kv_len outside [0, max_block * page_size] or above
+ * SKV_MAX_KEYS, or a negative keep, sets SKV_DEV_BAD_LEN and plans no move; a
+ * negative evicted word sets it and counts as 0.  A page outside the pool sets
+ * SKV_DEV_BAD_PAGE: its tokens come last.  score, pos and move are 16-byte
+ * aligned.  n_layer * n_req * Hkv <= 2^26.
+ */
+int kv_evict_plan(const skv_paged* cache, int32_t n_layer, int32_t n_req, const int32_t* kv_len,
+                  const int32_t* keep, const int32_t* evicted, int32_t n_sink, int32_t n_recent,
+                  const float* score, const int32_t* pos, int32_t* move, int32_t* n_move,
+                  void* stream);
+
+/*
+ * kv_evict_move -- the moves of kv_evict_plan: key, value, score and pos of
+ * the moved tokens, bit for bit, into their new places.  `cache` has the k and
+ * v of n_layer layers, one after the other; kv_len is the plan's.  The
+ * requests then hold keep[b] tokens (kv_paged_trim).  Places and tokens of a
+ * plan are apart, so the call may be repeated.  A count above kv_len / 2 or an
+ * index outside [0, kv_len) sets SKV_DEV_BAD_LEN, a page outside the pool
+ * SKV_DEV_BAD_PAGE; such moves are left out.
+ */
+int kv_evict_move(const skv_paged* cache, int32_t n_layer, int32_t n_req, const int32_t* kv_len,
+                  const int32_t* move, const int32_t* n_move, float* score, int32_t* pos,
+                  void* stream);
+
 /*
  * verify_sampled -- sampled acceptance of drafted tokens: the target model's
  * probabilities p, the drafter's q and given random numbers decide how many of

@@ -99,7 +99,7 @@ def select(score, pos, keep, after, n_sink, n_recent):
     if n <= keep:
         return []
     def rank(j):  # best first
-        if pos[j] < n_sink or pos[j] >= after - n_recent:
+        if pos[j] < n_sink or after - n_recent <= pos[j] < after:
             return (0, 0.0, j)
         s = float(score[j])
         return (2, 0.0, j) if math.isnan(s) else (1, -s, j)

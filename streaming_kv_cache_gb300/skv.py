@@ -32,7 +32,8 @@ EXPORTS = ("skv_version", "skv_status_string", "skv_last_cuda_error", "skv_row_c
            "stream_attn_window",
            "skv_verify_workspace_bytes", "stream_attn_verify",
            "kv_paged_plan", "kv_paged_write", "skv_attn_workspace_bytes", "paged_attn", "cross_attn",
-           "kv_paged_plan_evicting", "kv_paged_trim", "verify_sampled")
+           "kv_paged_plan_evicting", "kv_paged_trim", "verify_sampled", "paged_attn_weight", "kv_evict_plan",
+           "kv_evict_move")
 
 
 class SkvError(RuntimeError):
@@ -117,6 +118,10 @@ def lib():
                             ctypes.c_float, P], ctypes.c_int),
             "kv_paged_plan_evicting": ([pp, I32, I32, P, P, P, P, P, P, P, P, P], ctypes.c_int),
             "kv_paged_trim": ([pp, I32, P, P, I32, P, P, P], ctypes.c_int),
+            "paged_attn_weight": ([pp, I32, I32, I32, P, I64, P, P, P, P, P, P, P, P, SZ, ctypes.c_float, P],
+                                  ctypes.c_int),
+            "kv_evict_plan": ([pp, I32, I32, P, P, P, I32, I32, P, P, P, P, P], ctypes.c_int),
+            "kv_evict_move": ([pp, I32, I32, P, P, P, P, P, P], ctypes.c_int),
             "verify_sampled": ([I32, I32, I32, I32, P, P, P, I64, P, I64, P, P, P, P, P, P, P, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -892,3 +897,147 @@ def verify_sampled(p: torch.Tensor, token: torch.Tensor, q_start: torch.Tensor, 
     if rc:
         _check(rc, "verify_sampled")
     return accept_len, next_token, held
+
+
+class PagedScores:
+    """What eviction keeps beside a paged cache, in device memory:
+
+      score   fp32 [n_layer][n_page][Hkv][page_size]    weight that each token has got
+      pos     int32, the same shape                     its position
+      move    int32, the same shape                     the last plan's moves
+      n_move  int32 [n_layer][n_req][Hkv]               how many there are
+
+    score and pos may be one layer's ([n_page][Hkv][page_size]); move and
+    n_move may be left out where only paged_attn_weight is called.  layer(i)
+    is the part of layer i."""
+
+    __slots__ = ("score", "pos", "move", "n_move")
+
+    def __init__(self, score, pos, move=None, n_move=None):
+        if not isinstance(score, torch.Tensor):
+            raise TypeError("score must be a torch.Tensor")
+        if score.dim() == 3:
+            score, pos = score[None], pos[None]
+            move = move[None] if move is not None else None
+            n_move = n_move[None] if n_move is not None else None
+        if score.dim() != 4:
+            raise ValueError("score must have shape (layers, pages, kv heads, page_size), got %s" % (tuple(score.shape),))
+        if (move is None) != (n_move is None):
+            raise ValueError("move and n_move come together")
+        for t, dt, name in ((score, torch.float32, "score"), (pos, torch.int32, "pos"), (move, torch.int32, "move")):
+            if t is not None:
+                _need(t, score.shape, dt, name)
+                _on_dev(t.get_device(), name, score.get_device())
+        if n_move is not None:
+            if n_move.dim() != 3 or n_move.shape[0] != score.shape[0] or n_move.shape[2] != score.shape[2]:
+                raise ValueError("n_move must have shape (layers, requests, kv heads), got %s" % (tuple(n_move.shape),))
+            _need(n_move, n_move.shape, torch.int32, "n_move")
+            _on_dev(n_move.get_device(), "n_move", score.get_device())
+        self.score, self.pos, self.move, self.n_move = score, pos, move, n_move
+
+    @classmethod
+    def empty(cls, cache: PagedCache) -> "PagedScores":
+        """Those of all of a cache's layers (zeros)."""
+        if cache.k is None:
+            raise ValueError("the cache has no k and v")
+        shape = (len(cache._k), cache.n_page, cache.Hkv, cache.page_size)
+        i32 = dict(dtype=torch.int32, device=cache.k.device)
+        return cls(torch.zeros(shape, dtype=torch.float32, device=cache.k.device), torch.zeros(shape, **i32),
+                   torch.zeros(shape, **i32), torch.zeros((shape[0], cache.n_req, cache.Hkv), **i32))
+
+    def layer(self, i: int) -> "PagedScores":
+        if i < 0:
+            i = range(len(self.score))[i]
+        new = PagedScores.__new__(PagedScores)
+        new.score, new.pos = self.score[i:i + 1], self.pos[i:i + 1]
+        new.move, new.n_move = (t[i:i + 1] if t is not None else None for t in (self.move, self.n_move))
+        return new
+
+
+def _need_scores(cache, scores, dev):
+    """The scores are those of the cache's layers; how many these are."""
+    _need_pages(cache, dev)
+    shape = (len(cache._k), cache.n_page, cache.Hkv, cache.page_size)
+    if scores.score.shape != shape:
+        raise ValueError("the scores have shape %s, the cache %s" % (tuple(scores.score.shape), shape))
+    _on_dev(scores.score.get_device(), "score", dev)
+    return shape[0]
+
+
+def paged_attn_weight(cache: PagedCache, scores: PagedScores, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+                      lse: torch.Tensor, position: torch.Tensor, sm_scale: float, add: torch.Tensor | bool = True,
+                      ws: torch.Tensor | None = None) -> None:
+    """The attention weight of a step's rows into one layer's scores (cache
+    and scores of that layer): q, q_start, kv_len and sm_scale are
+    paged_attn's, lse is what it gave, position the plan's.  add: what the
+    weights are added to: the scores themselves (True), another pool like
+    them, or nothing (False: score then holds this step's weights alone)."""
+    dev = _call_device(q, "q")
+    if _need_scores(cache, scores, dev) != 1:
+        raise ValueError("paged_attn_weight is a call of one layer: cache.layer(i), scores.layer(i)")
+    n_req = cache.n_req
+    n, hq, qs = _rows(q, None, cache.d, cache._dtype, "q", dev)
+    _on(q_start, (n_req + 1,), torch.int32, "q_start", dev)
+    _on(kv_len, (n_req,), torch.int32, "kv_len", dev)
+    _on(lse, (hq, n), torch.float32, "lse", dev)
+    _on(position, (n,), torch.int32, "position", dev)
+    if add is True:
+        add = scores.score
+    elif isinstance(add, torch.Tensor):
+        shape = tuple(scores.score.shape)
+        _on(add, shape[1:] if add.dim() == 3 else shape, torch.float32, "add", dev)
+    elif add is not False and add is not None:
+        raise TypeError("add must be a torch.Tensor or a bool")
+    else:
+        add = None
+    if ws is None:
+        ws = attn_workspace(q.device)
+    elif not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a torch.Tensor")
+    else:
+        _on(ws, (ws.numel(),), torch.uint8, "ws", dev)
+    rc = lib().paged_attn_weight(cache._ref, hq, n_req, n, q.data_ptr(), qs, q_start.data_ptr(), kv_len.data_ptr(),
+                                 lse.data_ptr(), position.data_ptr(), add.data_ptr() if add is not None else None,
+                                 scores.score.data_ptr(), scores.pos.data_ptr(), ws.data_ptr(), ws.numel(), sm_scale,
+                                 _raw_stream(dev))
+    if rc:
+        _check(rc, "paged_attn_weight")
+
+
+def _need_moves(cache, scores, dev):
+    n_layer = _need_scores(cache, scores, dev)
+    if scores.move is None:
+        raise ValueError("the scores have no move and n_move")
+    if scores.n_move.shape[1] != cache.n_req:
+        raise ValueError("n_move is for %d requests, the cache for %d" % (scores.n_move.shape[1], cache.n_req))
+    return n_layer
+
+
+def kv_evict_plan(cache: PagedCache, scores: PagedScores, kv_len: torch.Tensor, keep: torch.Tensor, n_sink: int = 0,
+                  n_recent: int = 0) -> None:
+    """Which tokens stay, in every layer and kv head of the requests that hold
+    more than keep[b]: the n_sink first and n_recent last positions, then those
+    of the largest score.  The moves that bring them into the first keep[b]
+    places go to scores.move and scores.n_move."""
+    dev = _call_device(kv_len, "kv_len")
+    n_layer = _need_moves(cache, scores, dev)
+    _on(kv_len, (cache.n_req,), torch.int32, "kv_len", dev)
+    _on(keep, (cache.n_req,), torch.int32, "keep", dev)
+    evicted = cache.state.data_ptr() + 4 * (cache.n_req + 2) if cache.evicts else None
+    rc = lib().kv_evict_plan(cache._ref, n_layer, cache.n_req, kv_len.data_ptr(), keep.data_ptr(), evicted, n_sink, n_recent,
+                             scores.score.data_ptr(), scores.pos.data_ptr(), scores.move.data_ptr(), scores.n_move.data_ptr(),
+                             _raw_stream(dev))
+    if rc:
+        _check(rc, "kv_evict_plan")
+
+
+def kv_evict_move(cache: PagedCache, scores: PagedScores, kv_len: torch.Tensor) -> None:
+    """The moves of the last kv_evict_plan: keys, values, scores and positions,
+    in every layer.  The requests then hold keep[b] tokens: kv_paged_trim."""
+    dev = _call_device(kv_len, "kv_len")
+    n_layer = _need_moves(cache, scores, dev)
+    _on(kv_len, (cache.n_req,), torch.int32, "kv_len", dev)
+    rc = lib().kv_evict_move(cache._ref, n_layer, cache.n_req, kv_len.data_ptr(), scores.move.data_ptr(),
+                             scores.n_move.data_ptr(), scores.score.data_ptr(), scores.pos.data_ptr(), _raw_stream(dev))
+    if rc:
+        _check(rc, "kv_evict_move")

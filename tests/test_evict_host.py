@@ -193,3 +193,116 @@ def test_bad_verifications(L, bad):
 @pytest.mark.parametrize("big", [dict(n_req=(1 << 24) + 1), dict(n_tok=(1 << 30) + 1), dict(vocab=(1 << 30) + 1)])
 def test_verifications_refused_as_too_large(L, big):
     assert _sampled(L, **big) == skv.SKV_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------ eviction
+
+def test_oracle_select_by_hand():
+    score, pos = [5, 1, 9, 2, 2, 0.5], [0, 7, 3, 4, 5, 6]
+    assert EO.select(score, pos, 6, 8, 1, 2) == []
+    # protected: position 0, and 6 and 7; of the others the 9
+    assert EO.select(score, pos, 4, 8, 1, 2) == [(3, 5)]
+    assert EO.select(score, pos, 3, 8, 1, 2) == [(2, 5)]
+    # nothing protected: 9, 5, then the first of the two 2s
+    assert EO.select(score, pos, 3, 8, 0, 0) == [(1, 3)]
+    assert EO.select([0.0, -0.0, float("nan"), -1.0], [0, 1, 2, 3], 2, 4, 0, 0) == []
+    assert EO.select([float("nan"), -1.0, float("inf")], [0, 1, 2], 2, 3, 0, 0) == [(0, 2)]
+
+
+def test_oracle_select_keeps_the_best():
+    rng = np.random.default_rng(1)
+    for _ in range(50):
+        n = int(rng.integers(2, 60))
+        keep = int(rng.integers(1, n))
+        score, pos = rng.integers(0, 9, n).astype(float), rng.permutation(n)
+        place = list(range(n))
+        for to, src in EO.select(score, pos, keep, n, 2, 5):
+            assert to < keep <= src
+            place[to] = src
+        got = place[:keep]
+        assert len(set(got)) == keep
+        best = sorted(range(n), key=lambda j: (not (pos[j] < 2 or pos[j] >= n - 5), -score[j] if 2 <= pos[j] < n - 5 else 0, j))[:keep]
+        assert set(got) == set(best)
+
+
+def _weight(L, pool=None, hq=4, n_req=3, n_tok=5, q=FAKE * 5, qs=256, q_start=FAKE * 6, kv_len=FAKE * 7, lse=FAKE * 8,
+            position=FAKE * 9, add=FAKE * 10, score=FAKE * 10, pos=FAKE * 11, ws=FAKE * 4096, ws_bytes=None, scale=1.0):
+    n = L.skv_attn_workspace_bytes() if ws_bytes is None else ws_bytes
+    return L.paged_attn_weight(ctypes.byref(pool or _pool()), hq, n_req, n_tok, q, qs, q_start, kv_len, lse, position, add, score,
+                               pos, ws, n, scale, None)
+
+
+def _select(L, pool=None, n_layer=2, n_req=3, kv_len=FAKE * 5, keep=FAKE * 6, evicted=FAKE * 7, sink=1, recent=2, score=FAKE * 8,
+            pos=FAKE * 9, move=FAKE * 10, n_move=FAKE * 11):
+    return L.kv_evict_plan(ctypes.byref(pool or _pool()), n_layer, n_req, kv_len, keep, evicted, sink, recent, score, pos, move, n_move, None)
+
+
+def _move(L, pool=None, n_layer=2, n_req=3, kv_len=FAKE * 5, move=FAKE * 6, n_move=FAKE * 7, score=FAKE * 8, pos=FAKE * 9):
+    return L.kv_evict_move(ctypes.byref(pool or _pool()), n_layer, n_req, kv_len, move, n_move, score, pos, None)
+
+
+@no_gpu_here
+def test_good_evictions_reach_the_device_check(L):
+    for kw in (dict(), dict(add=None), dict(add=FAKE * 12), dict(pool=_pool(v=0)), dict(hq=256, qs=256 * 64, q=FAKE * 64),
+               dict(n_req=skv.SKV_PAGED_MAX_REQUESTS, q_start=FAKE * 32, kv_len=FAKE * 64, pool=_pool(block_table=FAKE * 128))):
+        assert _weight(L, **kw) in NO_GPU, kw
+    for kw in (dict(), dict(evicted=None), dict(pool=_pool(k=0, v=0)), dict(sink=0, recent=0), dict(sink=2 ** 31 - 1)):
+        assert _select(L, **kw) in NO_GPU, kw
+    assert _move(L) in NO_GPU
+
+
+def test_evictions_of_nothing(L):
+    assert _weight(L, n_req=0) == _weight(L, n_tok=0) == skv.SKV_OK
+    for call in (_select, _move):
+        assert call(L, n_layer=0) == call(L, n_req=0) == skv.SKV_OK
+
+
+@pytest.mark.parametrize("bad", [
+    dict(hq=0), dict(hq=3), dict(n_req=-1), dict(n_tok=-1), dict(q=None), dict(q=FAKE + 8), dict(qs=255), dict(qs=248), dict(q_start=None),
+    dict(kv_len=None), dict(kv_len=FAKE + 2), dict(lse=None), dict(position=None), dict(add=FAKE * 10 + 4), dict(add=FAKE * 12 + 2),
+    dict(score=None), dict(pos=None), dict(ws=None), dict(ws_bytes=16), dict(ws=FAKE * 4096 + 8), dict(scale=0.0), dict(scale=-1.0),
+    dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=3e38), dict(pos=FAKE * 10 + 4), dict(score=FAKE * 5), dict(pos=FAKE * 8 + 8),
+    dict(score=FAKE), dict(pos=FAKE * 3), dict(score=FAKE * 6), dict(pos=FAKE * 4), dict(ws=FAKE)])
+def test_bad_weights(L, bad):
+    assert _weight(L, **bad) == skv.SKV_ERR_INVALID, bad
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n_layer=-1), dict(n_req=-1), dict(kv_len=None), dict(keep=None), dict(keep=FAKE + 1), dict(evicted=FAKE + 2), dict(sink=-1),
+    dict(recent=-1), dict(score=None), dict(score=FAKE * 8 + 4), dict(pos=None), dict(pos=FAKE * 9 + 8), dict(move=None),
+    dict(move=FAKE * 10 + 8), dict(n_move=None), dict(move=FAKE * 8), dict(move=FAKE * 9 + 1024), dict(n_move=FAKE * 6), dict(n_move=FAKE * 10 + 32),
+    dict(move=FAKE * 5 - 32), dict(n_move=FAKE * 3), dict(n_move=FAKE * 4)])
+def test_bad_evict_plans(L, bad):
+    assert _select(L, **bad) == skv.SKV_ERR_INVALID, bad
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n_layer=-1), dict(n_req=-1), dict(kv_len=None), dict(move=None), dict(move=FAKE * 6 + 8), dict(n_move=None), dict(score=None),
+    dict(pos=None), dict(pos=FAKE * 9 + 4), dict(score=FAKE), dict(pos=FAKE * 2), dict(score=FAKE * 6), dict(pos=FAKE * 8 + 16),
+    dict(score=FAKE * 7 - 32), dict(pos=FAKE * 5 - 16), dict(score=FAKE * 3), dict(pos=FAKE * 4 - 1024),
+    dict(pool=_pool(v=FAKE + 64)), dict(pool=_pool(k=FAKE + 8)), dict(pool=_pool(head_dim=32)), dict(pool=_pool(v=0))])
+def test_bad_moves(L, bad):
+    assert _move(L, **bad) == skv.SKV_ERR_INVALID, bad
+
+
+@pytest.mark.parametrize("bad", [
+    dict(n_page=0), dict(page_size=24), dict(max_block=0), dict(status=0), dict(block_table=0), dict(n_kv_head=0), dict(n_kv_head=1 << 29)])
+def test_evictions_of_a_bad_pool(L, bad):
+    for call in (_weight, _select, _move):
+        assert call(L, pool=_pool(**bad)) == skv.SKV_ERR_INVALID, (call, bad)
+    assert L.paged_attn_weight(None, 4, 1, 1, *[FAKE] * 1, 256, *[FAKE] * 7, FAKE, 0, 1.0, None) == skv.SKV_ERR_INVALID
+    assert L.kv_evict_plan(None, 1, 1, FAKE, FAKE, None, 0, 0, FAKE, FAKE, FAKE, FAKE, None) == skv.SKV_ERR_INVALID
+    assert L.kv_evict_move(None, 1, 1, FAKE, FAKE, FAKE, FAKE, FAKE, None) == skv.SKV_ERR_INVALID
+
+
+def test_evictions_refused_as_too_large(L):
+    assert _weight(L, n_req=skv.SKV_PAGED_MAX_REQUESTS + 1) == skv.SKV_ERR_UNSUPPORTED
+    assert _weight(L, hq=258) == skv.SKV_ERR_UNSUPPORTED                 # 129 query heads per kv head
+    assert _weight(L, n_tok=1 << 30) == skv.SKV_ERR_UNSUPPORTED
+    for call in (_select, _move):
+        assert call(L, n_layer=1 << 15, n_req=1 << 11) == skv.SKV_ERR_UNSUPPORTED
+
+
+def test_scores_that_are_no_tensors():
+    with pytest.raises(TypeError):
+        skv.PagedScores(3, 4)
