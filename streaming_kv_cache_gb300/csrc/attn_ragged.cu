@@ -45,19 +45,17 @@
 // divides the page size, so that a key tile is 128 / BR boxes from any pages.
 // Value rows past the request's length are set to zero in shared memory: a
 // probability of 0 does not cancel a NaN there.
-#include <cudaTypedefs.h>
 #include <math.h>
 
 #include <atomic>
 
 #include "common.cuh"
+#include "launch.cuh"
 #include "ragged.h"
 #include "skv.h"
 #include "tc.cuh"
 
 namespace skv {
-
-PFN_cuTensorMapEncodeTiled_v12000 tmap_encode_fn();
 
 namespace {
 
@@ -1076,8 +1074,17 @@ ragged_attn_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   }
 }
 
-// SM count per device ordinal, asked once (threads that race store the same value)
+// Workspace: the shared units (a word of four per CTA), then (m, sum) and O of
+// two pieces per CTA, the first and the last of its share (any piece between
+// is a whole unit), at the larger form's rows and head size.
+constexpr int MAX_CTAS = 512;
+constexpr size_t WS_HEAD = MAX_CTAS * sizeof(int4);
+size_t ws_ml_bytes() { return (size_t)2 * sm_count() * 2 * BM * 2 * sizeof(float); }
+
+// SM count per device ordinal
 std::atomic<int> g_sms[64];
+
+}  // namespace
 
 int sm_count() {
   int dev = 0;
@@ -1089,37 +1096,6 @@ int sm_count() {
   }
   return n;
 }
-
-template <typename K>
-cudaError_t set_smem_once(K kernel, int bytes, int variant) {
-  static std::atomic<int> done[64][32];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && done[dev][variant].load(std::memory_order_relaxed)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev][variant].store(1, std::memory_order_relaxed);
-  return e;
-}
-
-// Workspace: the shared units (a word of four per CTA), then (m, sum) and O of
-// two pieces per CTA, the first and the last of its share (any piece between
-// is a whole unit), at the larger form's rows and head size.
-constexpr int MAX_CTAS = 512;
-constexpr size_t WS_HEAD = MAX_CTAS * sizeof(int4);
-size_t ws_ml_bytes() { return (size_t)2 * sm_count() * 2 * BM * 2 * sizeof(float); }
-
-bool encode_3d(CUtensorMap* m, bool f16, const void* base, const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2],
-               const cuuint32_t (&box)[3]) {
-  auto fn = tmap_encode_fn();
-  const cuuint32_t es[3] = {1, 1, 1};
-  return fn && fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                  const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
 
 size_t ragged_ws_bytes() { return WS_HEAD + ws_ml_bytes() + (size_t)2 * sm_count() * 2 * BM * 128 * sizeof(float); }
 

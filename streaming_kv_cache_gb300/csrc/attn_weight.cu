@@ -1,12 +1,33 @@
-// paged_attn_weight: the attention weight that each cached key has got from a
-// step's rows, added to what it had.
+// paged_attn_weight on the 5th-generation tensor cores (tcgen05 + TMEM): the
+// attention weight that each cached key has got from a step's rows, added to
+// what it had.
 //
 //   w[h][j] = sum over rows i that see key j and query heads g of kv head h of
 //             exp(scale q_ig . k_j - lse_ig)
+//
+// Keys are the rows of the MMA (M = 128) and queries its columns, so a TMEM
+// lane and the thread that reads it belong to one key: the sum over the
+// queries stays in a register and nothing is exchanged between threads.  A
+// unit is 256 keys (two tiles) of one (request, kv head) against the query
+// tiles that see them; a query tile packs TQ tokens x the G query heads that
+// share the kv head.  K is read once; with many rows the two key tiles stay in
+// shared memory while the query tiles pass, with few (decode) the key tiles
+// pass and a query tile is a few rows.
+//
+// Units form one sequence, ordered by request, kv head and key block, each as
+// long as its query tiles and unit_cost more; CTA c of a persistent grid takes
+// positions [c W, (c + 1) W) of it.  With SHARED a unit that several CTAs
+// share leaves its sums in the workspace, and a second kernel adds them up in
+// order, so that results do not depend on timing; else units stay whole.
+//
+//   warps 0 .. 7   a warpgroup per key tile, a thread per key: exponentials,
+//                  sums, scores
+//   warps 8 .. 11  K producer (TMA), Q producer (TMA), MMA issuer, scheduler
 #include <math.h>
 
 #include "common.cuh"
 #include "evict.h"
+#include "launch.cuh"
 #include "skv.h"
 #include "tc.cuh"
 
@@ -14,77 +35,598 @@ namespace skv {
 
 namespace {
 
-constexpr int KT = 128;   // keys of a tile, a thread each
+constexpr int BM = 128;       // keys of a key tile
+constexpr int UK = 2 * BM;    // and of a unit
+constexpr int BN = 128;       // rows of a query tile, at most
+constexpr int NT = 384;
+constexpr int EPI_WARPS = 8, WARP_K = 8, WARP_Q = 9, WARP_MMA = 10, WARP_SCHED = 11;
+constexpr int NP = 4;         // pieces in flight between the scheduler and the other warps
+constexpr int LIST = 512;     // requests with rows that a CTA knows ahead
 
-template <bool F16>
-__device__ __forceinline__ void unpack(uint32_t w, float& lo, float& hi) {
-  if constexpr (F16) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    lo = f.x;
-    hi = f.y;
+template <int D>
+struct WCfg {
+  static constexpr int KST = D == 128 ? 3 : 6, QST = D == 128 ? 3 : 6;
+  static constexpr int KT = BM * D * 2;        // bytes of a tile
+  static constexpr int HALF = BM * 128;        // one 64-dimension half of it
+  static constexpr int K_OFF = 0;
+  static constexpr int Q_OFF = KST * KT;
+  static constexpr int L_OFF = Q_OFF + QST * KT;             // logarithms of a query tile's columns, [EPI_WARPS][BN]
+  static constexpr int BAR_OFF = L_OFF + EPI_WARPS * BN * 4;
+  static constexpr int MISC_OFF = BAR_OFF + 48 * 8;
+  static constexpr int PIECE_OFF = MISC_OFF + 64;
+  static constexpr int LIST_OFF = PIECE_OFF + NP * 64;
+  static constexpr int SCAN_OFF = LIST_OFF + LIST * 2;
+  static constexpr int BYTES = SCAN_OFF + NT / 32 * 16;
+  static constexpr int ALLOC = BYTES + 1024;                 // slack for 1024-byte alignment
+  static_assert(ALLOC <= 232448, "shared memory");
+};
+
+template <int KST, int QST>
+struct WBars {
+  enum : int {
+    KFULL = 0,                 // K tile landed
+    KEMPTY = KFULL + KST,      // MMA commit: the piece is done with it
+    QFULL = KEMPTY + KST,      // Q tile landed
+    QEMPTY = QFULL + QST,      // MMA commit
+    SFULL = QEMPTY + QST,      // MMA commit: scores of key tile kt in buffer x (2 kt + x)
+    SFREE = SFULL + 4,         // its warps have read them
+    PCFULL = SFREE + 4,        // scheduler: piece published
+    PCEMPTY = PCFULL + NP,     // every other warp has read it
+    DRAIN = PCEMPTY + NP,      // MMA commit: everything issued is complete
+    COUNT
+  };
+  static_assert(COUNT <= 48, "barrier slots");
+};
+
+struct WParams {
+  WeightArgs w;
+  int G, TQ;              // query heads per kv head, tokens per query tile
+  int N;                  // columns of an MMA: TQ G, a multiple of 16
+  int BR, boxes;          // rows per TMA box, boxes per key tile
+  int unit_cost;          // positions that a unit takes before its query tiles
+  float scale_log2;
+  bool wait_poll;         // LIMITED: the limit is shorter than a try of a wait may sleep
+  uint64_t wait_cycles;   // and the limit of a wait
+  int4* ws_unit;          // [CTAs] the shared unit that starts in a CTA: pieces (0: none), request, kv head, key block
+  float* ws_sum;          // [2 * CTAs][UK]
+};
+
+// Query tiles [qa, qa + nt) of a unit.
+struct Piece {
+  int nt;          // 0: no more pieces
+  int qa;
+  int b, h, k0;    // request, kv head, first key
+  int q0, L, kv;   // the request's span
+  int slot;        // -1: the whole unit; else the workspace slot of its sums
+};
+static_assert(sizeof(Piece) <= 64, "piece slot");
+
+// A request's units, for one kv head.
+struct Units {
+  int L, old, nq, nkb;    // rows, keys before the step, query tiles, key blocks
+  __device__ __forceinline__ Units(const Span& s, int TQ) {
+    L = s.L;
+    old = s.kv - s.L;
+    nq = (s.L + TQ - 1) / TQ;
+    nkb = (s.kv + UK - 1) / UK;
+  }
+  // the first query tile that sees a key of block kb
+  __device__ __forceinline__ int first(int kb, int TQ) const { return max(0, kb * UK - old) / TQ; }
+  // blocks that every query tile sees
+  __device__ __forceinline__ int full(int TQ) const { return min(nkb, (old + TQ - 1) / UK + 1); }
+  __device__ __forceinline__ long long positions(int TQ, int cost) const {
+    const int f = full(TQ);
+    long long p = (long long)f * (cost + nq);
+    for (int kb = f; kb < nkb; ++kb) p += cost + nq - first(kb, TQ);
+    return p;
+  }
+};
+
+// Where key j of request b lies in the pools, -1 with a page outside the pool.
+__device__ __forceinline__ long long key_place(const RaggedArgs& r, int b, int h, int j) {
+  const int page = __ldcg(r.table + (size_t)b * r.max_block + j / r.page_size);
+  return page >= 0 && page < r.n_page ? ((long long)page * r.Hkv + h) * r.page_size + j % r.page_size : -1;
+}
+
+template <int D, bool F16, bool SHARED, bool LIMITED>
+__global__ void __launch_bounds__(NT, 1)
+attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ WParams p) {
+  using C = WCfg<D>;
+  using B = WBars<C::KST, C::QST>;
+  constexpr int KST = C::KST, QST = C::QST;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = tc::smem_u32(smem);
+  auto bar = [&](int i) { return sbase + C::BAR_OFF + 8u * i; };
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  int* s_rank = reinterpret_cast<int*>(smem + C::MISC_OFF + 8);      // the share's first request among those with rows
+  long long* s_off = reinterpret_cast<long long*>(smem + C::MISC_OFF + 16);
+  Piece* s_piece = reinterpret_cast<Piece*>(smem + C::PIECE_OFF);
+  uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + C::LIST_OFF);
+  struct Sums {
+    long long positions;
+    int active, pad;
+  };
+  Sums* s_scan = reinterpret_cast<Sums*>(smem + C::SCAN_OFF);
+
+  const RaggedArgs& r = p.w.r;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int TQ = p.TQ;
+
+  if (tid == 0) {
+    for (int i = 0; i < B::COUNT; ++i) {
+      int count = 1;
+      if (i >= B::SFREE && i < B::SFREE + 4) count = 4;
+      if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + EPI_WARPS;
+      tc::mbar_init(bar(i), count);
+    }
+    tc::fence_barrier_init();
+    tc::fence_proxy_async_smem();
+  }
+  if (warp == WARP_K) {
+    tc::tmem_alloc(tc::smem_u32(s_tmem), 512);
+    tc::tmem_relinquish();
+  }
+  if (lane == 0) {
+    if (warp == WARP_K) tc::prefetch_tmap(&tmap_k);
+    if (warp == WARP_Q) tc::prefetch_tmap(&tmap_q);
+  }
+  tc::grid_dep_wait();
+
+  // ------------------------------------------------------------ this CTA's share
+  long long total = 0, share, g0;
+  {
+    constexpr int PER = (SKV_PAGED_MAX_REQUESTS + NT - 1) / NT;
+    static_assert(PER <= 32, "a bit per request");
+    const int per = (r.n_req + NT - 1) / NT;
+    const int i0 = min(r.n_req, tid * per), i1 = min(r.n_req, i0 + per);
+    uint32_t rows = 0;                       // this thread's requests with rows
+    Sums sum{0, 0, 0};
+    auto cost = [&](const Span& s) { return s.L == 0 || s.kv == 0 ? 0ll : r.Hkv * Units(s, TQ).positions(TQ, p.unit_cost); };
+    for (int b = i0; b < i1; ++b) {
+      const Span s = request_span(r, b);
+      if (s.bad && blockIdx.x == 0) set_status(r.status, SKV_DEV_BAD_LEN);
+      const long long c = cost(s);
+      sum.positions += c;
+      if (c) {
+        ++sum.active;
+        rows |= 1u << (b - i0);
+      }
+    }
+    Sums incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, incl.positions, o);
+      const int v = __shfl_up_sync(0xffffffffu, incl.active, o);
+      if (lane >= o) {
+        incl.positions += t;
+        incl.active += v;
+      }
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long at = incl.positions - sum.positions;
+    int rank = incl.active - sum.active, active = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+      const Sums x = s_scan[w];
+      if (w == warp) {
+        at += total;
+        rank += active;
+      }
+      total += x.positions;
+      active += x.active;
+    }
+    share = max(1LL, (total + gridDim.x - 1) / gridDim.x);
+    g0 = blockIdx.x * share;
+    if (g0 >= total) {                       // nothing left for this CTA
+      if (SHARED && tid == 0) p.ws_unit[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (warp == WARP_K) tc::tmem_dealloc(*s_tmem, 512);
+      return;
+    }
+    if (g0 >= at && g0 < at + sum.positions) {
+      int k = rank;
+      for (int b = i0;; ++b) {
+        const long long c = rows >> (b - i0) & 1 ? cost(request_span(r, b)) : 0;
+        if (g0 < at + c) break;
+        at += c;
+        k += c > 0;
+      }
+      *s_rank = k;
+      *s_off = g0 - at;
+    }
+    __syncthreads();
+    const int k0 = *s_rank;
+    for (int b = i0; b < i1; ++b)
+      if (rows >> (b - i0) & 1) {
+        if (rank >= k0 && rank < k0 + LIST) s_list[rank - k0] = (uint16_t)b;
+        ++rank;
+      }
+  }
+  const long long g1 = min(g0 + share, total);
+
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  auto wait = [&](int b, uint32_t phase) {
+    if constexpr (LIMITED) {
+      if (p.wait_poll) return tc::mbar_poll(bar(b), phase & 1, p.wait_cycles);
+      return tc::mbar_sleep(bar(b), phase & 1, p.wait_cycles);
+    } else {
+      return tc::mbar_sleep(bar(b), phase & 1);
+    }
+  };
+  // all lanes go on or none
+  auto wait_all = [&](int b, uint32_t phase) { return (bool)__all_sync(0xffffffffu, wait(b, phase)); };
+  // for what a warp has started itself and must not leave behind: however short
+  // the caller's limit is
+  auto drain = [&](int b, uint32_t phase) { return tc::mbar_sleep(bar(b), phase & 1); };
+  auto take_piece = [&](int pi, Piece& pc) {
+    const int s = pi % NP;
+    if (!wait_all(B::PCFULL + s, pi / NP)) return false;
+    pc = s_piece[s];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar(B::PCEMPTY + s));
+    return true;
+  };
+  auto tiles_of = [&](const Piece& pc) { return pc.kv - pc.k0 > BM ? 2 : 1; };   // key tiles with keys
+
+  bool ok = true;
+  if (warp == WARP_K) {
+    // ------------------------------------------------------------ K producer
+    int n = 0;                               // tiles issued
+    Piece pc;
+    for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+      const int32_t* row = r.table + (size_t)pc.b * r.max_block;
+      for (int kt = 0; kt < tiles_of(pc); ++kt, ++n) {
+        // lane x issues box x of a tile: the page of its first row
+        const int r0 = pc.k0 + kt * BM, j = r0 + lane * p.BR;
+        const int id = lane < p.boxes && j < pc.kv ? __ldcg(row + j / r.page_size) : -1;
+        const int n_box = (min(BM, pc.kv - r0) + p.BR - 1) / p.BR;
+        const int st = n % KST;
+        if (n >= KST && !(ok = wait_all(B::KEMPTY + st, n / KST - 1))) break;
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar(B::KFULL + st), n_box * p.BR * 128 * (D / 64));
+        __syncwarp();
+        if (lane < n_box) {
+          // a page outside the pool reads as the zeros outside the map
+          const bool in = id >= 0 && id < r.n_page;
+          if (!in) set_status(r.status, SKV_DEV_BAD_PAGE);
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf)
+            tc::tma_load_3d(sbase + C::K_OFF + st * C::KT + hf * C::HALF + lane * p.BR * 128, &tmap_k, bar(B::KFULL + st),
+                            hf * 64, j % r.page_size, in ? id * r.Hkv + pc.h : -1);
+        }
+      }
+      if (!ok) break;
+    }
+    // the copies this warp started land before the CTA exits
+    for (int j = max(0, n - KST); j < n && drain(B::KFULL + j % KST, j / KST); ++j) {
+    }
+  } else if (warp == WARP_Q) {
+    // ------------------------------------------------------------ Q producer
+    int n = 0;
+    Piece pc;
+    for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+      for (int i = 0; i < pc.nt; ++i, ++n) {
+        const int st = n % QST;
+        if (n >= QST && !(ok = wait_all(B::QEMPTY + st, n / QST - 1))) break;
+        if (lane == 0) {
+          tc::mbar_arrive_expect_tx(bar(B::QFULL + st), TQ * p.G * 128 * (D / 64));
+#pragma unroll
+          for (int hf = 0; hf < D / 64; ++hf)
+            tc::tma_load_3d(sbase + C::Q_OFF + st * C::KT + hf * C::HALF, &tmap_q, bar(B::QFULL + st), hf * 64, pc.h * p.G,
+                            pc.q0 + (pc.qa + i) * TQ);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    for (int j = max(0, n - QST); j < n && drain(B::QFULL + j % QST, j / QST); ++j) {
+    }
+  } else if (warp == WARP_MMA) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t idesc = F16 ? tc::idesc_f16(BM, p.N) : tc::idesc_bf16(BM, p.N);
+    const uint64_t dk0 = tc::sdesc_sw128(sbase + C::K_OFF), dq0 = tc::sdesc_sw128(sbase + C::Q_OFF);
+    const bool lead = tc::elect_one();
+    int nk = 0, nq = 0, cnt0 = 0, cnt1 = 0;  // K tiles, Q tiles, and steps of either key tile so far
+    for (int pi = 0; ok; ++pi) {
+      const int slot = pi % NP;
+      if (!(ok = wait_all(B::PCFULL + slot, pi / NP))) break;
+      const int nt = s_piece[slot].nt, two = nt && tiles_of(s_piece[slot]) == 2;
+      __syncwarp();
+      if (lead) tc::mbar_arrive(bar(B::PCEMPTY + slot));
+      if (!nt) break;
+      for (int i = 0; i < nt && ok; ++i, ++nq) {
+        const int qs = nq % QST;
+        if (!(ok = wait_all(B::QFULL + qs, nq / QST))) break;
+        for (int kt = 0; kt <= two; ++kt) {
+          const int k = nk + kt, ks = k % KST;
+          int& cnt = kt ? cnt1 : cnt0;
+          const int x = 2 * kt + (cnt & 1);
+          if (i == 0 && !(ok = wait_all(B::KFULL + ks, k / KST))) break;
+          if (cnt >= 2 && !(ok = wait_all(B::SFREE + x, (cnt >> 1) - 1))) break;
+          tc::tc_fence_after();
+          if (lead) {
+            const uint64_t dk = tc::opaque(dk0 + ((uint32_t)(ks * C::KT) >> 4));
+            const uint64_t dq = tc::opaque(dq0 + ((uint32_t)(qs * C::KT) >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
+              tc::mma_ss(tmem + x * BN, dk + off, dq + off, idesc, kk > 0);
+            }
+            tc::mma_commit(bar(B::SFULL + x));
+            if (i == nt - 1) tc::mma_commit(bar(B::KEMPTY + ks));
+            if (kt == two) tc::mma_commit(bar(B::QEMPTY + qs));
+          }
+          ++cnt;
+        }
+      }
+      nk += 1 + two;
+    }
+    if (lead) tc::mma_commit(bar(B::DRAIN));   // every MMA issued completes before TMEM is released
+    drain(B::DRAIN, 0);
+  } else if (warp == WARP_SCHED) {
+    // ------------------------------------------------------------- scheduler
+    if (lane == 0) {
+      int at = 0;                              // place in the list of requests with rows
+      int b = s_list[0];
+      Span s = request_span(r, b);
+      Units u(s, TQ);
+      int h, kb;
+      long long pos;                           // of the unit's start
+      {
+        long long off = *s_off;
+        const long long per_head = u.positions(TQ, p.unit_cost);
+        h = (int)(off / per_head);
+        off -= h * per_head;
+        const int whole = p.unit_cost + u.nq;  // positions of a block that every query tile sees
+        kb = (int)min((long long)u.full(TQ), off / whole);
+        off -= (long long)kb * whole;
+        for (;; ++kb) {
+          const int len = whole - u.first(kb, TQ);
+          if (off < len) break;
+          off -= len;
+        }
+        pos = g0 - off;
+      }
+      int4 shared_unit = make_int4(0, 0, 0, 0);   // the unit that starts here and goes on in the next CTA
+      int pi = 0;
+      auto publish = [&](const Piece& pc) {
+        const int slot = pi % NP;
+        if (pi >= NP && !wait(B::PCEMPTY + slot, pi / NP - 1)) return false;
+        s_piece[slot] = pc;
+        tc::mbar_arrive(bar(B::PCFULL + slot));
+        ++pi;
+        return true;
+      };
+      while (pos < g1) {
+        Piece pc;
+        pc.qa = u.first(kb, TQ);
+        const int tiles = u.nq - pc.qa;
+        const long long u0 = pos + p.unit_cost, u1 = u0 + tiles;
+        pc.nt = tiles;
+        pc.slot = -1;
+        if (SHARED) {
+          const long long lo = max(u0, g0), hi = min(u1, g1);
+          pc.nt = (int)max(0LL, hi - lo);
+          if (u0 < g0 || u1 > g1) pc.slot = 2 * (int)blockIdx.x + (u0 < g0 ? 0 : 1);
+          if (u0 >= g0 && u0 < g1 && u1 > g1)
+            shared_unit = make_int4((int)((u1 - 1) / share) - (int)blockIdx.x + 1, b, h, kb);
+          pc.qa += (int)(lo - u0);
+        } else if (pos < g0) {
+          pc.nt = 0;                           // it started in the CTA before
+        }
+        if (pc.nt) {
+          pc.b = b;
+          pc.h = h;
+          pc.k0 = kb * UK;
+          pc.q0 = s.q0;
+          pc.L = s.L;
+          pc.kv = s.kv;
+          if (!(ok = publish(pc))) break;
+        }
+        pos = u1;
+        if (++kb == u.nkb) {
+          kb = 0;
+          if (++h == r.Hkv) {
+            h = 0;
+            if (pos < g1) {                    // the share goes on: some later request has rows
+              if (++at < LIST) b = s_list[at];
+              else ++b;
+              s = request_span(r, b);
+              while (s.L == 0 || s.kv == 0) s = request_span(r, ++b);
+              u = Units(s, TQ);
+            }
+          }
+        }
+      }
+      if (ok) {
+        Piece end{};
+        ok = publish(end);
+      }
+      if (SHARED) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);   // always written: the second kernel reads it
+      if (!ok) set_status(r.status, SKV_DEV_TIMEOUT);
+      ok = true;
+    }
   } else {
-    lo = bf16_lo(w);
-    hi = bf16_hi(w);
+    // ---------------------------------------------- exponentials and scores
+    const int kt = warp >> 2, lg = warp & 3;         // key tile, TMEM lane group
+    const int row = lg * 32 + lane;
+    const uint32_t t_lane = (uint32_t)(lg * 32) << 16;
+    // a warp keeps the logarithms of a query tile's columns for itself: four to
+    // a lane, loaded a tile ahead
+    float* s_log = reinterpret_cast<float*>(smem + C::L_OFF) + warp * BN;
+    int col_tok[4], col_off[4];                      // token of a column, and its offset in lse
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = lane * 4 + q;
+      col_tok[q] = c / p.G < TQ ? c / p.G : 1 << 30;
+      col_off[q] = c % p.G * r.n_tok + c / p.G;
+    }
+    const float sl = p.scale_log2;
+    const uint64_t sl2 = f2_pack(sl, sl);
+    int cnt = 0;                                     // steps of this key tile so far
+    Piece pc;
+    for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+      if (kt >= tiles_of(pc)) continue;
+      const int j = pc.k0 + kt * BM + row, old = pc.kv - pc.L;
+      const bool mine = j < pc.kv;
+      // of a whole unit: what the weight is added to
+      long long at = -1;
+      float w0 = 0.f;
+      if (pc.slot < 0 && mine) {
+        at = key_place(r, pc.b, pc.h, j);
+        if (at >= 0 && j < old && p.w.add) w0 = p.w.add[at];
+      }
+      const float* lse = p.w.lse + (size_t)pc.h * p.G * r.n_tok + pc.q0;
+      float log4[4];
+      auto load_log = [&](int t0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) log4[q] = col_tok[q] < pc.L - t0 ? lse[col_off[q] + t0] : -INFINITY;
+      };
+      load_log(pc.qa * TQ);
+      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+      for (int i = 0; i < pc.nt; ++i, ++cnt) {
+        const int t0 = (pc.qa + i) * TQ, x = 2 * kt + (cnt & 1);
+        const int nv = min(TQ, pc.L - t0) * p.G;     // columns with rows
+        const int c_lo = min(max(j - old - t0, 0), TQ) * p.G;   // the first that sees the key
+        // a row whose logarithm is not finite gives nothing
+        __syncwarp();
+        *reinterpret_cast<float4*>(s_log + lane * 4) =
+            make_float4(isfinite(log4[0]) ? log4[0] * -kLog2e : -INFINITY, isfinite(log4[1]) ? log4[1] * -kLog2e : -INFINITY,
+                        isfinite(log4[2]) ? log4[2] * -kLog2e : -INFINITY, isfinite(log4[3]) ? log4[3] * -kLog2e : -INFINITY);
+        __syncwarp();
+        if (i + 1 < pc.nt) load_log(t0 + TQ);
+        if (!(ok = wait_all(B::SFULL + x, cnt >> 1))) break;
+        tc::tc_fence_after();
+        const uint32_t tS = tmem + t_lane + x * BN;
+        const int n_ch = (nv + 31) / 32;
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < n_ch) tc::tmem_ld32(tS + c * 32, v[c]);
+        tc::tmem_wait_ld();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(B::SFREE + x));
+        const int lo_all = __reduce_max_sync(0xffffffffu, c_lo), lo_any = __reduce_min_sync(0xffffffffu, c_lo);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= n_ch || lo_any >= c * 32 + 32) continue;
+          if (lo_all > c * 32 || nv < c * 32 + 32) {
+            // some of the scores are of rows that do not see the key, or of none
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c * 32 + k < c_lo || c * 32 + k >= nv) v[c][k] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(s_log + c * 32 + k);
+            const uint64_t y0 = f2_fma(f2_pack(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), sl2, l4.x);
+            const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(v[c][k + 2]), __uint_as_float(v[c][k + 3])), sl2, l4.y);
+            float a0, a1, a2, a3;
+            f2_unpack(y0, a0, a1);
+            f2_unpack(y1, a2, a3);
+            const int q = k >> 2 & 1;
+            acc[2 * q] = f2_add(acc[2 * q], f2_pack(tc::ex2(a0), tc::ex2(a1)));
+            acc[2 * q + 1] = f2_add(acc[2 * q + 1], f2_pack(tc::ex2(a2), tc::ex2(a3)));
+          }
+        }
+      }
+      if (!ok) break;
+      const uint64_t s2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
+      float e0, e1;
+      f2_unpack(s2, e0, e1);
+      const float sum = e0 + e1;
+      if (SHARED && pc.slot >= 0) {
+        p.ws_sum[(size_t)pc.slot * UK + kt * BM + row] = sum;
+      } else if (at >= 0) {
+        p.w.score[at] = w0 + sum;
+        if (j >= old) p.w.pos[at] = p.w.position[pc.q0 + j - old];
+      }
+    }
+  }
+  if (!ok && lane == 0) set_status(r.status, SKV_DEV_TIMEOUT);
+
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == WARP_K) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(KT) attn_weight_kernel(const WeightArgs a) {
-  const RaggedArgs& r = a.r;
-  const int tid = threadIdx.x, G = r.Hq / r.Hkv;
+// The units that several CTAs share: their pieces' sums in order, and the scores.
+__global__ void __launch_bounds__(UK) weight_merge_kernel(const WParams p) {
   tc::grid_dep_wait();
-  long long first = 0;                       // tiles of the requests before
-  for (int b = 0; b < r.n_req; ++b) {
-    const Span s = request_span(r, b);
-    if (s.bad && blockIdx.x == 0 && tid == 0) set_status(r.status, SKV_DEV_BAD_LEN);
-    if (s.L == 0 || s.kv == 0) continue;
-    const int tiles = (s.kv + KT - 1) / KT;
-    const long long n = (long long)tiles * r.Hkv;
-    long long t = (blockIdx.x - first % gridDim.x + gridDim.x) % gridDim.x;
-    first += n;
-    for (; t < n; t += gridDim.x) {
-      const int h = (int)(t / tiles), j = (int)(t % tiles) * KT + tid;
-      if (j >= s.kv) continue;
-      const int page = r.table[(size_t)b * r.max_block + j / r.page_size];
-      if (page < 0 || page >= r.n_page) {
-        set_status(r.status, SKV_DEV_BAD_PAGE);
-        continue;
-      }
-      const size_t at = ((size_t)page * r.Hkv + h) * r.page_size + j % r.page_size;
-      const uint4* kr = reinterpret_cast<const uint4*>(r.k + at * D);
-      const int old = s.kv - s.L;            // keys before the step
-      float w = 0.f;
-      for (int i = max(0, j - old); i < s.L; ++i)
-        for (int g = 0; g < G; ++g) {
-          const uint4* qr = reinterpret_cast<const uint4*>(r.q + (s.q0 + i) * r.q_stride + (size_t)(h * G + g) * D);
-          const float l = a.lse[(size_t)(h * G + g) * r.n_tok + s.q0 + i];
-          float dot = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = kr[c], y = qr[c];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x0, x1, y0, y1;
-              unpack<F16>(xs[e], x0, x1);
-              unpack<F16>(ys[e], y0, y1);
-              dot += x0 * y0 + x1 * y1;
-            }
-          }
-          if (isfinite(l)) w += expf(r.sm_scale * dot - l);
-        }
-      if (j >= old) a.pos[at] = a.position[s.q0 + j - old];
-      a.score[at] = j < old && a.add ? a.add[at] + w : w;
-    }
-  }
+  const RaggedArgs& r = p.w.r;
+  const int4 u = __ldcg(p.ws_unit + blockIdx.x);
+  if (u.x == 0) return;
+  const Span s = request_span(r, u.y);
+  const int j = u.w * UK + threadIdx.x, old = s.kv - s.L;
+  if (j >= s.kv) return;
+  const long long at = key_place(r, u.y, u.z, j);
+  float sum = j < old && p.w.add && at >= 0 ? p.w.add[at] : 0.f;
+  float w = 0.f;
+  for (int k = 0; k < u.x; ++k)       // piece 0 is the last of its CTA's share, every other the first
+    w += __ldcg(p.ws_sum + (size_t)(2 * (blockIdx.x + k) + (k == 0 ? 1 : 0)) * UK + threadIdx.x);
+  if (at < 0) return;
+  p.w.score[at] = sum + w;
+  if (j >= old) p.w.pos[at] = p.w.position[s.q0 + j - old];
 }
 
 }  // namespace
 
 cudaError_t launch_attn_weight(const WeightArgs& a, int d, bool f16, cudaStream_t st) {
-  auto launch = [&](auto kernel) { return launch_dependent(kernel, dim3(152 * 8), KT, 0, st, a); };
-  if (d == 128) return f16 ? launch(attn_weight_kernel<128, true>) : launch(attn_weight_kernel<128, false>);
-  return f16 ? launch(attn_weight_kernel<64, true>) : launch(attn_weight_kernel<64, false>);
+  const RaggedArgs& r = a.r;
+  WParams p;
+  p.w = a;
+  p.G = r.Hq / r.Hkv;
+  const int most = BN / p.G;                 // tokens that a query tile may hold
+  const int mean = (r.n_tok + r.n_req - 1) / r.n_req;
+  p.TQ = 1;
+  while (p.TQ < most && p.TQ < mean) p.TQ *= 2;
+  p.TQ = min(p.TQ, most);
+  const bool shared = r.n_tok > (long long)r.n_req * most;
+  p.N = (p.TQ * p.G + 15) / 16 * 16;
+  p.unit_cost = 2;
+  p.BR = BM;
+  while (r.page_size % p.BR) p.BR /= 2;
+  p.boxes = BM / p.BR;
+  p.scale_log2 = r.sm_scale * kLog2e;
+  // in cycles at the 2.07 GHz maximum clock: a slower one only lengthens it
+  p.wait_cycles = (uint64_t)(min(r.wait_ns, (uint64_t)1 << 62) * 2.07);
+  p.wait_poll = r.wait_ns < tc::kSuspendHintNs;
+  constexpr int MAX_CTAS = 512;
+  const int grid = min(sm_count(), MAX_CTAS);
+  p.ws_unit = static_cast<int4*>(r.ws);
+  p.ws_sum = reinterpret_cast<float*>(static_cast<char*>(r.ws) + MAX_CTAS * sizeof(int4));
+  if (ragged_ws_bytes() < MAX_CTAS * sizeof(int4) + (size_t)2 * grid * UK * sizeof(float)) return cudaErrorInvalidValue;
+
+  CUtensorMap tq, tk;
+  const cuuint64_t dd = (cuuint64_t)d;
+  if (!encode_3d(&tq, f16, r.q, {dd, (cuuint64_t)r.Hq, (cuuint64_t)r.n_tok}, {dd * 2, (cuuint64_t)r.q_stride * 2},
+                 {64, (cuuint32_t)p.G, (cuuint32_t)p.TQ}) ||
+      !encode_3d(&tk, f16, r.k, {dd, (cuuint64_t)r.page_size, (cuuint64_t)r.n_page * r.Hkv}, {dd * 2, dd * 2 * r.page_size},
+                 {64, (cuuint32_t)p.BR, 1}))
+    return cudaErrorInvalidValue;
+  auto launch = [&](auto kernel, int smem, int variant) -> cudaError_t {
+    cudaError_t e = set_smem_once(kernel, smem, variant);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(kernel, dim3(grid), NT, smem, st, tq, tk, p);
+    if (e != cudaSuccess || !shared) return e;
+    return launch_dependent(weight_merge_kernel, dim3(grid), UK, 0, st, p);
+  };
+#define SKV_WEIGHT(DD, FF, SS, VAR)                                                                \
+  (r.wait_ns ? launch(attn_weight_kernel<DD, FF, SS, true>, WCfg<DD>::ALLOC, 8 + (VAR))            \
+             : launch(attn_weight_kernel<DD, FF, SS, false>, WCfg<DD>::ALLOC, VAR))
+#define SKV_WEIGHT_FORMS(DD, FF, VAR) (shared ? SKV_WEIGHT(DD, FF, true, VAR) : SKV_WEIGHT(DD, FF, false, VAR + 1))
+  if (d == 128) return f16 ? SKV_WEIGHT_FORMS(128, true, 0) : SKV_WEIGHT_FORMS(128, false, 2);
+  return f16 ? SKV_WEIGHT_FORMS(64, true, 4) : SKV_WEIGHT_FORMS(64, false, 6);
+#undef SKV_WEIGHT_FORMS
+#undef SKV_WEIGHT
 }
 
 }  // namespace skv
