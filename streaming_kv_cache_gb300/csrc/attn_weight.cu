@@ -41,6 +41,7 @@ constexpr int BN = 128;       // rows of a query tile, at most
 constexpr int NT = 384;
 constexpr int EPI_WARPS = 8, WARP_K = 8, WARP_Q = 9, WARP_MMA = 10, WARP_SCHED = 11;
 constexpr int NP = 4;         // pieces in flight between the scheduler and the other warps
+constexpr int CH = 64;        // scores that a thread takes from TMEM at a time
 constexpr int LIST = 512;     // requests with rows that a CTA knows ahead
 
 template <int D>
@@ -502,36 +503,33 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (!(ok = wait_all(B::SFULL + x, cnt >> 1))) break;
         tc::tc_fence_after();
         const uint32_t tS = tmem + t_lane + x * BN;
-        const int n_ch = (nv + 31) / 32;
-        uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < n_ch) tc::tmem_ld32(tS + c * 32, v[c]);
-        tc::tmem_wait_ld();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(B::SFREE + x));
         const int lo_all = __reduce_max_sync(0xffffffffu, c_lo), lo_any = __reduce_min_sync(0xffffffffu, c_lo);
+#pragma unroll 1
+        for (int c0 = 0; c0 < nv; c0 += CH) {
+          uint32_t v[CH];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= n_ch || lo_any >= c * 32 + 32) continue;
-          if (lo_all > c * 32 || nv < c * 32 + 32) {
+          for (int c = 0; c < CH; c += 32) tc::tmem_ld32(tS + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
+          tc::tmem_wait_ld();
+          if (c0 + CH >= nv) {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar(B::SFREE + x));
+          }
+          if (lo_any >= c0 + CH) continue;           // no key of the warp is seen by these rows
+          if (lo_all > c0 || nv < c0 + CH) {
             // some of the scores are of rows that do not see the key, or of none
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c * 32 + k < c_lo || c * 32 + k >= nv) v[c][k] = __float_as_uint(-INFINITY);
+            for (int k = 0; k < CH; ++k)
+              if (k < c_lo - c0 || k >= nv - c0) v[k] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(s_log + c * 32 + k);
-            const uint64_t y0 = f2_fma(f2_pack(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), sl2, l4.x);
-            const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(v[c][k + 2]), __uint_as_float(v[c][k + 3])), sl2, l4.y);
+          for (int k = 0; k < CH; k += 4) {
+            const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(s_log + c0 + k);
             float a0, a1, a2, a3;
-            f2_unpack(y0, a0, a1);
-            f2_unpack(y1, a2, a3);
-            const int q = k >> 2 & 1;
-            acc[2 * q] = f2_add(acc[2 * q], f2_pack(tc::ex2(a0), tc::ex2(a1)));
-            acc[2 * q + 1] = f2_add(acc[2 * q + 1], f2_pack(tc::ex2(a2), tc::ex2(a3)));
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), sl2, l4.x), a0, a1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), sl2, l4.y), a2, a3);
+            acc[k >> 1 & 2] = f2_add(acc[k >> 1 & 2], f2_pack(tc::ex2(a0), tc::ex2(a1)));
+            acc[k >> 1 & 2 | 1] = f2_add(acc[k >> 1 & 2 | 1], f2_pack(tc::ex2(a2), tc::ex2(a3)));
           }
         }
       }
