@@ -16,13 +16,12 @@
 //
 // Units form one sequence, ordered by request, kv head and key block, each as
 // long as its query tiles and unit_cost more; CTA c of a persistent grid takes
-// positions [c W, (c + 1) W) of it.  With SHARED a unit that several CTAs
-// share leaves its sums in the workspace, and a second kernel adds them up in
-// order, so that results do not depend on timing; else units stay whole.
+// positions [c W, (c + 1) W) of it.  In calls of many rows a unit that several
+// CTAs share leaves its sums in the workspace, and a second kernel adds them up
+// in order, so that results do not depend on timing; else units stay whole.
 //
-//   warps 0 .. 7   a warpgroup per key tile, a thread per key: exponentials,
-//                  sums, scores
-//   warps 8 .. 11  K producer (TMA), Q producer (TMA), MMA issuer, scheduler
+//   warps 0 .. 15  four warpgroups, a thread per key: exponentials, sums, scores
+//   then one each  K producer (TMA), Q producer (TMA), MMA issuer, scheduler
 #include <math.h>
 
 #include "common.cuh"
@@ -38,10 +37,11 @@ namespace {
 constexpr int BM = 128;       // keys of a key tile
 constexpr int UK = 2 * BM;    // and of a unit
 constexpr int BN = 128;       // rows of a query tile, at most
-constexpr int NT = 384;
-constexpr int EPI_WARPS = 8, WARP_K = 8, WARP_Q = 9, WARP_MMA = 10, WARP_SCHED = 11;
+constexpr int NT = 640;
+constexpr int EPI_WARPS = 16, WARP_K = 16, WARP_Q = 17, WARP_MMA = 18, WARP_SCHED = 19;
 constexpr int NP = 4;         // pieces in flight between the scheduler and the other warps
-constexpr int CH = 64;        // scores that a thread takes from TMEM at a time
+constexpr int LST = 4;        // query tiles whose logarithms are in shared memory
+constexpr int WC = BN / 4;    // columns of a warpgroup in the wide form
 constexpr int LIST = 512;     // requests with rows that a CTA knows ahead
 
 template <int D>
@@ -51,9 +51,10 @@ struct WCfg {
   static constexpr int HALF = BM * 128;        // one 64-dimension half of it
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = KST * KT;
-  static constexpr int L_OFF = Q_OFF + QST * KT;             // logarithms of a query tile's columns, [EPI_WARPS][BN]
-  static constexpr int BAR_OFF = L_OFF + EPI_WARPS * BN * 4;
-  static constexpr int MISC_OFF = BAR_OFF + 48 * 8;
+  static constexpr int L_OFF = Q_OFF + QST * KT;             // logarithms of query tiles' columns, [LST][BN]
+  static constexpr int X_OFF = L_OFF + LST * BN * 4;         // sums of the upper warpgroups' columns, [3][2][BM]
+  static constexpr int BAR_OFF = X_OFF + 3 * 2 * BM * 4;
+  static constexpr int MISC_OFF = BAR_OFF + 64 * 8;
   static constexpr int PIECE_OFF = MISC_OFF + 64;
   static constexpr int LIST_OFF = PIECE_OFF + NP * 64;
   static constexpr int SCAN_OFF = LIST_OFF + LIST * 2;
@@ -71,12 +72,16 @@ struct WBars {
     QEMPTY = QFULL + QST,      // MMA commit
     SFULL = QEMPTY + QST,      // MMA commit: scores of key tile kt in buffer x (2 kt + x)
     SFREE = SFULL + 4,         // its warps have read them
-    PCFULL = SFREE + 4,        // scheduler: piece published
+    LFULL = SFREE + 4,         // Q producer: logarithms of a query tile written
+    LEMPTY = LFULL + LST,      // its warps are done with them
+    XFULL = LEMPTY + LST,      // WIDE: the upper warpgroups' sums of a lane group's keys
+    XEMPTY = XFULL + 4,        // they have been added
+    PCFULL = XEMPTY + 4,       // scheduler: piece published
     PCEMPTY = PCFULL + NP,     // every other warp has read it
     DRAIN = PCEMPTY + NP,      // MMA commit: everything issued is complete
     COUNT
   };
-  static_assert(COUNT <= 48, "barrier slots");
+  static_assert(COUNT <= 64, "barrier slots");
 };
 
 struct WParams {
@@ -84,6 +89,7 @@ struct WParams {
   int G, TQ;              // query heads per kv head, tokens per query tile
   int N;                  // columns of an MMA: TQ G, a multiple of 16
   int BR, boxes;          // rows per TMA box, boxes per key tile
+  bool shared;            // WIDE: CTAs share units
   int unit_cost;          // positions that a unit takes before its query tiles
   float scale_log2;
   bool wait_poll;         // LIMITED: the limit is shorter than a try of a wait may sleep
@@ -129,7 +135,7 @@ __device__ __forceinline__ long long key_place(const RaggedArgs& r, int b, int h
   return page >= 0 && page < r.n_page ? ((long long)page * r.Hkv + h) * r.page_size + j % r.page_size : -1;
 }
 
-template <int D, bool F16, bool SHARED, bool LIMITED>
+template <int D, bool F16, bool WIDE, bool LIMITED>
 __global__ void __launch_bounds__(NT, 1)
 attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ WParams p) {
@@ -158,7 +164,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < B::COUNT; ++i) {
       int count = 1;
-      if (i >= B::SFREE && i < B::SFREE + 4) count = 4;
+      if (i >= B::SFREE && i < B::SFREE + 4) count = WIDE ? EPI_WARPS : 4;
+      if (i >= B::LEMPTY && i < B::LEMPTY + LST) count = WIDE ? EPI_WARPS : 8;
+      if (i >= B::XFULL && i < B::XFULL + 4) count = 3;
       if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + EPI_WARPS;
       tc::mbar_init(bar(i), count);
     }
@@ -222,7 +230,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     share = max(1LL, (total + gridDim.x - 1) / gridDim.x);
     g0 = blockIdx.x * share;
     if (g0 >= total) {                       // nothing left for this CTA
-      if (SHARED && tid == 0) p.ws_unit[blockIdx.x] = make_int4(0, 0, 0, 0);
+      if (p.shared && tid == 0) p.ws_unit[blockIdx.x] = make_int4(0, 0, 0, 0);
       if (warp == WARP_K) tc::tmem_dealloc(*s_tmem, 512);
       return;
     }
@@ -307,11 +315,27 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     }
   } else if (warp == WARP_Q) {
     // ------------------------------------------------------------ Q producer
+    // With a query tile come the logarithms of its columns, four to a lane,
+    // loaded a tile ahead: -lse log2 e, and -inf for a row that gives nothing.
     int n = 0;
+    int col_tok[4], col_off[4];              // token of a column, and its offset in lse
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = lane * 4 + q;
+      col_tok[q] = c / p.G < TQ ? c / p.G : 1 << 30;
+      col_off[q] = c % p.G * r.n_tok + c / p.G;
+    }
     Piece pc;
     for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+      const float* lse = p.w.lse + (size_t)pc.h * p.G * r.n_tok + pc.q0;
+      float lg[4];
+      auto load_log = [&](int t0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) lg[q] = col_tok[q] < pc.L - t0 ? lse[col_off[q] + t0] : INFINITY;
+      };
+      load_log(pc.qa * TQ);
       for (int i = 0; i < pc.nt; ++i, ++n) {
-        const int st = n % QST;
+        const int st = n % QST, ls = n % LST;
         if (n >= QST && !(ok = wait_all(B::QEMPTY + st, n / QST - 1))) break;
         if (lane == 0) {
           tc::mbar_arrive_expect_tx(bar(B::QFULL + st), TQ * p.G * 128 * (D / 64));
@@ -321,6 +345,16 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             pc.q0 + (pc.qa + i) * TQ);
         }
         __syncwarp();
+        if (n >= LST && !(ok = wait_all(B::LEMPTY + ls, n / LST - 1))) {
+          ++n;                               // the query tile is on its way
+          break;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) lg[q] = isfinite(lg[q]) ? lg[q] * -kLog2e : -INFINITY;
+        *reinterpret_cast<float4*>(smem + C::L_OFF + (ls * BN + lane * 4) * 4) = make_float4(lg[0], lg[1], lg[2], lg[3]);
+        if (i + 1 < pc.nt) load_log((pc.qa + i + 1) * TQ);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar(B::LFULL + ls));
       }
       if (!ok) break;
     }
@@ -409,7 +443,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const long long u0 = pos + p.unit_cost, u1 = u0 + tiles;
         pc.nt = tiles;
         pc.slot = -1;
-        if (SHARED) {
+        if (p.shared) {
           const long long lo = max(u0, g0), hi = min(u1, g1);
           pc.nt = (int)max(0LL, hi - lo);
           if (u0 < g0 || u1 > g1) pc.slot = 2 * (int)blockIdx.x + (u0 < g0 ? 0 : 1);
@@ -447,102 +481,151 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         Piece end{};
         ok = publish(end);
       }
-      if (SHARED) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);   // always written: the second kernel reads it
+      if (p.shared) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);   // always written: the second kernel reads it
       if (!ok) set_status(r.status, SKV_DEV_TIMEOUT);
       ok = true;
     }
   } else {
     // ---------------------------------------------- exponentials and scores
-    const int kt = warp >> 2, lg = warp & 3;         // key tile, TMEM lane group
-    const int row = lg * 32 + lane;
-    const uint32_t t_lane = (uint32_t)(lg * 32) << 16;
-    // a warp keeps the logarithms of a query tile's columns for itself: four to
-    // a lane, loaded a tile ahead
-    float* s_log = reinterpret_cast<float*>(smem + C::L_OFF) + warp * BN;
-    int col_tok[4], col_off[4];                      // token of a column, and its offset in lse
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = lane * 4 + q;
-      col_tok[q] = c / p.G < TQ ? c / p.G : 1 << 30;
-      col_off[q] = c % p.G * r.n_tok + c / p.G;
-    }
+    // WIDE: a warpgroup takes a quarter of the columns of both key tiles, so
+    // that a logarithm that it reads from shared memory serves two scores.
+    // Else two warpgroups, one per key tile, take all columns of every second
+    // piece, so that one pair's loads and stores run under the other's work.
+    const int wg = warp >> 2, lg = warp & 3;         // warpgroup, TMEM lane group
+    const int row = lg * 32 + lane, tile = WIDE ? 0 : wg & 1;   // key, and key tile or the first of two
+    const int col0 = WIDE ? wg * WC : 0;
+    constexpr int TILES = WIDE ? 2 : 1;              // key tiles of a thread
+    constexpr int CH = WIDE ? 16 : 32;               // scores of one that it takes from TMEM at a time
+    const uint32_t t_lane = tmem + ((uint32_t)(lg * 32) << 16);
+    const float* s_log = reinterpret_cast<const float*>(smem + C::L_OFF);
+    float* s_x = reinterpret_cast<float*>(smem + C::X_OFF) + row;
     const float sl = p.scale_log2;
     const uint64_t sl2 = f2_pack(sl, sl);
-    int cnt = 0;                                     // steps of this key tile so far
+    int n = 0;                                       // query tiles of the CTA so far
+    int cnt[2] = {};                                 // steps of either key tile so far
     Piece pc;
     for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
-      if (kt >= tiles_of(pc)) continue;
-      const int j = pc.k0 + kt * BM + row, old = pc.kv - pc.L;
-      const bool mine = j < pc.kv;
-      // of a whole unit: what the weight is added to
-      long long at = -1;
-      float w0 = 0.f;
-      if (pc.slot < 0 && mine) {
-        at = key_place(r, pc.b, pc.h, j);
-        if (at >= 0 && j < old && p.w.add) w0 = p.w.add[at];
+      const bool two = tiles_of(pc) == 2;
+      if (!WIDE && (pi & 1) != wg >> 1) {            // the other pair's
+        n += pc.nt;
+        cnt[0] += pc.nt;
+        cnt[1] += two ? pc.nt : 0;
+        continue;
       }
-      const float* lse = p.w.lse + (size_t)pc.h * p.G * r.n_tok + pc.q0;
-      float log4[4];
-      auto load_log = [&](int t0) {
+      if (!WIDE && tile && !two) {                   // no keys: the logarithms are given back
+        for (int i = 0; i < pc.nt && ok; ++i, ++n) {
+          ok = wait_all(B::LFULL + n % LST, n / LST);
+          if (lane == 0 && ok) tc::mbar_arrive(bar(B::LEMPTY + n % LST));
+        }
+        cnt[0] += pc.nt;
+        if (!ok) break;
+        continue;
+      }
+      const int j0 = pc.k0 + tile * BM + row, old = pc.kv - pc.L;   // the thread's key, or its first
+      const int jw = pc.k0 + tile * BM + lg * 32;                   // the warp's first
+      const bool store = !WIDE || wg == 0;           // this thread writes the scores
+      // of a whole unit: where they lie, and what the weights are added to
+      long long at[TILES];
+      float w0[TILES];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) log4[q] = col_tok[q] < pc.L - t0 ? lse[col_off[q] + t0] : -INFINITY;
-      };
-      load_log(pc.qa * TQ);
-      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-      for (int i = 0; i < pc.nt; ++i, ++cnt) {
-        const int t0 = (pc.qa + i) * TQ, x = 2 * kt + (cnt & 1);
+      for (int t = 0; t < TILES; ++t) {
+        const int j = j0 + t * BM;
+        at[t] = store && pc.slot < 0 && j < pc.kv ? key_place(r, pc.b, pc.h, j) : -1;
+        w0[t] = at[t] >= 0 && j < old && p.w.add ? p.w.add[at[t]] : 0.f;
+      }
+      uint64_t acc[TILES][2] = {};
+      for (int i = 0; i < pc.nt; ++i, ++n) {
+        const int t0 = (pc.qa + i) * TQ, ls = n % LST;
         const int nv = min(TQ, pc.L - t0) * p.G;     // columns with rows
-        const int c_lo = min(max(j - old - t0, 0), TQ) * p.G;   // the first that sees the key
-        // a row whose logarithm is not finite gives nothing
-        __syncwarp();
-        *reinterpret_cast<float4*>(s_log + lane * 4) =
-            make_float4(isfinite(log4[0]) ? log4[0] * -kLog2e : -INFINITY, isfinite(log4[1]) ? log4[1] * -kLog2e : -INFINITY,
-                        isfinite(log4[2]) ? log4[2] * -kLog2e : -INFINITY, isfinite(log4[3]) ? log4[3] * -kLog2e : -INFINITY);
-        __syncwarp();
-        if (i + 1 < pc.nt) load_log(t0 + TQ);
-        if (!(ok = wait_all(B::SFULL + x, cnt >> 1))) break;
-        tc::tc_fence_after();
-        const uint32_t tS = tmem + t_lane + x * BN;
-        const int lo_all = __reduce_max_sync(0xffffffffu, c_lo), lo_any = __reduce_min_sync(0xffffffffu, c_lo);
-#pragma unroll 1
-        for (int c0 = 0; c0 < nv; c0 += CH) {
-          uint32_t v[CH];
+        int x[TILES];                                // score buffers
 #pragma unroll
-          for (int c = 0; c < CH; c += 32) tc::tmem_ld32(tS + c0 + c, *reinterpret_cast<uint32_t(*)[32]>(v + c));
-          tc::tmem_wait_ld();
-          if (c0 + CH >= nv) {
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar(B::SFREE + x));
+        for (int t = 0; t < TILES; ++t) x[t] = 2 * (tile + t) + (cnt[tile + t] & 1);
+        ok = wait_all(B::LFULL + ls, n / LST) && wait_all(B::SFULL + x[0], cnt[tile] >> 1);
+        if (WIDE && two) ok = ok && wait_all(B::SFULL + x[TILES - 1], cnt[1] >> 1);
+        if (!ok) break;
+        ++cnt[0];
+        cnt[1] += two;
+        tc::tc_fence_after();
+        const int end = min(nv, WIDE ? col0 + WC : BN);
+        // every key of the warp is seen by every row of these columns
+        const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 && nv >= (WIDE ? col0 + WC : (end + CH - 1) / CH * CH) &&
+                         (!WIDE || two);
+#pragma unroll 1
+        for (int c0 = col0; c0 < end; c0 += CH) {
+          uint32_t v[TILES][CH];
+#pragma unroll
+          for (int t = 0; t < TILES; ++t) {
+            if constexpr (CH == 32) tc::tmem_ld32(t_lane + x[t] * BN + c0, v[t]);
+            else tc::tmem_ld16(t_lane + x[t] * BN + c0, v[t]);
           }
-          if (lo_any >= c0 + CH) continue;           // no key of the warp is seen by these rows
-          if (lo_all > c0 || nv < c0 + CH) {
+          tc::tmem_wait_ld();
+          if (!all) {
             // some of the scores are of rows that do not see the key, or of none
 #pragma unroll
-            for (int k = 0; k < CH; ++k)
-              if (k < c_lo - c0 || k >= nv - c0) v[k] = __float_as_uint(-INFINITY);
+            for (int t = 0; t < TILES; ++t) {
+              const int lo = t && !two ? CH : min(max(j0 + t * BM - old - t0, 0), TQ) * p.G - c0;
+#pragma unroll
+              for (int k = 0; k < CH; ++k)
+                if (k < lo || k >= nv - c0) v[t][k] = __float_as_uint(-INFINITY);
+            }
           }
 #pragma unroll
           for (int k = 0; k < CH; k += 4) {
-            const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(s_log + c0 + k);
-            float a0, a1, a2, a3;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), sl2, l4.x), a0, a1);
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(v[k + 2]), __uint_as_float(v[k + 3])), sl2, l4.y), a2, a3);
-            acc[k >> 1 & 2] = f2_add(acc[k >> 1 & 2], f2_pack(tc::ex2(a0), tc::ex2(a1)));
-            acc[k >> 1 & 2 | 1] = f2_add(acc[k >> 1 & 2 | 1], f2_pack(tc::ex2(a2), tc::ex2(a3)));
+            const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(s_log + ls * BN + c0 + k);
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+              float a0, a1, a2, a3;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[t][k]), __uint_as_float(v[t][k + 1])), sl2, l4.x), a0, a1);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[t][k + 2]), __uint_as_float(v[t][k + 3])), sl2, l4.y), a2, a3);
+              acc[t][0] = f2_add(acc[t][0], f2_pack(tc::ex2(a0), tc::ex2(a1)));
+              acc[t][1] = f2_add(acc[t][1], f2_pack(tc::ex2(a2), tc::ex2(a3)));
+            }
           }
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          tc::mbar_arrive(bar(B::SFREE + x[0]));
+          if (WIDE && two) tc::mbar_arrive(bar(B::SFREE + x[TILES - 1]));
+          tc::mbar_arrive(bar(B::LEMPTY + ls));
         }
       }
       if (!ok) break;
-      const uint64_t s2 = f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3]));
-      float e0, e1;
-      f2_unpack(s2, e0, e1);
-      const float sum = e0 + e1;
-      if (SHARED && pc.slot >= 0) {
-        p.ws_sum[(size_t)pc.slot * UK + kt * BM + row] = sum;
-      } else if (at >= 0) {
-        p.w.score[at] = w0 + sum;
-        if (j >= old) p.w.pos[at] = p.w.position[pc.q0 + j - old];
+      float sum[TILES];
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        float e0, e1;
+        f2_unpack(f2_add(acc[t][0], acc[t][1]), e0, e1);
+        sum[t] = e0 + e1;
+      }
+      if constexpr (WIDE) {
+        // the columns' sums meet in the first warpgroup, in their order
+        if (wg) {
+          if (pi && !(ok = wait_all(B::XEMPTY + lg, pi - 1))) break;
+          s_x[(wg - 1) * 2 * BM] = sum[0];
+          s_x[(wg - 1) * 2 * BM + BM] = sum[1];
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(B::XFULL + lg));
+        } else {
+          if (!(ok = wait_all(B::XFULL + lg, pi))) break;
+#pragma unroll
+          for (int w = 0; w < 3; ++w) {
+            sum[0] += s_x[w * 2 * BM];
+            sum[1] += s_x[w * 2 * BM + BM];
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(B::XEMPTY + lg));
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        const int j = j0 + t * BM;
+        if (WIDE && store && pc.slot >= 0) {
+          p.ws_sum[(size_t)pc.slot * UK + t * BM + row] = sum[t];
+        } else if (at[t] >= 0) {
+          p.w.score[at[t]] = w0[t] + sum[t];
+          if (j >= old) p.w.pos[at[t]] = p.w.position[pc.q0 + j - old];
+        }
       }
     }
   }
@@ -587,8 +670,9 @@ cudaError_t launch_attn_weight(const WeightArgs& a, int d, bool f16, cudaStream_
   p.TQ = 1;
   while (p.TQ < most && p.TQ < mean) p.TQ *= 2;
   p.TQ = min(p.TQ, most);
-  const bool shared = r.n_tok > (long long)r.n_req * most;
+  p.shared = r.n_tok > (long long)r.n_req * most;
   p.N = (p.TQ * p.G + 15) / 16 * 16;
+  const bool wide = p.N > 64;
   p.unit_cost = 2;
   p.BR = BM;
   while (r.page_size % p.BR) p.BR /= 2;
@@ -614,13 +698,13 @@ cudaError_t launch_attn_weight(const WeightArgs& a, int d, bool f16, cudaStream_
     cudaError_t e = set_smem_once(kernel, smem, variant);
     if (e != cudaSuccess) return e;
     e = launch_dependent(kernel, dim3(grid), NT, smem, st, tq, tk, p);
-    if (e != cudaSuccess || !shared) return e;
+    if (e != cudaSuccess || !p.shared) return e;
     return launch_dependent(weight_merge_kernel, dim3(grid), UK, 0, st, p);
   };
 #define SKV_WEIGHT(DD, FF, SS, VAR)                                                                \
   (r.wait_ns ? launch(attn_weight_kernel<DD, FF, SS, true>, WCfg<DD>::ALLOC, 8 + (VAR))            \
              : launch(attn_weight_kernel<DD, FF, SS, false>, WCfg<DD>::ALLOC, VAR))
-#define SKV_WEIGHT_FORMS(DD, FF, VAR) (shared ? SKV_WEIGHT(DD, FF, true, VAR) : SKV_WEIGHT(DD, FF, false, VAR + 1))
+#define SKV_WEIGHT_FORMS(DD, FF, VAR) (wide ? SKV_WEIGHT(DD, FF, true, VAR) : SKV_WEIGHT(DD, FF, false, VAR + 1))
   if (d == 128) return f16 ? SKV_WEIGHT_FORMS(128, true, 0) : SKV_WEIGHT_FORMS(128, false, 2);
   return f16 ? SKV_WEIGHT_FORMS(64, true, 4) : SKV_WEIGHT_FORMS(64, false, 6);
 #undef SKV_WEIGHT_FORMS
