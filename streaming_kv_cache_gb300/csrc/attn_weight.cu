@@ -70,9 +70,9 @@ struct WBars {
     KEMPTY = KFULL + KST,      // MMA commit: the piece is done with it
     QFULL = KEMPTY + KST,      // Q tile landed
     QEMPTY = QFULL + QST,      // MMA commit
-    SFULL = QEMPTY + QST,      // MMA commit: scores of key tile kt in buffer x (2 kt + x)
-    SFREE = SFULL + 4,         // its warps have read them
-    LFULL = SFREE + 4,         // Q producer: logarithms of a query tile written
+    SFULL = QEMPTY + QST,      // MMA commit: a step's scores, of both key tiles, in buffer x
+    SFREE = SFULL + 2,         // its warps have read them
+    LFULL = SFREE + 2,         // Q producer: logarithms of a query tile written
     LEMPTY = LFULL + LST,      // its warps are done with them
     XFULL = LEMPTY + LST,      // WIDE: the upper warpgroups' sums of a lane group's keys
     XEMPTY = XFULL + 4,        // they have been added
@@ -164,7 +164,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < B::COUNT; ++i) {
       int count = 1;
-      if (i >= B::SFREE && i < B::SFREE + 4) count = WIDE ? EPI_WARPS : 4;
+      if (i >= B::SFREE && i < B::SFREE + 2) count = WIDE ? EPI_WARPS : 8;
       if (i >= B::LEMPTY && i < B::LEMPTY + LST) count = WIDE ? EPI_WARPS : 8;
       if (i >= B::XFULL && i < B::XFULL + 4) count = 3;
       if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + EPI_WARPS;
@@ -365,7 +365,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const uint32_t idesc = F16 ? tc::idesc_f16(BM, p.N) : tc::idesc_bf16(BM, p.N);
     const uint64_t dk0 = tc::sdesc_sw128(sbase + C::K_OFF), dq0 = tc::sdesc_sw128(sbase + C::Q_OFF);
     const bool lead = tc::elect_one();
-    int nk = 0, nq = 0, cnt0 = 0, cnt1 = 0;  // K tiles, Q tiles, and steps of either key tile so far
+    int nk = 0, n = 0;                       // K tiles and steps so far
     for (int pi = 0; ok; ++pi) {
       const int slot = pi % NP;
       if (!(ok = wait_all(B::PCFULL + slot, pi / NP))) break;
@@ -373,29 +373,32 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       __syncwarp();
       if (lead) tc::mbar_arrive(bar(B::PCEMPTY + slot));
       if (!nt) break;
-      for (int i = 0; i < nt && ok; ++i, ++nq) {
-        const int qs = nq % QST;
-        if (!(ok = wait_all(B::QFULL + qs, nq / QST))) break;
-        for (int kt = 0; kt <= two; ++kt) {
-          const int k = nk + kt, ks = k % KST;
-          int& cnt = kt ? cnt1 : cnt0;
-          const int x = 2 * kt + (cnt & 1);
-          if (i == 0 && !(ok = wait_all(B::KFULL + ks, k / KST))) break;
-          if (cnt >= 2 && !(ok = wait_all(B::SFREE + x, (cnt >> 1) - 1))) break;
-          tc::tc_fence_after();
-          if (lead) {
-            const uint64_t dk = tc::opaque(dk0 + ((uint32_t)(ks * C::KT) >> 4));
+      for (int i = 0; i < nt; ++i, ++n) {
+        const int qs = n % QST, x = n & 1;
+        if (i == 0) {
+          ok = wait_all(B::KFULL + nk % KST, nk / KST);
+          if (two) ok = ok && wait_all(B::KFULL + (nk + 1) % KST, (nk + 1) / KST);
+        }
+        ok = ok && wait_all(B::QFULL + qs, n / QST);
+        if (n >= 2) ok = ok && wait_all(B::SFREE + x, (n >> 1) - 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (lead) {
+          for (int kt = 0; kt <= two; ++kt) {
+            const uint64_t dk = tc::opaque(dk0 + ((uint32_t)((nk + kt) % KST * C::KT) >> 4));
             const uint64_t dq = tc::opaque(dq0 + ((uint32_t)(qs * C::KT) >> 4));
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
-              tc::mma_ss(tmem + x * BN, dk + off, dq + off, idesc, kk > 0);
+              tc::mma_ss(tmem + (2 * x + kt) * BN, dk + off, dq + off, idesc, kk > 0);
             }
-            tc::mma_commit(bar(B::SFULL + x));
-            if (i == nt - 1) tc::mma_commit(bar(B::KEMPTY + ks));
-            if (kt == two) tc::mma_commit(bar(B::QEMPTY + qs));
           }
-          ++cnt;
+          tc::mma_commit(bar(B::SFULL + x));
+          tc::mma_commit(bar(B::QEMPTY + qs));
+          if (i == nt - 1) {
+            tc::mma_commit(bar(B::KEMPTY + nk % KST));
+            if (two) tc::mma_commit(bar(B::KEMPTY + (nk + 1) % KST));
+          }
         }
       }
       nk += 1 + two;
@@ -495,30 +498,19 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const int row = lg * 32 + lane, tile = WIDE ? 0 : wg & 1;   // key, and key tile or the first of two
     const int col0 = WIDE ? wg * WC : 0;
     constexpr int TILES = WIDE ? 2 : 1;              // key tiles of a thread
-    constexpr int CH = WIDE ? 16 : 32;               // scores of one that it takes from TMEM at a time
+    constexpr int CH = 32;                           // scores of one that it takes from TMEM at a time
+    static_assert(WC == CH, "the wide form takes its columns at once");
     const uint32_t t_lane = tmem + ((uint32_t)(lg * 32) << 16);
     const float* s_log = reinterpret_cast<const float*>(smem + C::L_OFF);
     float* s_x = reinterpret_cast<float*>(smem + C::X_OFF) + row;
     const float sl = p.scale_log2;
     const uint64_t sl2 = f2_pack(sl, sl);
-    int n = 0;                                       // query tiles of the CTA so far
-    int cnt[2] = {};                                 // steps of either key tile so far
+    int n = 0;                                       // steps of the CTA so far
     Piece pc;
     for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
       const bool two = tiles_of(pc) == 2;
       if (!WIDE && (pi & 1) != wg >> 1) {            // the other pair's
         n += pc.nt;
-        cnt[0] += pc.nt;
-        cnt[1] += two ? pc.nt : 0;
-        continue;
-      }
-      if (!WIDE && tile && !two) {                   // no keys: the logarithms are given back
-        for (int i = 0; i < pc.nt && ok; ++i, ++n) {
-          ok = wait_all(B::LFULL + n % LST, n / LST);
-          if (lane == 0 && ok) tc::mbar_arrive(bar(B::LEMPTY + n % LST));
-        }
-        cnt[0] += pc.nt;
-        if (!ok) break;
         continue;
       }
       const int j0 = pc.k0 + tile * BM + row, old = pc.kv - pc.L;   // the thread's key, or its first
@@ -537,28 +529,26 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       for (int i = 0; i < pc.nt; ++i, ++n) {
         const int t0 = (pc.qa + i) * TQ, ls = n % LST;
         const int nv = min(TQ, pc.L - t0) * p.G;     // columns with rows
-        int x[TILES];                                // score buffers
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) x[t] = 2 * (tile + t) + (cnt[tile + t] & 1);
-        ok = wait_all(B::LFULL + ls, n / LST) && wait_all(B::SFULL + x[0], cnt[tile] >> 1);
-        if (WIDE && two) ok = ok && wait_all(B::SFULL + x[TILES - 1], cnt[1] >> 1);
-        if (!ok) break;
-        ++cnt[0];
-        cnt[1] += two;
-        tc::tc_fence_after();
-        const int end = min(nv, WIDE ? col0 + WC : BN);
+        const int end = WIDE ? col0 + WC : tile && !two ? 0 : nv;
         // every key of the warp is seen by every row of these columns
-        const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 && nv >= (WIDE ? col0 + WC : (end + CH - 1) / CH * CH) &&
-                         (!WIDE || two);
+        const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 && nv >= (WIDE ? end : (end + CH - 1) / CH * CH) && (!WIDE || two);
+        const uint32_t tS = t_lane + (2 * (n & 1) + tile) * BN;
+        ok = wait_all(B::LFULL + ls, n / LST) && wait_all(B::SFULL + (n & 1), n >> 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        auto release = [&]() {                       // the scores have been read
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(B::SFREE + (n & 1)));
+        };
+        if (!WIDE && end == 0) release();
 #pragma unroll 1
         for (int c0 = col0; c0 < end; c0 += CH) {
           uint32_t v[TILES][CH];
 #pragma unroll
-          for (int t = 0; t < TILES; ++t) {
-            if constexpr (CH == 32) tc::tmem_ld32(t_lane + x[t] * BN + c0, v[t]);
-            else tc::tmem_ld16(t_lane + x[t] * BN + c0, v[t]);
-          }
+          for (int t = 0; t < TILES; ++t) tc::tmem_ld32(tS + t * BN + c0, v[t]);
           tc::tmem_wait_ld();
+          if (WIDE || c0 + CH >= end) release();
           if (!all) {
             // some of the scores are of rows that do not see the key, or of none
 #pragma unroll
@@ -582,13 +572,8 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             }
           }
         }
-        tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(bar(B::SFREE + x[0]));
-          if (WIDE && two) tc::mbar_arrive(bar(B::SFREE + x[TILES - 1]));
-          tc::mbar_arrive(bar(B::LEMPTY + ls));
-        }
+        if (lane == 0) tc::mbar_arrive(bar(B::LEMPTY + ls));
       }
       if (!ok) break;
       float sum[TILES];
