@@ -21,7 +21,7 @@
 // in order, so that results do not depend on timing; else units stay whole.
 //
 //   warps 0 .. 15  four warpgroups, a thread per key: exponentials, sums, scores
-//   then one each  K producer (TMA), Q producer (TMA), MMA issuer, scheduler
+//   then           scheduler and K producer (TMA), Q producer (TMA), two MMA issuers
 #include <math.h>
 
 #include "common.cuh"
@@ -38,10 +38,10 @@ constexpr int BM = 128;       // keys of a key tile
 constexpr int UK = 2 * BM;    // and of a unit
 constexpr int BN = 128;       // rows of a query tile, at most
 constexpr int NT = 640;
-constexpr int EPI_WARPS = 16, WARP_K = 16, WARP_Q = 17, WARP_MMA = 18, WARP_SCHED = 19;
+constexpr int EPI_WARPS = 16, WARP_K = 16, WARP_Q = 17, WARP_MMA = 18;   // two MMA warps
 constexpr int NP = 4;         // pieces in flight between the scheduler and the other warps
 constexpr int LST = 4;        // query tiles whose logarithms are in shared memory
-constexpr int WC = BN / 4;    // columns of a warpgroup in the wide form
+constexpr int WC = BN / 2;    // columns of a warpgroup in the wide form
 constexpr int LIST = 512;     // requests with rows that a CTA knows ahead
 
 template <int D>
@@ -164,8 +164,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < B::COUNT; ++i) {
       int count = 1;
-      if (i >= B::SFREE && i < B::SFREE + 2) count = WIDE ? EPI_WARPS : 8;
-      if (i >= B::LEMPTY && i < B::LEMPTY + LST) count = WIDE ? EPI_WARPS : 8;
+      if (i >= B::SFREE && i < B::SFREE + 2) count = 8;
+      if (i >= B::LEMPTY && i < B::LEMPTY + LST) count = 8;
+      if ((i >= B::KEMPTY && i < B::KEMPTY + KST) || i == B::DRAIN) count = 2;
       if (i >= B::XFULL && i < B::XFULL + 4) count = 3;
       if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + EPI_WARPS;
       tc::mbar_init(bar(i), count);
@@ -283,143 +284,58 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   auto tiles_of = [&](const Piece& pc) { return pc.kv - pc.k0 > BM ? 2 : 1; };   // key tiles with keys
 
   bool ok = true;
-  if (warp == WARP_K) {
-    // ------------------------------------------------------------ K producer
-    int n = 0;                               // tiles issued
-    Piece pc;
-    for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
-      const int32_t* row = r.table + (size_t)pc.b * r.max_block;
-      for (int kt = 0; kt < tiles_of(pc); ++kt, ++n) {
-        // lane x issues box x of a tile: the page of its first row
-        const int r0 = pc.k0 + kt * BM, j = r0 + lane * p.BR;
-        const int id = lane < p.boxes && j < pc.kv ? __ldcg(row + j / r.page_size) : -1;
-        const int n_box = (min(BM, pc.kv - r0) + p.BR - 1) / p.BR;
-        const int st = n % KST;
-        if (n >= KST && !(ok = wait_all(B::KEMPTY + st, n / KST - 1))) break;
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar(B::KFULL + st), n_box * p.BR * 128 * (D / 64));
-        __syncwarp();
-        if (lane < n_box) {
-          // a page outside the pool reads as the zeros outside the map
-          const bool in = id >= 0 && id < r.n_page;
-          if (!in) set_status(r.status, SKV_DEV_BAD_PAGE);
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf)
-            tc::tma_load_3d(sbase + C::K_OFF + st * C::KT + hf * C::HALF + lane * p.BR * 128, &tmap_k, bar(B::KFULL + st),
-                            hf * 64, j % r.page_size, in ? id * r.Hkv + pc.h : -1);
-        }
-      }
-      if (!ok) break;
-    }
-    // the copies this warp started land before the CTA exits
-    for (int j = max(0, n - KST); j < n && drain(B::KFULL + j % KST, j / KST); ++j) {
-    }
-  } else if (warp == WARP_Q) {
-    // ------------------------------------------------------------ Q producer
-    // With a query tile come the logarithms of its columns, four to a lane,
-    // loaded a tile ahead: -lse log2 e, and -inf for a row that gives nothing.
-    int n = 0;
-    int col_tok[4], col_off[4];              // token of a column, and its offset in lse
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = lane * 4 + q;
-      col_tok[q] = c / p.G < TQ ? c / p.G : 1 << 30;
-      col_off[q] = c % p.G * r.n_tok + c / p.G;
-    }
-    Piece pc;
-    for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
-      const float* lse = p.w.lse + (size_t)pc.h * p.G * r.n_tok + pc.q0;
-      float lg[4];
-      auto load_log = [&](int t0) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) lg[q] = col_tok[q] < pc.L - t0 ? lse[col_off[q] + t0] : INFINITY;
-      };
-      load_log(pc.qa * TQ);
-      for (int i = 0; i < pc.nt; ++i, ++n) {
-        const int st = n % QST, ls = n % LST;
-        if (n >= QST && !(ok = wait_all(B::QEMPTY + st, n / QST - 1))) break;
+  if (warp >= EPI_WARPS) {
+    // 512 x 104 + 128 x 64 = the 640 x 96 registers of the launch
+    tc::setmaxnreg_dec<64>();
+    if (warp == WARP_K) {
+      // --------------------------------------- scheduler and K producer, one warp
+      int n = 0, pi = 0;                         // tiles issued, pieces published
+      auto publish = [&](const Piece& pc) {
+        const int slot = pi % NP;
+        if (pi >= NP && !wait_all(B::PCEMPTY + slot, pi / NP - 1)) return false;
         if (lane == 0) {
-          tc::mbar_arrive_expect_tx(bar(B::QFULL + st), TQ * p.G * 128 * (D / 64));
-#pragma unroll
-          for (int hf = 0; hf < D / 64; ++hf)
-            tc::tma_load_3d(sbase + C::Q_OFF + st * C::KT + hf * C::HALF, &tmap_q, bar(B::QFULL + st), hf * 64, pc.h * p.G,
-                            pc.q0 + (pc.qa + i) * TQ);
+          s_piece[slot] = pc;
+          tc::mbar_arrive(bar(B::PCFULL + slot));
         }
         __syncwarp();
-        if (n >= LST && !(ok = wait_all(B::LEMPTY + ls, n / LST - 1))) {
-          ++n;                               // the query tile is on its way
-          break;
-        }
+        ++pi;
+        return true;
+      };
+      auto load = [&](const Piece& pc) {
+        const int32_t* row = r.table + (size_t)pc.b * r.max_block;
+        for (int kt = 0; kt < tiles_of(pc); ++kt, ++n) {
+          // lane x issues box x of a tile: the page of its first row
+          const int r0 = pc.k0 + kt * BM, j = r0 + lane * p.BR;
+          const int id = lane < p.boxes && j < pc.kv ? __ldcg(row + j / r.page_size) : -1;
+          const int n_box = (min(BM, pc.kv - r0) + p.BR - 1) / p.BR;
+          const int st = n % KST;
+          if (n >= KST && !wait_all(B::KEMPTY + st, n / KST - 1)) return false;
+          if (lane == 0) tc::mbar_arrive_expect_tx(bar(B::KFULL + st), n_box * p.BR * 128 * (D / 64));
+          __syncwarp();
+          if (lane < n_box) {
+            // a page outside the pool reads as the zeros outside the map
+            const bool in = id >= 0 && id < r.n_page;
+            if (!in) set_status(r.status, SKV_DEV_BAD_PAGE);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) lg[q] = isfinite(lg[q]) ? lg[q] * -kLog2e : -INFINITY;
-        *reinterpret_cast<float4*>(smem + C::L_OFF + (ls * BN + lane * 4) * 4) = make_float4(lg[0], lg[1], lg[2], lg[3]);
-        if (i + 1 < pc.nt) load_log((pc.qa + i + 1) * TQ);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(B::LFULL + ls));
-      }
-      if (!ok) break;
-    }
-    for (int j = max(0, n - QST); j < n && drain(B::QFULL + j % QST, j / QST); ++j) {
-    }
-  } else if (warp == WARP_MMA) {
-    // ------------------------------------------------------------ MMA issuer
-    const uint32_t idesc = F16 ? tc::idesc_f16(BM, p.N) : tc::idesc_bf16(BM, p.N);
-    const uint64_t dk0 = tc::sdesc_sw128(sbase + C::K_OFF), dq0 = tc::sdesc_sw128(sbase + C::Q_OFF);
-    const bool lead = tc::elect_one();
-    int nk = 0, n = 0;                       // K tiles and steps so far
-    for (int pi = 0; ok; ++pi) {
-      const int slot = pi % NP;
-      if (!(ok = wait_all(B::PCFULL + slot, pi / NP))) break;
-      const int nt = s_piece[slot].nt, two = nt && tiles_of(s_piece[slot]) == 2;
-      __syncwarp();
-      if (lead) tc::mbar_arrive(bar(B::PCEMPTY + slot));
-      if (!nt) break;
-      for (int i = 0; i < nt; ++i, ++n) {
-        const int qs = n % QST, x = n & 1;
-        if (i == 0) {
-          ok = wait_all(B::KFULL + nk % KST, nk / KST);
-          if (two) ok = ok && wait_all(B::KFULL + (nk + 1) % KST, (nk + 1) / KST);
-        }
-        ok = ok && wait_all(B::QFULL + qs, n / QST);
-        if (n >= 2) ok = ok && wait_all(B::SFREE + x, (n >> 1) - 1);
-        if (!ok) break;
-        tc::tc_fence_after();
-        if (lead) {
-          for (int kt = 0; kt <= two; ++kt) {
-            const uint64_t dk = tc::opaque(dk0 + ((uint32_t)((nk + kt) % KST * C::KT) >> 4));
-            const uint64_t dq = tc::opaque(dq0 + ((uint32_t)(qs * C::KT) >> 4));
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
-              tc::mma_ss(tmem + (2 * x + kt) * BN, dk + off, dq + off, idesc, kk > 0);
-            }
-          }
-          tc::mma_commit(bar(B::SFULL + x));
-          tc::mma_commit(bar(B::QEMPTY + qs));
-          if (i == nt - 1) {
-            tc::mma_commit(bar(B::KEMPTY + nk % KST));
-            if (two) tc::mma_commit(bar(B::KEMPTY + (nk + 1) % KST));
+            for (int hf = 0; hf < D / 64; ++hf)
+              tc::tma_load_3d(sbase + C::K_OFF + st * C::KT + hf * C::HALF + lane * p.BR * 128, &tmap_k, bar(B::KFULL + st),
+                              hf * 64, j % r.page_size, in ? id * r.Hkv + pc.h : -1);
           }
         }
-      }
-      nk += 1 + two;
-    }
-    if (lead) tc::mma_commit(bar(B::DRAIN));   // every MMA issued completes before TMEM is released
-    drain(B::DRAIN, 0);
-  } else if (warp == WARP_SCHED) {
-    // ------------------------------------------------------------- scheduler
-    if (lane == 0) {
-      int at = 0;                              // place in the list of requests with rows
+        return true;
+      };
+      int at = 0;                                // place in the list of requests with rows
       int b = s_list[0];
       Span s = request_span(r, b);
       Units u(s, TQ);
       int h, kb;
-      long long pos;                           // of the unit's start
+      long long pos;                             // of the unit's start
       {
         long long off = *s_off;
         const long long per_head = u.positions(TQ, p.unit_cost);
         h = (int)(off / per_head);
         off -= h * per_head;
-        const int whole = p.unit_cost + u.nq;  // positions of a block that every query tile sees
+        const int whole = p.unit_cost + u.nq;    // positions of a block that every query tile sees
         kb = (int)min((long long)u.full(TQ), off / whole);
         off -= (long long)kb * whole;
         for (;; ++kb) {
@@ -429,16 +345,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         pos = g0 - off;
       }
-      int4 shared_unit = make_int4(0, 0, 0, 0);   // the unit that starts here and goes on in the next CTA
-      int pi = 0;
-      auto publish = [&](const Piece& pc) {
-        const int slot = pi % NP;
-        if (pi >= NP && !wait(B::PCEMPTY + slot, pi / NP - 1)) return false;
-        s_piece[slot] = pc;
-        tc::mbar_arrive(bar(B::PCFULL + slot));
-        ++pi;
-        return true;
-      };
+      int4 shared_unit = make_int4(0, 0, 0, 0);  // the unit that starts here and goes on in the next CTA
       while (pos < g1) {
         Piece pc;
         pc.qa = u.first(kb, TQ);
@@ -454,7 +361,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             shared_unit = make_int4((int)((u1 - 1) / share) - (int)blockIdx.x + 1, b, h, kb);
           pc.qa += (int)(lo - u0);
         } else if (pos < g0) {
-          pc.nt = 0;                           // it started in the CTA before
+          pc.nt = 0;                             // it started in the CTA before
         }
         if (pc.nt) {
           pc.b = b;
@@ -463,14 +370,14 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           pc.q0 = s.q0;
           pc.L = s.L;
           pc.kv = s.kv;
-          if (!(ok = publish(pc))) break;
+          if (!(ok = publish(pc) && load(pc))) break;
         }
         pos = u1;
         if (++kb == u.nkb) {
           kb = 0;
           if (++h == r.Hkv) {
             h = 0;
-            if (pos < g1) {                    // the share goes on: some later request has rows
+            if (pos < g1) {                      // the share goes on: some later request has rows
               if (++at < LIST) b = s_list[at];
               else ++b;
               s = request_span(r, b);
@@ -480,28 +387,125 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
         }
       }
-      if (ok) {
-        Piece end{};
-        ok = publish(end);
+      if (ok) ok = publish(Piece{});
+      // always written: the second kernel reads it
+      if (p.shared && lane == 0) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);
+      // the copies this warp started land before the CTA exits
+      for (int j = max(0, n - KST); j < n && drain(B::KFULL + j % KST, j / KST); ++j) {
       }
-      if (p.shared) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);   // always written: the second kernel reads it
-      if (!ok) set_status(r.status, SKV_DEV_TIMEOUT);
-      ok = true;
+    } else if (warp == WARP_Q) {
+      // ------------------------------------------------------------ Q producer
+      // With a query tile come the logarithms of its columns, four to a lane,
+      // loaded a tile ahead: -lse log2 e, and -inf for a row that gives nothing.
+      int n = 0;
+      int col_tok[4], col_off[4];              // token of a column, and its offset in lse
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = lane * 4 + q;
+        col_tok[q] = c / p.G < TQ ? c / p.G : 1 << 30;
+        col_off[q] = c % p.G * r.n_tok + c / p.G;
+      }
+      Piece pc;
+      for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+        const float* lse = p.w.lse + (size_t)pc.h * p.G * r.n_tok + pc.q0;
+        float lg[4];
+        auto load_log = [&](int t0) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) lg[q] = col_tok[q] < pc.L - t0 ? lse[col_off[q] + t0] : INFINITY;
+        };
+        load_log(pc.qa * TQ);
+        for (int i = 0; i < pc.nt; ++i, ++n) {
+          const int st = n % QST, ls = n % LST;
+          if (n >= QST && !(ok = wait_all(B::QEMPTY + st, n / QST - 1))) break;
+          if (lane == 0) {
+            tc::mbar_arrive_expect_tx(bar(B::QFULL + st), TQ * p.G * 128 * (D / 64));
+#pragma unroll
+            for (int hf = 0; hf < D / 64; ++hf)
+              tc::tma_load_3d(sbase + C::Q_OFF + st * C::KT + hf * C::HALF, &tmap_q, bar(B::QFULL + st), hf * 64, pc.h * p.G,
+                              pc.q0 + (pc.qa + i) * TQ);
+          }
+          __syncwarp();
+          if (n >= LST && !(ok = wait_all(B::LEMPTY + ls, n / LST - 1))) {
+            ++n;                               // the query tile is on its way
+            break;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) lg[q] = isfinite(lg[q]) ? lg[q] * -kLog2e : -INFINITY;
+          *reinterpret_cast<float4*>(smem + C::L_OFF + (ls * BN + lane * 4) * 4) = make_float4(lg[0], lg[1], lg[2], lg[3]);
+          if (i + 1 < pc.nt) load_log((pc.qa + i + 1) * TQ);
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(bar(B::LFULL + ls));
+        }
+        if (!ok) break;
+      }
+      for (int j = max(0, n - QST); j < n && drain(B::QFULL + j % QST, j / QST); ++j) {
+      }
+    } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
+      // ----------------------------------------------------------- MMA issuers
+      // One for the even steps and one for the odd: the tensor pipe takes only a
+      // few MMAs ahead, so that one warp's waits and commits, about 650 cycles a
+      // step, would leave it idle; here the other's MMAs run under them.
+      const uint32_t idesc = F16 ? tc::idesc_f16(BM, p.N) : tc::idesc_bf16(BM, p.N);
+      const uint64_t dk0 = tc::sdesc_sw128(sbase + C::K_OFF), dq0 = tc::sdesc_sw128(sbase + C::Q_OFF);
+      const bool lead = tc::elect_one();
+      const int x = warp - WARP_MMA;           // its steps, and its score buffer
+      int nk = 0, n0 = 0;                      // K tiles and steps before the piece
+      for (int pi = 0; ok; ++pi) {
+        const int slot = pi % NP;
+        if (!(ok = wait_all(B::PCFULL + slot, pi / NP))) break;
+        const int nt = s_piece[slot].nt, two = nt && tiles_of(s_piece[slot]) == 2;
+        __syncwarp();
+        if (lead) tc::mbar_arrive(bar(B::PCEMPTY + slot));
+        if (!nt) break;
+        // in a piece without steps for this warp too: its word that it is done
+        // with a K stage must not come before the one on the stage's last use
+        ok = wait_all(B::KFULL + nk % KST, nk / KST);
+        if (two) ok = ok && wait_all(B::KFULL + (nk + 1) % KST, (nk + 1) / KST);
+        if (!ok) break;
+        for (int n = n0 + ((n0 ^ x) & 1); n < n0 + nt; n += 2) {
+          const int qs = n % QST;
+          ok = wait_all(B::QFULL + qs, n / QST);
+          if (n >= 2) ok = ok && wait_all(B::SFREE + x, (n >> 1) - 1);
+          if (!ok) break;
+          tc::tc_fence_after();
+          if (lead) {
+            for (int kt = 0; kt <= two; ++kt) {
+              const uint64_t dk = tc::opaque(dk0 + ((uint32_t)((nk + kt) % KST * C::KT) >> 4));
+              const uint64_t dq = tc::opaque(dq0 + ((uint32_t)(qs * C::KT) >> 4));
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
+                tc::mma_ss(tmem + (2 * x + kt) * BN, dk + off, dq + off, idesc, kk > 0);
+              }
+            }
+            tc::mma_commit(bar(B::SFULL + x));
+            tc::mma_commit(bar(B::QEMPTY + qs));
+          }
+        }
+        if (!ok) break;
+        if (lead)
+          for (int kt = 0; kt <= two; ++kt) tc::mma_commit(bar(B::KEMPTY + (nk + kt) % KST));
+        nk += 1 + two;
+        n0 += nt;
+      }
+      if (lead) tc::mma_commit(bar(B::DRAIN));   // every MMA issued completes before TMEM is released
+      drain(B::DRAIN, 0);
     }
   } else {
+    tc::setmaxnreg_inc<104>();
     // ---------------------------------------------- exponentials and scores
-    // WIDE: a warpgroup takes a quarter of the columns of both key tiles, so
-    // that a logarithm that it reads from shared memory serves two scores.
-    // Else two warpgroups, one per key tile, take all columns of every second
-    // piece, so that one pair's loads and stores run under the other's work.
+    // Two pairs of warpgroups.  WIDE: a pair takes every second step, so that
+    // one's waits and reads run under the other's exponentials; a warpgroup
+    // takes half the columns of both key tiles, so that a logarithm that it
+    // reads from shared memory serves two scores.  Else a pair takes every
+    // second piece, a warpgroup per key tile.
     const int wg = warp >> 2, lg = warp & 3;         // warpgroup, TMEM lane group
     const int row = lg * 32 + lane, tile = WIDE ? 0 : wg & 1;   // key, and key tile or the first of two
-    const int col0 = WIDE ? wg * WC : 0;
+    const int pair = wg >> 1, col0 = WIDE ? (wg & 1) * WC : 0;
     constexpr int TILES = WIDE ? 2 : 1;              // key tiles of a thread
     constexpr int CH = 32;                           // scores of one that it takes from TMEM at a time
-    static_assert(WC == CH, "the wide form takes its columns at once");
     const uint32_t t_lane = tmem + ((uint32_t)(lg * 32) << 16);
-    const float* s_log = reinterpret_cast<const float*>(smem + C::L_OFF);
+    const uint32_t s_log = sbase + C::L_OFF;
     float* s_x = reinterpret_cast<float*>(smem + C::X_OFF) + row;
     const float sl = p.scale_log2;
     const uint64_t sl2 = f2_pack(sl, sl);
@@ -509,29 +513,29 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     Piece pc;
     for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
       const bool two = tiles_of(pc) == 2;
-      if (!WIDE && (pi & 1) != wg >> 1) {            // the other pair's
+      if (!WIDE && (pi & 1) != pair) {               // the other pair's
         n += pc.nt;
         continue;
       }
       const int j0 = pc.k0 + tile * BM + row, old = pc.kv - pc.L;   // the thread's key, or its first
       const int jw = pc.k0 + tile * BM + lg * 32;                   // the warp's first
       const bool store = !WIDE || wg == 0;           // this thread writes the scores
-      // of a whole unit: where they lie, and what the weights are added to
-      long long at[TILES];
-      float w0[TILES];
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        const int j = j0 + t * BM;
-        at[t] = store && pc.slot < 0 && j < pc.kv ? key_place(r, pc.b, pc.h, j) : -1;
-        w0[t] = at[t] >= 0 && j < old && p.w.add ? p.w.add[at[t]] : 0.f;
+      // of a whole unit: where the scores lie and what the weights are added to;
+      // looked up ahead where a piece is short
+      long long at = -1;
+      float w0 = 0.f;
+      if (!WIDE && j0 < pc.kv) {
+        at = key_place(r, pc.b, pc.h, j0);
+        if (at >= 0 && j0 < old && p.w.add) w0 = p.w.add[at];
       }
       uint64_t acc[TILES][2] = {};
       for (int i = 0; i < pc.nt; ++i, ++n) {
+        if (WIDE && (n & 1) != pair) continue;       // the other pair's
         const int t0 = (pc.qa + i) * TQ, ls = n % LST;
         const int nv = min(TQ, pc.L - t0) * p.G;     // columns with rows
-        const int end = WIDE ? col0 + WC : tile && !two ? 0 : nv;
+        const int end = WIDE ? min(nv, col0 + WC) : tile && !two ? 0 : nv;
         // every key of the warp is seen by every row of these columns
-        const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 && nv >= (WIDE ? end : (end + CH - 1) / CH * CH) && (!WIDE || two);
+        const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 && nv >= (end + CH - 1) / CH * CH && (!WIDE || two);
         const uint32_t tS = t_lane + (2 * (n & 1) + tile) * BN;
         ok = wait_all(B::LFULL + ls, n / LST) && wait_all(B::SFULL + (n & 1), n >> 1);
         if (!ok) break;
@@ -541,14 +545,14 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(bar(B::SFREE + (n & 1)));
         };
-        if (!WIDE && end == 0) release();
+        if (end <= col0) release();
 #pragma unroll 1
         for (int c0 = col0; c0 < end; c0 += CH) {
           uint32_t v[TILES][CH];
 #pragma unroll
           for (int t = 0; t < TILES; ++t) tc::tmem_ld32(tS + t * BN + c0, v[t]);
           tc::tmem_wait_ld();
-          if (WIDE || c0 + CH >= end) release();
+          if (c0 + CH >= end) release();
           if (!all) {
             // some of the scores are of rows that do not see the key, or of none
 #pragma unroll
@@ -561,12 +565,13 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           }
 #pragma unroll
           for (int k = 0; k < CH; k += 4) {
-            const ulonglong2 l4 = *reinterpret_cast<const ulonglong2*>(s_log + ls * BN + c0 + k);
+            uint64_t l0, l1;
+            tc::ld_shared_pairs(s_log + (ls * BN + c0 + k) * 4, l0, l1);
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
               float a0, a1, a2, a3;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[t][k]), __uint_as_float(v[t][k + 1])), sl2, l4.x), a0, a1);
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[t][k + 2]), __uint_as_float(v[t][k + 3])), sl2, l4.y), a2, a3);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[t][k]), __uint_as_float(v[t][k + 1])), sl2, l0), a0, a1);
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(v[t][k + 2]), __uint_as_float(v[t][k + 3])), sl2, l1), a2, a3);
               acc[t][0] = f2_add(acc[t][0], f2_pack(tc::ex2(a0), tc::ex2(a1)));
               acc[t][1] = f2_add(acc[t][1], f2_pack(tc::ex2(a2), tc::ex2(a3)));
             }
@@ -602,14 +607,21 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           if (lane == 0) tc::mbar_arrive(bar(B::XEMPTY + lg));
         }
       }
+      if (!store) continue;
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         const int j = j0 + t * BM;
-        if (WIDE && store && pc.slot >= 0) {
+        if (WIDE && pc.slot >= 0) {
           p.ws_sum[(size_t)pc.slot * UK + t * BM + row] = sum[t];
-        } else if (at[t] >= 0) {
-          p.w.score[at[t]] = w0[t] + sum[t];
-          if (j >= old) p.w.pos[at[t]] = p.w.position[pc.q0 + j - old];
+          continue;
+        }
+        if (WIDE && j < pc.kv) {
+          at = key_place(r, pc.b, pc.h, j);
+          w0 = at >= 0 && j < old && p.w.add ? p.w.add[at] : 0.f;
+        }
+        if (at >= 0 && j < pc.kv) {
+          p.w.score[at] = w0 + sum[t];
+          if (j >= old) p.w.pos[at] = p.w.position[pc.q0 + j - old];
         }
       }
     }
