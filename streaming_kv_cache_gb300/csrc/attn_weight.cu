@@ -44,14 +44,21 @@ constexpr int LST = 4;        // query tiles whose logarithms are in shared memo
 constexpr int WC = BN / 2;    // columns of a warpgroup in the wide form
 constexpr int LIST = 512;     // requests with rows that a CTA knows ahead
 
-template <int D>
+template <int D, bool WIDE>
 struct WCfg {
-  static constexpr int KST = D == 128 ? 3 : 6, QST = D == 128 ? 3 : 6;
-  static constexpr int KT = BM * D * 2;        // bytes of a tile
+  // K and Q stages.  Many rows: the key tiles stay, the query tiles pass.  Few
+  // (64 columns at most): the key tiles pass, and the bytes in flight hide
+  // HBM's latency.
+  static constexpr int QR = WIDE ? BN : 64;    // rows of a query stage
+  static constexpr int KST = WIDE ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
+  static constexpr int QST = WIDE ? (D == 128 ? 3 : 6) : (D == 128 ? 3 : 4);
+  static constexpr int KT = BM * D * 2;        // bytes of a key tile
   static constexpr int HALF = BM * 128;        // one 64-dimension half of it
+  static constexpr int QT = QR * D * 2;        // and of a query stage
+  static constexpr int QHALF = QR * 128;
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = KST * KT;
-  static constexpr int L_OFF = Q_OFF + QST * KT;             // logarithms of query tiles' columns, [LST][BN]
+  static constexpr int L_OFF = Q_OFF + QST * QT;             // logarithms of query tiles' columns, [LST][BN]
   static constexpr int X_OFF = L_OFF + LST * BN * 4;         // sums of the upper warpgroups' columns, [3][2][BM]
   static constexpr int BAR_OFF = X_OFF + 3 * 2 * BM * 4;
   static constexpr int MISC_OFF = BAR_OFF + 64 * 8;
@@ -88,7 +95,8 @@ struct WParams {
   WeightArgs w;
   int G, TQ;              // query heads per kv head, tokens per query tile
   int N;                  // columns of an MMA: TQ G, a multiple of 16
-  int BR, boxes;          // rows per TMA box, boxes per key tile
+  int BR, boxes;          // rows per TMA box, boxes per key tile (8 at most)
+  uint32_t ps_m;          // fastdiv multiplier of the page size
   bool shared;            // WIDE: CTAs share units
   int unit_cost;          // positions that a unit takes before its query tiles
   float scale_log2;
@@ -139,7 +147,7 @@ template <int D, bool F16, bool WIDE, bool LIMITED>
 __global__ void __launch_bounds__(NT, 1)
 attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ WParams p) {
-  using C = WCfg<D>;
+  using C = WCfg<D, WIDE>;
   using B = WBars<C::KST, C::QST>;
   constexpr int KST = C::KST, QST = C::QST;
   extern __shared__ uint8_t smem_raw[];
@@ -283,13 +291,50 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   };
   auto tiles_of = [&](const Piece& pc) { return pc.kv - pc.k0 > BM ? 2 : 1; };   // key tiles with keys
 
+  // The page of box `lane & 7` of key tile kt of a piece; nothing is done with
+  // the number before it is needed, so that the load does not stop the warp.
+  auto page_of = [&](const Piece& pc, int kt) {
+    const int x = lane & 7, j = pc.k0 + kt * BM + x * p.BR;
+    int in_page, id = -1;
+    const int at = fastdiv(j, r.page_size, p.ps_m, in_page);
+    if (x < p.boxes && j < pc.kv) id = __ldcg(r.table + (size_t)pc.b * r.max_block + at);
+    return id;
+  };
+  // Key tile kt of a piece, the CTA's nth, into its stage: a box at a time by
+  // one lane, which is the shorter way for eight of them (small pages) than a
+  // box by each of eight lanes.
+  auto load_keys = [&](const Piece& pc, int kt, int n, int id) {
+    const int j0 = pc.k0 + kt * BM, st = n % KST;
+    const int n_box = (min(BM, pc.kv - j0) + p.BR - 1) / p.BR;
+    int in_page;
+    fastdiv(j0 + (lane & 7) * p.BR, r.page_size, p.ps_m, in_page);
+    // a page outside the pool reads as the zeros outside the map
+    const bool in = id >= 0 && id < r.n_page;
+    if (!in && lane < n_box) set_status(r.status, SKV_DEV_BAD_PAGE);
+    const int z = in ? id * r.Hkv + pc.h : -1;
+    if (n >= KST && !wait_all(B::KEMPTY + st, n / KST - 1)) return false;
+    if (lane == 0) tc::mbar_arrive_expect_tx(bar(B::KFULL + st), n_box * p.BR * 128 * (D / 64));
+    const uint32_t dst = sbase + C::K_OFF + st * C::KT;
+    for (int x = 0; x < n_box; ++x) {
+      const int yx = __shfl_sync(0xffffffffu, in_page, x), zx = __shfl_sync(0xffffffffu, z, x);
+      if (lane == 0) {
+#pragma unroll
+        for (int hf = 0; hf < D / 64; ++hf)
+          tc::tma_load_3d(dst + hf * C::HALF + x * p.BR * 128, &tmap_k, bar(B::KFULL + st), hf * 64, yx, zx);
+      }
+    }
+    __syncwarp();
+    return true;
+  };
+
   bool ok = true;
   if (warp >= EPI_WARPS) {
     // 512 x 104 + 128 x 64 = the 640 x 96 registers of the launch
     tc::setmaxnreg_dec<64>();
     if (warp == WARP_K) {
       // --------------------------------------- scheduler and K producer, one warp
-      int n = 0, pi = 0;                         // tiles issued, pieces published
+      int n = 0, pi = 0;                         // key tiles so far, pieces published
+      uint32_t mine = 0;                         // of the last tiles (bit 0: the last), those that this warp loads
       auto publish = [&](const Piece& pc) {
         const int slot = pi % NP;
         if (pi >= NP && !wait_all(B::PCEMPTY + slot, pi / NP - 1)) return false;
@@ -299,29 +344,6 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         __syncwarp();
         ++pi;
-        return true;
-      };
-      auto load = [&](const Piece& pc) {
-        const int32_t* row = r.table + (size_t)pc.b * r.max_block;
-        for (int kt = 0; kt < tiles_of(pc); ++kt, ++n) {
-          // lane x issues box x of a tile: the page of its first row
-          const int r0 = pc.k0 + kt * BM, j = r0 + lane * p.BR;
-          const int id = lane < p.boxes && j < pc.kv ? __ldcg(row + j / r.page_size) : -1;
-          const int n_box = (min(BM, pc.kv - r0) + p.BR - 1) / p.BR;
-          const int st = n % KST;
-          if (n >= KST && !wait_all(B::KEMPTY + st, n / KST - 1)) return false;
-          if (lane == 0) tc::mbar_arrive_expect_tx(bar(B::KFULL + st), n_box * p.BR * 128 * (D / 64));
-          __syncwarp();
-          if (lane < n_box) {
-            // a page outside the pool reads as the zeros outside the map
-            const bool in = id >= 0 && id < r.n_page;
-            if (!in) set_status(r.status, SKV_DEV_BAD_PAGE);
-#pragma unroll
-            for (int hf = 0; hf < D / 64; ++hf)
-              tc::tma_load_3d(sbase + C::K_OFF + st * C::KT + hf * C::HALF + lane * p.BR * 128, &tmap_k, bar(B::KFULL + st),
-                              hf * 64, j % r.page_size, in ? id * r.Hkv + pc.h : -1);
-          }
-        }
         return true;
       };
       int at = 0;                                // place in the list of requests with rows
@@ -346,58 +368,80 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         pos = g0 - off;
       }
       int4 shared_unit = make_int4(0, 0, 0, 0);  // the unit that starts here and goes on in the next CTA
-      while (pos < g1) {
-        Piece pc;
-        pc.qa = u.first(kb, TQ);
-        const int tiles = u.nq - pc.qa;
-        const long long u0 = pos + p.unit_cost, u1 = u0 + tiles;
-        pc.nt = tiles;
-        pc.slot = -1;
-        if (p.shared) {
-          const long long lo = max(u0, g0), hi = min(u1, g1);
-          pc.nt = (int)max(0LL, hi - lo);
-          if (u0 < g0 || u1 > g1) pc.slot = 2 * (int)blockIdx.x + (u0 < g0 ? 0 : 1);
-          if (u0 >= g0 && u0 < g1 && u1 > g1)
-            shared_unit = make_int4((int)((u1 - 1) / share) - (int)blockIdx.x + 1, b, h, kb);
-          pc.qa += (int)(lo - u0);
-        } else if (pos < g0) {
-          pc.nt = 0;                             // it started in the CTA before
-        }
-        if (pc.nt) {
+      // the next piece of the share; nt 0: none
+      auto next_piece = [&]() {
+        Piece pc{};
+        while (pos < g1 && !pc.nt) {
+          pc.qa = u.first(kb, TQ);
+          const int tiles = u.nq - pc.qa;
+          const long long u0 = pos + p.unit_cost, u1 = u0 + tiles;
+          pc.nt = tiles;
+          pc.slot = -1;
+          if (p.shared) {
+            const long long lo = max(u0, g0), hi = min(u1, g1);
+            pc.nt = (int)max(0LL, hi - lo);
+            if (u0 < g0 || u1 > g1) pc.slot = 2 * (int)blockIdx.x + (u0 < g0 ? 0 : 1);
+            if (u0 >= g0 && u0 < g1 && u1 > g1)
+              shared_unit = make_int4((int)((u1 - 1) / share) - (int)blockIdx.x + 1, b, h, kb);
+            pc.qa += (int)(lo - u0);
+          } else if (pos < g0) {
+            pc.nt = 0;                           // it started in the CTA before
+          }
           pc.b = b;
           pc.h = h;
           pc.k0 = kb * UK;
           pc.q0 = s.q0;
           pc.L = s.L;
           pc.kv = s.kv;
-          if (!(ok = publish(pc) && load(pc))) break;
-        }
-        pos = u1;
-        if (++kb == u.nkb) {
-          kb = 0;
-          if (++h == r.Hkv) {
-            h = 0;
-            if (pos < g1) {                      // the share goes on: some later request has rows
-              if (++at < LIST) b = s_list[at];
-              else ++b;
-              s = request_span(r, b);
-              while (s.L == 0 || s.kv == 0) s = request_span(r, ++b);
-              u = Units(s, TQ);
+          pos = u1;
+          if (++kb == u.nkb) {
+            kb = 0;
+            if (++h == r.Hkv) {
+              h = 0;
+              if (pos < g1) {                    // the share goes on: some later request has rows
+                if (++at < LIST) b = s_list[at];
+                else ++b;
+                s = request_span(r, b);
+                while (s.L == 0 || s.kv == 0) s = request_span(r, ++b);
+                u = Units(s, TQ);
+              }
             }
           }
         }
+        return pc;
+      };
+      // a piece ahead, so that its pages' numbers come while the one before loads
+      Piece pc = next_piece();
+      int id0 = page_of(pc, 0), id1 = WIDE ? page_of(pc, 1) : 0;
+      while (pc.nt) {
+        const Piece next = next_piece();
+        const int next0 = page_of(next, 0), next1 = WIDE ? page_of(next, 1) : 0;
+        if (!(ok = publish(pc) && load_keys(pc, 0, n, id0))) break;
+        ++n;
+        mine = mine << 1 | 1;
+        if (tiles_of(pc) == 2) {
+          // (not WIDE: the Q producer's)
+          if (WIDE && !(ok = load_keys(pc, 1, n, id1))) break;
+          ++n;
+          mine = mine << 1 | WIDE;
+        }
+        pc = next;
+        id0 = next0;
+        id1 = next1;
       }
       if (ok) ok = publish(Piece{});
       // always written: the second kernel reads it
       if (p.shared && lane == 0) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);
       // the copies this warp started land before the CTA exits
-      for (int j = max(0, n - KST); j < n && drain(B::KFULL + j % KST, j / KST); ++j) {
-      }
+      for (int j = max(0, n - KST); j < n; ++j)
+        if (mine >> (n - 1 - j) & 1 && !drain(B::KFULL + j % KST, j / KST)) break;
     } else if (warp == WARP_Q) {
       // ------------------------------------------------------------ Q producer
       // With a query tile come the logarithms of its columns, four to a lane,
       // loaded a tile ahead: -lse log2 e, and -inf for a row that gives nothing.
-      int n = 0;
+      // Not WIDE: this warp loads the second key tile of a piece too.
+      int n = 0, nk = 0;                       // query and key tiles so far
+      uint32_t mine = 0;                       // of the last key tiles (bit 0: the last), those that this warp loads
       int col_tok[4], col_off[4];              // token of a column, and its offset in lse
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -407,6 +451,8 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       Piece pc;
       for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+        const bool two = tiles_of(pc) == 2;
+        const int id = !WIDE && two ? page_of(pc, 1) : 0;
         const float* lse = p.w.lse + (size_t)pc.h * p.G * r.n_tok + pc.q0;
         float lg[4];
         auto load_log = [&](int t0) {
@@ -414,6 +460,15 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           for (int q = 0; q < 4; ++q) lg[q] = col_tok[q] < pc.L - t0 ? lse[col_off[q] + t0] : INFINITY;
         };
         load_log(pc.qa * TQ);
+        if (!WIDE) {
+          ++nk;
+          mine <<= 1;
+          if (two) {
+            if (!(ok = load_keys(pc, 1, nk, id))) break;
+            ++nk;
+            mine = mine << 1 | 1;
+          }
+        }
         for (int i = 0; i < pc.nt; ++i, ++n) {
           const int st = n % QST, ls = n % LST;
           if (n >= QST && !(ok = wait_all(B::QEMPTY + st, n / QST - 1))) break;
@@ -421,7 +476,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             tc::mbar_arrive_expect_tx(bar(B::QFULL + st), TQ * p.G * 128 * (D / 64));
 #pragma unroll
             for (int hf = 0; hf < D / 64; ++hf)
-              tc::tma_load_3d(sbase + C::Q_OFF + st * C::KT + hf * C::HALF, &tmap_q, bar(B::QFULL + st), hf * 64, pc.h * p.G,
+              tc::tma_load_3d(sbase + C::Q_OFF + st * C::QT + hf * C::QHALF, &tmap_q, bar(B::QFULL + st), hf * 64, pc.h * p.G,
                               pc.q0 + (pc.qa + i) * TQ);
           }
           __syncwarp();
@@ -440,6 +495,8 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       for (int j = max(0, n - QST); j < n && drain(B::QFULL + j % QST, j / QST); ++j) {
       }
+      for (int j = max(0, nk - KST); j < nk; ++j)
+        if (mine >> (nk - 1 - j) & 1 && !drain(B::KFULL + j % KST, j / KST)) break;
     } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
       // ----------------------------------------------------------- MMA issuers
       // One for the even steps and one for the odd: the tensor pipe takes only a
@@ -471,11 +528,12 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           if (lead) {
             for (int kt = 0; kt <= two; ++kt) {
               const uint64_t dk = tc::opaque(dk0 + ((uint32_t)((nk + kt) % KST * C::KT) >> 4));
-              const uint64_t dq = tc::opaque(dq0 + ((uint32_t)(qs * C::KT) >> 4));
+              const uint64_t dq = tc::opaque(dq0 + ((uint32_t)(qs * C::QT) >> 4));
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::HALF + (kk & 3) * 32) >> 4;
-                tc::mma_ss(tmem + (2 * x + kt) * BN, dk + off, dq + off, idesc, kk > 0);
+                const uint32_t in = (kk & 3) * 32;
+                tc::mma_ss(tmem + (2 * x + kt) * BN, dk + (((kk >> 2) * C::HALF + in) >> 4),
+                           dq + (((kk >> 2) * C::QHALF + in) >> 4), idesc, kk > 0);
               }
             }
             tc::mma_commit(bar(B::SFULL + x));
@@ -674,6 +732,7 @@ cudaError_t launch_attn_weight(const WeightArgs& a, int d, bool f16, cudaStream_
   p.BR = BM;
   while (r.page_size % p.BR) p.BR /= 2;
   p.boxes = BM / p.BR;
+  p.ps_m = fastdiv_m((uint32_t)r.page_size);
   p.scale_log2 = r.sm_scale * kLog2e;
   // in cycles at the 2.07 GHz maximum clock: a slower one only lengthens it
   p.wait_cycles = (uint64_t)(min(r.wait_ns, (uint64_t)1 << 62) * 2.07);
@@ -699,8 +758,8 @@ cudaError_t launch_attn_weight(const WeightArgs& a, int d, bool f16, cudaStream_
     return launch_dependent(weight_merge_kernel, dim3(grid), UK, 0, st, p);
   };
 #define SKV_WEIGHT(DD, FF, SS, VAR)                                                                \
-  (r.wait_ns ? launch(attn_weight_kernel<DD, FF, SS, true>, WCfg<DD>::ALLOC, 8 + (VAR))            \
-             : launch(attn_weight_kernel<DD, FF, SS, false>, WCfg<DD>::ALLOC, VAR))
+  (r.wait_ns ? launch(attn_weight_kernel<DD, FF, SS, true>, WCfg<DD, SS>::ALLOC, 8 + (VAR))        \
+             : launch(attn_weight_kernel<DD, FF, SS, false>, WCfg<DD, SS>::ALLOC, VAR))
 #define SKV_WEIGHT_FORMS(DD, FF, VAR) (wide ? SKV_WEIGHT(DD, FF, true, VAR) : SKV_WEIGHT(DD, FF, false, VAR + 1))
   if (d == 128) return f16 ? SKV_WEIGHT_FORMS(128, true, 0) : SKV_WEIGHT_FORMS(128, false, 2);
   return f16 ? SKV_WEIGHT_FORMS(64, true, 4) : SKV_WEIGHT_FORMS(64, false, 6);
