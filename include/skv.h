@@ -763,8 +763,8 @@ int kv_evict_move(const skv_paged* cache, int32_t n_layer, int32_t n_req, const 
  * without the draft where q is NULL), p of row n-1 where none was, and p too
  * where w is all zeros; and held[b] = kv_len[b] - n + accept_len[b] + 1, the
  * tokens of the request that stay, which kv_paged_trim takes as keep (held may
- * be kv_len itself).  Sums are whole numbers of 2^-55, each entry rounded to
- * one (under 2^-56: to 0): the same on every run and in any split of a row.
+ * be kv_len itself).  Sums are whole numbers of 2^-55, each entry cut to one
+ * (under 2^-55: to 0): the same on every run and in any split of a row.
  *
  * An entry outside [0, 2] (NaN among them) counts as 0 and sets
  * SKV_DEV_BAD_PROB where a sum meets it; a row whose sum is 0 or passes 8 sets

@@ -11,6 +11,7 @@ namespace skv {
 
 struct SampleArgs {
   int n_req, n_tok, n_vocab;
+  int ctas;                   // of a request (a cluster)
   const int32_t* q_start;     // [n_req + 1]
   const int32_t* token;       // [n_tok]
   const void *p, *q;          // [n_tok][n_vocab]; q null: drafts without probabilities

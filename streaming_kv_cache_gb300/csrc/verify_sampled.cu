@@ -7,7 +7,7 @@
 //   draft was rejected, w = p of the last row where none was
 //
 // The comparison is exact: the product of two 24-bit significands fits a
-// double.  So are the sums, up to 2^-56 per entry: probabilities are summed as
+// double.  So are the sums, up to 2^-55 per entry: probabilities are summed as
 // whole numbers of 2^-55, which come out the same in any order, so that the
 // token does not depend on how a row is split over threads (sums in fp32 would
 // move the borders between tokens by about 1e-9, and one draw in some
@@ -24,9 +24,9 @@ namespace skv {
 
 namespace {
 
-constexpr int VT = 512;               // threads per CTA
+constexpr int VT = 512;               // threads per CTA, at most
 constexpr int NW = VT / 32;
-constexpr float FIX = 36028797018963968.f;      // 2^55: the unit of the sums
+constexpr int MAX_CLUSTER = 16;       // CTAs of a request, at most
 constexpr float MOST = 2.f;                     // an entry above is no probability
 constexpr uint64_t LIMIT = 1ull << 58;          // nor a row whose sum passes 8
 
@@ -36,20 +36,43 @@ __device__ __forceinline__ float value(__half x) { return __half2float(x); }
 
 __device__ __forceinline__ bool is_prob(float x) { return x >= 0.f && x <= MOST; }   // false for NaN
 __device__ __forceinline__ float prob(float x) { return is_prob(x) ? x : 0.f; }
-__device__ __forceinline__ long long fixed(float x) { return __float2ll_rn(x * FIX); }
+
+// An entry in units of 2^-55, cut: its 24-bit significand shifted by its
+// exponent (the conversion instruction to 64 bits takes ten times as long: 64
+// requests over 151,936 entries 55 us, FIXED_US so).  Sets odd and gives 0 for
+// what is no probability.
+__device__ __forceinline__ long long fixed(float x, bool& odd) {
+  const uint32_t u = __float_as_uint(x);
+  const bool ok = u <= __float_as_uint(MOST);          // not for a sign, nor NaN
+  odd |= !ok && u != 0x80000000u;                      // -0 is 0
+  const uint32_t top = ((u & 0x7FFFFFu) | 0x800000u) << 1;
+  const uint32_t s = min(128u - (u >> 23), 63u);       // zeros and subnormals go out
+  return ok ? (long long)(((uint64_t)top << 32) >> s) : 0;
+}
 
 enum Mode { REST, FULL, WITHOUT };    // max(p - q, 0); p; p but for the rejected token
 
-template <typename T>
-__global__ void __launch_bounds__(VT) verify_sampled_kernel(const SampleArgs a) {
+// One cluster per request: its CTAs' warps take runs of the row, sum them, and
+// the warp whose run holds the draw goes over it once more, out of L1 or L2.
+// VEC: rows start on 16-byte boundaries and are read 16 bytes a lane; else an
+// entry a lane.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs a) {
+  constexpr int W = VEC ? 16 / (int)sizeof(T) : 1;   // entries of a lane at a time
+  constexpr int U = VEC ? 4 : 8;                     // loads of each row in flight
   __shared__ unsigned long long s_warp[NW];
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ unsigned long long s_total[2][MAX_CLUSTER];
+  const int nw = blockDim.x >> 5;                    // warps of the CTA
+  const int ctas = a.ctas, rank = ctas > 1 ? (int)tc::cluster_ctarank() : 0;
+  const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // it has started
   tc::grid_dep_wait();
   const int lo = a.q_start[b], hi = a.q_start[b + 1];
   const bool bad = lo < 0 || hi < lo || hi > a.n_tok;
   const int n = bad ? 0 : hi - lo;
   if (n == 0) {
-    if (tid == 0) {
+    if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (tid == 0 && rank == 0) {
       if (bad) set_status(a.status, SKV_DEV_BAD_LEN);
       a.accept_len[b] = 0;
       a.next_token[b] = -1;
@@ -59,6 +82,7 @@ __global__ void __launch_bounds__(VT) verify_sampled_kernel(const SampleArgs a) 
   }
   const T* P = static_cast<const T*>(a.p);
   const T* Q = static_cast<const T*>(a.q);
+  const float r = a.r[b];
 
   // accepted drafts: every warp finds out for itself, a lane per draft
   int acc = n - 1, x = -1;            // x: the draft that was rejected
@@ -83,7 +107,7 @@ __global__ void __launch_bounds__(VT) verify_sampled_kernel(const SampleArgs a) 
       break;
     }
   }
-  if (tid == 0) {
+  if (tid == 0 && rank == 0) {
     if (acc < n - 1 && (x < 0 || x >= a.n_vocab)) set_status(a.status, SKV_DEV_BAD_TOKEN);
     a.accept_len[b] = acc;
     if (a.held) a.held[b] = a.kv_len[b] - n + acc + 1;
@@ -92,63 +116,108 @@ __global__ void __launch_bounds__(VT) verify_sampled_kernel(const SampleArgs a) 
   const T* prow = P + (lo + acc) * a.p_stride;
   const T* qrow = Q ? Q + (lo + acc) * a.q_stride : nullptr;
   int mode = acc == n - 1 ? FULL : Q ? REST : WITHOUT;
-  // entry i of the distribution, in units of 2^-55
   bool odd = false;                   // an entry that is no probability
-  auto entry = [&](int i) -> unsigned long long {
-    const float pv = value(prow[i]);
-    odd |= !is_prob(pv);
-    long long w = fixed(prob(pv));
-    if (mode == REST) {
-      const float qv = value(qrow[i]);
-      odd |= !is_prob(qv);
-      w = max(w - fixed(prob(qv)), 0LL);
-    }
-    return mode == WITHOUT && i == x ? 0ull : (unsigned long long)w;
+  // entries [i, i + W) of a row; those past its end are 0
+  struct Entries {
+    T v[W];
   };
-  // a warp takes a run of the vocabulary
-  const int per = (a.n_vocab + NW * 32 - 1) / (NW * 32) * 32;
-  const int i0 = min((long long)a.n_vocab, (long long)warp * per), i1 = min((long long)a.n_vocab, (long long)i0 + per);
-  for (;;) {
+  auto load = [&](const T* row, int i) {
+    Entries e;
+    if (i + W <= a.n_vocab) {
+      if constexpr (VEC) *reinterpret_cast<uint4*>(e.v) = *reinterpret_cast<const uint4*>(row + i);
+      else e.v[0] = row[i];
+    } else {
+#pragma unroll
+      for (int k = 0; k < W; ++k) e.v[k] = i + k < a.n_vocab ? row[i + k] : T(0.f);
+    }
+    return e;
+  };
+  // entry i + k of the distribution, in units of 2^-55
+  auto weight = [&](const Entries& pe, const Entries& qe, int i, int k) -> unsigned long long {
+    long long w = fixed(value(pe.v[k]), odd);
+    if (mode == REST) w = max(w - fixed(value(qe.v[k]), odd), 0LL);
+    return mode == WITHOUT && i + k == x ? 0ull : (unsigned long long)w;
+  };
+  // this warp's run: chunks [c0, c1) of 32 W entries
+  const int chunks = (a.n_vocab + 32 * W - 1) / (32 * W), warps = ctas * nw, gw = rank * nw + warp;
+  const int c0 = (int)((long long)gw * chunks / warps), c1 = (int)((long long)(gw + 1) * chunks / warps);
+  for (int round = 0;; ++round) {
     unsigned long long s = 0;
     bool over = false;
-    for (int i = i0 + lane; i < i1; i += 32) {
-      s += entry(i);
-      if (s > LIMIT) {
-        over = true;
-        s = 0;
-      }
+    for (int c = c0; c < c1; c += U) {
+      Entries pe[U], qe[U];
+#pragma unroll
+      for (int v = 0; v < U; ++v)
+        if (c + v < c1) {
+          const int i = ((c + v) * 32 + lane) * W;
+          pe[v] = load(prow, i);
+          if (mode == REST) qe[v] = load(qrow, i);
+        }
+#pragma unroll
+      for (int v = 0; v < U; ++v)
+        if (c + v < c1) {
+          const int i = ((c + v) * 32 + lane) * W;
+#pragma unroll
+          for (int k = 0; k < W; ++k) s += weight(pe[v], qe[v], i, k);
+          if (s > LIMIT) {
+            over = true;
+            s = 0;
+          }
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     over = __any_sync(0xffffffffu, over) || s > LIMIT;
+    if (over) s = LIMIT + 1;
+    if (lane == 0) s_warp[warp] = s;
     __syncthreads();
-    if (lane == 0) s_warp[warp] = over ? LIMIT + 1 : s;
-    __syncthreads();
-    unsigned long long total = 0, before = 0;
-    for (int w = 0; w < NW; ++w) {
-      if (w == warp) before = total;
-      total += s_warp[w];
-      over |= s_warp[w] > LIMIT;
+    // sums of the CTA's warps, then of the cluster's CTAs; a sum that is too
+    // large stays so
+    unsigned long long mine = 0, before = 0;
+    for (int w = 0; w < nw; ++w) {
+      if (w == warp) before = mine;
+      mine += s_warp[w];
+    }
+    mine = min(mine, (unsigned long long)LIMIT + 1);
+    unsigned long long total = mine;
+    if (ctas > 1) {
+      if (round == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // all have started
+      if (tid < ctas) {
+        const uint32_t to = tc::map_to_cta(tc::smem_u32(&s_total[round][rank]), (uint32_t)tid);
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to), "l"(mine) : "memory");
+      }
+      tc::cluster_sync();
+      total = 0;
+      for (int c = 0; c < ctas; ++c) {
+        if (c == rank) before += total;
+        total += s_total[round][c];
+      }
     }
     if (total == 0 && mode != FULL) {   // nothing is left of p: p itself
       mode = FULL;
+      __syncthreads();
       continue;
     }
-    if (over || total == 0 || total > LIMIT) {
-      if (tid == 0) {
+    if (total == 0 || total > LIMIT) {
+      if (tid == 0 && rank == 0) {
         a.next_token[b] = -1;
         set_status(a.status, SKV_DEV_BAD_PROB);
       }
       break;
     }
-    const float r = a.r[b];
     // a running sum passes r total iff it passes its whole part; NaN: the first entry
     const unsigned long long at = r > 0.f ? min(total - 1, (unsigned long long)((double)total * (double)fminf(r, 1.f))) : 0ull;
     if (at >= before && at - before < s) {
       unsigned long long run = before;
-      for (int i = i0 + lane;; i += 32) {
-        const unsigned long long w = i < i1 ? entry(i) : 0ull;
-        unsigned long long incl = w;
+      for (int c = c0; c < c1; ++c) {
+        const int i = (c * 32 + lane) * W;
+        const Entries pe = load(prow, i);
+        Entries qe;
+        if (mode == REST) qe = load(qrow, i);
+        unsigned long long w[W], sum = 0;
+#pragma unroll
+        for (int k = 0; k < W; ++k) sum += w[k] = weight(pe, qe, i, k);
+        unsigned long long incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
@@ -156,7 +225,16 @@ __global__ void __launch_bounds__(VT) verify_sampled_kernel(const SampleArgs a) 
         }
         const uint32_t past = __ballot_sync(0xffffffffu, run + incl > at);
         if (past) {
-          if (lane == __ffs(past) - 1) a.next_token[b] = i;
+          if (lane == __ffs(past) - 1) {
+            unsigned long long cum = run + incl - sum;
+            int found = i;
+#pragma unroll
+            for (int k = 0; k < W; ++k) {
+              cum += w[k];
+              found += cum <= at;        // the first that passes, and none after it counts
+            }
+            a.next_token[b] = found;
+          }
           break;
         }
         run += __shfl_sync(0xffffffffu, incl, 31);
@@ -167,12 +245,39 @@ __global__ void __launch_bounds__(VT) verify_sampled_kernel(const SampleArgs a) 
   if (__any_sync(0xffffffffu, odd) && lane == 0) set_status(a.status, SKV_DEV_BAD_PROB);
 }
 
+template <typename T>
+cudaError_t launch(const SampleArgs& in, cudaStream_t st) {
+  SampleArgs a = in;
+  const bool vec = ((uintptr_t)a.p | (uintptr_t)a.q) % 16 == 0 && a.p_stride * sizeof(T) % 16 == 0 &&
+                   (!a.q || a.q_stride * sizeof(T) % 16 == 0);
+  const int threads = a.n_req < 16 ? VT : VT / 2;
+  a.ctas = 1;
+  while (a.ctas < MAX_CLUSTER && a.ctas * a.n_req < 304 && a.n_vocab > a.ctas * 2048) a.ctas *= 2;
+  auto kernel = vec ? verify_sampled_kernel<T, true> : verify_sampled_kernel<T, false>;
+  if (a.ctas > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)a.n_req * a.ctas);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 }  // namespace
 
 cudaError_t launch_verify_sampled(const SampleArgs& a, int dtype, cudaStream_t st) {
-  auto launch = [&](auto kernel) { return launch_dependent(kernel, dim3((unsigned)a.n_req), VT, 0, st, a); };
-  if (dtype == SKV_FP32) return launch(verify_sampled_kernel<float>);
-  return dtype == SKV_FP16 ? launch(verify_sampled_kernel<__half>) : launch(verify_sampled_kernel<__nv_bfloat16>);
+  if (dtype == SKV_FP32) return launch<float>(a, st);
+  return dtype == SKV_FP16 ? launch<__half>(a, st) : launch<__nv_bfloat16>(a, st);
 }
 
 }  // namespace skv
