@@ -43,11 +43,23 @@ __device__ __forceinline__ int held_tokens(const EvictArgs& a, int b, bool& bad)
 // ---------------------------------------------------------------------------
 // Plan.  A token's key orders what stays: protected tokens (the first and the
 // most recent positions) above all others, then by score; equal keys go to
-// the lowest index.  The keep-th largest key is found digit by digit, 8 bits
-// at a time, from histograms; then one pass in index order tells kept tokens
-// from the others and numbers the free places and the tokens that move.
+// the lowest index.  The keep-th largest key is found digit by digit, 11, 11
+// and 10 bits, from histograms in shared memory; then scans in index order tell
+// kept tokens from the others and number the free places and the tokens that
+// move.
+//
+// A cluster per (layer, request, kv head).  A thread takes a run of up to KEYS
+// consecutive tokens and keeps their keys in registers, so that scores and
+// positions are read once; a CTA takes SLICE tokens at a time.  How many CTAs
+// of the cluster take part goes by the request's own length, which the host
+// does not know: the others leave at once.  Longer requests than the cluster
+// holds go over their tokens again for every digit.
 
-constexpr int ET = 512;
+constexpr int ET = 256;
+constexpr int KEYS = 32;
+constexpr int SLICE = ET * KEYS;
+constexpr int BINS = 2048;
+constexpr int EVICT_CLUSTER = 8;
 
 // order of floats as unsigned numbers; -0 as 0, NaN below all
 __device__ __forceinline__ uint32_t order_of(float s) {
@@ -56,140 +68,245 @@ __device__ __forceinline__ uint32_t order_of(float s) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(ET) evict_plan_kernel(const EvictArgs a) {
-  __shared__ int s_hist[256];
-  __shared__ int s_sum[3][ET / 32];
-  __shared__ uint32_t s_prefix;
+// sum over the threads before this one, and over all
+__device__ __forceinline__ int block_prefix(int v, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = incl;
+  __syncthreads();
+  int before = incl - v;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < ET / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  return before;
+}
+
+__global__ void __launch_bounds__(ET, 4) evict_plan_kernel(const EvictArgs a) {
+  __shared__ int s_hist[BINS];
+  __shared__ int s_warp[ET / 32];
+  __shared__ int s_cta[2][EVICT_CLUSTER][2];   // of the cluster's CTAs: equal keys; free places and moving tokens
+  __shared__ uint32_t s_digit;
   __shared__ int s_rank;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x % a.Hkv, b = blockIdx.x / a.Hkv % a.n_req, layer = blockIdx.x / a.Hkv / a.n_req;
+  const int tid = threadIdx.x;
+  const int unit = blockIdx.x / a.parts;
+  int rank_cta = a.parts > 1 ? (int)tc::cluster_ctarank() : 0;
+  const int h = unit % a.Hkv, b = unit / a.Hkv % a.n_req, layer = unit / a.Hkv / a.n_req;
   tc::grid_dep_wait();
   bool bad;
   const int m = held_tokens(a, b, bad), keep = a.keep[b];
   const int gone = a.evicted ? a.evicted[b] : 0;
-  if ((bad || keep < 0 || gone < 0) && tid == 0 && h == 0 && layer == 0) set_status(a.status, SKV_DEV_BAD_LEN);
+  if ((bad || keep < 0 || gone < 0) && tid == 0 && rank_cta == 0 && h == 0 && layer == 0) set_status(a.status, SKV_DEV_BAD_LEN);
   int32_t* n_move = a.n_move + ((size_t)layer * a.n_req + b) * a.Hkv + h;
-  if (keep <= 0 || m <= keep) {          // all stay, or none
-    if (tid == 0) *n_move = 0;
+  if (keep <= 0 || m <= keep) {              // all stay, or none
+    if (tid == 0 && rank_cta == 0) *n_move = 0;
     return;
   }
+  // CTAs that take part: as many as hold the tokens in registers, more where
+  // the launch has few requests
+  const int ctas = min(a.parts, (m + a.per_cta - 1) / a.per_cta);
+  if (rank_cta >= ctas) return;
   const Place place = place_of(a, b, h);
   const size_t pool = (size_t)layer * a.n_page * a.Hkv * a.page_size;
   const float* score = a.score + pool;
   const int32_t* pos = a.pos + pool;
   int32_t* move = a.move + pool;
   const long long next = (long long)max(gone, 0) + m;      // the next token's position
-  auto key = [&](int j) -> uint32_t {
-    const long long at = place(j);
-    if (at < 0) return 0;
-    const int p = pos[at];
-    return p < a.n_sink || (p >= next - a.n_recent && p < next) ? 0xFFFFFFFFu : order_of(score[at]);
+  const int safe_lo = (int)min(max(next - a.n_recent, 0LL), 0x7FFFFFFFLL);
+  const int safe_hi = (int)min(next, 0x7FFFFFFFLL);
+  // this CTA's tokens, and a thread's run of them: a multiple of 4, so that a
+  // group of 4 lies in one page
+  const int per = (m + ctas - 1) / ctas + 3 & ~3;
+  const int t_lo = min((long long)m, (long long)rank_cta * per), t_hi = min(m, t_lo + per);
+  const int rounds = max(1, (t_hi - t_lo + SLICE - 1) / SLICE);
+  const int run = rounds > 1 ? KEYS : (t_hi - t_lo + ET - 1) / ET + 3 & ~3;
+  bool lost = false;                         // a page outside the pool
+  uint32_t key[KEYS];
+  int j0 = 0;                                // the run's first token
+  auto load_keys = [&](int round) {
+    j0 = t_lo + round * SLICE + tid * run;
+#pragma unroll
+    for (int g = 0; g < KEYS / 4; ++g) {
+      const int j = j0 + 4 * g;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) key[4 * g + k] = 0;
+      if (4 * g >= run || j >= t_hi) continue;
+      const long long at = place(j);
+      if (at < 0) {
+        lost = true;
+        continue;
+      }
+      const float4 s = *reinterpret_cast<const float4*>(score + at);
+      const int4 p = *reinterpret_cast<const int4*>(pos + at);
+      const float sv[4] = {s.x, s.y, s.z, s.w};
+      const int pv[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool safe = pv[k] < a.n_sink || (pv[k] >= safe_lo && pv[k] < safe_hi);
+        key[4 * g + k] = safe ? 0xFFFFFFFFu : order_of(sv[k]);
+      }
+    }
   };
+  // tokens of the run that there are
+  auto count = [&]() { return max(0, min(run, t_hi - j0)); };
+
   // the keep-th largest key: `prefix` its digits so far, `rank` its rank among
   // the keys that share them
   uint32_t prefix = 0;
   int rank = keep;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += ET) s_hist[i] = 0;
+  load_keys(0);
+#pragma unroll 1
+  for (int digit = 0; digit < 3; ++digit) {
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
+    for (int i = tid; i < BINS; i += ET) s_hist[i] = 0;
     __syncthreads();
-    for (int j = tid; j < m; j += ET) {
-      const uint32_t k = key(j);
-      if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&s_hist[k >> shift & 255], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // digits from the top, 8 to a lane
-      int c[8], sum = 0;
+    int top = 0;                             // protected tokens: many with one key, counted without atomics
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) load_keys(round);
+      const int n = count();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum += c[i] = s_hist[255 - (lane * 8 + i)];
-      int incl = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += t;
+      for (int i = 0; i < KEYS; ++i) {
+        const bool in = i < n && (digit == 0 || key[i] >> (shift + bits) == prefix);
+        if (in && key[i] == 0xFFFFFFFFu) ++top;
+        else if (in) atomicAdd(&s_hist[key[i] >> shift & ((1 << bits) - 1)], 1);
       }
-      int above = incl - sum;
-      if (above < rank && incl >= rank) {
+    }
+    top = __reduce_add_sync(0xffffffffu, top);
+    if ((tid & 31) == 0 && top) atomicAdd(&s_hist[(1 << bits) - 1], top);
+    __syncthreads();
+    // bins from the top, 8 to a thread; all of the cluster's CTAs
+    int c[BINS / ET], sum = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (above < rank && above + c[i] >= rank) {
-            s_prefix = prefix << 8 | (255 - (lane * 8 + i));
-            s_rank = rank - above;
-          }
-          above += c[i];
+    for (int i = 0; i < BINS / ET; ++i) c[i] = s_hist[BINS - 1 - (tid * (BINS / ET) + i)];
+    if (ctas > 1) {
+      tc::cluster_sync();
+      for (int o = 1; o < ctas; ++o) {
+        const int other = rank_cta + o < ctas ? rank_cta + o : rank_cta + o - ctas;
+        const uint32_t from = tc::map_to_cta(tc::smem_u32(&s_hist[BINS - (tid + 1) * (BINS / ET)]), (uint32_t)other);
+#pragma unroll
+        for (int i = 0; i < BINS / ET; ++i) {
+          int x;
+          asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(x) : "r"(from + 4 * (BINS / ET - 1 - i)));
+          c[i] += x;
         }
       }
+      tc::cluster_sync();
+    }
+#pragma unroll
+    for (int i = 0; i < BINS / ET; ++i) sum += c[i];
+    int total;
+    int above = block_prefix(sum, s_warp, total);
+    if (above < rank && above + sum >= rank) {
+#pragma unroll
+      for (int i = 0; i < BINS / ET; ++i) {
+        if (above < rank && above + c[i] >= rank) {
+          s_digit = BINS - 1 - (tid * (BINS / ET) + i);
+          s_rank = rank - above;
+        }
+        above += c[i];
+      }
     }
     __syncthreads();
-    prefix = s_prefix;
+    prefix = prefix << bits | s_digit;
     rank = s_rank;
   }
-  // in index order: of the keys equal to the keep-th largest the first `rank`
-  // stay; free places and moving tokens in ascending order
-  int eq0 = 0, hole0 = 0, come0 = 0;     // before this round's tokens
-  bool lost = false;                     // a page outside the pool
-  for (int j0 = 0; j0 < m; j0 += ET) {
-    const int j = j0 + tid;
-    const bool in = j < m;
-    const uint32_t k = in ? key(j) : 0;
-    const bool eq = in && k == prefix;
-    const uint32_t me = __ballot_sync(0xffffffffu, eq);
-    const uint32_t before = (1u << lane) - 1;
-    if (lane == 0) s_sum[0][warp] = __popc(me);
-    __syncthreads();
-    int eq_at = eq0 + __popc(me & before), eq_all = 0;
-    for (int w = 0; w < ET / 32; ++w) {
-      if (w < warp) eq_at += s_sum[0][w];
-      eq_all += s_sum[0][w];
-    }
-    const bool kept = in && (k > prefix || (eq && eq_at < rank));
-    const bool hole = in && j < keep && !kept, come = in && j >= keep && kept;
-    const uint32_t mh = __ballot_sync(0xffffffffu, hole), mc = __ballot_sync(0xffffffffu, come);
-    if (lane == 0) {
-      s_sum[1][warp] = __popc(mh);
-      s_sum[2][warp] = __popc(mc);
-    }
-    __syncthreads();
-    int hole_at = hole0 + __popc(mh & before), come_at = come0 + __popc(mc & before);
-    for (int w = 0; w < ET / 32; ++w) {
-      if (w < warp) {
-        hole_at += s_sum[1][w];
-        come_at += s_sum[2][w];
+
+  // In index order: of the keys equal to the keep-th largest the first `rank`
+  // stay; free places and moving tokens are numbered in ascending order.  The
+  // CTAs of a cluster count first what lies before each of them.
+  int eq0 = 0, hole0 = 0, come0 = 0;
+  // pass 0: equal keys of the CTA; 1: its free places and moving tokens; 2: the moves
+#pragma unroll 1
+  for (int pass = ctas > 1 ? 0 : 2; pass < 3; ++pass) {
+    int eq_run = eq0, hole_run = hole0, come_run = come0;
+    for (int round = 0; round < rounds; ++round) {
+      if (rounds > 1) load_keys(round);
+      const int n = count();
+      int eq = 0;
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) eq += i < n && key[i] == prefix;
+      int all;
+      int eq_at = eq_run + block_prefix(eq, s_warp, all);
+      eq_run += all;
+      if (pass == 0) continue;
+      uint32_t kept = 0;                     // a bit per token of the run
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) {
+        const bool same = key[i] == prefix;
+        if (i < n && (key[i] > prefix || (same && eq_at < rank))) kept |= 1u << i;
+        eq_at += i < n && same;
       }
-      hole0 += s_sum[1][w];
-      come0 += s_sum[2][w];
+      const uint32_t in = n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1;
+      const int below = max(0, min(keep - j0, 32));           // tokens of the run in the first keep places
+      const uint32_t low = below >= 32 ? 0xFFFFFFFFu : (1u << below) - 1;
+      uint32_t hole = in & low & ~kept, come = in & ~low & kept;
+      const int at = block_prefix(__popc(hole) << 16 | __popc(come), s_warp, all);
+      int hole_at = hole_run + (at >> 16), come_at = come_run + (at & 0xFFFF);
+      hole_run += all >> 16;
+      come_run += all & 0xFFFF;
+      if (pass == 1) continue;
+      for (; hole; hole &= hole - 1, ++hole_at) {
+        const long long to = place(2 * hole_at);
+        if (to >= 0) move[to] = j0 + __ffs(hole) - 1;
+      }
+      for (; come; come &= come - 1, ++come_at) {
+        const long long to = place(2 * come_at + 1);
+        if (to >= 0) move[to] = j0 + __ffs(come) - 1;
+      }
     }
-    eq0 += eq_all;
-    if (hole || come) {
-      const long long at = place(hole ? 2 * hole_at : 2 * come_at + 1);
-      if (at >= 0) move[at] = j;
+    if (pass == 2) {
+      if (tid == 0 && rank_cta == ctas - 1) *n_move = come_run;
+      break;
     }
-    lost |= in && place(j) < 0;
-    __syncthreads();
+    // to every CTA of the cluster
+    if (tid < ctas) {
+      const uint32_t to = tc::map_to_cta(tc::smem_u32(&s_cta[pass][rank_cta][0]), (uint32_t)tid);
+      asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(to), "r"(pass ? hole_run : eq_run), "r"(come_run) : "memory");
+    }
+    tc::cluster_sync();
+    for (int c = 0; c < rank_cta; ++c) {
+      if (pass == 0) {
+        eq0 += s_cta[0][c][0];
+      } else {
+        hole0 += s_cta[1][c][0];
+        come0 += s_cta[1][c][1];
+      }
+    }
   }
   if (__syncthreads_or(lost) && tid == 0) set_status(a.status, SKV_DEV_BAD_PAGE);
-  if (tid == 0) *n_move = come0;
 }
 
 // ---------------------------------------------------------------------------
-// Move.  D / 8 lanes take 16 bytes of a row each, of its key and its value;
-// bound by HBM.
+// Move.  D / 8 lanes take 16 bytes of a row each, of its key and its value; a
+// warp takes every parts-th batch of moves of one (layer, request, kv head),
+// and all loads of a batch are out before its first store.  Bound by HBM.
 
 constexpr int MT = 256;
+constexpr int MU = 4;           // moves in flight per D / 8 lanes
 
 template <int D>
 __global__ void __launch_bounds__(MT) evict_move_kernel(const EvictArgs a) {
-  constexpr int LANES = D / 8, PER = MT / LANES;     // moves that a CTA has in flight
-  const int unit = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+  constexpr int LANES = D / 8, PER = 32 / LANES;     // moves that a warp takes side by side
+  const int worker = blockIdx.x * (MT / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int unit = worker / a.parts, part = worker % a.parts;
+  if (unit >= a.n_layer * a.n_req * a.Hkv) return;
   const int h = unit % a.Hkv, b = unit / a.Hkv % a.n_req, layer = unit / a.Hkv / a.n_req;
-  const int c = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  const int c = lane % LANES, sub = lane / LANES;
   tc::grid_dep_wait();
   bool bad;
   const int m = held_tokens(a, b, bad);
-  int n = a.n_move[((size_t)layer * a.n_req + b) * a.Hkv + h];
+  const int n = a.n_move[unit];
   bad |= n < 0 || n > m / 2;
   if (bad) {
-    if (part == 0 && threadIdx.x == 0) set_status(a.status, SKV_DEV_BAD_LEN);
+    if (part == 0 && lane == 0) set_status(a.status, SKV_DEV_BAD_LEN);
     return;
   }
   const Place place = place_of(a, b, h);
@@ -197,39 +314,95 @@ __global__ void __launch_bounds__(MT) evict_move_kernel(const EvictArgs a) {
   const int32_t* move = a.move + pool;
   uint4* k = reinterpret_cast<uint4*>(a.k) + pool * LANES;
   uint4* v = reinterpret_cast<uint4*>(a.v) + pool * LANES;
-  for (int i = part * PER + sub; i < n; i += a.parts * PER) {
-    const long long at = place(2 * i);
-    int2 p = make_int2(0, 0);
-    if (at >= 0) p = *reinterpret_cast<const int2*>(move + at);
-    if (p.x < 0 || p.x >= m || p.y < 0 || p.y >= m) {
-      if (c == 0) set_status(a.status, SKV_DEV_BAD_LEN);
-      continue;
+  for (int i0 = part * PER * MU + sub; i0 < n; i0 += a.parts * PER * MU) {
+    int2 pair[MU];
+    int fault[MU];                           // status bits of a move that is left out
+    long long at[MU];
+#pragma unroll
+    for (int u = 0; u < MU; ++u) {
+      const int i = i0 + u * PER;
+      pair[u] = make_int2(0, 0);
+      at[u] = i < n ? place(2 * i) : -1;
+      fault[u] = at[u] >= 0 ? 0 : SKV_DEV_BAD_PAGE;
+      if (at[u] >= 0) pair[u] = *reinterpret_cast<const int2*>(move + at[u]);
     }
-    const long long to = place(p.x), from = place(p.y);
-    if (at < 0 || to < 0 || from < 0) {
-      if (c == 0) set_status(a.status, SKV_DEV_BAD_PAGE);
-      continue;
+    long long to[MU], from[MU];
+#pragma unroll
+    for (int u = 0; u < MU; ++u) {
+      if (pair[u].x < 0 || pair[u].x >= m || pair[u].y < 0 || pair[u].y >= m) {
+        fault[u] = SKV_DEV_BAD_LEN;
+        pair[u] = make_int2(0, 0);
+      }
+      to[u] = from[u] = -1;
+      if (i0 + u * PER < n) {
+        to[u] = place(pair[u].x);
+        from[u] = place(pair[u].y);
+        if (to[u] < 0 || from[u] < 0) fault[u] |= SKV_DEV_BAD_PAGE;
+        if (fault[u]) {
+          if (c == 0) set_status(a.status, fault[u]);
+          to[u] = -1;
+        }
+      }
     }
-    k[to * LANES + c] = k[from * LANES + c];
-    v[to * LANES + c] = v[from * LANES + c];
-    if (c == 0) {
-      a.score[pool + to] = a.score[pool + from];
-      a.pos[pool + to] = a.pos[pool + from];
-    }
+    uint4 kv[MU], vv[MU];
+    float sc[MU];
+    int ps[MU];
+#pragma unroll
+    for (int u = 0; u < MU; ++u)
+      if (to[u] >= 0) {
+        kv[u] = k[from[u] * LANES + c];
+        vv[u] = v[from[u] * LANES + c];
+        if (c == 0) {
+          sc[u] = a.score[pool + from[u]];
+          ps[u] = a.pos[pool + from[u]];
+        }
+      }
+#pragma unroll
+    for (int u = 0; u < MU; ++u)
+      if (to[u] >= 0) {
+        k[to[u] * LANES + c] = kv[u];
+        v[to[u] * LANES + c] = vv[u];
+        if (c == 0) {
+          a.score[pool + to[u]] = sc[u];
+          a.pos[pool + to[u]] = ps[u];
+        }
+      }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_evict_plan(const EvictArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)a.n_layer * a.n_req * a.Hkv;
-  return launch_dependent(evict_plan_kernel, dim3(grid), ET, 0, st, a);
+cudaError_t launch_evict_plan(const EvictArgs& in, cudaStream_t st) {
+  EvictArgs a = in;
+  const long long units = (long long)a.n_layer * a.n_req * a.Hkv;
+  const long long room = min((long long)a.max_block * a.page_size, (long long)kMaxKeys);   // tokens that a request may hold
+  // CTAs of a cluster: what holds a full table row in registers; and where that
+  // leaves SMs idle, shorter slices
+  a.per_cta = SLICE;
+  while (a.per_cta > 1024 && units * ((room + a.per_cta - 1) / a.per_cta) < 304) a.per_cta /= 2;
+  a.parts = 1;
+  while (a.parts < EVICT_CLUSTER && (long long)a.parts * a.per_cta < room) a.parts *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)(units * a.parts));
+  cfg.blockDim = dim3(ET);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.parts > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, evict_plan_kernel, a);
 }
 
 cudaError_t launch_evict_move(const EvictArgs& a, int d, cudaStream_t st) {
   EvictArgs p = a;
-  p.parts = 8;
-  const unsigned grid = (unsigned)a.n_layer * a.n_req * a.Hkv * p.parts;
+  const long long units = (long long)a.n_layer * a.n_req * a.Hkv;
+  // some 8,000 warps: one wave
+  p.parts = (int)max(1LL, min(256LL, 8192 / units));
+  const unsigned grid = (unsigned)((units * p.parts + MT / 32 - 1) / (MT / 32));
   auto launch = [&](auto kernel) { return launch_dependent(kernel, dim3(grid), MT, 0, st, p); };
   return d == 128 ? launch(evict_move_kernel<128>) : launch(evict_move_kernel<64>);
 }

@@ -30,7 +30,8 @@ struct EvictArgs {
   const int32_t* kv_len;      // [n_req]
   const int32_t *keep, *evicted;
   int n_sink, n_recent;
-  int parts;                  // CTAs per (layer, request, kv head) of a move
+  int parts;                  // CTAs of a (layer, request, kv head)
+  int per_cta;                // of a plan: tokens from which on one more of them takes part
   float* score;               // pools [n_layer][n_page][Hkv][page_size]
   int32_t* pos;
   int32_t* move;

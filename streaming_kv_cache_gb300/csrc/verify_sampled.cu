@@ -38,9 +38,7 @@ __device__ __forceinline__ bool is_prob(float x) { return x >= 0.f && x <= MOST;
 __device__ __forceinline__ float prob(float x) { return is_prob(x) ? x : 0.f; }
 
 // An entry in units of 2^-55, cut: its 24-bit significand shifted by its
-// exponent (the conversion instruction to 64 bits takes ten times as long: 64
-// requests over 151,936 entries 55 us, FIXED_US so).  Sets odd and gives 0 for
-// what is no probability.
+// exponent.  Sets odd and gives 0 for what is no probability.
 __device__ __forceinline__ long long fixed(float x, bool& odd) {
   const uint32_t u = __float_as_uint(x);
   const bool ok = u <= __float_as_uint(MOST);          // not for a sign, nor NaN
@@ -48,6 +46,22 @@ __device__ __forceinline__ long long fixed(float x, bool& odd) {
   const uint32_t top = ((u & 0x7FFFFFu) | 0x800000u) << 1;
   const uint32_t s = min(128u - (u >> 23), 63u);       // zeros and subnormals go out
   return ok ? (long long)(((uint64_t)top << 32) >> s) : 0;
+}
+
+// The same for many entries in [0, 2], as three whole numbers of 32 bits in
+// units of 2^-19, 2^-42 and 2^-55 that sums are taken of one by one.  Added
+// to 16 and cut, an entry leaves its first part in the sum's low bits; what it
+// lacks is exact, and goes on to 2^-19 and 2^-32.  Seven additions and no
+// 64-bit arithmetic: fixed() takes 17 instructions, and a conversion to 64 bits
+// ten times as long (64 requests over 151,936 entries: 55 us with the
+// conversion, 34 with fixed(), 20.6 so).
+struct Limbs {
+  uint32_t a, b, c;
+};
+__device__ __forceinline__ Limbs limbs(float x) {
+  const float a = __fadd_rz(x, 16.f), r = x - (a - 16.f);
+  const float b = __fadd_rz(r, 0x1p-19f), q = r - (b - 0x1p-19f);
+  return {__float_as_uint(a), __float_as_uint(b), __float_as_uint(__fadd_rz(q, 0x1p-32f))};
 }
 
 enum Mode { REST, FULL, WITHOUT };    // max(p - q, 0); p; p but for the rejected token
@@ -59,8 +73,8 @@ enum Mode { REST, FULL, WITHOUT };    // max(p - q, 0); p; p but for the rejecte
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs a) {
   constexpr int W = VEC ? 16 / (int)sizeof(T) : 1;   // entries of a lane at a time
-  constexpr int U = VEC ? 4 : 8;                     // loads of each row in flight
-  __shared__ unsigned long long s_warp[NW];
+  constexpr int U = VEC ? (sizeof(T) == 4 ? 4 : 2) : 8;   // loads of each row in flight
+  __shared__ unsigned long long s_warp[NW], s_part[NW];
   __shared__ unsigned long long s_total[2][MAX_CLUSTER];
   const int nw = blockDim.x >> 5;                    // warps of the CTA
   const int ctas = a.ctas, rank = ctas > 1 ? (int)tc::cluster_ctarank() : 0;
@@ -122,13 +136,18 @@ __global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs 
     T v[W];
   };
   auto load = [&](const T* row, int i) {
-    Entries e;
+    Entries e{};
     if (i + W <= a.n_vocab) {
-      if constexpr (VEC) *reinterpret_cast<uint4*>(e.v) = *reinterpret_cast<const uint4*>(row + i);
-      else e.v[0] = row[i];
-    } else {
+      if constexpr (VEC) {
+        const uint4 raw = *reinterpret_cast<const uint4*>(row + i);
+        e = *reinterpret_cast<const Entries*>(&raw);
+      } else {
+        e.v[0] = row[i];
+      }
+    } else if (VEC && i < a.n_vocab) {
 #pragma unroll
-      for (int k = 0; k < W; ++k) e.v[k] = i + k < a.n_vocab ? row[i + k] : T(0.f);
+      for (int k = 0; k < W; ++k)
+        if (i + k < a.n_vocab) e.v[k] = row[i + k];
     }
     return e;
   };
@@ -144,26 +163,49 @@ __global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs 
   for (int round = 0;; ++round) {
     unsigned long long s = 0;
     bool over = false;
+    uint32_t most = 0;                // of the entries' bits: above those of 2 with a sign, a NaN or a large one
     for (int c = c0; c < c1; c += U) {
       Entries pe[U], qe[U];
 #pragma unroll
-      for (int v = 0; v < U; ++v)
-        if (c + v < c1) {
-          const int i = ((c + v) * 32 + lane) * W;
-          pe[v] = load(prow, i);
-          if (mode == REST) qe[v] = load(qrow, i);
-        }
+      for (int v = 0; v < U; ++v) {
+        const int i = c + v < c1 ? ((c + v) * 32 + lane) * W : a.n_vocab;
+        pe[v] = load(prow, i);
+        qe[v] = mode == REST ? load(qrow, i) : Entries{};
+      }
+      int da = 0, db = 0, dc = 0;
 #pragma unroll
       for (int v = 0; v < U; ++v)
-        if (c + v < c1) {
-          const int i = ((c + v) * 32 + lane) * W;
 #pragma unroll
-          for (int k = 0; k < W; ++k) s += weight(pe[v], qe[v], i, k);
-          if (s > LIMIT) {
-            over = true;
-            s = 0;
-          }
+        for (int k = 0; k < W; ++k) {
+          const float pv = value(pe[v].v[k]), qv = value(qe[v].v[k]);
+          most = max(max(most, __float_as_uint(pv)), __float_as_uint(qv));
+          const Limbs x1 = limbs(pv), x2 = limbs(fminf(pv, qv));     // max(p - q, 0) = p - min(p, q)
+          da += x1.a - x2.a;
+          db += x1.b - x2.b;
+          dc += x1.c - x2.c;
         }
+      s += ((long long)da << 36) + ((long long)db << 13) + dc;
+      if (s > LIMIT) {
+        over = true;
+        s = 0;
+      }
+    }
+    if (most > __float_as_uint(MOST)) {
+      // once more, entry by entry
+      s = 0;
+      over = false;
+      for (int c = c0; c < c1; ++c) {
+        const int i = (c * 32 + lane) * W;
+        const Entries pe = load(prow, i), qe = mode == REST ? load(qrow, i) : Entries{};
+#pragma unroll
+        for (int k = 0; k < W; ++k) s += weight(pe, qe, i, k);
+        if (s > LIMIT) {
+          over = true;
+          s = 0;
+        }
+      }
+    } else if (mode == WITHOUT && x >= 0 && x < a.n_vocab && x / W / 32 >= c0 && x / W / 32 < c1 && x / W % 32 == lane) {
+      s -= fixed(value(prow[x]), odd);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -173,11 +215,8 @@ __global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs 
     __syncthreads();
     // sums of the CTA's warps, then of the cluster's CTAs; a sum that is too
     // large stays so
-    unsigned long long mine = 0, before = 0;
-    for (int w = 0; w < nw; ++w) {
-      if (w == warp) before = mine;
-      mine += s_warp[w];
-    }
+    unsigned long long mine = 0, before = 0;     // of this CTA, and of those before it
+    for (int w = 0; w < nw; ++w) mine += s_warp[w];
     mine = min(mine, (unsigned long long)LIMIT + 1);
     unsigned long long total = mine;
     if (ctas > 1) {
@@ -189,7 +228,7 @@ __global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs 
       tc::cluster_sync();
       total = 0;
       for (int c = 0; c < ctas; ++c) {
-        if (c == rank) before += total;
+        if (c == rank) before = total;
         total += s_total[round][c];
       }
     }
@@ -207,37 +246,71 @@ __global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs 
     }
     // a running sum passes r total iff it passes its whole part; NaN: the first entry
     const unsigned long long at = r > 0.f ? min(total - 1, (unsigned long long)((double)total * (double)fminf(r, 1.f))) : 0ull;
-    if (at >= before && at - before < s) {
+    if (at >= before && at - before < mine) {
+      // This CTA's part of the row has it.  The run of the warp that it falls
+      // in is gone over by all warps, SU chunks each at a time: by that warp
+      // alone, a load's latency for every chunk, it took 12 of 38 us.
+      constexpr int SU = 2;
       unsigned long long run = before;
-      for (int c = c0; c < c1; ++c) {
-        const int i = (c * 32 + lane) * W;
-        const Entries pe = load(prow, i);
-        Entries qe;
-        if (mode == REST) qe = load(qrow, i);
-        unsigned long long w[W], sum = 0;
+      int w = 0;
+      while (at - run >= s_warp[w]) run += s_warp[w++];
+      const int first = (int)((long long)(rank * nw + w) * chunks / warps);
+      const int last = (int)((long long)(rank * nw + w + 1) * chunks / warps);
+      for (int c = first; c < last; c += nw * SU) {
+        unsigned long long part[SU][W], sum = 0;
+        const int mc = c + warp * SU;
+        Entries pe[SU], qe[SU];
 #pragma unroll
-        for (int k = 0; k < W; ++k) sum += w[k] = weight(pe, qe, i, k);
-        unsigned long long incl = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += t;
+        for (int v = 0; v < SU; ++v) {
+          const int i = mc + v < last ? ((mc + v) * 32 + lane) * W : a.n_vocab;
+          pe[v] = load(prow, i);
+          qe[v] = mode == REST ? load(qrow, i) : Entries{};
         }
-        const uint32_t past = __ballot_sync(0xffffffffu, run + incl > at);
-        if (past) {
-          if (lane == __ffs(past) - 1) {
-            unsigned long long cum = run + incl - sum;
-            int found = i;
+        unsigned long long chunk_sum[SU];
 #pragma unroll
-            for (int k = 0; k < W; ++k) {
-              cum += w[k];
-              found += cum <= at;        // the first that passes, and none after it counts
-            }
-            a.next_token[b] = found;
+        for (int v = 0; v < SU; ++v) {
+          chunk_sum[v] = 0;
+#pragma unroll
+          for (int k = 0; k < W; ++k) {
+            part[v][k] = weight(pe[v], qe[v], ((mc + v) * 32 + lane) * W, k);
+            chunk_sum[v] += part[v][k];
           }
-          break;
+          sum += chunk_sum[v];
         }
-        run += __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) s_part[warp] = sum;
+        __syncthreads();
+        int f = 0;                       // the warp whose chunks hold it
+        while (f < nw && at - run >= s_part[f]) run += s_part[f++];
+        if (f == warp) {
+#pragma unroll
+          for (int v = 0; v < SU; ++v) {
+            unsigned long long incl = chunk_sum[v];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const unsigned long long t = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += t;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, run + incl > at);
+            if (past) {
+              if (lane == __ffs(past) - 1) {
+                unsigned long long cum = run + incl - chunk_sum[v];
+                int found = ((mc + v) * 32 + lane) * W;
+#pragma unroll
+                for (int k = 0; k < W; ++k) {
+                  cum += part[v][k];
+                  found += cum <= at;    // the first that passes, and none after it counts
+                }
+                a.next_token[b] = found;
+              }
+              break;
+            }
+            run += __shfl_sync(0xffffffffu, incl, 31);
+          }
+        }
+        if (f < nw) break;
+        __syncthreads();
       }
     }
     break;
