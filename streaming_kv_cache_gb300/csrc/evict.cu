@@ -55,9 +55,7 @@ __device__ __forceinline__ int held_tokens(const EvictArgs& a, int b, bool& bad)
 // does not know: the others leave at once.  Longer requests than the cluster
 // holds go over their tokens again for every digit.
 
-constexpr int ET = 256;
 constexpr int KEYS = 32;
-constexpr int SLICE = ET * KEYS;
 constexpr int BINS = 2048;
 constexpr int EVICT_CLUSTER = 8;
 
@@ -69,6 +67,7 @@ __device__ __forceinline__ uint32_t order_of(float s) {
 }
 
 // sum over the threads before this one, and over all
+template <int ET>
 __device__ __forceinline__ int block_prefix(int v, int* s_warp, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
@@ -90,7 +89,9 @@ __device__ __forceinline__ int block_prefix(int v, int* s_warp, int& total) {
   return before;
 }
 
-__global__ void __launch_bounds__(ET, 4) evict_plan_kernel(const EvictArgs a) {
+template <int ET>
+__global__ void __launch_bounds__(ET, 1024 / ET) evict_plan_kernel(const EvictArgs a) {
+  constexpr int SLICE = ET * KEYS;
   __shared__ int s_hist[BINS];
   __shared__ int s_warp[ET / 32];
   __shared__ int s_cta[2][EVICT_CLUSTER][2];   // of the cluster's CTAs: equal keys; free places and moving tokens
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(ET, 4) evict_plan_kernel(const EvictArgs a) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const bool safe = pv[k] < a.n_sink || (pv[k] >= safe_lo && pv[k] < safe_hi);
-        key[4 * g + k] = safe ? 0xFFFFFFFFu : order_of(sv[k]);
+        key[4 * g + k] = j + k >= t_hi ? 0 : safe ? 0xFFFFFFFFu : order_of(sv[k]);
       }
     }
   };
@@ -168,19 +169,24 @@ __global__ void __launch_bounds__(ET, 4) evict_plan_kernel(const EvictArgs a) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
     for (int i = tid; i < BINS; i += ET) s_hist[i] = 0;
     __syncthreads();
-    int top = 0;                             // protected tokens: many with one key, counted without atomics
+    int top = 0;                             // protected tokens: many of one key, counted without atomics
+    const uint32_t mask = (1u << bits) - 1;
     for (int round = 0; round < rounds; ++round) {
       if (rounds > 1) load_keys(round);
-      const int n = count();
 #pragma unroll
-      for (int i = 0; i < KEYS; ++i) {
-        const bool in = i < n && (digit == 0 || key[i] >> (shift + bits) == prefix);
-        if (in && key[i] == 0xFFFFFFFFu) ++top;
-        else if (in) atomicAdd(&s_hist[key[i] >> shift & ((1 << bits) - 1)], 1);
+      for (int g = 0; g < KEYS; g += 4) {
+        if (g >= run) break;
+#pragma unroll
+        for (int i = g; i < g + 4; ++i) {
+          const uint32_t k = key[i];
+          if (digit && k >> (shift + bits) != prefix) continue;
+          if (k == 0xFFFFFFFFu) ++top;
+          else if (k) atomicAdd(&s_hist[k >> shift & mask], 1);
+        }
       }
     }
     top = __reduce_add_sync(0xffffffffu, top);
-    if ((tid & 31) == 0 && top) atomicAdd(&s_hist[(1 << bits) - 1], top);
+    if ((tid & 31) == 0 && top) atomicAdd(&s_hist[mask], top);
     __syncthreads();
     // bins from the top, 8 to a thread; all of the cluster's CTAs
     int c[BINS / ET], sum = 0;
@@ -203,7 +209,8 @@ __global__ void __launch_bounds__(ET, 4) evict_plan_kernel(const EvictArgs a) {
 #pragma unroll
     for (int i = 0; i < BINS / ET; ++i) sum += c[i];
     int total;
-    int above = block_prefix(sum, s_warp, total);
+    const int rank_before = rank;
+    int above = block_prefix<ET>(sum, s_warp, total);
     if (above < rank && above + sum >= rank) {
 #pragma unroll
       for (int i = 0; i < BINS / ET; ++i) {
@@ -214,9 +221,14 @@ __global__ void __launch_bounds__(ET, 4) evict_plan_kernel(const EvictArgs a) {
         above += c[i];
       }
     }
+    if (tid == 0 && total < rank) {          // the rest of the rank falls to keys of 0, which no bin counts
+      s_digit = 0;
+      s_rank = rank - total;
+    }
     __syncthreads();
     prefix = prefix << bits | s_digit;
     rank = s_rank;
+    if (total < rank_before) break;
   }
 
   // In index order: of the keys equal to the keep-th largest the first `rank`
@@ -230,25 +242,27 @@ __global__ void __launch_bounds__(ET, 4) evict_plan_kernel(const EvictArgs a) {
     for (int round = 0; round < rounds; ++round) {
       if (rounds > 1) load_keys(round);
       const int n = count();
-      int eq = 0;
+      const uint32_t in = n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1;   // a bit per token of the run
+      uint32_t kept = 0, same = 0;
 #pragma unroll
-      for (int i = 0; i < KEYS; ++i) eq += i < n && key[i] == prefix;
+      for (int g = 0; g < KEYS; g += 4) {
+        if (g >= run) break;
+#pragma unroll
+        for (int i = g; i < g + 4; ++i) {
+          if (key[i] > prefix) kept |= 1u << i;
+          if (key[i] == prefix) same |= 1u << i;
+        }
+      }
+      same &= in;
       int all;
-      int eq_at = eq_run + block_prefix(eq, s_warp, all);
+      int eq_at = eq_run + block_prefix<ET>(__popc(same), s_warp, all);
       eq_run += all;
       if (pass == 0) continue;
-      uint32_t kept = 0;                     // a bit per token of the run
-#pragma unroll
-      for (int i = 0; i < KEYS; ++i) {
-        const bool same = key[i] == prefix;
-        if (i < n && (key[i] > prefix || (same && eq_at < rank))) kept |= 1u << i;
-        eq_at += i < n && same;
-      }
-      const uint32_t in = n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1;
+      for (; same && eq_at < rank; same &= same - 1, ++eq_at) kept |= same & -same;
       const int below = max(0, min(keep - j0, 32));           // tokens of the run in the first keep places
       const uint32_t low = below >= 32 ? 0xFFFFFFFFu : (1u << below) - 1;
       uint32_t hole = in & low & ~kept, come = in & ~low & kept;
-      const int at = block_prefix(__popc(hole) << 16 | __popc(come), s_warp, all);
+      const int at = block_prefix<ET>(__popc(hole) << 16 | __popc(come), s_warp, all);
       int hole_at = hole_run + (at >> 16), come_at = come_run + (at & 0xFFFF);
       hole_run += all >> 16;
       come_run += all & 0xFFFF;
@@ -376,9 +390,10 @@ cudaError_t launch_evict_plan(const EvictArgs& in, cudaStream_t st) {
   EvictArgs a = in;
   const long long units = (long long)a.n_layer * a.n_req * a.Hkv;
   const long long room = min((long long)a.max_block * a.page_size, (long long)kMaxKeys);   // tokens that a request may hold
-  // CTAs of a cluster: what holds a full table row in registers; and where that
-  // leaves SMs idle, shorter slices
-  a.per_cta = SLICE;
+  // 512 threads where 256 do not hold a full table row in registers.  CTAs of a
+  // cluster: what holds it; and where that leaves SMs idle, shorter slices.
+  const int threads = room > 256 * KEYS ? 512 : 256;
+  a.per_cta = threads * KEYS;
   while (a.per_cta > 1024 && units * ((room + a.per_cta - 1) / a.per_cta) < 304) a.per_cta /= 2;
   a.parts = 1;
   while (a.parts < EVICT_CLUSTER && (long long)a.parts * a.per_cta < room) a.parts *= 2;
@@ -390,11 +405,11 @@ cudaError_t launch_evict_plan(const EvictArgs& in, cudaStream_t st) {
   attr[1].val.clusterDim.x = (unsigned)a.parts;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3((unsigned)(units * a.parts));
-  cfg.blockDim = dim3(ET);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = a.parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, evict_plan_kernel, a);
+  return cudaLaunchKernelEx(&cfg, threads == 512 ? evict_plan_kernel<512> : evict_plan_kernel<256>, a);
 }
 
 cudaError_t launch_evict_move(const EvictArgs& a, int d, cudaStream_t st) {
