@@ -159,18 +159,24 @@ __global__ void __launch_bounds__(ET, 1024 / ET) evict_plan_kernel(const EvictAr
   // tokens of the run that there are
   auto count = [&]() { return max(0, min(run, t_hi - j0)); };
 
-  // the keep-th largest key: `prefix` its digits so far, `rank` its rank among
-  // the keys that share them
+  // The keep-th largest key: `prefix` its digits so far, `rank` its rank among
+  // the keys that share them.  Protected tokens (many of one key, the top bin's
+  // only one: the largest score is +inf) are counted without atomics; keys of
+  // 0, the lowest, by no bin.
   uint32_t prefix = 0;
   int rank = keep;
   load_keys(0);
 #pragma unroll 1
   for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bits = digit == 2 ? 10 : 11;
+    // keys from lo on, span of them: those with the prefix
+    const uint32_t lo = digit ? max(prefix << (shift + bits), 1u) : 1u;
+    const uint32_t span = digit ? (prefix << (shift + bits)) + (1u << (shift + bits)) - lo : 0xFFFFFFFEu;
+    const uint32_t mask = ((1u << bits) - 1) << 2;
     for (int i = tid; i < BINS; i += ET) s_hist[i] = 0;
     __syncthreads();
-    int top = 0;                             // protected tokens: many of one key, counted without atomics
-    const uint32_t mask = (1u << bits) - 1;
+    const uint32_t hist = tc::smem_u32(s_hist);
+    int top = 0;
     for (int round = 0; round < rounds; ++round) {
       if (rounds > 1) load_keys(round);
 #pragma unroll
@@ -179,14 +185,17 @@ __global__ void __launch_bounds__(ET, 1024 / ET) evict_plan_kernel(const EvictAr
 #pragma unroll
         for (int i = g; i < g + 4; ++i) {
           const uint32_t k = key[i];
-          if (digit && k >> (shift + bits) != prefix) continue;
-          if (k == 0xFFFFFFFFu) ++top;
-          else if (k) atomicAdd(&s_hist[k >> shift & mask], 1);
+          const uint32_t bin = hist + ((digit == 2 ? k << 2 : k >> (shift - 2)) & mask);
+          asm volatile("{\n .reg .pred p;\n setp.lt.u32 p, %1, %2;\n @p red.shared.add.u32 [%0], 1;\n}\n"
+                       ::"r"(bin), "r"(k - lo), "r"(span) : "memory");
+          if (digit == 0) top += k == 0xFFFFFFFFu;
         }
       }
     }
-    top = __reduce_add_sync(0xffffffffu, top);
-    if ((tid & 31) == 0 && top) atomicAdd(&s_hist[mask], top);
+    if (digit == 0) {
+      top = __reduce_add_sync(0xffffffffu, top);
+      if ((tid & 31) == 0 && top) atomicAdd(&s_hist[BINS - 1], top);
+    }
     __syncthreads();
     // bins from the top, 8 to a thread; all of the cluster's CTAs
     int c[BINS / ET], sum = 0;
@@ -229,6 +238,10 @@ __global__ void __launch_bounds__(ET, 1024 / ET) evict_plan_kernel(const EvictAr
     prefix = prefix << bits | s_digit;
     rank = s_rank;
     if (total < rank_before) break;
+    if (prefix == BINS - 1 && digit == 0) {
+      prefix = 0xFFFFFFFFu;
+      break;
+    }
   }
 
   // In index order: of the keys equal to the keep-th largest the first `rank`
