@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(ET, 1024 / ET) evict_plan_kernel(const EvictAr
   constexpr int SLICE = ET * KEYS;
   __shared__ int s_hist[BINS];
   __shared__ int s_warp[ET / 32];
+  __shared__ uint16_t s_list[SLICE];           // tokens of a round, by their offset
   __shared__ int s_cta[2][EVICT_CLUSTER][2];   // of the cluster's CTAs: equal keys; free places and moving tokens
   __shared__ uint32_t s_digit;
   __shared__ int s_rank;
@@ -276,18 +277,22 @@ __global__ void __launch_bounds__(ET, 1024 / ET) evict_plan_kernel(const EvictAr
       const uint32_t low = below >= 32 ? 0xFFFFFFFFu : (1u << below) - 1;
       uint32_t hole = in & low & ~kept, come = in & ~low & kept;
       const int at = block_prefix<ET>(__popc(hole) << 16 | __popc(come), s_warp, all);
-      int hole_at = hole_run + (at >> 16), come_at = come_run + (at & 0xFFFF);
-      hole_run += all >> 16;
-      come_run += all & 0xFFFF;
-      if (pass == 1) continue;
-      for (; hole; hole &= hole - 1, ++hole_at) {
-        const long long to = place(2 * hole_at);
-        if (to >= 0) move[to] = j0 + __ffs(hole) - 1;
+      const int holes = all >> 16, comes = all & 0xFFFF;
+      if (pass == 2) {
+        // into shared memory in their order, then out, a thread per entry
+        int to = at >> 16;
+        for (; hole; hole &= hole - 1) s_list[to++] = (uint16_t)(tid * run + __ffs(hole) - 1);
+        to = holes + (at & 0xFFFF);
+        for (; come; come &= come - 1) s_list[to++] = (uint16_t)(tid * run + __ffs(come) - 1);
+        __syncthreads();
+        const int base = t_lo + round * SLICE;
+        for (int i = tid; i < holes + comes; i += ET) {
+          const long long entry = place(i < holes ? 2 * (hole_run + i) : 2 * (come_run + i - holes) + 1);
+          if (entry >= 0) move[entry] = base + s_list[i];
+        }
       }
-      for (; come; come &= come - 1, ++come_at) {
-        const long long to = place(2 * come_at + 1);
-        if (to >= 0) move[to] = j0 + __ffs(come) - 1;
-      }
+      hole_run += holes;
+      come_run += comes;
     }
     if (pass == 2) {
       if (tid == 0 && rank_cta == ctas - 1) *n_move = come_run;
