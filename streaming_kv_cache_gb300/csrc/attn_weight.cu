@@ -21,7 +21,8 @@
 // in order, so that results do not depend on timing; else units stay whole.
 //
 //   warps 0 .. 15  four warpgroups, a thread per key: exponentials, sums, scores
-//   then           scheduler and K producer (TMA), Q producer (TMA), two MMA issuers
+//   then           scheduler and K producer (TMA), Q producer (TMA), two MMA
+//                  issuers; with few rows three more K producers
 #include <math.h>
 
 #include "common.cuh"
@@ -37,8 +38,8 @@ namespace {
 constexpr int BM = 128;       // keys of a key tile
 constexpr int UK = 2 * BM;    // and of a unit
 constexpr int BN = 128;       // rows of a query tile, at most
-constexpr int NT = 640;
 constexpr int EPI_WARPS = 16, WARP_K = 16, WARP_Q = 17, WARP_MMA = 18;   // two MMA warps
+constexpr int WARP_MORE = 20;     // in the narrow form, three more K producers
 constexpr int NP = 4;         // pieces in flight between the scheduler and the other warps
 constexpr int LST = 4;        // query tiles whose logarithms are in shared memory
 constexpr int WC = BN / 2;    // columns of a warpgroup in the wide form
@@ -46,6 +47,12 @@ constexpr int LIST = 512;     // requests with rows that a CTA knows ahead
 
 template <int D, bool WIDE>
 struct WCfg {
+  static constexpr int NT = WIDE ? 640 : 768;
+  // K producers of a key tile.  A copy of a small page's 16 rows takes the
+  // issuing warp some 150 cycles, a key tile of them 2500, in which HBM would
+  // bring two: with few rows each half of each tile has a warp (64 requests, pages of 16
+  // tokens: 135 us with one warp per tile, 111 so).
+  static constexpr int PARTS = WIDE ? 1 : 2;
   // K and Q stages.  Many rows: the key tiles stay, the query tiles pass.  Few
   // (64 columns at most): the key tiles pass, and the bytes in flight hide
   // HBM's latency.
@@ -61,7 +68,7 @@ struct WCfg {
   static constexpr int L_OFF = Q_OFF + QST * QT;             // logarithms of query tiles' columns, [LST][BN]
   static constexpr int X_OFF = L_OFF + LST * BN * 4;         // sums of the upper warpgroups' columns, [3][2][BM]
   static constexpr int BAR_OFF = X_OFF + 3 * 2 * BM * 4;
-  static constexpr int MISC_OFF = BAR_OFF + 64 * 8;
+  static constexpr int MISC_OFF = BAR_OFF + 72 * 8;
   static constexpr int PIECE_OFF = MISC_OFF + 64;
   static constexpr int LIST_OFF = PIECE_OFF + NP * 64;
   static constexpr int SCAN_OFF = LIST_OFF + LIST * 2;
@@ -70,11 +77,11 @@ struct WCfg {
   static_assert(ALLOC <= 232448, "shared memory");
 };
 
-template <int KST, int QST>
+template <int KST, int QST, int PARTS>
 struct WBars {
   enum : int {
-    KFULL = 0,                 // K tile landed
-    KEMPTY = KFULL + KST,      // MMA commit: the piece is done with it
+    KFULL = 0,                 // a part of a K tile landed
+    KEMPTY = KFULL + PARTS * KST,   // MMA commit: the piece is done with it
     QFULL = KEMPTY + KST,      // Q tile landed
     QEMPTY = QFULL + QST,      // MMA commit
     SFULL = QEMPTY + QST,      // MMA commit: a step's scores, of both key tiles, in buffer x
@@ -88,7 +95,7 @@ struct WBars {
     DRAIN = PCEMPTY + NP,      // MMA commit: everything issued is complete
     COUNT
   };
-  static_assert(COUNT <= 64, "barrier slots");
+  static_assert(COUNT <= 72, "barrier slots");
 };
 
 struct WParams {
@@ -144,12 +151,12 @@ __device__ __forceinline__ long long key_place(const RaggedArgs& r, int b, int h
 }
 
 template <int D, bool F16, bool WIDE, bool LIMITED>
-__global__ void __launch_bounds__(NT, 1)
+__global__ void __launch_bounds__(WCfg<D, WIDE>::NT, 1)
 attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ WParams p) {
   using C = WCfg<D, WIDE>;
-  using B = WBars<C::KST, C::QST>;
-  constexpr int KST = C::KST, QST = C::QST;
+  using B = WBars<C::KST, C::QST, C::PARTS>;
+  constexpr int KST = C::KST, QST = C::QST, PARTS = C::PARTS, NT = C::NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = tc::smem_u32(smem);
@@ -176,7 +183,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (i >= B::LEMPTY && i < B::LEMPTY + LST) count = 8;
       if ((i >= B::KEMPTY && i < B::KEMPTY + KST) || i == B::DRAIN) count = 2;
       if (i >= B::XFULL && i < B::XFULL + 4) count = 3;
-      if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = 3 + EPI_WARPS;
+      if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = (WIDE ? 3 : 6) + EPI_WARPS;
       tc::mbar_init(bar(i), count);
     }
     tc::fence_barrier_init();
@@ -300,10 +307,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if (x < p.boxes && j < pc.kv) id = __ldcg(r.table + (size_t)pc.b * r.max_block + at);
     return id;
   };
-  // Key tile kt of a piece, the CTA's nth, into its stage: a box at a time by
-  // one lane, which is the shorter way for eight of them (small pages) than a
-  // box by each of eight lanes.
-  auto load_keys = [&](const Piece& pc, int kt, int n, int id) {
+  // Part `part` of key tile kt of a piece, the CTA's nth, into its stage: a half
+  // of the dimensions (d = 64: every second box), a box at a time by one lane.
+  auto load_keys = [&](const Piece& pc, int kt, int part, int n, int id) {
     const int j0 = pc.k0 + kt * BM, st = n % KST;
     const int n_box = (min(BM, pc.kv - j0) + p.BR - 1) / p.BR;
     int in_page;
@@ -313,23 +319,35 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if (!in && lane < n_box) set_status(r.status, SKV_DEV_BAD_PAGE);
     const int z = in ? id * r.Hkv + pc.h : -1;
     if (n >= KST && !wait_all(B::KEMPTY + st, n / KST - 1)) return false;
-    if (lane == 0) tc::mbar_arrive_expect_tx(bar(B::KFULL + st), n_box * p.BR * 128 * (D / 64));
+    constexpr bool BOXES = PARTS == 2 && D == 64;
+    const int first = BOXES ? part : 0, step = BOXES ? 2 : 1;
+    constexpr int HALVES = PARTS == 2 ? 1 : D / 64;     // of this part's boxes
+    const int h0 = PARTS == 2 && D == 128 ? part : 0;
+    const uint32_t full = bar(B::KFULL + part * KST + st);
+    if (lane == 0) tc::mbar_arrive_expect_tx(full, max(0, (n_box - first + step - 1) / step) * p.BR * 128 * HALVES);
     const uint32_t dst = sbase + C::K_OFF + st * C::KT;
-    for (int x = 0; x < n_box; ++x) {
+    for (int x = first; x < n_box; x += step) {
       const int yx = __shfl_sync(0xffffffffu, in_page, x), zx = __shfl_sync(0xffffffffu, z, x);
       if (lane == 0) {
 #pragma unroll
-        for (int hf = 0; hf < D / 64; ++hf)
-          tc::tma_load_3d(dst + hf * C::HALF + x * p.BR * 128, &tmap_k, bar(B::KFULL + st), hf * 64, yx, zx);
+        for (int hf = 0; hf < HALVES; ++hf)
+          tc::tma_load_3d(dst + (h0 + hf) * C::HALF + x * p.BR * 128, &tmap_k, full, (h0 + hf) * 64, yx, zx);
       }
     }
     __syncwarp();
     return true;
   };
+  // the last copies that a warp has started into a part land before the CTA
+  // exits; mine: which of the last tiles are (bit 0: the last of n)
+  auto drain_keys = [&](int part, int n, uint32_t mine) {
+    for (int j = max(0, n - KST); j < n; ++j)
+      if (mine >> (n - 1 - j) & 1 && !tc::mbar_sleep(bar(B::KFULL + part * KST + j % KST), (j / KST) & 1)) break;
+  };
 
   bool ok = true;
   if (warp >= EPI_WARPS) {
-    // 512 x 104 + 128 x 64 = the 640 x 96 registers of the launch
+    // 512 x 104 + 128 x 64 = the 640 x 96 registers of the launch; with few rows
+    // 512 x 88 + 256 x 64 = 768 x 80
     tc::setmaxnreg_dec<64>();
     if (warp == WARP_K) {
       // --------------------------------------- scheduler and K producer, one warp
@@ -416,12 +434,11 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       while (pc.nt) {
         const Piece next = next_piece();
         const int next0 = page_of(next, 0), next1 = WIDE ? page_of(next, 1) : 0;
-        if (!(ok = publish(pc) && load_keys(pc, 0, n, id0))) break;
+        if (!(ok = publish(pc) && load_keys(pc, 0, 0, n, id0))) break;
         ++n;
         mine = mine << 1 | 1;
         if (tiles_of(pc) == 2) {
-          // (not WIDE: the Q producer's)
-          if (WIDE && !(ok = load_keys(pc, 1, n, id1))) break;
+          if (WIDE && !(ok = load_keys(pc, 1, 0, n, id1))) break;
           ++n;
           mine = mine << 1 | WIDE;
         }
@@ -432,16 +449,12 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (ok) ok = publish(Piece{});
       // always written: the second kernel reads it
       if (p.shared && lane == 0) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);
-      // the copies this warp started land before the CTA exits
-      for (int j = max(0, n - KST); j < n; ++j)
-        if (mine >> (n - 1 - j) & 1 && !drain(B::KFULL + j % KST, j / KST)) break;
+      drain_keys(0, n, mine);
     } else if (warp == WARP_Q) {
       // ------------------------------------------------------------ Q producer
       // With a query tile come the logarithms of its columns, four to a lane,
       // loaded a tile ahead: -lse log2 e, and -inf for a row that gives nothing.
-      // Not WIDE: this warp loads the second key tile of a piece too.
-      int n = 0, nk = 0;                       // query and key tiles so far
-      uint32_t mine = 0;                       // of the last key tiles (bit 0: the last), those that this warp loads
+      int n = 0;
       int col_tok[4], col_off[4];              // token of a column, and its offset in lse
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -451,8 +464,6 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       Piece pc;
       for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
-        const bool two = tiles_of(pc) == 2;
-        const int id = !WIDE && two ? page_of(pc, 1) : 0;
         const float* lse = p.w.lse + (size_t)pc.h * p.G * r.n_tok + pc.q0;
         float lg[4];
         auto load_log = [&](int t0) {
@@ -460,15 +471,6 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           for (int q = 0; q < 4; ++q) lg[q] = col_tok[q] < pc.L - t0 ? lse[col_off[q] + t0] : INFINITY;
         };
         load_log(pc.qa * TQ);
-        if (!WIDE) {
-          ++nk;
-          mine <<= 1;
-          if (two) {
-            if (!(ok = load_keys(pc, 1, nk, id))) break;
-            ++nk;
-            mine = mine << 1 | 1;
-          }
-        }
         for (int i = 0; i < pc.nt; ++i, ++n) {
           const int st = n % QST, ls = n % LST;
           if (n >= QST && !(ok = wait_all(B::QEMPTY + st, n / QST - 1))) break;
@@ -495,8 +497,22 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       }
       for (int j = max(0, n - QST); j < n && drain(B::QFULL + j % QST, j / QST); ++j) {
       }
-      for (int j = max(0, nk - KST); j < nk; ++j)
-        if (mine >> (nk - 1 - j) & 1 && !drain(B::KFULL + j % KST, j / KST)) break;
+    } else if (!WIDE && warp >= WARP_MORE && warp < WARP_MORE + 3) {
+      // ------------------------------------------- the other parts of key tiles
+      const int kt = (warp - WARP_MORE + 1) >> 1, part = (warp - WARP_MORE + 1) & 1;
+      int n = 0;                               // key tiles so far
+      uint32_t mine = 0;
+      Piece pc;
+      for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
+        const int tiles = tiles_of(pc);
+        for (int t = 0; t < tiles && ok; ++t) {
+          if (t == kt && !(ok = load_keys(pc, kt, part, n, page_of(pc, kt)))) break;
+          ++n;
+          mine = mine << 1 | (t == kt);
+        }
+        if (!ok) break;
+      }
+      drain_keys(part, n, mine);
     } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
       // ----------------------------------------------------------- MMA issuers
       // One for the even steps and one for the odd: the tensor pipe takes only a
@@ -516,8 +532,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         if (!nt) break;
         // in a piece without steps for this warp too: its word that it is done
         // with a K stage must not come before the one on the stage's last use
-        ok = wait_all(B::KFULL + nk % KST, nk / KST);
-        if (two) ok = ok && wait_all(B::KFULL + (nk + 1) % KST, (nk + 1) / KST);
+        ok = true;
+        for (int k = nk; k <= nk + two && ok; ++k)
+          for (int part = 0; part < PARTS && ok; ++part) ok = wait_all(B::KFULL + part * KST + k % KST, k / KST);
         if (!ok) break;
         for (int n = n0 + ((n0 ^ x) & 1); n < n0 + nt; n += 2) {
           const int qs = n % QST;
@@ -550,7 +567,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       drain(B::DRAIN, 0);
     }
   } else {
-    tc::setmaxnreg_inc<104>();
+    tc::setmaxnreg_inc<WIDE ? 104 : 88>();
     // ---------------------------------------------- exponentials and scores
     // Two pairs of warpgroups.  WIDE: a pair takes every second step, so that
     // one's waits and reads run under the other's exponentials; a warpgroup
@@ -750,16 +767,16 @@ cudaError_t launch_attn_weight(const WeightArgs& a, int d, bool f16, cudaStream_
       !encode_3d(&tk, f16, r.k, {dd, (cuuint64_t)r.page_size, (cuuint64_t)r.n_page * r.Hkv}, {dd * 2, dd * 2 * r.page_size},
                  {64, (cuuint32_t)p.BR, 1}))
     return cudaErrorInvalidValue;
-  auto launch = [&](auto kernel, int smem, int variant) -> cudaError_t {
+  auto launch = [&](auto kernel, int threads, int smem, int variant) -> cudaError_t {
     cudaError_t e = set_smem_once(kernel, smem, variant);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kernel, dim3(grid), NT, smem, st, tq, tk, p);
+    e = launch_dependent(kernel, dim3(grid), threads, smem, st, tq, tk, p);
     if (e != cudaSuccess || !p.shared) return e;
     return launch_dependent(weight_merge_kernel, dim3(grid), UK, 0, st, p);
   };
-#define SKV_WEIGHT(DD, FF, SS, VAR)                                                                \
-  (r.wait_ns ? launch(attn_weight_kernel<DD, FF, SS, true>, WCfg<DD, SS>::ALLOC, 8 + (VAR))        \
-             : launch(attn_weight_kernel<DD, FF, SS, false>, WCfg<DD, SS>::ALLOC, VAR))
+#define SKV_WEIGHT(DD, FF, SS, VAR)                                                                                 \
+  (r.wait_ns ? launch(attn_weight_kernel<DD, FF, SS, true>, WCfg<DD, SS>::NT, WCfg<DD, SS>::ALLOC, 8 + (VAR))      \
+             : launch(attn_weight_kernel<DD, FF, SS, false>, WCfg<DD, SS>::NT, WCfg<DD, SS>::ALLOC, VAR))
 #define SKV_WEIGHT_FORMS(DD, FF, VAR) (wide ? SKV_WEIGHT(DD, FF, true, VAR) : SKV_WEIGHT(DD, FF, false, VAR + 1))
   if (d == 128) return f16 ? SKV_WEIGHT_FORMS(128, true, 0) : SKV_WEIGHT_FORMS(128, false, 2);
   return f16 ? SKV_WEIGHT_FORMS(64, true, 4) : SKV_WEIGHT_FORMS(64, false, 6);
