@@ -681,7 +681,11 @@ int kv_paged_trim(const skv_paged* cache, int32_t n_req, const int32_t* state, c
  * A wait inside the kernel that passes cache->wait_ns sets SKV_DEV_TIMEOUT:
  * the requests' scores and positions are then undefined.
  * score and pos share no byte with anything else of the call (refused).
- * n_req <= SKV_PAGED_MAX_REQUESTS, other limits as for paged_attn.
+ * The call is one kernel launch, two where there are more than
+ * n_req * floor(128 / (Hq / Hkv)) rows.
+ * n_req <= SKV_PAGED_MAX_REQUESTS and n_tok <= 2^18 floor(128 / (Hq / Hkv)) (so
+ * that no wait lasts as long as a unit of keys against millions of rows);
+ * other limits as for paged_attn.
  */
 int paged_attn_weight(const skv_paged* cache, int32_t n_q_head, int32_t n_req, int32_t n_tok,
                       const void* q, int64_t q_stride, const int32_t* q_start,

@@ -111,7 +111,9 @@ int paged_attn_weight(const skv_paged* cache, int32_t n_q_head, int32_t n_req, i
   if ((long long)c->n_page * c->n_kv_head > 0x7FFFFFFFLL || !aligned(c->k, 16)) return SKV_ERR_INVALID;
   if (n_q_head < 1 || n_q_head % c->n_kv_head || n_req < 0 || n_tok < 0) return SKV_ERR_INVALID;
   if (n_q_head / c->n_kv_head > 128 || n_req > SKV_PAGED_MAX_REQUESTS) return SKV_ERR_UNSUPPORTED;
-  if (n_tok > (1 << 30) || (long long)n_tok * n_q_head > 0x7FFFFFFFLL) return SKV_ERR_UNSUPPORTED;
+  // a unit's query tiles, a microsecond or two each, end long before a wait gives up
+  if (n_tok > (1 << 18) * (128 / (n_q_head / c->n_kv_head)) || (long long)n_tok * n_q_head > 0x7FFFFFFFLL)
+    return SKV_ERR_UNSUPPORTED;
   if (!(sm_scale > 0.f) || isinf(sm_scale * skv::kLog2e)) return SKV_ERR_INVALID;
   if (n_req == 0 || n_tok == 0) return SKV_OK;
   if (!tensor_ok(q, q_stride, n_q_head, c->head_dim) || !aligned(q_start, 4) || !aligned(kv_len, 4)) return SKV_ERR_INVALID;

@@ -299,6 +299,9 @@ def test_evictions_refused_as_too_large(L):
     assert _weight(L, n_req=skv.SKV_PAGED_MAX_REQUESTS + 1) == skv.SKV_ERR_UNSUPPORTED
     assert _weight(L, hq=258) == skv.SKV_ERR_UNSUPPORTED                 # 129 query heads per kv head
     assert _weight(L, n_tok=1 << 30) == skv.SKV_ERR_UNSUPPORTED
+    # 2^18 query tiles of 64 tokens (two query heads per kv head); 2^31 rows
+    assert _weight(L, n_tok=(1 << 24) + 1) == skv.SKV_ERR_UNSUPPORTED
+    assert _weight(L, hq=256, qs=256 * 64, n_tok=(1 << 18) + 1) == skv.SKV_ERR_UNSUPPORTED
     for call in (_select, _move):
         assert call(L, n_layer=1 << 15, n_req=1 << 11) == skv.SKV_ERR_UNSUPPORTED
 
