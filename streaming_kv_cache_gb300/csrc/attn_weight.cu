@@ -20,6 +20,13 @@
 // CTAs share leaves its sums in the workspace, and a second kernel adds them up
 // in order, so that results do not depend on timing; else units stay whole.
 //
+// A step is a query tile against the unit's two key tiles.  Steps run in two
+// lines, each with an MMA issuer, a score buffer, a pair of warpgroups and its
+// own query stages: with many rows the even and the odd steps, with few the
+// even and the odd pieces.  A wait names the parity of a phase only, so whoever
+// waits on a barrier waits for each of its phases, in order; a line's barriers
+// serve that line alone.
+//
 //   warps 0 .. 15  four warpgroups, a thread per key: exponentials, sums, scores
 //   then           scheduler and K producer (TMA), Q producer (TMA), two MMA
 //                  issuers; with few rows three more K producers
@@ -41,7 +48,7 @@ constexpr int BN = 128;       // rows of a query tile, at most
 constexpr int EPI_WARPS = 16, WARP_K = 16, WARP_Q = 17, WARP_MMA = 18;   // two MMA warps
 constexpr int WARP_MORE = 20;     // in the narrow form, three more K producers
 constexpr int NP = 4;         // pieces in flight between the scheduler and the other warps
-constexpr int LST = 4;        // query tiles whose logarithms are in shared memory
+constexpr int LL = 2;         // query tiles of a line whose logarithms are in shared memory
 constexpr int WC = BN / 2;    // columns of a warpgroup in the wide form
 constexpr int LIST = 512;     // requests with rows that a CTA knows ahead
 
@@ -57,16 +64,17 @@ struct WCfg {
   // (64 columns at most): the key tiles pass, and the bytes in flight hide
   // HBM's latency.
   static constexpr int QR = WIDE ? BN : 64;    // rows of a query stage
-  static constexpr int KST = WIDE ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 10);
-  static constexpr int QST = WIDE ? (D == 128 ? 3 : 6) : (D == 128 ? 3 : 4);
+  static constexpr int KST = WIDE ? (D == 128 ? 2 : 6) : (D == 128 ? 4 : 10);
+  static constexpr int QST = WIDE ? (D == 128 ? 4 : 6) : 4;
+  static_assert(QST % 2 == 0, "a half for either line of steps");
   static constexpr int KT = BM * D * 2;        // bytes of a key tile
   static constexpr int HALF = BM * 128;        // one 64-dimension half of it
   static constexpr int QT = QR * D * 2;        // and of a query stage
   static constexpr int QHALF = QR * 128;
   static constexpr int K_OFF = 0;
   static constexpr int Q_OFF = KST * KT;
-  static constexpr int L_OFF = Q_OFF + QST * QT;             // logarithms of query tiles' columns, [LST][BN]
-  static constexpr int X_OFF = L_OFF + LST * BN * 4;         // sums of the upper warpgroups' columns, [3][2][BM]
+  static constexpr int L_OFF = Q_OFF + QST * QT;             // logarithms of query tiles' columns, [2 LL][BN]
+  static constexpr int X_OFF = L_OFF + 2 * LL * BN * 4;         // sums of the upper warpgroups' columns, [3][2][BM]
   static constexpr int BAR_OFF = X_OFF + 3 * 2 * BM * 4;
   static constexpr int MISC_OFF = BAR_OFF + 72 * 8;
   static constexpr int PIECE_OFF = MISC_OFF + 64;
@@ -84,11 +92,11 @@ struct WBars {
     KEMPTY = KFULL + PARTS * KST,   // MMA commit: the piece is done with it
     QFULL = KEMPTY + KST,      // Q tile landed
     QEMPTY = QFULL + QST,      // MMA commit
-    SFULL = QEMPTY + QST,      // MMA commit: a step's scores, of both key tiles, in buffer x
+    SFULL = QEMPTY + QST,      // MMA commit: a step's scores, of both key tiles, in its line's buffer
     SFREE = SFULL + 2,         // its warps have read them
     LFULL = SFREE + 2,         // Q producer: logarithms of a query tile written
-    LEMPTY = LFULL + LST,      // its warps are done with them
-    XFULL = LEMPTY + LST,      // WIDE: the upper warpgroups' sums of a lane group's keys
+    LEMPTY = LFULL + 2 * LL,      // its warps are done with them
+    XFULL = LEMPTY + 2 * LL,      // WIDE: the upper warpgroups' sums of a lane group's keys
     XEMPTY = XFULL + 4,        // they have been added
     PCFULL = XEMPTY + 4,       // scheduler: piece published
     PCEMPTY = PCFULL + NP,     // every other warp has read it
@@ -156,7 +164,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                    const __grid_constant__ WParams p) {
   using C = WCfg<D, WIDE>;
   using B = WBars<C::KST, C::QST, C::PARTS>;
-  constexpr int KST = C::KST, QST = C::QST, PARTS = C::PARTS, NT = C::NT;
+  constexpr int KST = C::KST, QST = C::QST, QL = QST / 2, PARTS = C::PARTS, NT = C::NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = tc::smem_u32(smem);
@@ -180,7 +188,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     for (int i = 0; i < B::COUNT; ++i) {
       int count = 1;
       if (i >= B::SFREE && i < B::SFREE + 2) count = 8;
-      if (i >= B::LEMPTY && i < B::LEMPTY + LST) count = 8;
+      if (i >= B::LEMPTY && i < B::LEMPTY + 2 * LL) count = 8;
       if ((i >= B::KEMPTY && i < B::KEMPTY + KST) || i == B::DRAIN) count = 2;
       if (i >= B::XFULL && i < B::XFULL + 4) count = 3;
       if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = (WIDE ? 3 : 6) + EPI_WARPS;
@@ -337,6 +345,8 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     __syncwarp();
     return true;
   };
+  // another warp's nth tile: its stage's phase is waited for all the same
+  auto pass_keys = [&](int n) { return n < KST || wait_all(B::KEMPTY + n % KST, n / KST - 1); };
   // the last copies that a warp has started into a part land before the CTA
   // exits; mine: which of the last tiles are (bit 0: the last of n)
   auto drain_keys = [&](int part, int n, uint32_t mine) {
@@ -438,7 +448,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         ++n;
         mine = mine << 1 | 1;
         if (tiles_of(pc) == 2) {
-          if (WIDE && !(ok = load_keys(pc, 1, 0, n, id1))) break;
+          if (!(ok = WIDE ? load_keys(pc, 1, 0, n, id1) : pass_keys(n))) break;
           ++n;
           mine = mine << 1 | WIDE;
         }
@@ -454,7 +464,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       // ------------------------------------------------------------ Q producer
       // With a query tile come the logarithms of its columns, four to a lane,
       // loaded a tile ahead: -lse log2 e, and -inf for a row that gives nothing.
-      int n = 0;
+      int steps = 0, line[2] = {};             // steps so far, and of either line
       int col_tok[4], col_off[4];              // token of a column, and its offset in lse
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -471,9 +481,10 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           for (int q = 0; q < 4; ++q) lg[q] = col_tok[q] < pc.L - t0 ? lse[col_off[q] + t0] : INFINITY;
         };
         load_log(pc.qa * TQ);
-        for (int i = 0; i < pc.nt; ++i, ++n) {
-          const int st = n % QST, ls = n % LST;
-          if (n >= QST && !(ok = wait_all(B::QEMPTY + st, n / QST - 1))) break;
+        for (int i = 0; i < pc.nt; ++i, ++steps) {
+          const int x = WIDE ? steps & 1 : pi & 1, m = line[x];
+          const int st = x * QL + m % QL, ls = x * LL + m % LL;
+          if (m >= QL && !(ok = wait_all(B::QEMPTY + st, m / QL - 1))) break;
           if (lane == 0) {
             tc::mbar_arrive_expect_tx(bar(B::QFULL + st), TQ * p.G * 128 * (D / 64));
 #pragma unroll
@@ -482,10 +493,8 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                               pc.q0 + (pc.qa + i) * TQ);
           }
           __syncwarp();
-          if (n >= LST && !(ok = wait_all(B::LEMPTY + ls, n / LST - 1))) {
-            ++n;                               // the query tile is on its way
-            break;
-          }
+          ++line[x];
+          if (m >= LL && !(ok = wait_all(B::LEMPTY + ls, m / LL - 1))) break;
 #pragma unroll
           for (int q = 0; q < 4; ++q) lg[q] = isfinite(lg[q]) ? lg[q] * -kLog2e : -INFINITY;
           *reinterpret_cast<float4*>(smem + C::L_OFF + (ls * BN + lane * 4) * 4) = make_float4(lg[0], lg[1], lg[2], lg[3]);
@@ -495,8 +504,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         if (!ok) break;
       }
-      for (int j = max(0, n - QST); j < n && drain(B::QFULL + j % QST, j / QST); ++j) {
-      }
+      for (int x = 0; x < 2; ++x)
+        for (int j = max(0, line[x] - QL); j < line[x] && drain(B::QFULL + x * QL + j % QL, j / QL); ++j) {
+        }
     } else if (!WIDE && warp >= WARP_MORE && warp < WARP_MORE + 3) {
       // ------------------------------------------- the other parts of key tiles
       const int kt = (warp - WARP_MORE + 1) >> 1, part = (warp - WARP_MORE + 1) & 1;
@@ -506,7 +516,8 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
         const int tiles = tiles_of(pc);
         for (int t = 0; t < tiles && ok; ++t) {
-          if (t == kt && !(ok = load_keys(pc, kt, part, n, page_of(pc, kt)))) break;
+          ok = t == kt ? load_keys(pc, kt, part, n, page_of(pc, kt)) : pass_keys(n);
+          if (!ok) break;
           ++n;
           mine = mine << 1 | (t == kt);
         }
@@ -515,14 +526,14 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       drain_keys(part, n, mine);
     } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
       // ----------------------------------------------------------- MMA issuers
-      // One for the even steps and one for the odd: the tensor pipe takes only a
-      // few MMAs ahead, so that one warp's waits and commits, about 650 cycles a
-      // step, would leave it idle; here the other's MMAs run under them.
+      // One for either line: the tensor pipe takes only a few MMAs ahead, so that
+      // one warp's waits and commits, about 650 cycles a step, would leave it
+      // idle; here the other's MMAs run under them.
       const uint32_t idesc = F16 ? tc::idesc_f16(BM, p.N) : tc::idesc_bf16(BM, p.N);
       const uint64_t dk0 = tc::sdesc_sw128(sbase + C::K_OFF), dq0 = tc::sdesc_sw128(sbase + C::Q_OFF);
       const bool lead = tc::elect_one();
-      const int x = warp - WARP_MMA;           // its steps, and its score buffer
-      int nk = 0, n0 = 0;                      // K tiles and steps before the piece
+      const int x = warp - WARP_MMA;           // its line
+      int nk = 0, n0 = 0, m = 0;               // K tiles and steps before the piece, steps of the line so far
       for (int pi = 0; ok; ++pi) {
         const int slot = pi % NP;
         if (!(ok = wait_all(B::PCFULL + slot, pi / NP))) break;
@@ -536,10 +547,11 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         for (int k = nk; k <= nk + two && ok; ++k)
           for (int part = 0; part < PARTS && ok; ++part) ok = wait_all(B::KFULL + part * KST + k % KST, k / KST);
         if (!ok) break;
-        for (int n = n0 + ((n0 ^ x) & 1); n < n0 + nt; n += 2) {
-          const int qs = n % QST;
-          ok = wait_all(B::QFULL + qs, n / QST);
-          if (n >= 2) ok = ok && wait_all(B::SFREE + x, (n >> 1) - 1);
+        const int mine = WIDE ? (nt + ((n0 ^ x) & 1 ? 0 : 1)) >> 1 : (pi & 1) == x ? nt : 0;   // steps of the piece
+        for (int i = 0; i < mine; ++i, ++m) {
+          const int qs = x * QL + m % QL;
+          ok = wait_all(B::QFULL + qs, m / QL);
+          if (m >= 1) ok = ok && wait_all(B::SFREE + x, m - 1);
           if (!ok) break;
           tc::tc_fence_after();
           if (lead) {
@@ -584,7 +596,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     float* s_x = reinterpret_cast<float*>(smem + C::X_OFF) + row;
     const float sl = p.scale_log2;
     const uint64_t sl2 = f2_pack(sl, sl);
-    int n = 0;                                       // steps of the CTA so far
+    int n = 0, m = 0;                                // steps of the CTA and of the line so far
     Piece pc;
     for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
       const bool two = tiles_of(pc) == 2;
@@ -606,19 +618,19 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       uint64_t acc[TILES][2] = {};
       for (int i = 0; i < pc.nt; ++i, ++n) {
         if (WIDE && (n & 1) != pair) continue;       // the other pair's
-        const int t0 = (pc.qa + i) * TQ, ls = n % LST;
+        const int t0 = (pc.qa + i) * TQ, ls = pair * LL + m % LL;
         const int nv = min(TQ, pc.L - t0) * p.G;     // columns with rows
         const int end = WIDE ? min(nv, col0 + WC) : tile && !two ? 0 : nv;
         // every key of the warp is seen by every row of these columns
         const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 && nv >= (end + CH - 1) / CH * CH && (!WIDE || two);
-        const uint32_t tS = t_lane + (2 * (n & 1) + tile) * BN;
-        ok = wait_all(B::LFULL + ls, n / LST) && wait_all(B::SFULL + (n & 1), n >> 1);
+        const uint32_t tS = t_lane + (2 * pair + tile) * BN;
+        ok = wait_all(B::LFULL + ls, m / LL) && wait_all(B::SFULL + pair, m);
         if (!ok) break;
         tc::tc_fence_after();
         auto release = [&]() {                       // the scores have been read
           tc::tc_fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(bar(B::SFREE + (n & 1)));
+          if (lane == 0) tc::mbar_arrive(bar(B::SFREE + pair));
         };
         if (end <= col0) release();
 #pragma unroll 1
@@ -654,6 +666,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar(B::LEMPTY + ls));
+        ++m;
       }
       if (!ok) break;
       float sum[TILES];
