@@ -23,9 +23,10 @@
 // A step is a query tile against the unit's two key tiles.  Steps run in two
 // lines, each with an MMA issuer, a score buffer, a pair of warpgroups and its
 // own query stages: with many rows the even and the odd steps, with few the
-// even and the odd pieces.  A wait names the parity of a phase only, so whoever
-// waits on a barrier waits for each of its phases, in order; a line's barriers
-// serve that line alone.
+// even and the odd pieces.  A wait names the parity of a phase only.  So whoever
+// waits on a barrier waits for each of its phases, and no phase ends without
+// those that wait for the one before: a line's barriers serve that line alone,
+// a K ring its own producers.
 //
 //   warps 0 .. 15  four warpgroups, a thread per key: exponentials, sums, scores
 //   then           scheduler and K producer (TMA), Q producer (TMA), two MMA
@@ -64,8 +65,11 @@ struct WCfg {
   // (64 columns at most): the key tiles pass, and the bytes in flight hide
   // HBM's latency.
   static constexpr int QR = WIDE ? BN : 64;    // rows of a query stage
-  static constexpr int KST = WIDE ? (D == 128 ? 2 : 6) : (D == 128 ? 4 : 10);
-  static constexpr int QST = WIDE ? (D == 128 ? 4 : 6) : 4;
+  static constexpr int KST = WIDE ? (D == 128 ? 3 : 6) : (D == 128 ? 4 : 10);
+  static constexpr int QST = WIDE ? (D == 128 ? 2 : 6) : 4;
+  // either key tile of a piece has a ring of its own where it has producers of its own
+  static constexpr int KR = WIDE ? KST : KST / 2;
+  static_assert(WIDE || KST % 2 == 0, "a ring for either key tile");
   static_assert(QST % 2 == 0, "a half for either line of steps");
   static constexpr int KT = BM * D * 2;        // bytes of a key tile
   static constexpr int HALF = BM * 128;        // one 64-dimension half of it
@@ -164,7 +168,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                    const __grid_constant__ WParams p) {
   using C = WCfg<D, WIDE>;
   using B = WBars<C::KST, C::QST, C::PARTS>;
-  constexpr int KST = C::KST, QST = C::QST, QL = QST / 2, PARTS = C::PARTS, NT = C::NT;
+  constexpr int KST = C::KST, QST = C::QST, QL = QST / 2, KR = C::KR, PARTS = C::PARTS, NT = C::NT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = tc::smem_u32(smem);
@@ -315,10 +319,12 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if (x < p.boxes && j < pc.kv) id = __ldcg(r.table + (size_t)pc.b * r.max_block + at);
     return id;
   };
-  // Part `part` of key tile kt of a piece, the CTA's nth, into its stage: a half
+  // The stage of key tile kt of a piece, its ring's nth.
+  auto k_stage = [&](int kt, int n) { return (WIDE ? 0 : kt * KR) + n % KR; };
+  // Part `part` of key tile kt of a piece, its ring's nth, into its stage: a half
   // of the dimensions (d = 64: every second box), a box at a time by one lane.
   auto load_keys = [&](const Piece& pc, int kt, int part, int n, int id) {
-    const int j0 = pc.k0 + kt * BM, st = n % KST;
+    const int j0 = pc.k0 + kt * BM, st = k_stage(kt, n);
     const int n_box = (min(BM, pc.kv - j0) + p.BR - 1) / p.BR;
     int in_page;
     fastdiv(j0 + (lane & 7) * p.BR, r.page_size, p.ps_m, in_page);
@@ -326,7 +332,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     const bool in = id >= 0 && id < r.n_page;
     if (!in && lane < n_box) set_status(r.status, SKV_DEV_BAD_PAGE);
     const int z = in ? id * r.Hkv + pc.h : -1;
-    if (n >= KST && !wait_all(B::KEMPTY + st, n / KST - 1)) return false;
+    if (n >= KR && !wait_all(B::KEMPTY + st, n / KR - 1)) return false;
     constexpr bool BOXES = PARTS == 2 && D == 64;
     const int first = BOXES ? part : 0, step = BOXES ? 2 : 1;
     constexpr int HALVES = PARTS == 2 ? 1 : D / 64;     // of this part's boxes
@@ -345,13 +351,10 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     __syncwarp();
     return true;
   };
-  // another warp's nth tile: its stage's phase is waited for all the same
-  auto pass_keys = [&](int n) { return n < KST || wait_all(B::KEMPTY + n % KST, n / KST - 1); };
-  // the last copies that a warp has started into a part land before the CTA
-  // exits; mine: which of the last tiles are (bit 0: the last of n)
-  auto drain_keys = [&](int part, int n, uint32_t mine) {
-    for (int j = max(0, n - KST); j < n; ++j)
-      if (mine >> (n - 1 - j) & 1 && !tc::mbar_sleep(bar(B::KFULL + part * KST + j % KST), (j / KST) & 1)) break;
+  // the last of the n copies that a warp has started into a ring land before the CTA exits
+  auto drain_keys = [&](int kt, int part, int n) {
+    for (int j = max(0, n - KR); j < n && tc::mbar_sleep(bar(B::KFULL + part * KST + k_stage(kt, j)), (j / KR) & 1); ++j) {
+    }
   };
 
   bool ok = true;
@@ -361,8 +364,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     tc::setmaxnreg_dec<64>();
     if (warp == WARP_K) {
       // --------------------------------------- scheduler and K producer, one warp
-      int n = 0, pi = 0;                         // key tiles so far, pieces published
-      uint32_t mine = 0;                         // of the last tiles (bit 0: the last), those that this warp loads
+      int n = 0, pi = 0;                         // key tiles of this warp so far, pieces published
       auto publish = [&](const Piece& pc) {
         const int slot = pi % NP;
         if (pi >= NP && !wait_all(B::PCEMPTY + slot, pi / NP - 1)) return false;
@@ -446,11 +448,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int next0 = page_of(next, 0), next1 = WIDE ? page_of(next, 1) : 0;
         if (!(ok = publish(pc) && load_keys(pc, 0, 0, n, id0))) break;
         ++n;
-        mine = mine << 1 | 1;
-        if (tiles_of(pc) == 2) {
-          if (!(ok = WIDE ? load_keys(pc, 1, 0, n, id1) : pass_keys(n))) break;
+        if (WIDE && tiles_of(pc) == 2) {
+          if (!(ok = load_keys(pc, 1, 0, n, id1))) break;
           ++n;
-          mine = mine << 1 | WIDE;
         }
         pc = next;
         id0 = next0;
@@ -459,7 +459,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (ok) ok = publish(Piece{});
       // always written: the second kernel reads it
       if (p.shared && lane == 0) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);
-      drain_keys(0, n, mine);
+      drain_keys(0, 0, n);
     } else if (warp == WARP_Q) {
       // ------------------------------------------------------------ Q producer
       // With a query tile come the logarithms of its columns, four to a lane,
@@ -510,20 +510,14 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     } else if (!WIDE && warp >= WARP_MORE && warp < WARP_MORE + 3) {
       // ------------------------------------------- the other parts of key tiles
       const int kt = (warp - WARP_MORE + 1) >> 1, part = (warp - WARP_MORE + 1) & 1;
-      int n = 0;                               // key tiles so far
-      uint32_t mine = 0;
+      int n = 0;                               // tiles of the ring so far
       Piece pc;
       for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
-        const int tiles = tiles_of(pc);
-        for (int t = 0; t < tiles && ok; ++t) {
-          ok = t == kt ? load_keys(pc, kt, part, n, page_of(pc, kt)) : pass_keys(n);
-          if (!ok) break;
-          ++n;
-          mine = mine << 1 | (t == kt);
-        }
-        if (!ok) break;
+        if (kt == 1 && tiles_of(pc) == 1) continue;
+        if (!(ok = load_keys(pc, kt, part, n, page_of(pc, kt)))) break;
+        ++n;
       }
-      drain_keys(part, n, mine);
+      drain_keys(kt, part, n);
     } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
       // ----------------------------------------------------------- MMA issuers
       // One for either line: the tensor pipe takes only a few MMAs ahead, so that
@@ -533,7 +527,8 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       const uint64_t dk0 = tc::sdesc_sw128(sbase + C::K_OFF), dq0 = tc::sdesc_sw128(sbase + C::Q_OFF);
       const bool lead = tc::elect_one();
       const int x = warp - WARP_MMA;           // its line
-      int nk = 0, n0 = 0, m = 0;               // K tiles and steps before the piece, steps of the line so far
+      int k0 = 0, k1 = WIDE ? 1 : 0;           // either key tile's number in its ring
+      int n0 = 0, m = 0;                       // steps before the piece, steps of the line so far
       for (int pi = 0; ok; ++pi) {
         const int slot = pi % NP;
         if (!(ok = wait_all(B::PCFULL + slot, pi / NP))) break;
@@ -544,8 +539,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         // in a piece without steps for this warp too: its word that it is done
         // with a K stage must not come before the one on the stage's last use
         ok = true;
-        for (int k = nk; k <= nk + two && ok; ++k)
-          for (int part = 0; part < PARTS && ok; ++part) ok = wait_all(B::KFULL + part * KST + k % KST, k / KST);
+        for (int kt = 0; kt <= two && ok; ++kt)
+          for (int part = 0; part < PARTS && ok; ++part)
+            ok = wait_all(B::KFULL + part * KST + k_stage(kt, kt ? k1 : k0), (kt ? k1 : k0) / KR);
         if (!ok) break;
         const int mine = WIDE ? (nt + ((n0 ^ x) & 1 ? 0 : 1)) >> 1 : (pi & 1) == x ? nt : 0;   // steps of the piece
         for (int i = 0; i < mine; ++i, ++m) {
@@ -556,7 +552,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           tc::tc_fence_after();
           if (lead) {
             for (int kt = 0; kt <= two; ++kt) {
-              const uint64_t dk = tc::opaque(dk0 + ((uint32_t)((nk + kt) % KST * C::KT) >> 4));
+              const uint64_t dk = tc::opaque(dk0 + ((uint32_t)(k_stage(kt, kt ? k1 : k0) * C::KT) >> 4));
               const uint64_t dq = tc::opaque(dq0 + ((uint32_t)(qs * C::QT) >> 4));
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
@@ -571,8 +567,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         if (!ok) break;
         if (lead)
-          for (int kt = 0; kt <= two; ++kt) tc::mma_commit(bar(B::KEMPTY + (nk + kt) % KST));
-        nk += 1 + two;
+          for (int kt = 0; kt <= two; ++kt) tc::mma_commit(bar(B::KEMPTY + k_stage(kt, kt ? k1 : k0)));
+        k0 += WIDE ? 1 + two : 1;
+        k1 += WIDE ? 1 + two : two;
         n0 += nt;
       }
       if (lead) tc::mma_commit(bar(B::DRAIN));   // every MMA issued completes before TMEM is released
