@@ -113,7 +113,7 @@ struct WBars {
 struct WParams {
   WeightArgs w;
   int G, TQ;              // query heads per kv head, tokens per query tile
-  int N;                  // columns of an MMA: TQ G, a multiple of 16
+  int N;                  // columns of an MMA: TQ G, up to a multiple of 16 (wide: 32)
   int BR, boxes;          // rows per TMA box, boxes per key tile (8 at most)
   uint32_t ps_m;          // fastdiv multiplier of the page size
   bool shared;            // WIDE: CTAs share units
@@ -199,6 +199,18 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       tc::mbar_init(bar(i), count);
     }
     tc::fence_barrier_init();
+    tc::fence_proxy_async_smem();
+  }
+  if (WIDE) {
+    // Rows of the query stages that no copy writes, where a tile holds fewer than
+    // N: their columns then have scores of 0 and, with logarithms of -inf, weigh
+    // nothing without a mask (seven heads per kv head leave two of 128).
+    const int q0 = TQ * p.G, idle = p.N - q0;
+    for (int i = tid; i < idle * QST * (D / 64) * 8; i += NT) {
+      const int c = i & 7, hf = i / 8 % (D / 64), row = i / 8 / (D / 64);
+      *reinterpret_cast<uint4*>(smem + C::Q_OFF + row / idle * C::QT + hf * C::QHALF + (q0 + row % idle) * 128 + c * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    }
     tc::fence_proxy_async_smem();
   }
   if (warp == WARP_K) {
@@ -618,8 +630,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int t0 = (pc.qa + i) * TQ, ls = pair * LL + m % LL;
         const int nv = min(TQ, pc.L - t0) * p.G;     // columns with rows
         const int end = WIDE ? min(nv, col0 + WC) : tile && !two ? 0 : nv;
-        // every key of the warp is seen by every row of these columns
-        const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 && nv >= (end + CH - 1) / CH * CH && (!WIDE || two);
+        // every key of the warp is seen by every row of the tile, which is full
+        const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 &&
+                         (WIDE ? two && t0 + TQ <= pc.L : nv >= (end + CH - 1) / CH * CH);
         const uint32_t tS = t_lane + (2 * pair + tile) * BN;
         ok = wait_all(B::LFULL + ls, m / LL) && wait_all(B::SFULL + pair, m);
         if (!ok) break;
@@ -753,8 +766,8 @@ cudaError_t launch_attn_weight(const WeightArgs& a, int d, bool f16, cudaStream_
   while (p.TQ < most && p.TQ < mean) p.TQ *= 2;
   p.TQ = min(p.TQ, most);
   p.shared = r.n_tok > (long long)r.n_req * most;
-  p.N = (p.TQ * p.G + 15) / 16 * 16;
-  const bool wide = p.N > 64;
+  const bool wide = p.TQ * p.G > 64;
+  p.N = wide ? (p.TQ * p.G + 31) / 32 * 32 : (p.TQ * p.G + 15) / 16 * 16;   // wide: whole reads of 32 columns
   p.unit_cost = 2;
   p.BR = BM;
   while (r.page_size % p.BR) p.BR /= 2;
