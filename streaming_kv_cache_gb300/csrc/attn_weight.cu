@@ -14,6 +14,13 @@
 // shared memory while the query tiles pass, with few (decode) the key tiles
 // pass and a query tile is a few rows.
 //
+// With many rows it is bound by the loop of a score buffer, from its release over
+// the MMAs and their signal to the reads that release it again: 1950 cycles a
+// step of 1024 cycles of MMAs and as many of exponentials, and tensor memory holds
+// no third buffer (four chunks of 2,048 tokens over 6 to 13 k keys, 32 query and 8
+// kv heads of 128: 515 us, 1220 TFLOP/s).  With few it streams K (64 requests of
+// 0.4 to 8 k keys in pages of 16 tokens: 112 us, 5.1 TB/s).
+//
 // Units form one sequence, ordered by request, kv head and key block, each as
 // long as its query tiles and unit_cost more; CTA c of a persistent grid takes
 // positions [c W, (c + 1) W) of it.  In calls of many rows a unit that several
@@ -59,7 +66,7 @@ struct WCfg {
   // K producers of a key tile.  A copy of a small page's 16 rows takes the
   // issuing warp some 150 cycles, a key tile of them 2500, in which HBM would
   // bring two: with few rows each half of each tile has a warp (64 requests, pages of 16
-  // tokens: 135 us with one warp per tile, 111 so).
+  // tokens: 135 us with one warp per tile, 112 so).
   static constexpr int PARTS = WIDE ? 1 : 2;
   // K and Q stages.  Many rows: the key tiles stay, the query tiles pass.  Few
   // (64 columns at most): the key tiles pass, and the bytes in flight hide
@@ -188,16 +195,15 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int TQ = p.TQ;
 
-  if (tid == 0) {
-    for (int i = 0; i < B::COUNT; ++i) {
-      int count = 1;
-      if (i >= B::SFREE && i < B::SFREE + 2) count = 8;
-      if (i >= B::LEMPTY && i < B::LEMPTY + 2 * LL) count = 8;
-      if ((i >= B::KEMPTY && i < B::KEMPTY + KST) || i == B::DRAIN) count = 2;
-      if (i >= B::XFULL && i < B::XFULL + 4) count = 3;
-      if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = (WIDE ? 3 : 6) + EPI_WARPS;
-      tc::mbar_init(bar(i), count);
-    }
+  if (tid < B::COUNT) {
+    const int i = tid;
+    int count = 1;
+    if (i >= B::SFREE && i < B::SFREE + 2) count = 8;
+    if (i >= B::LEMPTY && i < B::LEMPTY + 2 * LL) count = 8;
+    if ((i >= B::KEMPTY && i < B::KEMPTY + KST) || i == B::DRAIN) count = 2;
+    if (i >= B::XFULL && i < B::XFULL + 4) count = 3;
+    if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = (WIDE ? 3 : 6) + EPI_WARPS;
+    tc::mbar_init(bar(i), count);
     tc::fence_barrier_init();
     tc::fence_proxy_async_smem();
   }

@@ -54,7 +54,7 @@ __device__ __forceinline__ long long fixed(float x, bool& odd) {
 // lacks is exact, and goes on to 2^-19 and 2^-32.  Seven additions and no
 // 64-bit arithmetic: fixed() takes 17 instructions, and a conversion to 64 bits
 // ten times as long (64 requests over 151,936 entries: 55 us with the
-// conversion, 34 with fixed(), 20.6 so).
+// conversion, 34 with fixed(), 20.8 so).
 struct Limbs {
   uint32_t a, b, c;
 };
@@ -66,8 +66,10 @@ __device__ __forceinline__ Limbs limbs(float x) {
 
 enum Mode { REST, FULL, WITHOUT };    // max(p - q, 0); p; p but for the rejected token
 
-// One cluster per request: its CTAs' warps take runs of the row, sum them, and
-// the warp whose run holds the draw goes over it once more, out of L1 or L2.
+// One cluster per request: its CTAs' warps take runs of the row and sum them;
+// the CTA whose part holds the draw goes over one warp's run once more, out of
+// L1 or L2.  One request is bound by latency (9.7 us for 8 drafts over 151,936
+// entries), many by that chain and HBM (64 requests 20.8 us, 0.55 of its rate).
 // VEC: rows start on 16-byte boundaries and are read 16 bytes a lane; else an
 // entry a lane.
 template <typename T, bool VEC>
@@ -323,6 +325,9 @@ cudaError_t launch(const SampleArgs& in, cudaStream_t st) {
   SampleArgs a = in;
   const bool vec = ((uintptr_t)a.p | (uintptr_t)a.q) % 16 == 0 && a.p_stride * sizeof(T) % 16 == 0 &&
                    (!a.q || a.q_stride * sizeof(T) % 16 == 0);
+  // Few requests: large CTAs and clusters (one request in a cluster of 8 13.4 us,
+  // of 16 9.3); many: all CTAs at once (64 requests with clusters of 4 and 256
+  // threads 50 us, of 8 38).
   const int threads = a.n_req < 16 ? VT : VT / 2;
   a.ctas = 1;
   while (a.ctas < MAX_CLUSTER && a.ctas * a.n_req < 304 && a.n_vocab > a.ctas * 2048) a.ctas *= 2;

@@ -92,6 +92,27 @@ def test_evict_long(held, keep):
         _plan(1, held, keep, 128, 1, 1, 4, 100, kind)
 
 
+@pytest.mark.parametrize("held,keep", [([300, 9000, 20000], [299, 4000, 19999]), ([5], [2]), ([16385, 40], [1, 39])])
+def test_evict_of_short_requests_in_long_table_rows(held, keep):
+    """Rows that hold 144,000 tokens: CTAs of a cluster that a request does not
+    need leave before the others meet."""
+    _plan(6, held, keep, 16, 2, 1, 2, 30, "weights", cols=9000)
+
+
+def test_evict_layer_by_layer():
+    """One layer's cache and scores give what all layers at once give."""
+    whole, ws = _plan(21, [333, 150], [100, 149], 16, 2, 3, 3, 20, "ties")
+    again, s2 = _plan(21, [333, 150], [100, 149], 16, 2, 3, 3, 20, "ties")
+    kv, keep = ints([333, 150]), ints([60, 140])
+    skv.kv_evict_plan(whole, ws, kv, keep, 3, 20)
+    skv.kv_evict_move(whole, ws, kv)
+    for l in (-1, 0, 1):
+        skv.kv_evict_plan(again.layer(l), s2.layer(l), kv, keep, 3, 20)
+        skv.kv_evict_move(again.layer(l), s2.layer(l), kv)
+    for x, y in ((whole._k, again._k), (whole._v, again._v), (ws.score, s2.score), (ws.pos, s2.pos), (ws.move, s2.move), (ws.n_move, s2.n_move)):
+        assert torch.equal(x, y)
+
+
 def test_evict_without_evicted_words():
     _plan(2, [90, 33], [40, 32], 16, 2, 1, 2, 5, "weights", evicted=False)
 
