@@ -15,6 +15,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "evict.h"
 #include "skv.h"
@@ -320,6 +322,34 @@ __global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs 
   if (__any_sync(0xffffffffu, odd) && lane == 0) set_status(a.status, SKV_DEV_BAD_PROB);
 }
 
+// CTAs that a cluster may have: 16 where the device can hold one so large (more
+// than 8 is not portable), asked once per device and kernel.
+template <typename T, typename K>
+cudaError_t largest_cluster(K kernel, int variant, int& most) {
+  static std::atomic<int> known[64][2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  most = dev >= 0 && dev < 64 ? known[dev][variant].load(std::memory_order_relaxed) : 0;
+  if (most) return cudaSuccess;
+  if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = MAX_CLUSTER;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(MAX_CLUSTER);
+  cfg.blockDim = dim3(VT);
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int fit = 0;
+  e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  most = fit > 0 ? MAX_CLUSTER : 8;
+  if (dev >= 0 && dev < 64) known[dev][variant].store(most, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 template <typename T>
 cudaError_t launch(const SampleArgs& in, cudaStream_t st) {
   SampleArgs a = in;
@@ -329,13 +359,14 @@ cudaError_t launch(const SampleArgs& in, cudaStream_t st) {
   // of 16 9.3); many: all CTAs at once (64 requests with clusters of 4 and 256
   // threads 50 us, of 8 38).
   const int threads = a.n_req < 16 ? VT : VT / 2;
-  a.ctas = 1;
-  while (a.ctas < MAX_CLUSTER && a.ctas * a.n_req < 304 && a.n_vocab > a.ctas * 2048) a.ctas *= 2;
   auto kernel = vec ? verify_sampled_kernel<T, true> : verify_sampled_kernel<T, false>;
-  if (a.ctas > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  int most = 8;
+  if (a.n_req * 8 < 304) {
+    const cudaError_t e = largest_cluster<T>(kernel, vec, most);
     if (e != cudaSuccess) return e;
   }
+  a.ctas = 1;
+  while (a.ctas < most && a.ctas * a.n_req < 304 && a.n_vocab > a.ctas * 2048) a.ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
