@@ -19,7 +19,7 @@
 // step of 1024 cycles of MMAs and as many of exponentials, and tensor memory holds
 // no third buffer (four chunks of 2,048 tokens over 6 to 13 k keys, 32 query and 8
 // kv heads of 128: 515 us, 1220 TFLOP/s).  With few it streams K (64 requests of
-// 0.4 to 8 k keys in pages of 16 tokens: 112 us, 5.1 TB/s).
+// 0.4 to 8 k keys in pages of 16 tokens: 105 us, 5.4 TB/s).
 //
 // Units form one sequence, ordered by request, kv head and key block, each as
 // long as its query tiles and unit_cost more; CTA c of a persistent grid takes
@@ -36,8 +36,8 @@
 // a K ring its own producers.
 //
 //   warps 0 .. 15  four warpgroups, a thread per key: exponentials, sums, scores
-//   then           scheduler and K producer (TMA), Q producer (TMA), two MMA
-//                  issuers; with few rows three more K producers
+//   then           scheduler (with many rows K producer too), Q producer (TMA),
+//                  two MMA issuers; with few rows four K producers (TMA)
 #include <math.h>
 
 #include "common.cuh"
@@ -54,7 +54,7 @@ constexpr int BM = 128;       // keys of a key tile
 constexpr int UK = 2 * BM;    // and of a unit
 constexpr int BN = 128;       // rows of a query tile, at most
 constexpr int EPI_WARPS = 16, WARP_K = 16, WARP_Q = 17, WARP_MMA = 18;   // two MMA warps
-constexpr int WARP_MORE = 20;     // in the narrow form, three more K producers
+constexpr int WARP_MORE = 20;     // in the narrow form, four K producers
 constexpr int NP = 4;         // pieces in flight between the scheduler and the other warps
 constexpr int LL = 2;         // query tiles of a line whose logarithms are in shared memory
 constexpr int WC = BN / 2;    // columns of a warpgroup in the wide form
@@ -65,8 +65,9 @@ struct WCfg {
   static constexpr int NT = WIDE ? 640 : 768;
   // K producers of a key tile.  A copy of a small page's 16 rows takes the
   // issuing warp some 150 cycles, a key tile of them 2500, in which HBM would
-  // bring two: with few rows each half of each tile has a warp (64 requests, pages of 16
-  // tokens: 135 us with one warp per tile, 112 so).
+  // bring two: with few rows each half of each tile has a warp of its own (64 requests, pages of
+  // 16 tokens: 135 us with one warp per tile, 112 with the scheduler as one of four,
+  // 105 so).
   static constexpr int PARTS = WIDE ? 1 : 2;
   // K and Q stages.  Many rows: the key tiles stay, the query tiles pass.  Few
   // (64 columns at most): the key tiles pass, and the bytes in flight hide
@@ -202,7 +203,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     if (i >= B::LEMPTY && i < B::LEMPTY + 2 * LL) count = 8;
     if ((i >= B::KEMPTY && i < B::KEMPTY + KST) || i == B::DRAIN) count = 2;
     if (i >= B::XFULL && i < B::XFULL + 4) count = 3;
-    if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = (WIDE ? 3 : 6) + EPI_WARPS;
+    if (i >= B::PCEMPTY && i < B::PCEMPTY + NP) count = (WIDE ? 3 : 7) + EPI_WARPS;
     tc::mbar_init(bar(i), count);
     tc::fence_barrier_init();
     tc::fence_proxy_async_smem();
@@ -381,7 +382,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     // 512 x 88 + 256 x 64 = 768 x 80
     tc::setmaxnreg_dec<64>();
     if (warp == WARP_K) {
-      // --------------------------------------- scheduler and K producer, one warp
+      // --------------------------- scheduler, and in the wide form K producer, one warp
       int n = 0, pi = 0;                         // key tiles of this warp so far, pieces published
       auto publish = [&](const Piece& pc) {
         const int slot = pi % NP;
@@ -460,15 +461,16 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       };
       // a piece ahead, so that its pages' numbers come while the one before loads
       Piece pc = next_piece();
-      int id0 = page_of(pc, 0), id1 = WIDE ? page_of(pc, 1) : 0;
+      int id0 = WIDE ? page_of(pc, 0) : 0, id1 = WIDE ? page_of(pc, 1) : 0;
       while (pc.nt) {
         const Piece next = next_piece();
-        const int next0 = page_of(next, 0), next1 = WIDE ? page_of(next, 1) : 0;
-        if (!(ok = publish(pc) && load_keys(pc, 0, 0, n, id0))) break;
-        ++n;
-        if (WIDE && tiles_of(pc) == 2) {
-          if (!(ok = load_keys(pc, 1, 0, n, id1))) break;
-          ++n;
+        const int next0 = WIDE ? page_of(next, 0) : 0, next1 = WIDE ? page_of(next, 1) : 0;
+        if (!(ok = publish(pc))) break;
+        if (WIDE) {
+          for (int kt = 0; kt < tiles_of(pc) && ok; ++kt) {
+            if ((ok = load_keys(pc, kt, 0, n, kt ? id1 : id0))) ++n;
+          }
+          if (!ok) break;
         }
         pc = next;
         id0 = next0;
@@ -477,7 +479,7 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       if (ok) ok = publish(Piece{});
       // always written: the second kernel reads it
       if (p.shared && lane == 0) p.ws_unit[blockIdx.x] = ok ? shared_unit : make_int4(0, 0, 0, 0);
-      drain_keys(0, 0, n);
+      if (WIDE) drain_keys(0, 0, n);
     } else if (warp == WARP_Q) {
       // ------------------------------------------------------------ Q producer
       // With a query tile come the logarithms of its columns, four to a lane,
@@ -525,9 +527,9 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       for (int x = 0; x < 2; ++x)
         for (int j = max(0, line[x] - QL); j < line[x] && drain(B::QFULL + x * QL + j % QL, j / QL); ++j) {
         }
-    } else if (!WIDE && warp >= WARP_MORE && warp < WARP_MORE + 3) {
-      // ------------------------------------------- the other parts of key tiles
-      const int kt = (warp - WARP_MORE + 1) >> 1, part = (warp - WARP_MORE + 1) & 1;
+    } else if (!WIDE && warp >= WARP_MORE) {
+      // ------------------------------------- K producers: either tile, either part
+      const int kt = (warp - WARP_MORE) >> 1, part = (warp - WARP_MORE) & 1;
       int n = 0;                               // tiles of the ring so far
       Piece pc;
       for (int pi = 0; (ok = take_piece(pi, pc)) && pc.nt; ++pi) {
