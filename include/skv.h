@@ -745,9 +745,11 @@ int kv_evict_move(const skv_paged* cache, int32_t n_layer, int32_t n_req, const 
  * distributed as the target's own would be.  (stream_attn_verify's ids are the
  * greedy form.)
  *
- * Request b owns rows [q_start[b], q_start[b+1]), n of them (kv_paged_plan's
- * q_start): row 0 is the last accepted token, rows 1 .. n-1 the drafts.  Row i
- * of p and q is the distribution after token i.
+ * Request b owns rows [q_start[b], q_start[b+1]), n of them: row 0 is the last
+ * accepted token, rows 1 .. n-1 the drafts.  Row i of p and q is the
+ * distribution after token i.  The spans are kv_paged_plan's where every
+ * request of the step has a block; a prompt's rows are no drafts, and a request
+ * with some has its last row alone here, in a packing of the call's own.
  *
  * token:  device int32 [n_tok]
  * p:      device [n_tok][n_vocab] of dtype (SKV_BF16, SKV_FP16 or SKV_FP32),
