@@ -116,8 +116,7 @@ __global__ void __launch_bounds__(ET, 1024 / ET) evict_plan_kernel(const EvictAr
     if (tid == 0 && rank_cta == 0) *n_move = 0;
     return;
   }
-  // CTAs that take part: as many as hold the tokens in registers, more where
-  // the launch has few requests
+  // CTAs that take part: as many as hold the tokens in registers
   const int ctas = min(a.parts, (m + a.per_cta - 1) / a.per_cta);
   if (rank_cta >= ctas) return;
   const Place place = place_of(a, b, h);
@@ -418,11 +417,12 @@ cudaError_t launch_evict_plan(const EvictArgs& in, cudaStream_t st) {
   // As many threads as hold a full table row in registers: with 256 where 128
   // do, 64 requests at a budget of 2,048 take 41 us instead of 31; a cluster of
   // two CTAs of 256 instead of 512 threads 174 us for prompts instead of 98.
-  // CTAs of a cluster: what holds it; and where that leaves SMs idle, shorter
-  // slices.
+  // A cluster has as many CTAs as hold the row, and no more where that leaves SMs
+  // idle: its barriers cost more than shorter slices save (one request of 3,000
+  // tokens, 8 kv heads, over four CTAs 23.8 us, in one 9.5; of 60,000 tokens and 4
+  // layers over eight 91 us, over four 38).
   const int threads = room > 256 * KEYS ? 512 : room > 128 * KEYS ? 256 : 128;
   a.per_cta = threads * KEYS;
-  while (a.per_cta > 1024 && units * ((room + a.per_cta - 1) / a.per_cta) < 304) a.per_cta /= 2;
   a.parts = 1;
   while (a.parts < EVICT_CLUSTER && (long long)a.parts * a.per_cta < room) a.parts *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -446,7 +446,7 @@ cudaError_t launch_evict_move(const EvictArgs& a, int d, cudaStream_t st) {
   EvictArgs p = a;
   const long long units = (long long)a.n_layer * a.n_req * a.Hkv;
   // some 8,000 warps: one wave (32,000: prompts 114 -> 103 us, 64 requests with a move each 4.6 -> 8.3)
-  p.parts = (int)max(1LL, min(256LL, 8192 / units));
+  p.parts = (int)max(1LL, 8192 / units);
   const unsigned grid = (unsigned)((units * p.parts + MT / 32 - 1) / (MT / 32));
   auto launch = [&](auto kernel) { return launch_dependent(kernel, dim3(grid), MT, 0, st, p); };
   return d == 128 ? launch(evict_move_kernel<128>) : launch(evict_move_kernel<64>);

@@ -31,7 +31,7 @@ struct EvictArgs {
   const int32_t *keep, *evicted;
   int n_sink, n_recent;
   int parts;                  // CTAs of a (layer, request, kv head)
-  int per_cta;                // of a plan: tokens from which on one more of them takes part
+  int per_cta;                // of a plan: tokens that one of them holds
   float* score;               // pools [n_layer][n_page][Hkv][page_size]
   int32_t* pos;
   int32_t* move;
