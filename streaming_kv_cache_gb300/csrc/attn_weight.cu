@@ -7,7 +7,7 @@
 //
 // Keys are the rows of the MMA (M = 128) and queries its columns, so a TMEM
 // lane and the thread that reads it belong to one key: the sum over the
-// queries stays in a register and nothing is exchanged between threads.  A
+// queries stays in a register, and threads meet at a unit's end at most.  A
 // unit is 256 keys (two tiles) of one (request, kv head) against the query
 // tiles that see them; a query tile packs TQ tokens x the G query heads that
 // share the kv head.  K is read once; with many rows the two key tiles stay in

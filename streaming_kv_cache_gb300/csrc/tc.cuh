@@ -183,23 +183,6 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity, uint64
   return ok != 0;
 }
 
-// The same without the suspend hint (with it the wait sleeps in steps of its
-// own beside the hardware's): for waits on the critical path of a chain.
-__device__ __forceinline__ bool mbar_watch(uint32_t bar, uint32_t parity, uint64_t cycles = 1ull << 32) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 t0, t;\n mov.b32 %0, 1;\n"
-      " mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
-      " mov.u64 t0, %%clock64;\n"
-      "TRY:\n mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
-      " mov.u64 t, %%clock64;\n sub.u64 t, t, t0;\n setp.lt.u64 q, t, %3;\n @q bra TRY;\n mov.b32 %0, 0;\n"
-      "DONE:\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "l"(cycles)
-      : "memory");
-  return ok != 0;
-}
-
 // The same without sleeping, for limits shorter than a try of try_wait takes.
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint64_t cycles) {
   const long long t0 = clock64();
