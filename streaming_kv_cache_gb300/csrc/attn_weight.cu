@@ -184,6 +184,8 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   int* s_rank = reinterpret_cast<int*>(smem + C::MISC_OFF + 8);      // the share's first request among those with rows
   long long* s_off = reinterpret_cast<long long*>(smem + C::MISC_OFF + 16);
+  int* s_odd = reinterpret_cast<int*>(smem + C::MISC_OFF + 24);      // [2 LL] beside the logarithms: some row gives nothing
+  static_assert(24 + 2 * LL * sizeof(int) <= 64, "misc slots");
   Piece* s_piece = reinterpret_cast<Piece*>(smem + C::PIECE_OFF);
   uint16_t* s_list = reinterpret_cast<uint16_t*>(smem + C::LIST_OFF);
   struct Sums {
@@ -484,6 +486,10 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
       // ------------------------------------------------------------ Q producer
       // With a query tile come the logarithms of its columns, four to a lane,
       // loaded a tile ahead: -lse log2 e, and -inf for a row that gives nothing.
+      // Such a row's scores are most often not finite either, and a NaN or +inf
+      // outlasts -inf: a tile that has one says so, and its scores are looked
+      // through (all others pay for the word with 1.6% of a mixed batch at d = 64, and
+      // less than 1% of decode steps and chunks).
       int steps = 0, line[2] = {};             // steps so far, and of either line
       int col_tok[4], col_off[4];              // token of a column, and its offset in lse
 #pragma unroll
@@ -515,10 +521,17 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
           __syncwarp();
           ++line[x];
           if (m >= LL && !(ok = wait_all(B::LEMPTY + ls, m / LL - 1))) break;
+          bool odd = false;                    // of the columns with rows
 #pragma unroll
-          for (int q = 0; q < 4; ++q) lg[q] = isfinite(lg[q]) ? lg[q] * -kLog2e : -INFINITY;
+          for (int q = 0; q < 4; ++q) {
+            const bool fin = isfinite(lg[q]);
+            odd |= !fin && col_tok[q] < pc.L - (pc.qa + i) * TQ;
+            lg[q] = fin ? lg[q] * -kLog2e : -INFINITY;
+          }
           *reinterpret_cast<float4*>(smem + C::L_OFF + (ls * BN + lane * 4) * 4) = make_float4(lg[0], lg[1], lg[2], lg[3]);
           if (i + 1 < pc.nt) load_log((pc.qa + i + 1) * TQ);
+          odd = __any_sync(0xffffffffu, odd);
+          if (lane == 0) s_odd[ls] = odd;
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(bar(B::LFULL + ls));
         }
@@ -639,11 +652,13 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         const int nv = min(TQ, pc.L - t0) * p.G;     // columns with rows
         const int end = WIDE ? min(nv, col0 + WC) : tile && !two ? 0 : nv;
         // every key of the warp is seen by every row of the tile, which is full
-        const bool all = jw + (TILES - 1) * BM + 31 - old <= t0 &&
-                         (WIDE ? two && t0 + TQ <= pc.L : nv >= (end + CH - 1) / CH * CH);
+        bool all = jw + (TILES - 1) * BM + 31 - old <= t0 &&
+                   (WIDE ? two && t0 + TQ <= pc.L : nv >= (end + CH - 1) / CH * CH);
         const uint32_t tS = t_lane + (2 * pair + tile) * BN;
         ok = wait_all(B::LFULL + ls, m / LL) && wait_all(B::SFULL + pair, m);
         if (!ok) break;
+        const bool odd = tc::ld_shared_s32(sbase + C::MISC_OFF + 24 + ls * 4) != 0;
+        all &= !odd;
         tc::tc_fence_after();
         auto release = [&]() {                       // the scores have been read
           tc::tc_fence_before();
@@ -666,6 +681,16 @@ attn_weight_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
               for (int k = 0; k < CH; ++k)
                 if (k < lo || k >= nv - c0) v[t][k] = __float_as_uint(-INFINITY);
+            }
+            if (odd) {
+              // nor those of a row that gives nothing, whatever they are
+#pragma unroll
+              for (int k = 0; k < CH; ++k) {
+                const bool none = tc::ld_shared_s32(s_log + (ls * BN + c0 + k) * 4) == __float_as_int(-INFINITY);
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+                  if (none) v[t][k] = __float_as_uint(-INFINITY);
+              }
             }
           }
 #pragma unroll
