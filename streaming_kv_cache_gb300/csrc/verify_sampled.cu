@@ -8,7 +8,8 @@
 //
 // The comparison is exact: the product of two 24-bit significands fits a
 // double.  So are the sums, up to 2^-55 per entry: probabilities are summed as
-// whole numbers of 2^-55, which come out the same in any order, so that the
+// whole numbers of 2^-55, which come out the same in any order, and r times
+// their sum is cut to a whole number without rounding, so that the
 // token does not depend on how a row is split over threads (sums in fp32 would
 // move the borders between tokens by about 1e-9, and one draw in some
 // thousands over a vocabulary of 151,936 lies nearer to one than that).
@@ -64,6 +65,17 @@ __device__ __forceinline__ Limbs limbs(float x) {
   const float a = __fadd_rz(x, 16.f), r = x - (a - 16.f);
   const float b = __fadd_rz(r, 0x1p-19f), q = r - (b - 0x1p-19f);
   return {__float_as_uint(a), __float_as_uint(b), __float_as_uint(__fadd_rz(q, 0x1p-32f))};
+}
+
+// The whole part of r total, exact, for r below 1 (of r <= 0: 0) and total up to 2^58:
+// r is its significand times 2^-s, s at least 24.  In doubles the product would be off
+// by up to 6, a total of 2^55 having 56 bits.
+__device__ __forceinline__ unsigned long long share_of(unsigned long long total, float r) {
+  if (!(r > 0.f)) return 0;
+  const uint32_t u = __float_as_uint(r), e = max(u >> 23, 1u), s = 150 - e;
+  const unsigned long long m = (u & 0x7FFFFFu) | (u >> 23 ? 0x800000u : 0u);
+  const unsigned long long lo = total * m, hi = __umul64hi(total, m);      // hi below 2^18
+  return s < 64 ? hi << (64 - s) | lo >> s : s < 128 ? hi >> (s - 64) : 0;
 }
 
 enum Mode { REST, FULL, WITHOUT };    // max(p - q, 0); p; p but for the rejected token
@@ -249,7 +261,7 @@ __global__ void __launch_bounds__(VT, 2) verify_sampled_kernel(const SampleArgs 
       break;
     }
     // a running sum passes r total iff it passes its whole part; NaN: the first entry
-    const unsigned long long at = r > 0.f ? min(total - 1, (unsigned long long)((double)total * (double)fminf(r, 1.f))) : 0ull;
+    const unsigned long long at = r < 1.f ? share_of(total, r) : r >= 1.f ? total - 1 : 0ull;
     if (at >= before && at - before < mine) {
       // This CTA's part of the row has it.  The run of the warp that it falls
       // in is gone over by all warps, SU chunks each at a time: by that warp
