@@ -522,8 +522,9 @@ class PagedCache:
 
     theta gives the rope table of positions below max_block * page_size, or
     rope_len (None: keys and queries are not rotated).  evicts: tokens may be
-    evicted, so that a request's positions go on past the tokens that it holds
-    and rope_len is what limits them.  The layers of a model share
+    evicted, so that a request's positions go on past the tokens that it holds:
+    with theta rope_len is what limits them and has to be given, because a
+    token at a position past the table is not written.  The layers of a model share
     everything but k and v: layer(i) is the cache of one of them.  wait_ns
     limits every wait inside paged_attn (0: two seconds) and may be set later;
     everything else is fixed, because the calls keep its addresses.
@@ -536,6 +537,8 @@ class PagedCache:
 
     def __init__(self, n_page, page_size, Hkv, d, n_req, max_block, theta=None, dtype=torch.bfloat16,
                  n_layer=1, device="cuda", wait_ns=0, evicts=False, rope_len=None):
+        if evicts and theta is not None and rope_len is None:
+            raise ValueError("an evicting cache with theta needs rope_len: its positions go on past max_block * page_size")
         dev = torch.device(device)
         shape = (n_layer, n_page, Hkv, page_size, d)
         i32 = dict(dtype=torch.int32, device=dev)
