@@ -1027,6 +1027,8 @@ def kv_evict_plan(cache: PagedCache, scores: PagedScores, kv_len: torch.Tensor, 
     _on(kv_len, (cache.n_req,), torch.int32, "kv_len", dev)
     _on(keep, (cache.n_req,), torch.int32, "keep", dev)
     evicted = cache.state.data_ptr() + 4 * (cache.n_req + 2) if cache.evicts else None
+    # positions end at 2^31 - 1: larger counts protect no more (32 bits would be cut from them)
+    n_sink, n_recent = (min(max(n, -1), 0x7FFFFFFF) for n in (n_sink, n_recent))
     rc = lib().kv_evict_plan(cache._ref, n_layer, cache.n_req, kv_len.data_ptr(), keep.data_ptr(), evicted, n_sink, n_recent,
                              scores.score.data_ptr(), scores.pos.data_ptr(), scores.move.data_ptr(), scores.n_move.data_ptr(),
                              _raw_stream(dev))
