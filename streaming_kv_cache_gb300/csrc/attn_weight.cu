@@ -14,12 +14,18 @@
 // shared memory while the query tiles pass, with few (decode) the key tiles
 // pass and a query tile is a few rows.
 //
-// With many rows it is bound by the loop of a score buffer, from its release over
-// the MMAs and their signal to the reads that release it again: 1950 cycles a
-// step of 1024 cycles of MMAs and as many of exponentials, and tensor memory holds
-// no third buffer (four chunks of 2,048 tokens over 6 to 13 k keys, 32 query and 8
-// kv heads of 128: 515 us, 1220 TFLOP/s).  With few it streams K (64 requests of
-// 0.4 to 8 k keys in pages of 16 tokens: 105 us, 5.4 TB/s).
+// With many rows either pipe is idle half the time.  A step has 1024 cycles of MMAs
+// and as many of exponentials, and the two lines of steps (below) run in phase:
+// the odd line's MMAs start some 500 cycles after the even line's, both score
+// buffers are full 1850 cycles after their MMAs' start, then both lines take
+// exponentials, and 3700 cycles after the first start comes the next (time stamps
+// of one CTA).  Nothing but the release of its own buffer orders an issuer (four
+// chunks of 2,048 tokens over 6 to 13 k keys, 32 query and 8 kv heads of 128:
+// 515 us, 1220 TFLOP/s).  With few rows it streams K (64 requests of 0.4 to 8 k
+// keys in pages of 16 tokens: 105 us, 5.4 TB/s).  Between them lie mixed calls: a tile
+// that some of the keys do not see costs half as much again, and a unit against one
+// row what its one K producer takes for its copies (pages of 48 tokens: 16 of them,
+// 4800 cycles).
 //
 // Units form one sequence, ordered by request, kv head and key block, each as
 // long as its query tiles and unit_cost more; CTA c of a persistent grid takes
@@ -793,6 +799,14 @@ cudaError_t launch_attn_weight(const WeightArgs& a, int d, bool f16, cudaStream_
   WParams p;
   p.w = a;
   p.G = r.Hq / r.Hkv;
+  // The form goes by the call's rows and slots, which is all that the host knows:
+  // a tile holds the tokens that a slot has on average, and units are shared where
+  // that is more than a tile.  Idle slots, and single tokens beside a chunk, make the
+  // chunk's tiles small and leave its units whole.  32 query and 8 kv heads of 128: a
+  // chunk of 2,048 tokens over 8,192 keys takes 121 us in up to 16 slots, 163 in
+  // 64, 423 in 256, 1850 in 1,024, 3690 in 4,096; one of 512 tokens over 4,096 keys 32
+  // in 4 slots, 315 in 256.  One decoding request of 3,136 keys takes 9.5 us, in 4,096
+  // slots 13, beside 63 padding rows 12.
   const int most = BN / p.G;                 // tokens that a query tile may hold
   const int mean = (r.n_tok + r.n_req - 1) / r.n_req;
   p.TQ = 1;

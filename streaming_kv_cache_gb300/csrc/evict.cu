@@ -56,7 +56,8 @@ __device__ __forceinline__ int held_tokens(const EvictArgs& a, int b, bool& bad)
 // holds go over their tokens again for every digit.
 //
 // Bound by instructions and by the barriers of a CTA's chain, not by the 8 bytes
-// a token: 64 requests one token over 2,048, 4 layers and 8 kv heads, 28 us; four
+// a token: 64 requests one token over 2,048, 4 layers and 8 kv heads, 28 us with table
+// rows of up to 4,096 tokens (more with longer ones: launch_evict_plan); four
 // prompts of 6 to 12.8 k tokens, 36 layers, 86 us (HBM would take 16).
 
 constexpr int KEYS = 32;
@@ -421,6 +422,9 @@ cudaError_t launch_evict_plan(const EvictArgs& in, cudaStream_t st) {
   // idle: its barriers cost more than shorter slices save (one request of 3,000
   // tokens, 8 kv heads, over four CTAs 23.8 us, in one 9.5; of 60,000 tokens and 4
   // layers over eight 91 us, over four 38).
+  // The host knows the rows, not what the requests hold: the 64 requests of 2,049
+  // tokens take 28 us with rows of up to 4,096 tokens, 37 of 8,192, 71 of 12,864 and of
+  // 16,384, 135 of 32,768, 207 of 131,072.
   const int threads = room > 256 * KEYS ? 512 : room > 128 * KEYS ? 256 : 128;
   a.per_cta = threads * KEYS;
   a.parts = 1;

@@ -369,7 +369,7 @@ cudaError_t launch(const SampleArgs& in, cudaStream_t st) {
                    (!a.q || a.q_stride * sizeof(T) % 16 == 0);
   // Few requests: large CTAs and clusters (one request in a cluster of 8 13.4 us,
   // of 16 9.3); many: all CTAs at once (64 requests with clusters of 4 and 256
-  // threads 50 us, of 8 38).
+  // threads 50 us, of 8 38).  304: two CTAs for each of the 152 SMs.
   const int threads = a.n_req < 16 ? VT : VT / 2;
   auto kernel = vec ? verify_sampled_kernel<T, true> : verify_sampled_kernel<T, false>;
   int most = 8;
